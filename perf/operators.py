@@ -266,7 +266,7 @@ def _own(s):
             out["top_ids"], out["top_logprobs"] = r.top_ids, r.top_logprobs
         if c["kind"] == "logprob_train":
             out["grad_logits"] = vpa.token_logprobs_backward(
-                s["x"], v, w, sh, s["tok"], r.lse, r.entropy, s["g_lp"], s["g_ent"])
+                s["x"], v, w, sh, s["tok"], r.row_stats, s["g_lp"], s["g_ent"])
         return out
     if c["kind"] == "linear":
         return dict(y=vpa.head_linear(s["x"], s["w"], s["b"], c["act"], s["r"],
