@@ -614,3 +614,10 @@ def verify_ragged(logits, vocab, shard_width, n_shards, cu, draft_ids, total_dra
                                  block_draft, block_bonus, stream=stream)
     return greedy_verify_ragged(dst, bst, cu, draft_ids, total, with_targets, prefilling, accept,
                                 stream=stream)
+
+
+# The language-model head's operators (include/vpa_head.h).
+from .head import (ACTIVATIONS, HEAD_SYMBOLS, MAX_ROW_TOKENS, MAX_TOP,  # noqa: E402
+                   TokenLogprobs, combine_logprobs, head_call, head_lib, head_linear,
+                   head_linear_backward, layer_norm, layer_norm_backward, logprob_stats,
+                   logprobs_workspace, token_logprobs, token_logprobs_backward)

@@ -1,13 +1,15 @@
 """Build libvpa.so (HIP, gfx950) in-tree with hipcc, and the binding's
-CPython marshalling module _vpa_call with the host C compiler.
+CPython marshalling modules _vpa_call and _vpa_head_call with the host C
+compiler.
 
     python -m vocab_argmax_amd._build          # or: vocab_argmax_amd._build.build()
 
 Sources are compiled in parallel into vocab_argmax_amd/_build/ and linked into
 vocab_argmax_amd/libvpa.so.  Packed-fp32 instructions are disabled for the
-device code (the path has no float arithmetic; the flag keeps it that way).
-_vpa_call (csrc/pycall.c) does not link the library: the binding hands it the
-entry points of the libvpa.so it has loaded.
+device code.
+_vpa_call (csrc/pycall.c) and _vpa_head_call (csrc/headcall.c) do not link the
+library: the binding hands them the entry points of the libvpa.so it has
+loaded.
 """
 import os
 import shutil
@@ -21,9 +23,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvpa.so")
-SOURCES = ["api.hip", "block_stats.hip", "chunk_stats.hip", "reduce.hip"]
+SOURCES = ["api.hip", "block_stats.hip", "chunk_stats.hip", "reduce.hip",
+           "head_api.hip", "logprob.hip", "linear.hip", "layer_norm.hip"]
 ARCH = "gfx950"
-PYCALL = os.path.join(PKG, "_vpa_call" + sysconfig.get_config_var("EXT_SUFFIX"))
+MODULES = {"_vpa_call": "pycall.c", "_vpa_head_call": "headcall.c"}
 
 
 def hipcc() -> str:
@@ -67,25 +70,27 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(one, SOURCES))
     link(objs, LIB)
-    build_pycall(verbose)
+    for name, src in MODULES.items():
+        build_module(name, src, verbose)
     return LIB
 
 
-def build_pycall(verbose: bool = False) -> str:
-    """Compile csrc/pycall.c into the _vpa_call extension module."""
+def build_module(name: str, src: str, verbose: bool = False) -> str:
+    """Compile a marshalling module of csrc/ as a CPython extension."""
     cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
     if not cc:
-        raise RuntimeError("no host C compiler (gcc / cc) for _vpa_call")
+        raise RuntimeError(f"no host C compiler (gcc / cc) for {name}")
+    out = os.path.join(PKG, name + sysconfig.get_config_var("EXT_SUFFIX"))
     cmd = [cc, "-O2", "-std=gnu11", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC",
            f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}",
-           os.path.join(CSRC, "pycall.c"), "-o", PYCALL + ".tmp"]
+           os.path.join(CSRC, src), "-o", out + ".tmp"]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"_vpa_call failed to build:\n{res.stdout}\n{res.stderr}")
-    os.replace(PYCALL + ".tmp", PYCALL)
-    return PYCALL
+        raise RuntimeError(f"{name} failed to build:\n{res.stdout}\n{res.stderr}")
+    os.replace(out + ".tmp", out)
+    return out
 
 
 if __name__ == "__main__":

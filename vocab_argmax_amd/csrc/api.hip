@@ -10,6 +10,7 @@
 #include <mutex>
 #include <string>
 
+#include "vpa_host.h"
 #include "vpa_internal.h"
 
 // The statistics of vpa_top_tokens_noalloc: a file-scope device array.
@@ -21,8 +22,10 @@
 static __device__ __align__(256) vpa_stat scratch[VPA_NOALLOC_WORKSPACE_BYTES / sizeof(vpa_stat)];
 
 namespace {
-
 thread_local std::string g_last_error;
+}
+
+namespace vpa {
 
 vpa_status fail(vpa_status st, const char* fmt, ...) {
     char buf[512];
@@ -38,42 +41,11 @@ vpa_status hip_fail(hipError_t e, const char* what) {
     return fail(VPA_ERR_HIP, "%s: HIP error %d (%s)", what, (int)e, hipGetErrorString(e));
 }
 
-vpa_status ok() {
-    return VPA_OK;
-}
-
-// The dtype argument's integer value.  A C caller may pass any int as a
-// vpa_dtype, but in C++ loading an enum outside the range of its
-// enumerators is undefined (even to pass it on), so every entry point reads
-// its dtype argument's bytes as an int first and works with that int.
 int dtype_value(const vpa_dtype* dt) {
     static_assert(sizeof(vpa_dtype) == sizeof(int), "vpa_dtype is int-sized");
     int raw;
     memcpy(&raw, dt, sizeof raw);
     return raw;
-}
-
-int esize_of(int dt) {
-    return dt == VPA_BF16 ? 2 : (dt == VPA_F32 ? 4 : 0);
-}
-
-bool aligned(const void* p, size_t a) {
-    return ((uintptr_t)p % a) == 0;
-}
-
-// Slots per shard M (the most global blocks any shard touches), -1 if invalid.
-// At most VPA_MAX_SHARDS shards, so the scan below stays short.
-int64_t slots(int64_t w, int64_t s, int64_t b) {
-    if (w < 1 || s < 1 || s > VPA_MAX_SHARDS || b < 1)
-        return -1;
-    int64_t m = 0;
-    for (int64_t i = 0; i < s; ++i) {
-        const int64_t lo = i * w;
-        const int64_t n = (lo + w - 1) / b - lo / b + 1;
-        if (n > m)
-            m = n;
-    }
-    return m;
 }
 
 vpa_status check_vocab(const vpa_vocab& v) {
@@ -94,6 +66,34 @@ vpa_status check_dtype(int dt) {
     if (esize_of(dt) == 0)
         return fail(VPA_ERR_UNSUPPORTED, "dtype %d is not VPA_F32 or VPA_BF16", dt);
     return ok();
+}
+
+vpa_status check_dispatch(int64_t threads, const char* what) {
+    if (threads > kMaxDispatchThreads)
+        return fail(VPA_ERR_INVALID, "%s: %lld work-items exceed one dispatch (2^32 - 1)", what,
+                    (long long)threads);
+    return ok();
+}
+
+}  // namespace vpa
+
+namespace {
+
+using namespace vpa;
+
+// Slots per shard M (the most global blocks any shard touches), -1 if invalid.
+// At most VPA_MAX_SHARDS shards, so the scan below stays short.
+int64_t slots(int64_t w, int64_t s, int64_t b) {
+    if (w < 1 || s < 1 || s > VPA_MAX_SHARDS || b < 1)
+        return -1;
+    int64_t m = 0;
+    for (int64_t i = 0; i < s; ++i) {
+        const int64_t lo = i * w;
+        const int64_t n = (lo + w - 1) / b - lo / b + 1;
+        if (n > m)
+            m = n;
+    }
+    return m;
 }
 
 // Shared checks of the logits-reading calls; fills `t` with the geometry.
@@ -168,13 +168,6 @@ vpa_status check_epilogue(const vpa_epilogue* epi, int64_t min_len, int64_t* map
         return fail(VPA_ERR_INVALID, "mapped ids are required exactly when a d2t table is given");
     if (mapped && !aligned(mapped, 8))
         return fail(VPA_ERR_INVALID, "mapped not 8-byte aligned");
-    return ok();
-}
-
-vpa_status check_dispatch(int64_t threads, const char* what) {
-    if (threads > vpa::kMaxDispatchThreads)
-        return fail(VPA_ERR_INVALID, "%s: %lld work-items exceed one dispatch (2^32 - 1)", what,
-                    (long long)threads);
     return ok();
 }
 

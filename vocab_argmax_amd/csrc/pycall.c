@@ -20,16 +20,7 @@
  * This module converts arguments and nothing else: all validation of the
  * values, and every step of the computation, stays in the library.
  */
-#define PY_SSIZE_T_CLEAN
-#include <Python.h>
-
-#include <stdarg.h>
-#include <stdint.h>
-#include <string.h>
-
-#include "vpa.h"
-
-_Static_assert(sizeof(vpa_dtype) == sizeof(int32_t), "vpa_dtype is passed as an int32");
+#include "pycall_args.h"
 
 static __typeof__(&vpa_block_stats) p_block_stats;
 static __typeof__(&vpa_verify_stats) p_verify_stats;
@@ -41,10 +32,7 @@ static __typeof__(&vpa_top_tokens_noalloc) p_top_tokens_noalloc;
 static __typeof__(&vpa_greedy_verify) p_greedy_verify;
 static __typeof__(&vpa_greedy_verify_ragged) p_greedy_verify_ragged;
 
-static const struct {
-    const char* name;
-    void** slot;
-} k_entries[] = {
+static const struct entry k_entries[] = {
     {"vpa_block_stats", (void**)&p_block_stats},
     {"vpa_verify_stats", (void**)&p_verify_stats},
     {"vpa_verify_stats_rows", (void**)&p_verify_stats_rows},
@@ -56,138 +44,6 @@ static const struct {
     {"vpa_greedy_verify_ragged", (void**)&p_greedy_verify_ragged},
 };
 #define N_ENTRIES ((int)(sizeof(k_entries) / sizeof(k_entries[0])))
-
-static int to_i64(PyObject* o, int64_t* out) {
-    long long v = PyLong_AsLongLong(o);
-    if (v == -1 && PyErr_Occurred()) return 0;
-    *out = (int64_t)v;
-    return 1;
-}
-
-static int to_i32(PyObject* o, int32_t* out) {
-    long long v = PyLong_AsLongLong(o);
-    if (v == -1 && PyErr_Occurred()) return 0;
-    if (v < INT32_MIN || v > INT32_MAX) {
-        PyErr_Format(PyExc_OverflowError, "%lld does not fit a 32-bit argument", v);
-        return 0;
-    }
-    *out = (int32_t)v;
-    return 1;
-}
-
-static int to_size(PyObject* o, size_t* out) {
-    size_t v = PyLong_AsSize_t(o);
-    if (v == (size_t)-1 && PyErr_Occurred()) return 0;
-    *out = v;
-    return 1;
-}
-
-static int to_ptr(PyObject* o, void** out) {
-    if (o == Py_None) {
-        *out = NULL;
-        return 1;
-    }
-    unsigned long long v = PyLong_AsUnsignedLongLong(o);
-    if (v == (unsigned long long)-1 && PyErr_Occurred()) return 0;
-    *out = (void*)(uintptr_t)v;
-    return 1;
-}
-
-/* Converts args[0..nargs) by `fmt`, one character per Python argument:
- *   p pointer (void**), l int64 (int64_t*), i int32 (int32_t*), z size_t
- *   (size_t*), d dtype (vpa_dtype*, an int32 value), V vocab (vpa_vocab*, three
- *   arguments), e epilogue (vpa_epilogue* storage, then const vpa_epilogue**
- *   set to it or to NULL). */
-static int parse(const char* name, PyObject* const* args, Py_ssize_t nargs, const char* fmt,
-                 ...) {
-    Py_ssize_t want = 0;
-    for (const char* f = fmt; *f; ++f) want += (*f == 'V') ? 3 : 1;
-    if (nargs != want) {
-        PyErr_Format(PyExc_TypeError, "%s takes %zd arguments (%zd given)", name, want, nargs);
-        return 0;
-    }
-    va_list ap;
-    va_start(ap, fmt);
-    int ok = 1;
-    Py_ssize_t a = 0;
-    for (const char* f = fmt; ok && *f; ++f) {
-        switch (*f) {
-        case 'p':
-            ok = to_ptr(args[a++], va_arg(ap, void**));
-            break;
-        case 'l':
-            ok = to_i64(args[a++], va_arg(ap, int64_t*));
-            break;
-        case 'i':
-            ok = to_i32(args[a++], va_arg(ap, int32_t*));
-            break;
-        case 'z':
-            ok = to_size(args[a++], va_arg(ap, size_t*));
-            break;
-        case 'd': {
-            int32_t v = 0;
-            vpa_dtype* out = va_arg(ap, vpa_dtype*);
-            ok = to_i32(args[a++], &v);
-            /* the library reads the argument's bytes as an int, so any int32
-             * reaches its own range check */
-            if (ok) memcpy(out, &v, sizeof(v));
-            break;
-        }
-        case 'V': {
-            vpa_vocab* v = va_arg(ap, vpa_vocab*);
-            ok = to_i64(args[a], &v->vocab) && to_i64(args[a + 1], &v->shard_width) &&
-                 to_i32(args[a + 2], &v->n_shards);
-            a += 3;
-            break;
-        }
-        case 'e': {
-            vpa_epilogue* e = va_arg(ap, vpa_epilogue*);
-            const vpa_epilogue** pe = va_arg(ap, const vpa_epilogue**);
-            PyObject* o = args[a++];
-            if (o == Py_None) {
-                *pe = NULL;
-                break;
-            }
-            if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 3) {
-                PyErr_SetString(PyExc_TypeError,
-                                "an epilogue is None or a tuple (d2t, d2t_len, scale)");
-                ok = 0;
-                break;
-            }
-            void* d2t = NULL;
-            double scale = 0.0;
-            ok = to_ptr(PyTuple_GET_ITEM(o, 0), &d2t) &&
-                 to_i64(PyTuple_GET_ITEM(o, 1), &e->d2t_len);
-            if (ok) {
-                scale = PyFloat_AsDouble(PyTuple_GET_ITEM(o, 2));
-                ok = !(scale == -1.0 && PyErr_Occurred());
-            }
-            e->d2t = (const int64_t*)d2t;
-            e->scale = (float)scale;
-            *pe = e;
-            break;
-        }
-        default:
-            PyErr_Format(PyExc_SystemError, "%s: bad format character", name);
-            ok = 0;
-        }
-    }
-    va_end(ap);
-    return ok;
-}
-
-static int bound(const char* name, const void* fn) {
-    if (fn) return 1;
-    PyErr_Format(PyExc_RuntimeError, "%s is not bound: call bind() with its address first", name);
-    return 0;
-}
-
-#define RETURN_STATUS(call)                                                                     \
-    do {                                                                                        \
-        vpa_status st_;                                                                         \
-        Py_BEGIN_ALLOW_THREADS st_ = (call);                                                    \
-        Py_END_ALLOW_THREADS return PyLong_FromLong((long)st_);                                 \
-    } while (0)
 
 static PyObject* py_block_stats(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     (void)self;
@@ -330,44 +186,14 @@ static PyObject* py_greedy_verify_ragged(PyObject* self, PyObject* const* args,
 
 static PyObject* py_bind(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     (void)self;
-    if (nargs != 2 || !PyUnicode_Check(args[0])) {
-        PyErr_SetString(PyExc_TypeError, "bind(name: str, address: int)");
-        return NULL;
-    }
-    const char* name = PyUnicode_AsUTF8(args[0]);
-    void* addr = NULL;
-    if (!name || !to_ptr(args[1], &addr)) return NULL;
-    if (!addr) {
-        PyErr_Format(PyExc_ValueError, "bind(%s): null address", name);
-        return NULL;
-    }
-    for (int i = 0; i < N_ENTRIES; ++i) {
-        if (strcmp(k_entries[i].name, name) == 0) {
-            *k_entries[i].slot = addr;
-            Py_RETURN_NONE;
-        }
-    }
-    PyErr_Format(PyExc_KeyError, "%s is not an entry point this module calls", name);
-    return NULL;
+    return bind_entry(k_entries, N_ENTRIES, args, nargs);
 }
 
 static PyObject* py_entries(PyObject* self, PyObject* unused) {
     (void)self;
     (void)unused;
-    PyObject* t = PyTuple_New(N_ENTRIES);
-    if (!t) return NULL;
-    for (int i = 0; i < N_ENTRIES; ++i) {
-        PyObject* s = PyUnicode_FromString(k_entries[i].name);
-        if (!s) {
-            Py_DECREF(t);
-            return NULL;
-        }
-        PyTuple_SET_ITEM(t, i, s);
-    }
-    return t;
+    return entry_names(k_entries, N_ENTRIES);
 }
-
-#define FASTCALL(f) (PyCFunction)(void (*)(void))(f), METH_FASTCALL
 
 static PyMethodDef k_methods[] = {
     {"vpa_block_stats", FASTCALL(py_block_stats), "vpa_block_stats (include/vpa.h)"},

@@ -1,0 +1,85 @@
+// vpa_math.h -- device helpers of the head's operators: element conversion,
+// base-2 exponentials, and sums over a wavefront or workgroup.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace vpa {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Element types by size: bf16 is a uint16_t pattern in memory.
+template <int ESIZE>
+struct elem;
+template <>
+struct elem<2> {
+    using type = uint16_t;
+};
+template <>
+struct elem<4> {
+    using type = float;
+};
+
+__device__ __forceinline__ float to_f32(uint16_t h) {
+    return __builtin_bit_cast(float, (uint32_t)h << 16);
+}
+__device__ __forceinline__ float to_f32(float f) {
+    return f;
+}
+// fp32 to bf16, round to nearest even (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const f32x2 f = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
+}
+__device__ __forceinline__ void from_f32(uint16_t& d, float f) {
+    d = __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+__device__ __forceinline__ void from_f32(float& d, float f) {
+    d = f;
+}
+
+// 2^x by the hardware instruction: within 1 ulp, results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+    return __builtin_amdgcn_exp2f(x);
+}
+
+// Sum over the 64 lanes of a wavefront; every lane holds the result.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        v += __shfl_xor(v, off, 64);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        v = fmaxf(v, __shfl_xor(v, off, 64));
+    return v;
+}
+
+// Sum over a workgroup of WAVES wavefronts through `lds` (WAVES floats);
+// every thread holds the result.  Callers leave a barrier between two uses
+// of the same lds.
+template <int WAVES>
+__device__ __forceinline__ float block_sum(float v, float* lds) {
+    v = wave_sum(v);
+    if constexpr (WAVES == 1)
+        return v;
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float r = 0.0f;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i)
+        r += lds[i];
+    return r;
+}
+
+}  // namespace vpa

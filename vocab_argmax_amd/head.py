@@ -1,0 +1,442 @@
+"""The language-model head's operators: layer norm, the head's products and
+token log probabilities, each with its backward pass (include/vpa_head.h).
+
+The same thin binding as the package's greedy path, whose names re-export
+these: functions check devices, dtypes and strides, allocate outputs with
+torch, pass addresses and the current HIP stream, and every step of the
+computation runs in libvpa.so's HIP kernels.  Matrices are 2-D with
+contiguous columns and any row stride.
+
+The functions take part in no autograd graph: a backward pass is a call of
+its own, with the forward call's saved tensors as arguments (see
+examples/draft_head.py for a training step).
+"""
+import ctypes
+import functools
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import (VPA_BF16, VPA_F32, Vocab, _check, _dtype_code, _logits_ld, _on, _out_tensor,
+               _stream, _stream_arg, _vocab, _vp, lib)
+
+MAX_TOP = 64             # VPA_MAX_TOP
+MAX_ROW_TOKENS = 64      # VPA_MAX_ROW_TOKENS
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}   # vpa_act
+
+# Every symbol include/vpa_head.h declares; the first five are host-only.
+HEAD_SYMBOLS = ("vpa_logprobs_workspace", "vpa_logprob_words", "vpa_head_linear_workspace",
+                "vpa_head_linear_backward_workspace", "vpa_layer_norm_backward_workspace",
+                "vpa_logprob_stats", "vpa_combine_logprobs", "vpa_token_logprobs",
+                "vpa_token_logprobs_backward", "vpa_head_linear", "vpa_head_linear_backward",
+                "vpa_layer_norm", "vpa_layer_norm_backward")
+
+_bound_to = None
+_call_mod = None
+
+
+def _bind(loaded):
+    i64, i32, vp, sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
+    dt, f32 = ctypes.c_int, ctypes.c_float
+    signatures = {
+        "vpa_logprobs_workspace": (sz, [Vocab, i32, i64, i32]),
+        "vpa_logprob_words": (i32, [i32, i32]),
+        "vpa_head_linear_workspace": (sz, [dt, i64, i64, i64]),
+        "vpa_head_linear_backward_workspace": (sz, [dt, i64, i64, i64]),
+        "vpa_layer_norm_backward_workspace": (sz, [i64, i64]),
+        "vpa_logprob_stats": (dt, [vp, dt, i64, Vocab, i32, i32, i64, vp, i32, i32, vp, sz, vp, vp]),
+        "vpa_combine_logprobs": (dt, [vp, Vocab, i64, vp, i32, i32, vp, vp, vp, vp, vp, vp]),
+        "vpa_token_logprobs": (dt, [vp, dt, i64, Vocab, i64, vp, i32, i32, vp, sz, vp, vp, vp, vp,
+                                    vp, vp]),
+        "vpa_token_logprobs_backward": (dt, [vp, dt, i64, Vocab, i32, i32, i64, vp, i32, vp, vp,
+                                             vp, vp, i64, i64, vp]),
+        "vpa_head_linear": (dt, [vp, i64, vp, i64, vp, vp, i64, dt, i64, i64, i64, i32, vp, i64,
+                                 dt, vp, i64, vp, sz, vp]),
+        "vpa_head_linear_backward": (dt, [vp, i64, vp, i64, vp, i64, vp, i64, dt, i64, i64, i64,
+                                          i32, vp, i64, vp, i64, vp, vp, sz, vp]),
+        "vpa_layer_norm": (dt, [vp, i64, dt, vp, vp, dt, i64, i64, f32, vp, i64, vp, vp, vp]),
+        "vpa_layer_norm_backward": (dt, [vp, i64, vp, i64, dt, vp, dt, vp, vp, i64, i64, vp, i64,
+                                         vp, vp, vp, sz, vp]),
+    }
+    for name, (res, args) in signatures.items():
+        fn = getattr(loaded, name)
+        fn.restype, fn.argtypes = res, args
+
+
+def head_lib():
+    """The loaded libvpa.so with the head operators' signatures set."""
+    global _bound_to, _call_mod
+    loaded = lib()
+    if _bound_to is not loaded:
+        _bind(loaded)
+        try:
+            from . import _vpa_head_call
+        except ImportError as e:
+            raise RuntimeError("vocab_argmax_amd/_vpa_head_call is missing: build it with "
+                               f"`python -m vocab_argmax_amd._build` ({e})") from None
+        for name in _vpa_head_call.entries():
+            _vpa_head_call.bind(name, ctypes.cast(getattr(loaded, name), ctypes.c_void_p).value)
+        for fn in (_logprobs_workspace, _linear_workspace, _linear_grad_workspace,
+                   _norm_grad_workspace):
+            fn.cache_clear()
+        _call_mod, _bound_to = _vpa_head_call, loaded
+    return loaded
+
+
+def head_call():
+    """The launch entry points of include/vpa_head.h, bound to the loaded
+    libvpa.so (csrc/headcall.c); they take their C arguments in order."""
+    head_lib()
+    return _call_mod
+
+
+@functools.lru_cache(maxsize=256)
+def _logprobs_workspace(vocab, width, shards, n_local, rows, n_top):
+    return int(head_lib().vpa_logprobs_workspace(_vocab(vocab, width, shards), n_local, rows,
+                                                 n_top))
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_workspace(code, rows, outer, inner):
+    return int(head_lib().vpa_head_linear_workspace(code, rows, outer, inner))
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_grad_workspace(code, rows, outer, inner):
+    return int(head_lib().vpa_head_linear_backward_workspace(code, rows, outer, inner))
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_grad_workspace(rows, cols):
+    return int(head_lib().vpa_layer_norm_backward_workspace(rows, cols))
+
+
+def _workspace(workspace, need, device):
+    """A caller's workspace (a contiguous device tensor of at least `need`
+    bytes) or a new one; None if none is needed."""
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    if not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _matrix(t, name, device, dtype, shape):
+    """A 2-D operand with contiguous columns -> its row stride."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s columns must be contiguous (stride 1)")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _rows_of(t, name):
+    """The 2-D first operand of a call -> (rows, cols, row stride, dtype code)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s columns must be contiguous (stride 1)")
+    return (t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1],
+            VPA_BF16 if t.dtype == torch.bfloat16 else VPA_F32)
+
+
+# ---------------------------------------------------------------------------
+# token log probabilities
+# ---------------------------------------------------------------------------
+
+class TokenLogprobs(NamedTuple):
+    """Results of token_logprobs / combine_logprobs for N rows."""
+    logprobs: Optional[torch.Tensor]      # float32, the shape of token_ids
+    lse: torch.Tensor                     # float32 [N]: log sum exp of the row
+    entropy: torch.Tensor                 # float32 [N], nats (a column of row_stats)
+    top_ids: Optional[torch.Tensor]       # int32 [N, n_top]
+    top_logprobs: Optional[torch.Tensor]  # float32 [N, n_top]
+    row_stats: torch.Tensor               # float32 [N, 3]: max, log of the scaled sum, entropy
+
+
+def _tokens(token_ids, n, device):
+    """token_ids int32 [N] or [N, T] -> T (0 for None)."""
+    if token_ids is None:
+        return 0
+    if token_ids.dtype != torch.int32 or not token_ids.is_contiguous():
+        raise ValueError("token_ids must be a contiguous int32 tensor")
+    if token_ids.device != device:
+        raise ValueError(f"token_ids is on {token_ids.device}, logits on {device}")
+    if token_ids.dim() not in (1, 2) or token_ids.shape[0] != n:
+        raise ValueError(f"token_ids has shape {tuple(token_ids.shape)}, expected ({n},) or "
+                         f"({n}, tokens)")
+    return 1 if token_ids.dim() == 1 else token_ids.shape[1]
+
+
+def _logprob_outputs(n, token_ids, n_tokens, n_top, device):
+    """All outputs as views of one allocation; -> (TokenLogprobs, addresses)."""
+    words = n * (4 + n_tokens + 2 * n_top)
+    buf = torch.empty(words, dtype=torch.float32, device=device)
+    stats = buf.as_strided((n, 3), (3, 1), 0)
+    lse = buf.as_strided((n,), (1,), 3 * n)
+    lp = ids = tops = None
+    at = 4 * n
+    if n_tokens:
+        lp = buf.as_strided(token_ids.shape, token_ids.stride(), at)
+        at += n * n_tokens
+    if n_top:
+        ids = buf.view(torch.int32).as_strided((n, n_top), (n_top, 1), at)
+        tops = buf.as_strided((n, n_top), (n_top, 1), at + n * n_top)
+    out = TokenLogprobs(lp, lse, buf.as_strided((n,), (3,), 2), ids, tops, stats)
+    return out, (_vp(lp), lse.data_ptr(), stats.data_ptr(), _vp(ids), _vp(tops))
+
+
+@_stream_arg
+def token_logprobs(logits, vocab, shard_width, n_shards, token_ids=None, n_top=0,
+                   workspace=None, *, stream=None):
+    """Log probabilities of given tokens, entropy and the n_top most likely
+    tokens of each row, over all shards -> TokenLogprobs.
+
+    logits [N, ld], bf16 or fp32, holds the S shards side by side (ld >=
+    vocab).  token_ids: int32 [N] or [N, T], T <= MAX_ROW_TOKENS; -1 is a
+    placeholder with log probability 0, another id outside the vocabulary
+    gives NaN.  Alternatives come by value, the lower id first among equals.
+    Masked columns hold -inf.  workspace: optional device tensor of at least
+    logprobs_workspace() bytes."""
+    ld = _logits_ld(logits)
+    n, dev = logits.shape[0], logits.device
+    n_tokens = _tokens(token_ids, n, dev)
+    fn = head_call().vpa_token_logprobs
+    need = _logprobs_workspace(vocab, shard_width, n_shards, n_shards, n, n_top)
+    ws = _workspace(workspace, need, dev)
+    out, ptrs = _logprob_outputs(n, token_ids, n_tokens, max(n_top, 0), dev)
+    _check(_on(dev, fn, logits.data_ptr(), _dtype_code(logits), ld, vocab, shard_width, n_shards,
+               n, _vp(token_ids), n_tokens, n_top, _vp(ws), _bytes(ws), *ptrs,
+               _stream(stream, dev)))
+    return out
+
+
+def logprobs_workspace(vocab, shard_width, n_shards, n_rows, n_top=0, n_local=None) -> int:
+    """Workspace bytes of token_logprobs (n_local None) or logprob_stats."""
+    return _logprobs_workspace(vocab, shard_width, n_shards,
+                               n_shards if n_local is None else n_local, n_rows, n_top)
+
+
+@_stream_arg
+def logprob_stats(logits, vocab, shard_width, n_shards, token_ids=None, n_top=0, first_shard=0,
+                  n_local=None, workspace=None, *, stream=None):
+    """Records of shards first_shard..first_shard+n_local-1 for a job whose
+    ranks hold one shard each: int32 [n_local][N][words].  Gathered in rank
+    order along dim 0 they go to combine_logprobs.  logits [N, ld]: column 0
+    is global column first_shard * W; token_ids are global."""
+    ld = _logits_ld(logits)
+    n, dev = logits.shape[0], logits.device
+    if n_local is None:
+        n_local = n_shards - first_shard
+    n_tokens = _tokens(token_ids, n, dev)
+    words = head_lib().vpa_logprob_words(n_tokens, n_top)
+    if words < 0:
+        raise ValueError(f"at most {MAX_ROW_TOKENS} tokens and {MAX_TOP} alternatives a row")
+    ws = _workspace(workspace, _logprobs_workspace(vocab, shard_width, n_shards, n_local, n,
+                                                   n_top), dev)
+    out = torch.empty((max(n_local, 0), n, words), dtype=torch.int32, device=dev)
+    _check(_on(dev, head_call().vpa_logprob_stats, logits.data_ptr(), _dtype_code(logits), ld,
+               vocab, shard_width, n_shards, first_shard, n_local, n, _vp(token_ids), n_tokens,
+               n_top, _vp(ws), _bytes(ws), out.data_ptr(), _stream(stream, dev)))
+    return out
+
+
+@_stream_arg
+def combine_logprobs(stats, vocab, shard_width, token_ids=None, n_top=0, *, stream=None):
+    """All shards' records int32 [S][N][words] -> TokenLogprobs."""
+    if stats.dtype != torch.int32 or stats.dim() != 3 or not stats.is_contiguous():
+        raise ValueError("stats must be a contiguous int32 [shards][rows][words] tensor")
+    if not stats.is_cuda:
+        raise ValueError("stats must be a device tensor")
+    s, n, words = stats.shape
+    dev = stats.device
+    n_tokens = _tokens(token_ids, n, dev)
+    if words != head_lib().vpa_logprob_words(n_tokens, n_top):
+        raise ValueError(f"records of {words} words do not hold {n_tokens} tokens and {n_top} "
+                         "alternatives")
+    out, ptrs = _logprob_outputs(n, token_ids, n_tokens, n_top, dev)
+    _check(_on(dev, head_call().vpa_combine_logprobs, stats.data_ptr(), vocab, shard_width, s, n,
+               _vp(token_ids), n_tokens, n_top, *ptrs, _stream(stream, dev)))
+    return out
+
+
+@_stream_arg
+def token_logprobs_backward(logits, vocab, shard_width, n_shards, token_ids, row_stats,
+                            grad_logprobs, grad_entropy=None, first_shard=0, n_local=None,
+                            out=None, *, stream=None):
+    """Gradient by the logits, of their type and shape, for the gradients of
+    logprobs (float32, the shape of token_ids) and, optionally, of the
+    entropy (float32 [N]).  row_stats: the forward call's.  Columns past the
+    vocabulary get 0.  out: the gradient's tensor; it may be the logits
+    themselves, which are then replaced."""
+    ld = _logits_ld(logits)
+    n, dev = logits.shape[0], logits.device
+    if n_local is None:
+        n_local = n_shards - first_shard
+    n_tokens = _tokens(token_ids, n, dev)
+    if (grad_logprobs is None) != (token_ids is None):
+        raise ValueError("grad_logprobs goes with token_ids")
+    for name, t, count in (("grad_logprobs", grad_logprobs, n * n_tokens),
+                           ("grad_entropy", grad_entropy, n), ("row_stats", row_stats, 3 * n)):
+        if t is not None:
+            _out_tensor(t, name, torch.float32, count, dev)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    gld = _matrix(out, "out", dev, logits.dtype, logits.shape)
+    _check(_on(dev, head_call().vpa_token_logprobs_backward, logits.data_ptr(),
+               _dtype_code(logits), ld, vocab, shard_width, n_shards, first_shard, n_local, n,
+               _vp(token_ids) if n_tokens else None, n_tokens, row_stats.data_ptr(),
+               _vp(grad_logprobs) if n_tokens else None, _vp(grad_entropy), out.data_ptr(), gld,
+               out.shape[1], _stream(stream, dev)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the head's products
+# ---------------------------------------------------------------------------
+
+def _activation(name):
+    try:
+        return ACTIVATIONS[name]
+    except KeyError:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, not {name!r}") \
+            from None
+
+
+@_stream_arg
+def head_linear(x, weight, bias=None, activation="none", residual=None, out=None, out_dtype=None,
+                with_pre=False, workspace=None, *, stream=None):
+    """y = residual + activation(x weight^T + bias) -> y [rows, outer], or
+    (y, pre) with_pre, pre = x weight^T + bias for the backward pass.
+
+    x [rows, inner], weight [outer, inner], bias [outer], residual [rows,
+    outer], all of x's dtype (bf16 or fp32).  activation: "none", "relu",
+    "gelu" (erf) or "silu".  out / out_dtype: y's tensor or type (x's dtype or
+    float32); out may be the residual itself, or one shard's columns of a
+    wider logits tensor."""
+    rows, inner, ldx, code = _rows_of(x, "x")
+    dev = x.device
+    if weight.dim() != 2:
+        raise ValueError("weight must be 2-D [outer, inner]")
+    outer = weight.shape[0]
+    ldw = _matrix(weight, "weight", dev, x.dtype, (outer, inner))
+    if bias is not None:
+        _out_tensor(bias, "bias", x.dtype, outer, dev)
+    ldr = 0 if residual is None else _matrix(residual, "residual", dev, x.dtype, (rows, outer))
+    if out is None:
+        out = torch.empty((rows, outer), dtype=out_dtype or x.dtype, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    if out.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"the output must be {x.dtype} or float32, not {out.dtype}")
+    ldy = _matrix(out, "out", dev, out.dtype, (rows, outer))
+    pre = torch.empty((rows, outer), dtype=x.dtype, device=dev) if with_pre else None
+    fn = head_call().vpa_head_linear
+    ws = _workspace(workspace, _linear_workspace(code, rows, outer, inner), dev)
+    _check(_on(dev, fn, x.data_ptr(), ldx, weight.data_ptr(), ldw, _vp(bias), _vp(residual), ldr,
+               code, rows, outer, inner, _activation(activation), out.data_ptr(), ldy,
+               VPA_F32 if out.dtype == torch.float32 else VPA_BF16, _vp(pre), outer, _vp(ws),
+               _bytes(ws), _stream(stream, dev)))
+    return (out, pre) if with_pre else out
+
+
+@_stream_arg
+def head_linear_backward(grad, x, weight, pre=None, activation="none", need_x=True,
+                         need_weight=True, need_bias=True, workspace=None, *, stream=None):
+    """(grad_x, grad_weight, grad_bias) of head_linear for the gradient of y
+    [rows, outer], each None where not needed; the residual's gradient is
+    `grad` itself.  pre: head_linear's, required with an activation."""
+    rows, outer, ldg, code = _rows_of(grad, "grad")
+    dev, dt = grad.device, grad.dtype
+    act = _activation(activation)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [rows, inner]")
+    inner = x.shape[1]
+    ldx = _matrix(x, "x", dev, dt, (rows, inner))
+    ldw = _matrix(weight, "weight", dev, dt, (outer, inner))
+    if act and pre is None:
+        raise ValueError(f"the backward pass of {activation} needs pre")
+    ldp = _matrix(pre, "pre", dev, dt, (rows, outer)) if act else 0
+    gx = torch.empty((rows, inner), dtype=dt, device=dev) if need_x else None
+    gw = torch.empty((outer, inner), dtype=dt, device=dev) if need_weight else None
+    gb = torch.empty(outer, dtype=dt, device=dev) if need_bias else None
+    fn = head_call().vpa_head_linear_backward
+    ws = _workspace(workspace, _linear_grad_workspace(code, rows, outer, inner), dev)
+    _check(_on(dev, fn, grad.data_ptr(), ldg, x.data_ptr(), ldx, weight.data_ptr(), ldw,
+               _vp(pre) if act else None, ldp, code, rows, outer, inner, act, _vp(gx), inner,
+               _vp(gw), inner, _vp(gb), _vp(ws), _bytes(ws), _stream(stream, dev)))
+    return gx, gw, gb
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+# ---------------------------------------------------------------------------
+
+def _norm_weight(t, name, like, wdtype, cols):
+    if t is None:
+        return wdtype
+    if t.dtype not in (like.dtype, torch.float32):
+        raise TypeError(f"{name} must be {like.dtype} or float32, not {t.dtype}")
+    if wdtype is not None and t.dtype != wdtype:
+        raise TypeError(f"weight and bias must have one dtype, not {wdtype} and {t.dtype}")
+    _out_tensor(t, name, t.dtype, cols, like.device)
+    return t.dtype
+
+
+@_stream_arg
+def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, with_stats=False, *, stream=None):
+    """y = (x - mean) / sqrt(variance + eps) * weight + bias over each row of
+    x [rows, cols] -> y, or (y, mean, rstd) with_stats (float32 [rows], for
+    the backward pass).  weight, bias [cols]: x's dtype or float32.  out may
+    be x itself."""
+    rows, cols, ldx, code = _rows_of(x, "x")
+    dev = x.device
+    wdt = _norm_weight(bias, "bias", x, _norm_weight(weight, "weight", x, None, cols), cols)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    ldy = _matrix(out, "out", dev, x.dtype, (rows, cols))
+    mean = rstd = None
+    if with_stats:
+        buf = torch.empty(2 * rows, dtype=torch.float32, device=dev)
+        mean, rstd = buf.as_strided((rows,), (1,), 0), buf.as_strided((rows,), (1,), rows)
+    _check(_on(dev, head_call().vpa_layer_norm, x.data_ptr(), ldx, code, _vp(weight), _vp(bias),
+               VPA_F32 if (wdt or x.dtype) == torch.float32 else VPA_BF16, rows, cols, eps,
+               out.data_ptr(), ldy, _vp(mean), _vp(rstd), _stream(stream, dev)))
+    return (out, mean, rstd) if with_stats else out
+
+
+@_stream_arg
+def layer_norm_backward(grad, x, mean, rstd, weight=None, need_x=True, need_weight=True,
+                        need_bias=True, workspace=None, *, stream=None):
+    """(grad_x, grad_weight, grad_bias) of layer_norm for the gradient of y,
+    each None where not needed.  mean, rstd: the forward call's.  grad_weight
+    and grad_bias have weight's dtype (x's where weight is None)."""
+    rows, cols, ldg, code = _rows_of(grad, "grad")
+    dev, dt = grad.device, grad.dtype
+    ldx = _matrix(x, "x", dev, dt, (rows, cols))
+    wdt = _norm_weight(weight, "weight", grad, None, cols) or dt
+    _out_tensor(mean, "mean", torch.float32, rows, dev)
+    _out_tensor(rstd, "rstd", torch.float32, rows, dev)
+    gx = torch.empty((rows, cols), dtype=dt, device=dev) if need_x else None
+    gw = torch.empty(cols, dtype=wdt, device=dev) if need_weight else None
+    gb = torch.empty(cols, dtype=wdt, device=dev) if need_bias else None
+    fn = head_call().vpa_layer_norm_backward
+    need = _norm_grad_workspace(rows, cols) if need_weight or need_bias else 0
+    ws = _workspace(workspace, need, dev)
+    _check(_on(dev, fn, grad.data_ptr(), ldg, x.data_ptr(), ldx, code, _vp(weight),
+               VPA_F32 if wdt == torch.float32 else VPA_BF16, mean.data_ptr(), rstd.data_ptr(),
+               rows, cols, _vp(gx), cols, _vp(gw), _vp(gb), _vp(ws), _bytes(ws),
+               _stream(stream, dev)))
+    return gx, gw, gb
