@@ -1,5 +1,6 @@
 // linear.hip -- the head's products: y = residual + act(x W^T + bias) and the
 // products of its backward pass, on the matrix cores with fp32 accumulation.
+#include "gemm_tile.h"
 #include "vpa_head_internal.h"
 #include "vpa_math.h"
 
@@ -106,6 +107,189 @@ __global__ __launch_bounds__(kThreads) void gemm_any_kernel(GemmTask t) {
         }
 }
 
+// Four results of consecutive n: 16- or 8-byte accesses (every row of the
+// outputs and the residual is aligned for them).
+template <typename T, int ACT>
+__device__ __forceinline__ void store_results(const GemmTask& t, int64_t m, int64_t n, f32x4 acc) {
+    using V = T __attribute__((ext_vector_type(4)));
+    if (t.bias)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc[i] += to_f32(((const T*)t.bias)[n + i]);
+    auto put = [](T* p, f32x4 v) {
+        if constexpr (sizeof(T) == 2)
+            *(uint2*)p = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else
+            *(f32x4*)p = v;
+    };
+    if (t.pre)
+        put((T*)t.pre + m * t.ldp + n, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        acc[i] = act<ACT>(acc[i]);
+    if (t.residual) {
+        const V r = *(const V*)((const T*)t.residual + m * t.ldr + n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc[i] += to_f32((T)r[i]);
+    }
+    if (t.out_f32)
+        *(f32x4*)((float*)t.y + m * t.ldy + n) = acc;
+    else
+        put((T*)t.y + m * t.ldy + n, acc);
+}
+
+// A wavefront's 64 x 64 results from accumulators to memory, through its own
+// 16 KiB of LDS so that a store instruction covers whole rows: 4 rows of 64
+// where `vec` says that rows are aligned for 4 elements, else one row, an
+// element a lane.  Rows of LDS have 16 chunks of 16 bytes, chunk c of row r
+// at c ^ (r & 15).
+template <typename T, int ACT>
+__device__ __forceinline__ void store_block(const GemmTask& t, bool vec, float* part, char* lds,
+                                            int64_t m0, int64_t n0, const f32x4 (&acc)[4][4]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = i * 16 + (lane & 15), c = j * 4 + (lane >> 4);
+            *(f32x4*)(lds + r * 256 + ((c ^ (r & 15)) << 4)) = acc[i][j];
+        }
+    // this LDS is the wavefront's alone and its accesses execute in order; the
+    // fences keep the compiler to it
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (vec && n0 + 64 <= t.n) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < 64; r0 += 16) {
+            f32x4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = r0 + k * 4 + (lane >> 4), c = lane & 15;
+                v[k] = *(const f32x4*)(lds + r * 256 + ((c ^ (r & 15)) << 4));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t m = m0 + r0 + k * 4 + (lane >> 4), n = n0 + (lane & 15) * 4;
+                if (m >= t.m)
+                    continue;
+                if (part)
+                    *(f32x4*)(part + m * t.n + n) = v[k];
+                else
+                    store_results<T, ACT>(t, m, n, v[k]);
+            }
+        }
+        return;
+    }
+    const int64_t n = n0 + lane;
+#pragma unroll 4
+    for (int r = 0; r < 64; ++r) {
+        const float v = *(const float*)(lds + r * 256 + (((lane >> 2) ^ (r & 15)) << 4) +
+                                        (lane & 3) * 4);
+        const int64_t m = m0 + r;
+        if (m >= t.m || n >= t.n)
+            continue;
+        if (part)
+            part[m * t.n + n] = v;
+        else
+            store_result<T, ACT>(t, m, n, v);
+    }
+}
+
+// The tiled product (gemm_tile.h): WM x WN wavefronts, each with BM/WM x
+// BN/WN of the tile in its accumulators.  With part set, blockIdx.y is a
+// slice of k and the raw sums go to part[slice][m][n].
+template <int ESIZE, bool AK, bool BK, int BM, int BN, int WM, int WN, int ACT>
+__global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint32_t tiles_m,
+                                                                uint32_t tiles_n,
+                                                                int64_t stages_per_slice,
+                                                                bool vec, float* part) {
+    using T = typename elem<ESIZE>::type;
+    constexpr int NT = WM * WN * 64;
+    constexpr int IM = BM / WM / 16, JN = BN / WN / 16;
+    static_assert(IM % 4 == 0 && JN == 4, "the epilogue stores blocks of 64 x 64");
+    using LA = TileLoader<ESIZE, AK, BM, NT>;
+    using LB = TileLoader<ESIZE, BK, BN, NT>;
+    __shared__ __align__(1024) char lds0[LA::BYTES + LB::BYTES];
+    __shared__ __align__(1024) char lds1[LA::BYTES + LB::BYTES];
+    uint32_t tm, tn;
+    tile_of_block(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
+    LA la;
+    LB lb;
+    la.init(t.a, AK ? t.a_m : t.a_k, m0, t.m);
+    lb.init(t.b, BK ? t.b_n : t.b_k, n0, t.n);
+    const int64_t whole = t.k / LA::KB, all = (t.k + LA::KB - 1) / LA::KB;
+    const int64_t s0 = blockIdx.y * stages_per_slice;
+    const int64_t end = s0 + stages_per_slice < all ? s0 + stages_per_slice : all;
+    f32x4 acc[IM][JN] = {};
+    auto stage = [&](int64_t s, char* lds) {
+        la.load(s, lds);
+        lb.load(s, lds + LA::BYTES);
+    };
+    auto multiply = [&](const char* lds) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            u32x4_t av[IM], bv[JN];
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+                bv[j] = LB::fragment(lds + LA::BYTES, wn + j * 16, s);
+#pragma unroll
+            for (int i = 0; i < IM; ++i)
+                av[i] = LA::fragment(lds, wm + i * 16, s);
+#pragma unroll
+            for (int i = 0; i < IM; ++i)
+#pragma unroll
+                for (int j = 0; j < JN; ++j)
+                    acc[i][j] = mma<ESIZE>(bv[j], av[i], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);      // one step's fragments at a time
+        }
+    };
+    // a stage that k ends in comes first, so that the loop has whole ones only
+    const int64_t s1 = end < whole ? end : whole;
+    if (end > whole) {
+        la.load_tail(whole, t.k, lds1);
+        lb.load_tail(whole, t.k, lds1 + LA::BYTES);
+    }
+    if (s0 < s1)
+        stage(s0, lds0);
+    if (end > whole) {
+        __syncthreads();
+        multiply(lds1);
+    }
+    for (int64_t s = s0; s < s1; s += 2) {
+        __syncthreads();
+        if (s + 1 < s1)
+            stage(s + 1, lds1);
+        multiply(lds0);
+        if (s + 1 >= s1)
+            break;
+        __syncthreads();
+        if (s + 2 < s1)
+            stage(s + 2, lds0);
+        multiply(lds1);
+    }
+    __syncthreads();
+    if (part)
+        part += (int64_t)blockIdx.y * t.m * t.n;
+    char* mine = wave * 16384 < LA::BYTES + LB::BYTES
+                     ? lds0 + wave * 16384 : lds1 + (wave * 16384 - LA::BYTES - LB::BYTES);
+#pragma unroll
+    for (int h = 0; h < IM / 4; ++h) {
+        f32x4 block[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                block[i][j] = acc[h * 4 + i][j];
+        store_block<T, ACT>(t, vec, part, mine, m0 + wm + h * 64, n0 + wn, block);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void dz_kernel(DzTask t, int32_t splits) {
     const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -152,6 +336,51 @@ hipError_t launch_gemm_any(const GemmTask& t, hipStream_t stream) {
     }
 }
 
+// The tiled kernel moves 16 bytes at a time: an operand with contiguous k
+// needs rows of 16-byte aligned address, one with contiguous rows a multiple
+// of 16 bytes of them too.  Offsets within a tile are 32 bits.
+bool tile_operand(int esize, const void* p, int64_t ld, bool k1, int64_t rows) {
+    const int64_t vec = 16 / esize;
+    return (uintptr_t)p % 16 == 0 && ld % vec == 0 && ld <= ((int64_t)1 << 21) &&
+           (k1 || rows % vec == 0);
+}
+
+bool vec4(const void* p, int64_t ld, int esize) {
+    return !p || ((uintptr_t)p % (4 * esize) == 0 && ld % 4 == 0);
+}
+
+template <int ESIZE, bool AK, bool BK, int ACT>
+hipError_t launch_tile(const GemmTask& t, hipStream_t stream) {
+    // fp32's instructions take 8 times as long for the same bytes, so half the
+    // tile feeds them, and its fragments leave registers free
+    constexpr int BM = ESIZE == 2 ? 256 : 128, BN = BM, WM = 2, WN = BN / 64;
+    const uint32_t tm = (uint32_t)((t.m + BM - 1) / BM), tn = (uint32_t)((t.n + BN - 1) / BN);
+    const int64_t stages = (t.k * ESIZE + 127) / 128;
+    const bool vec = vec4(t.y, t.ldy, t.out_f32 ? 4 : ESIZE) && vec4(t.pre, t.ldp, ESIZE) &&
+                     vec4(t.residual, t.ldr, ESIZE);
+    return launch(gemm_tile_kernel<ESIZE, AK, BK, BM, BN, WM, WN, ACT>, dim3(tm * tn),
+                  dim3(WM * WN * 64), 0, stream, t, tm, tn, stages, vec, nullptr);
+}
+
+template <int ESIZE>
+hipError_t launch_tile_any(const GemmTask& t, hipStream_t stream) {
+    const bool ak = t.a_k == 1, bk = t.b_k == 1;
+    if (!ak)
+        return launch_tile<ESIZE, false, false, VPA_ACT_NONE>(t, stream);
+    if (!bk)
+        return launch_tile<ESIZE, true, false, VPA_ACT_NONE>(t, stream);
+    switch (t.act) {
+    case VPA_ACT_RELU:
+        return launch_tile<ESIZE, true, true, VPA_ACT_RELU>(t, stream);
+    case VPA_ACT_GELU:
+        return launch_tile<ESIZE, true, true, VPA_ACT_GELU>(t, stream);
+    case VPA_ACT_SILU:
+        return launch_tile<ESIZE, true, true, VPA_ACT_SILU>(t, stream);
+    default:
+        return launch_tile<ESIZE, true, true, VPA_ACT_NONE>(t, stream);
+    }
+}
+
 template <typename T>
 hipError_t launch_dz_typed(const DzTask& t, hipStream_t stream) {
     const int32_t splits = dz_splits(t.rows, t.cols);
@@ -187,6 +416,11 @@ int64_t gemm_threads(int64_t m, int64_t n) {
 }
 
 hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream) {
+    const bool ak = t.a_k == 1, bk = t.b_k == 1;
+    if (t.m >= 128 && t.n >= 128 && t.k >= 64 &&
+        tile_operand(esize, t.a, ak ? t.a_m : t.a_k, ak, t.m) &&
+        tile_operand(esize, t.b, bk ? t.b_n : t.b_k, bk, t.n))
+        return esize == 2 ? launch_tile_any<2>(t, stream) : launch_tile_any<4>(t, stream);
     return esize == 2 ? launch_gemm_any<2>(t, stream) : launch_gemm_any<4>(t, stream);
 }
 
