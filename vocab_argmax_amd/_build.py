@@ -24,7 +24,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvpa.so")
 SOURCES = ["api.hip", "block_stats.hip", "chunk_stats.hip", "reduce.hip",
-           "head_api.hip", "logprob.hip", "linear.hip", "layer_norm.hip"]
+           "head_api.hip", "logprob.hip", "linear.hip", "linear_rows.hip", "gemm_bf16.hip",
+           "gemm_f32.hip", "layer_norm.hip"]
 ARCH = "gfx950"
 MODULES = {"_vpa_call": "pycall.c", "_vpa_head_call": "headcall.c"}
 

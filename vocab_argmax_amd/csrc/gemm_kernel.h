@@ -1,0 +1,167 @@
+// gemm_kernel.h -- the tiled product's kernel (see gemm_tile.h) and its
+// launch, instantiated for one element size by gemm_bf16.hip and gemm_f32.hip.
+#pragma once
+
+#include "gemm_tile.h"
+#include "linear_common.h"
+
+namespace vpa {
+namespace {
+
+// WM x WN wavefronts, each with BM/WM x BN/WN of the tile in its
+// accumulators.  With part set, blockIdx.y is a slice of k and the raw sums
+// go to part[slice][m][n].
+template <int ESIZE, bool AK, bool BK, bool DIRECT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint32_t tiles_m,
+                                                                uint32_t tiles_n,
+                                                                int64_t stages_per_slice,
+                                                                bool vec, float* part) {
+    using T = typename elem<ESIZE>::type;
+    constexpr int NT = WM * WN * 64;
+    constexpr int IM = BM / WM / 16, JN = BN / WN / 16;
+    static_assert(IM % 4 == 0 && JN == 4, "the epilogue stores blocks of 64 x 64");
+    using LA = TileLoader<ESIZE, AK, DIRECT, BM, NT>;
+    using LB = TileLoader<ESIZE, BK, DIRECT, BN, NT>;
+    __shared__ __align__(1024) char lds0[LA::BYTES + LB::BYTES];
+    __shared__ __align__(1024) char lds1[LA::BYTES + LB::BYTES];
+    uint32_t tm, tn;
+    tile_of_block(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
+    LA la;
+    LB lb;
+    la.init(t.a, AK ? t.a_m : t.a_k, m0, t.m_readable);
+    lb.init(t.b, BK ? t.b_n : t.b_k, n0, t.n);
+    const int64_t whole = t.k / LA::KB, all = (t.k + LA::KB - 1) / LA::KB;
+    const int64_t s0 = blockIdx.y * stages_per_slice;
+    const int64_t end = s0 + stages_per_slice < all ? s0 + stages_per_slice : all;
+    f32x4 acc[IM][JN] = {};
+    auto stage = [&](int64_t s, char* lds) {
+        la.load(s, lds);
+        lb.load(s, lds + LA::BYTES);
+    };
+    auto multiply = [&](const char* lds) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            u32x4_t av[IM], bv[JN];
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+                bv[j] = LB::fragment(lds + LA::BYTES, wn + j * 16, s);
+#pragma unroll
+            for (int i = 0; i < IM; ++i)
+                av[i] = LA::fragment(lds, wm + i * 16, s);
+#pragma unroll
+            for (int i = 0; i < IM; ++i)
+#pragma unroll
+                for (int j = 0; j < JN; ++j)
+                    acc[i][j] = mma<ESIZE>(bv[j], av[i], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);      // one step's fragments at a time
+        }
+    };
+    // a stage that k ends in comes first, so that the loop has whole ones only
+    const int64_t s1 = end < whole ? end : whole;
+    if (end > whole) {
+        la.load_tail(whole, t.k, lds1);
+        lb.load_tail(whole, t.k, lds1 + LA::BYTES);
+    }
+    if constexpr (DIRECT) {
+        if (s0 < s1)
+            stage(s0, lds0);
+        if (end > whole) {
+            __syncthreads();
+            multiply(lds1);
+        }
+        for (int64_t s = s0; s < s1; s += 2) {
+            __syncthreads();
+            if (s + 1 < s1)
+                stage(s + 1, lds1);
+            multiply(lds0);
+            if (s + 1 >= s1)
+                break;
+            __syncthreads();
+            if (s + 2 < s1)
+                stage(s + 2, lds0);
+            multiply(lds1);
+        }
+    } else {
+        u32x4_t va[LA::LOADS], vb[LB::LOADS];
+        auto fetch = [&](int64_t s) {
+            la.fetch(s, va);
+            lb.fetch(s, vb);
+        };
+        auto put = [&](char* lds) {
+            LA::put(va, lds);
+            LB::put(vb, lds + LA::BYTES);
+        };
+        if (end > whole) {
+            __syncthreads();
+            multiply(lds1);
+        }
+        if (s0 < s1) {
+            fetch(s0);
+            put(lds0);
+        }
+        for (int64_t s = s0; s < s1; s += 2) {
+            __syncthreads();
+            if (s + 1 < s1)
+                fetch(s + 1);
+            multiply(lds0);
+            if (s + 1 >= s1)
+                break;
+            put(lds1);
+            __syncthreads();
+            if (s + 2 < s1)
+                fetch(s + 2);
+            multiply(lds1);
+            if (s + 2 < s1)
+                put(lds0);
+        }
+    }
+    __syncthreads();
+    if (part)
+        part += (int64_t)blockIdx.y * t.m * t.n;
+    char* mine = wave * 16384 < LA::BYTES + LB::BYTES
+                     ? lds0 + wave * 16384 : lds1 + (wave * 16384 - LA::BYTES - LB::BYTES);
+#pragma unroll
+    for (int h = 0; h < IM / 4; ++h) {
+        f32x4 block[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                block[i][j] = acc[h * 4 + i][j];
+        store_block<T>(t, vec, part, mine, m0 + wm + h * 64, n0 + wn, block);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+template <int ESIZE, bool AK, bool BK, bool DIRECT, int BM, int BN, int WM, int WN>
+hipError_t launch_tile(const GemmTask& t, const GemmPlan& p, hipStream_t stream) {
+    const uint32_t tm = (uint32_t)((t.m + BM - 1) / BM), tn = (uint32_t)((t.n + BN - 1) / BN);
+    return launch(gemm_tile_kernel<ESIZE, AK, BK, DIRECT, BM, BN, WM, WN>,
+                  dim3(tm * tn, (uint32_t)p.slices), dim3(WM * WN * 64), 0, stream, t, tm, tn,
+                  p.stages_per_slice, p.vec, p.slices > 1 ? (float*)t.ws : nullptr);
+}
+
+template <int ESIZE, bool AK, bool BK>
+hipError_t launch_layout(const GemmTask& t, const GemmPlan& p, hipStream_t stream) {
+    if (!p.direct)
+        return launch_tile<ESIZE, AK, BK, false, 128, 128, 2, 2>(t, p, stream);
+    if constexpr (ESIZE == 2)
+        if (p.tile == 256)
+            return launch_tile<ESIZE, AK, BK, true, 256, 256, 2, 4>(t, p, stream);
+    return launch_tile<ESIZE, AK, BK, true, 128, 128, 2, 2>(t, p, stream);
+}
+
+template <int ESIZE>
+hipError_t launch_tiles(const GemmTask& t, const GemmPlan& p, hipStream_t stream) {
+    if (t.a_k != 1)
+        return launch_layout<ESIZE, false, false>(t, p, stream);
+    return t.b_k != 1 ? launch_layout<ESIZE, true, false>(t, p, stream)
+                      : launch_layout<ESIZE, true, true>(t, p, stream);
+}
+
+}  // namespace
+}  // namespace vpa

@@ -8,6 +8,11 @@
 // rows contiguous ([k][row]); the latter is read from LDS with the
 // transposing read, so all four layouts run on the same loop.
 //
+// Direct loads need addresses aligned to 16 bytes (and whole chunks of rows).
+// Where an operand has other strides, its stages go through registers
+// (DIRECT false): 16-byte loads of any alignment before the product, LDS
+// writes after it.
+//
 // LDS layout, k contiguous: row r has 8 chunks of 16 bytes; chunk c lies at
 // position c ^ ((r >> 1) & 7), so that the 16 rows a fragment read touches
 // fall into different banks.  Rows contiguous: row k has chunks of 32 bytes;
@@ -30,9 +35,24 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef const __attribute__((address_space(1))) void* global_ptr;
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
+// 16 bytes at any element address.
+struct __attribute__((packed, aligned(2))) Loose16 {
+    u32x4_t v;
+};
+
+template <bool DIRECT>
+struct tile_offset {
+    using type = uint32_t;
+};
+template <>
+struct tile_offset<false> {
+    using type = int64_t;
+};
+
 // One operand's tile of ROWS rows and one stage of k, for NT threads.
-template <int ESIZE, bool K1, int ROWS, int NT>
+template <int ESIZE, bool K1, bool DIRECT, int ROWS, int NT>
 struct TileLoader {
+    using T = typename elem<ESIZE>::type;
     static constexpr int VEC = 16 / ESIZE;              // elements of a 16-byte chunk
     static constexpr int KB = 128 / ESIZE;              // k of a stage
     static constexpr int BYTES = ROWS * 128;
@@ -41,16 +61,26 @@ struct TileLoader {
 
     const char* base;            // the tile's first row at k = 0
     int64_t k_step;              // bytes from a stage to the next
-    uint32_t off[LOADS];         // bytes from base (+ k) of each of this thread's chunks
+    int32_t left;                // rows from the tile's first
+    // bytes from base (+ k) of each of this thread's chunks; direct loads are
+    // given operands whose tiles span less than 4 GiB
+    using Offset = typename tile_offset<DIRECT>::type;
+    Offset off[LOADS];
 
     static __device__ __forceinline__ int swizzle(int k) {
         constexpr int n = ROWS * ESIZE / 32;            // 32-byte chunks of a row
         return ((k & 3) | (((k >> 3) & 3) << 2)) & (n - 1);
     }
-    // first row and, for the operand, row count, stride in elements
+    // first row of the tile's chunk at position pos of LDS row r (k strided)
+    static __device__ __forceinline__ int column(int r, int pos) {
+        return ((pos >> 1) ^ swizzle(r)) * (32 / ESIZE) + (pos & 1) * VEC;
+    }
+    // first row, and the operand's row count and stride in elements; with
+    // DIRECT and rows contiguous, `rows` may count readable padding
     __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t row0, int64_t rows) {
         base = (const char*)p + (K1 ? row0 * ld : row0) * ESIZE;
         k_step = (K1 ? KB : KB * ld) * ESIZE;
+        left = rows - row0 < ROWS ? (int32_t)(rows - row0) : ROWS;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int id = i * NT + threadIdx.x;
@@ -58,14 +88,13 @@ struct TileLoader {
             int64_t o;
             if constexpr (K1) {
                 // rows past the operand repeat its last one: their products are not stored
-                const int64_t row = row0 + r < rows ? r : rows - 1 - row0;
+                const int row = r < left ? r : left - 1;
                 o = row * ld + (pos ^ ((r >> 1) & 7)) * VEC;
             } else {
-                int64_t col = ((pos >> 1) ^ swizzle(r)) * (32 / ESIZE) + (pos & 1) * VEC;
-                col = row0 + col + VEC <= rows ? col : rows - VEC - row0;
-                o = r * ld + col;
+                const int col = column(r, pos);
+                o = r * ld + (DIRECT && col + VEC > left ? left - VEC : col);
             }
-            off[i] = (uint32_t)(o * ESIZE);
+            off[i] = (Offset)(o * ESIZE);
         }
     }
     // a whole stage, straight to LDS
@@ -77,30 +106,58 @@ struct TileLoader {
             __builtin_amdgcn_global_load_lds((global_ptr)(p + off[i]),
                                              (lds_ptr)(lds + i * NT * 16 + wave_base), 16, 0, 0);
     }
-    // the stage that k ends in: chunks past k become 0
-    __device__ __forceinline__ void load_tail(int64_t stage, int64_t k, char* lds) const {
-        using T = typename elem<ESIZE>::type;
+    // a whole stage to registers, and from there to LDS
+    __device__ __forceinline__ void fetch(int64_t stage, u32x4_t (&v)[LOADS]) const {
         const char* p = base + stage * k_step;
-        const int left = (int)(k - stage * KB);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            if constexpr (!K1) {
+                const int id = i * NT + threadIdx.x;
+                const int col = column(id / ROW_CHUNKS, id % ROW_CHUNKS);
+                if (col + VEC > left) {                 // the operand's last columns
+                    v[i] = part(p + off[i], left - col);
+                    continue;
+                }
+            }
+            v[i] = ((const Loose16*)(p + off[i]))->v;
+        }
+    }
+    static __device__ __forceinline__ void put(const u32x4_t (&v)[LOADS], char* lds) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            *(u32x4_t*)(lds + (i * NT + threadIdx.x) * 16) = v[i];
+    }
+    // the first n elements of a chunk (n may be 0 or negative), 0 after them
+    static __device__ __forceinline__ u32x4_t part(const char* p, int n) {
+        union {
+            T e[VEC];
+            u32x4_t v;
+        } u;
+        u.v = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (e < n)
+                u.e[e] = ((const T*)p)[e];
+        return u.v;
+    }
+    // the stage that k ends in: 0 past k
+    __device__ __forceinline__ void load_tail(int64_t stage, int64_t k, char* lds) const {
+        const char* p = base + stage * k_step;
+        const int k_left = (int)(k - stage * KB);
 #pragma unroll 1
         for (int i = 0; i < LOADS; ++i) {
             const int id = i * NT + threadIdx.x;
             const int r = id / ROW_CHUNKS, pos = id % ROW_CHUNKS;
-            const int k0 = K1 ? (pos ^ ((r >> 1) & 7)) * VEC : r;
-            uint32_t o = 0;
+            Offset o = 0;
 #pragma unroll
             for (int j = 0; j < LOADS; ++j)
                 o = j == i ? off[j] : o;
-            union {
-                T e[VEC];
-                u32x4_t v;
-            } u;
-            u.v = u32x4_t{0, 0, 0, 0};
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if ((K1 ? k0 + e : k0) < left)
-                    u.e[e] = ((const T*)(p + o))[e];
-            *(u32x4_t*)(lds + id * 16) = u.v;
+            int n;
+            if constexpr (K1)
+                n = k_left - (pos ^ ((r >> 1) & 7)) * VEC;
+            else
+                n = r >= k_left ? 0 : (DIRECT ? VEC : left - column(r, pos));
+            *(u32x4_t*)(lds + id * 16) = part(p + o, n);
         }
     }
     // the fragment of 16 rows from `row`, 64 bytes of k from chunk s * 4

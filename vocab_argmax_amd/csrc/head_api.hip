@@ -166,11 +166,16 @@ struct LinearGradSizes {
     size_t dz, part, gemm;
     size_t total() const { return dz + part + gemm; }
 };
+// dz's row stride: 16-byte rows, so that both products load it directly.
+int64_t dz_stride(int esize, int64_t outer) {
+    const int64_t vec = 16 / esize;
+    return (outer + vec - 1) / vec * vec;
+}
 LinearGradSizes linear_grad_sizes(int esize, int64_t rows, int64_t outer, int64_t inner,
-                                  bool act, bool bias, bool gx, bool gw) {
+                                  bool dz, bool bias, bool gx, bool gw) {
     LinearGradSizes z{};
-    if (act && (gx || gw))
-        z.dz = round256((size_t)rows * (size_t)outer * (size_t)esize);
+    if (dz && (gx || gw))
+        z.dz = round256((size_t)rows * (size_t)dz_stride(esize, outer) * (size_t)esize);
     if (bias)
         z.part = round256((size_t)dz_splits(rows, outer) * (size_t)outer * 4);
     const size_t wx = gx ? gemm_workspace(esize, rows, inner, outer, true, false) : 0;
@@ -380,7 +385,8 @@ vpa_status vpa_head_linear(const void* x, int64_t ldx, const void* weight, int64
         return st;
     if (residual == y && residual && (ldr != ldy || odt != dt))
         return fail(VPA_ERR_INVALID, "y in the residual's place needs its row stride and type");
-    if ((st = check_dispatch(gemm_threads(rows, outer), "vpa_head_linear")) != VPA_OK ||
+    if ((st = check_dispatch(gemm_threads(e, rows, outer, inner, true, true),
+                             "vpa_head_linear")) != VPA_OK ||
         (st = check_workspace("vpa_head_linear", workspace, workspace_bytes,
                               vpa_head_linear_workspace(dtype, rows, outer, inner))) != VPA_OK)
         return st;
@@ -391,7 +397,7 @@ vpa_status vpa_head_linear(const void* x, int64_t ldx, const void* weight, int64
     t.b = weight;
     t.b_n = ldw;
     t.b_k = 1;
-    t.m = rows;
+    t.m = t.m_readable = rows;
     t.n = outer;
     t.k = inner;
     t.bias = bias;
@@ -433,12 +439,15 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
          (st = check_matrix("grad_weight", grad_weight, e, ldgw, inner)) != VPA_OK) ||
         (grad_bias && (st = check_vector("grad_bias", grad_bias, e)) != VPA_OK))
         return st;
-    const LinearGradSizes z = linear_grad_sizes(e, rows, outer, inner, has_act,
+    // without an activation dz is grad, unless its rows are not aligned: a
+    // copy costs one pass over grad, the products' unaligned loads more
+    const bool copy = has_act || ldg % (16 / e) != 0 || !aligned(grad, 16);
+    const LinearGradSizes z = linear_grad_sizes(e, rows, outer, inner, copy,
                                                 grad_bias != nullptr, grad_x != nullptr,
                                                 grad_weight != nullptr);
-    if ((grad_x && (st = check_dispatch(gemm_threads(rows, inner),
+    if ((grad_x && (st = check_dispatch(gemm_threads(e, rows, inner, outer, true, false),
                                         "vpa_head_linear_backward")) != VPA_OK) ||
-        (grad_weight && (st = check_dispatch(gemm_threads(outer, inner),
+        (grad_weight && (st = check_dispatch(gemm_threads(e, outer, inner, rows, false, false),
                                              "vpa_head_linear_backward")) != VPA_OK) ||
         (st = check_dispatch(dz_threads(rows, outer), "vpa_head_linear_backward")) != VPA_OK)
         return st;
@@ -448,7 +457,7 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
     hipStream_t s = (hipStream_t)stream;
     char* ws = (char*)workspace;
     const void* dz = grad;
-    int64_t lddz = ldg;
+    int64_t lddz = ldg, dz_cols = outer;
     hipError_t he = hipSuccess;
     if (z.dz || grad_bias) {
         DzTask d{};
@@ -460,7 +469,7 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
         d.rows = rows;
         d.cols = outer;
         d.dz = z.dz ? ws : nullptr;
-        d.ldz = outer;
+        d.ldz = dz_stride(e, outer);
         d.bias = grad_bias;
         // no rows: the sums have no slices, and the finishing kernel writes 0
         d.part = grad_bias && rows > 0 ? (float*)(ws + z.dz) : nullptr;
@@ -468,7 +477,7 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
             return hip_fail(he, "vpa_head_linear_backward (dz) launch");
         if (z.dz) {
             dz = ws;
-            lddz = outer;
+            lddz = dz_cols = d.ldz;
         }
     }
     void* gws = ws ? ws + z.dz + z.part : nullptr;
@@ -480,7 +489,7 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
         t.b = weight;
         t.b_n = 1;
         t.b_k = ldw;
-        t.m = rows;
+        t.m = t.m_readable = rows;
         t.n = inner;
         t.k = outer;
         t.y = grad_x;
@@ -499,6 +508,7 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
         t.b_n = 1;
         t.b_k = ldx;
         t.m = outer;
+        t.m_readable = dz_cols;
         t.n = inner;
         t.k = rows;
         t.y = grad_weight;

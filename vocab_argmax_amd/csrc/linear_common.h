@@ -1,0 +1,153 @@
+// linear_common.h -- the epilogue of the head's products: activations with
+// their slopes, and the stores of finished results.
+#pragma once
+
+#include "vpa_head_internal.h"
+#include "vpa_math.h"
+
+namespace vpa {
+
+// Activations and their slopes, in fp32.
+template <int ACT>
+__device__ __forceinline__ float act(float z) {
+    if constexpr (ACT == VPA_ACT_RELU)
+        return z < 0.0f ? 0.0f : z;                // NaN stays
+    if constexpr (ACT == VPA_ACT_GELU)
+        return 0.5f * z * (1.0f + erff(z * 0.70710678118654752440f));
+    if constexpr (ACT == VPA_ACT_SILU)
+        return z / (1.0f + exp2_fast(-z * kLog2e));
+    return z;
+}
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+    if constexpr (ACT == VPA_ACT_RELU)
+        return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    if constexpr (ACT == VPA_ACT_GELU)
+        return 0.5f * (1.0f + erff(z * 0.70710678118654752440f)) +
+               z * exp2_fast(-0.5f * kLog2e * z * z) * 0.39894228040143267794f;
+    if constexpr (ACT == VPA_ACT_SILU) {
+        const float q = 1.0f / (1.0f + exp2_fast(-z * kLog2e));
+        return q * (1.0f + z * (1.0f - q));
+    }
+    return 1.0f;
+}
+
+// The activation of an epilogue, chosen at run time: a uniform branch.
+__device__ __forceinline__ float act_any(int32_t a, float z) {
+    switch (a) {
+    case VPA_ACT_RELU:
+        return act<VPA_ACT_RELU>(z);
+    case VPA_ACT_GELU:
+        return act<VPA_ACT_GELU>(z);
+    case VPA_ACT_SILU:
+        return act<VPA_ACT_SILU>(z);
+    default:
+        return z;
+    }
+}
+
+// One finished product of the epilogue.
+template <typename T>
+__device__ __forceinline__ void store_result(const GemmTask& t, int64_t m, int64_t n, float acc) {
+    const float z = acc + (t.bias ? to_f32(((const T*)t.bias)[n]) : 0.0f);
+    if (t.pre)
+        from_f32(((T*)t.pre)[m * t.ldp + n], z);
+    float y = act_any(t.act, z);
+    if (t.residual)
+        y += to_f32(((const T*)t.residual)[m * t.ldr + n]);
+    if (t.out_f32)
+        ((float*)t.y)[m * t.ldy + n] = y;
+    else
+        from_f32(((T*)t.y)[m * t.ldy + n], y);
+}
+
+// Four results of consecutive n: 16- or 8-byte accesses (every row of the
+// outputs and the residual is aligned for them).
+template <typename T>
+__device__ __forceinline__ void store_results(const GemmTask& t, int64_t m, int64_t n, f32x4 acc) {
+    using V = T __attribute__((ext_vector_type(4)));
+    if (t.bias)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc[i] += to_f32(((const T*)t.bias)[n + i]);
+    auto put = [](T* p, f32x4 v) {
+        if constexpr (sizeof(T) == 2)
+            *(uint2*)p = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else
+            *(f32x4*)p = v;
+    };
+    if (t.pre)
+        put((T*)t.pre + m * t.ldp + n, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        acc[i] = act_any(t.act, acc[i]);
+    if (t.residual) {
+        const V r = *(const V*)((const T*)t.residual + m * t.ldr + n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc[i] += to_f32((T)r[i]);
+    }
+    if (t.out_f32)
+        *(f32x4*)((float*)t.y + m * t.ldy + n) = acc;
+    else
+        put((T*)t.y + m * t.ldy + n, acc);
+}
+
+// A wavefront's 64 x 64 results from accumulators to memory, through its own
+// 16 KiB of LDS so that a store instruction covers whole rows: 4 rows of 64
+// where `vec` says that rows are aligned for 4 elements, else one row, an
+// element a lane.  Rows of LDS have 16 chunks of 16 bytes, chunk c of row r
+// at c ^ (r & 15).
+template <typename T>
+__device__ __forceinline__ void store_block(const GemmTask& t, bool vec, float* part, char* lds,
+                                            int64_t m0, int64_t n0, const f32x4 (&acc)[4][4]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = i * 16 + (lane & 15), c = j * 4 + (lane >> 4);
+            *(f32x4*)(lds + r * 256 + ((c ^ (r & 15)) << 4)) = acc[i][j];
+        }
+    // this LDS is the wavefront's alone and its accesses execute in order; the
+    // fences keep the compiler to it
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (vec && n0 + 64 <= t.n) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < 64; r0 += 16) {
+            f32x4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = r0 + k * 4 + (lane >> 4), c = lane & 15;
+                v[k] = *(const f32x4*)(lds + r * 256 + ((c ^ (r & 15)) << 4));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t m = m0 + r0 + k * 4 + (lane >> 4), n = n0 + (lane & 15) * 4;
+                if (m >= t.m)
+                    continue;
+                if (part)
+                    *(f32x4*)(part + m * t.n + n) = v[k];
+                else
+                    store_results<T>(t, m, n, v[k]);
+            }
+        }
+        return;
+    }
+    const int64_t n = n0 + lane;
+#pragma unroll 4
+    for (int r = 0; r < 64; ++r) {
+        const float v = *(const float*)(lds + r * 256 + (((lane >> 2) ^ (r & 15)) << 4) +
+                                        (lane & 3) * 4);
+        const int64_t m = m0 + r;
+        if (m >= t.m || n >= t.n)
+            continue;
+        if (part)
+            part[m * t.n + n] = v;
+        else
+            store_result<T>(t, m, n, v);
+    }
+}
+
+}  // namespace vpa

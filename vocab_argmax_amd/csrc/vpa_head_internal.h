@@ -80,11 +80,14 @@ hipError_t launch_logprob_grad(int esize, const LogprobGradTask& t, hipStream_t 
 
 // C[m][n] = sum_k A(m, k) B(n, k), A(m, k) = a[m*a_m + k*a_k] (one of the two
 // strides is 1), B alike, then the epilogue y = residual + act(C + bias[n]).
+// The layouts used: k contiguous in both (a product with a weight), in A
+// alone (grad_x) and in neither (grad_weight).
 struct GemmTask {
     const void* a;
     const void* b;
     int64_t a_m, a_k, b_n, b_k;
     int64_t m, n, k;
+    int64_t m_readable;       // columns of A that may be read where a_m is 1 (>= m)
     const void* bias;
     const void* residual;
     int64_t ldr;
@@ -96,9 +99,27 @@ struct GemmTask {
     int32_t act;
     void* ws;                 // gemm_workspace() bytes
 };
+// How a product is cut; everything but `direct` and `vec` follows from sizes.
+struct GemmPlan {
+    bool rows_kernel;         // few rows: linear_rows.hip
+    int32_t tile;             // 256 or 128: rows and columns of a workgroup's tile
+    int32_t slices;           // of k, joined by a second kernel
+    int64_t stages_per_slice; // stages of 128 bytes of k
+    bool direct;              // operands' strides allow direct loads to LDS
+    bool vec;                 // outputs' and residual's allow 4-element accesses
+};
+GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
 size_t gemm_workspace(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
-int64_t gemm_threads(int64_t m, int64_t n);
+int64_t gemm_threads(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
 hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream);
+
+hipError_t launch_gemm_tiles_bf16(const GemmTask& t, const GemmPlan& p, hipStream_t stream);
+hipError_t launch_gemm_tiles_f32(const GemmTask& t, const GemmPlan& p, hipStream_t stream);
+
+// The product for few rows of A (linear_rows.hip), k contiguous in both.
+constexpr int kRowsKernelMost = 64;
+int64_t linear_rows_threads(int64_t m, int64_t n);
+hipError_t launch_linear_rows(int esize, const GemmTask& t, hipStream_t stream);
 
 // dz = grad * act'(pre) (of the operands' type, skipped if dz is null), and
 // the column sums of dz (before rounding) into `bias` (skipped if null).
