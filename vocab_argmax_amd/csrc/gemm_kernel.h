@@ -19,7 +19,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
     using T = typename elem<ESIZE>::type;
     constexpr int NT = WM * WN * 64;
     constexpr int IM = BM / WM / 16, JN = BN / WN / 16;
-    static_assert(IM % 4 == 0 && JN == 4, "the epilogue stores blocks of 64 x 64");
+    static_assert(IM % 4 == 0 && JN % 4 == 0 && JN <= IM, "the epilogue stores blocks of 64 x 64");
     using LA = TileLoader<ESIZE, AK, DIRECT, BM, NT>;
     using LB = TileLoader<ESIZE, BK, DIRECT, BN, NT>;
     __shared__ __align__(1024) char lds0[LA::BYTES + LB::BYTES];
@@ -36,21 +36,19 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
     const int64_t whole = t.k / LA::KB, all = (t.k + LA::KB - 1) / LA::KB;
     const int64_t s0 = blockIdx.y * stages_per_slice;
     const int64_t end = s0 + stages_per_slice < all ? s0 + stages_per_slice : all;
+    const typename LA::Place pa = LA::place(wm);
+    const typename LB::Place pb = LB::place(wn);
     f32x4 acc[IM][JN] = {};
-    auto stage = [&](int64_t s, char* lds) {
-        la.load(s, lds);
-        lb.load(s, lds + LA::BYTES);
-    };
     auto multiply = [&](const char* lds) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             u32x4_t av[IM], bv[JN];
 #pragma unroll
             for (int j = 0; j < JN; ++j)
-                bv[j] = LB::fragment(lds + LA::BYTES, wn + j * 16, s);
+                bv[j] = LB::fragment(lds + LA::BYTES, pb, j, s);
 #pragma unroll
             for (int i = 0; i < IM; ++i)
-                av[i] = LA::fragment(lds, wm + i * 16, s);
+                av[i] = LA::fragment(lds, pa, i, s);
 #pragma unroll
             for (int i = 0; i < IM; ++i)
 #pragma unroll
@@ -66,24 +64,67 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
         lb.load_tail(whole, t.k, lds1 + LA::BYTES);
     }
     if constexpr (DIRECT) {
-        if (s0 < s1)
-            stage(s0, lds0);
+        // One stage of the loop: the fragments of its first step are in
+        // registers; while a step's products run, the next step's fragments
+        // are read into the registers that they free.  Before the second
+        // step one barrier says both that the next stage has landed and
+        // that every wavefront has read this stage, whose buffer the stage
+        // after next then fills.
+        const typename LA::Direct da = la.direct();
+        const typename LB::Direct db = lb.direct();
+        auto stage = [&](int64_t s, char* lds) {
+            la.load(da, s, lds);
+            lb.load(db, s, lds + LA::BYTES);
+        };
+        u32x4_t av[IM], bv[JN];
+        auto read_all = [&](const char* lds) {
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+                bv[j] = LB::fragment(lds + LA::BYTES, pb, j, 0);
+#pragma unroll
+            for (int i = 0; i < IM; ++i)
+                av[i] = LA::fragment(lds, pa, i, 0);
+        };
+        auto step = [&](const char* next, int next_step) {
+            const typename LA::Place a = pa.again();
+            const typename LB::Place b = pb.again();
+#pragma unroll
+            for (int i = 0; i < IM; ++i) {
+#pragma unroll
+                for (int j = 0; j < JN; ++j) {
+                    acc[i][j] = mma<ESIZE>(bv[j], av[i], acc[i][j]);
+                    if (i == IM - 1)
+                        bv[j] = LB::fragment(next + LA::BYTES, b, j, next_step);
+                }
+                av[i] = LA::fragment(next, a, i, next_step);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
         if (end > whole) {
-            __syncthreads();
+            stage_barrier();
             multiply(lds1);
+            stage_barrier();
         }
-        for (int64_t s = s0; s < s1; s += 2) {
-            __syncthreads();
-            if (s + 1 < s1)
-                stage(s + 1, lds1);
-            multiply(lds0);
-            if (s + 1 >= s1)
-                break;
-            __syncthreads();
+        if (s0 < s1) {
+            stage(s0, lds0);
+            if (s0 + 1 < s1)
+                stage(s0 + 1, lds1);
+            stage_barrier();
+            read_all(lds0);
+            step(lds0, 1);
+        }
+        // the loop starts at a barrier, where nothing is outstanding
+        for (int64_t s = s0; s + 1 < s1; ++s) {
+            char* now = (s - s0) & 1 ? lds1 : lds0;
+            char* next = (s - s0) & 1 ? lds0 : lds1;
+            stage_barrier();
             if (s + 2 < s1)
-                stage(s + 2, lds0);
-            multiply(lds1);
+                stage(s + 2, now);
+            step(next, 0);
+            step(next, 1);
         }
+        if (s0 < s1)
+            step(lds0, 0);                       // (what it reads is not used)
     } else {
         u32x4_t va[LA::LOADS], vb[LB::LOADS];
         auto fetch = [&](int64_t s) {
@@ -95,7 +136,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
             LB::put(vb, lds + LA::BYTES);
         };
         if (end > whole) {
-            __syncthreads();
+            stage_barrier();
             multiply(lds1);
         }
         if (s0 < s1) {
@@ -103,14 +144,14 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
             put(lds0);
         }
         for (int64_t s = s0; s < s1; s += 2) {
-            __syncthreads();
+            stage_barrier();
             if (s + 1 < s1)
                 fetch(s + 1);
             multiply(lds0);
             if (s + 1 >= s1)
                 break;
             put(lds1);
-            __syncthreads();
+            stage_barrier();
             if (s + 2 < s1)
                 fetch(s + 2);
             multiply(lds1);
@@ -118,23 +159,25 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
                 put(lds0);
         }
     }
-    __syncthreads();
+    stage_barrier();
     if (part)
         part += (int64_t)blockIdx.y * t.m * t.n;
     char* mine = wave * 16384 < LA::BYTES + LB::BYTES
                      ? lds0 + wave * 16384 : lds1 + (wave * 16384 - LA::BYTES - LB::BYTES);
 #pragma unroll
-    for (int h = 0; h < IM / 4; ++h) {
-        f32x4 block[4][4];
+    for (int h = 0; h < IM / 4; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int g = 0; g < JN / 4; ++g) {
+            f32x4 block[4][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                block[i][j] = acc[h * 4 + i][j];
-        store_block<T>(t, vec, part, mine, m0 + wm + h * 64, n0 + wn, block);
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    }
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    block[i][j] = acc[h * 4 + i][g * 4 + j];
+            store_block<T>(t, vec, part, mine, m0 + wm + h * 64, n0 + wn + g * 64, block);
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
 }
 
 template <int ESIZE, bool AK, bool BK, bool DIRECT, int BM, int BN, int WM, int WN>

@@ -40,14 +40,13 @@ struct __attribute__((packed, aligned(2))) Loose16 {
     u32x4_t v;
 };
 
-template <bool DIRECT>
-struct tile_offset {
-    using type = uint32_t;
-};
-template <>
-struct tile_offset<false> {
-    using type = int64_t;
-};
+// A pointer that is the same in every lane, as one.
+__device__ __forceinline__ void* uniform(const void* p) {
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (void*)(((uint64_t)hi << 32) | lo);
+}
 
 // One operand's tile of ROWS rows and one stage of k, for NT threads.
 template <int ESIZE, bool K1, bool DIRECT, int ROWS, int NT>
@@ -56,70 +55,98 @@ struct TileLoader {
     static constexpr int VEC = 16 / ESIZE;              // elements of a 16-byte chunk
     static constexpr int KB = 128 / ESIZE;              // k of a stage
     static constexpr int BYTES = ROWS * 128;
-    static constexpr int LOADS = BYTES / 16 / NT;
-    static constexpr int ROW_CHUNKS = K1 ? 8 : ROWS / VEC;   // 16-byte chunks of an LDS row
+    static constexpr int LOADS = BYTES / 16 / NT;       // 16-byte chunks of a thread
+    static constexpr int ROW_CHUNKS = K1 ? 8 : ROWS / VEC;   // of an LDS row
+    static constexpr int ROWS_PER_LOAD = NT / ROW_CHUNKS;    // LDS rows from load to load
+    // loads after which the swizzle of a thread's LDS row repeats
+    static constexpr int PERIOD = K1 ? (ROWS_PER_LOAD % 16 == 0 ? 1 : LOADS)
+                                     : (32 / ROWS_PER_LOAD < LOADS ? 32 / ROWS_PER_LOAD : LOADS);
+    static_assert(NT % ROW_CHUNKS == 0 && LOADS % PERIOD == 0, "whole rows a load");
 
     const char* base;            // the tile's first row at k = 0
-    int64_t k_step;              // bytes from a stage to the next
-    int32_t left;                // rows from the tile's first
-    // bytes from base (+ k) of each of this thread's chunks; direct loads are
-    // given operands whose tiles span less than 4 GiB
-    using Offset = typename tile_offset<DIRECT>::type;
-    Offset off[LOADS];
+    int64_t ld;                  // bytes from LDS row to LDS row
+    int32_t left;                // rows of the operand from the tile's first (at most ROWS)
 
     static __device__ __forceinline__ int swizzle(int k) {
         constexpr int n = ROWS * ESIZE / 32;            // 32-byte chunks of a row
         return ((k & 3) | (((k >> 3) & 3) << 2)) & (n - 1);
     }
-    // first row of the tile's chunk at position pos of LDS row r (k strided)
-    static __device__ __forceinline__ int column(int r, int pos) {
-        return ((pos >> 1) ^ swizzle(r)) * (32 / ESIZE) + (pos & 1) * VEC;
+    // operand element (from the LDS row's first) of the chunk at position pos of LDS row r
+    static __device__ __forceinline__ int element(int r, int pos) {
+        if constexpr (K1)
+            return (pos ^ ((r >> 1) & 7)) * VEC;
+        else
+            return ((pos >> 1) ^ swizzle(r)) * (32 / ESIZE) + (pos & 1) * VEC;
+    }
+    static __device__ __forceinline__ int lds_row(int i) {
+        return i * ROWS_PER_LOAD + threadIdx.x / ROW_CHUNKS;
+    }
+    static __device__ __forceinline__ int position() {
+        return threadIdx.x % ROW_CHUNKS;
+    }
+    // bytes from base (+ k) of this thread's chunk of load i
+    __device__ __forceinline__ int64_t offset(int i) const {
+        const int r = lds_row(i);
+        // rows past the operand repeat its last one: their products are not stored
+        const int row = K1 && r >= left ? left - 1 : r;
+        return row * ld + element(r, position()) * ESIZE;
     }
     // first row, and the operand's row count and stride in elements; with
     // DIRECT and rows contiguous, `rows` may count readable padding
-    __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t row0, int64_t rows) {
-        base = (const char*)p + (K1 ? row0 * ld : row0) * ESIZE;
-        k_step = (K1 ? KB : KB * ld) * ESIZE;
+    __device__ __forceinline__ void init(const void* p, int64_t stride, int64_t row0,
+                                         int64_t rows) {
+        base = (const char*)p + (K1 ? row0 * stride : row0) * ESIZE;
+        ld = stride * ESIZE;
         left = rows - row0 < ROWS ? (int32_t)(rows - row0) : ROWS;
+    }
+    __device__ __forceinline__ const char* at_stage(int64_t stage) const {
+        return base + stage * (K1 ? 128 : KB * ld);
+    }
+
+    // This thread's 32-bit offsets for direct loads, which see the tile's
+    // stage as a buffer that ends with the operand's last element: a chunk
+    // past it is not read (its products are not stored).
+    struct Direct {
+        uint32_t off[PERIOD];
+        uint32_t step;           // bytes of PERIOD loads
+        uint32_t size;           // of the buffer
+    };
+    __device__ __forceinline__ Direct direct() const {
+        Direct d;
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int id = i * NT + threadIdx.x;
-            const int r = id / ROW_CHUNKS, pos = id % ROW_CHUNKS;
-            int64_t o;
-            if constexpr (K1) {
-                // rows past the operand repeat its last one: their products are not stored
-                const int row = r < left ? r : left - 1;
-                o = row * ld + (pos ^ ((r >> 1) & 7)) * VEC;
-            } else {
-                const int col = column(r, pos);
-                o = r * ld + (DIRECT && col + VEC > left ? left - VEC : col);
-            }
-            off[i] = (Offset)(o * ESIZE);
-        }
+        for (int i = 0; i < PERIOD; ++i)
+            d.off[i] = (uint32_t)(lds_row(i) * ld + element(lds_row(i), position()) * ESIZE);
+        d.step = (uint32_t)(PERIOD * ROWS_PER_LOAD * ld);
+        d.size = (uint32_t)(K1 ? (left - 1) * ld + 128 : (KB - 1) * ld + left * ESIZE);
+        return d;
     }
     // a whole stage, straight to LDS
-    __device__ __forceinline__ void load(int64_t stage, char* lds) const {
-        const char* p = base + stage * k_step;
-        const int wave_base = (threadIdx.x & ~63) * 16;
+    __device__ __forceinline__ void load(const Direct& d, int64_t stage, char* lds) const {
+#ifdef __HIP_DEVICE_COMPILE__    // the host pass has no buffer type
+        const auto buf = __builtin_amdgcn_make_buffer_rsrc(
+            uniform(at_stage(stage)), 0, __builtin_amdgcn_readfirstlane(d.size), 0x00020000);
+        const int wave_base = __builtin_amdgcn_readfirstlane((threadIdx.x & ~63) * 16);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i)
-            __builtin_amdgcn_global_load_lds((global_ptr)(p + off[i]),
-                                             (lds_ptr)(lds + i * NT * 16 + wave_base), 16, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_ptr)(lds + i * NT * 16 + wave_base),
+                                                     16, d.off[i % PERIOD] + i / PERIOD * d.step,
+                                                     0, 0, 0);
+#endif
     }
     // a whole stage to registers, and from there to LDS
     __device__ __forceinline__ void fetch(int64_t stage, u32x4_t (&v)[LOADS]) const {
-        const char* p = base + stage * k_step;
+        const char* p = at_stage(stage);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
+            const int64_t o = offset(i);
             if constexpr (!K1) {
-                const int id = i * NT + threadIdx.x;
-                const int col = column(id / ROW_CHUNKS, id % ROW_CHUNKS);
+                const int col = element(lds_row(i), position());
                 if (col + VEC > left) {                 // the operand's last columns
-                    v[i] = part(p + off[i], left - col);
+                    v[i] = part(p + o, left - col);
                     continue;
                 }
             }
-            v[i] = ((const Loose16*)(p + off[i]))->v;
+            v[i] = ((const Loose16*)(p + o))->v;
         }
     }
     static __device__ __forceinline__ void put(const u32x4_t (&v)[LOADS], char* lds) {
@@ -142,58 +169,87 @@ struct TileLoader {
     }
     // the stage that k ends in: 0 past k
     __device__ __forceinline__ void load_tail(int64_t stage, int64_t k, char* lds) const {
-        const char* p = base + stage * k_step;
+        const char* p = at_stage(stage);
         const int k_left = (int)(k - stage * KB);
 #pragma unroll 1
         for (int i = 0; i < LOADS; ++i) {
-            const int id = i * NT + threadIdx.x;
-            const int r = id / ROW_CHUNKS, pos = id % ROW_CHUNKS;
-            Offset o = 0;
-#pragma unroll
-            for (int j = 0; j < LOADS; ++j)
-                o = j == i ? off[j] : o;
-            int n;
-            if constexpr (K1)
-                n = k_left - (pos ^ ((r >> 1) & 7)) * VEC;
-            else
-                n = r >= k_left ? 0 : (DIRECT ? VEC : left - column(r, pos));
-            *(u32x4_t*)(lds + id * 16) = part(p + o, n);
+            const int r = lds_row(i), e = element(r, position());
+            const int n = K1 ? k_left - e : (r < k_left ? left - e : 0);
+            *(u32x4_t*)(lds + (i * NT + threadIdx.x) * 16) = part(p + offset(i), n);
         }
     }
-    // the fragment of 16 rows from `row`, 64 bytes of k from chunk s * 4
-    static __device__ __forceinline__ u32x4_t fragment(const char* lds, int row, int s) {
-        const int lane = threadIdx.x & 63;
+    // Fragments: 16 rows, 64 bytes of k (step 0 or 1 of a stage).  A lane's
+    // LDS address is worked out once for the wavefront's first row (a multiple
+    // of 64); fragment i, 16 i rows on, is a constant distance away (k
+    // contiguous), or differs in the bits of the 32-byte chunk (k strided).
+    struct Place {
+        uint32_t at[K1 ? 2 : 1];
+        // The same places, unknown to the compiler: it would otherwise keep
+        // the sums with every fragment's and buffer's distance in registers
+        // around the loop, which do not fit.
+        __device__ __forceinline__ Place again() const {
+            Place p = *this;
+#pragma unroll
+            for (int i = 0; i < (K1 ? 2 : 1); ++i)
+                asm volatile("" : "+v"(p.at[i]));
+            return p;
+        }
+    };
+    static __device__ __forceinline__ Place place(int row) {
+        const int lane = threadIdx.x & 63, q = lane >> 4;
+        Place p;
         if constexpr (K1) {
-            const int r = row + (lane & 15), c = s * 4 + (lane >> 4);
-            return *(const u32x4_t*)(lds + r * 128 + ((c ^ ((r >> 1) & 7)) << 4));
+            const int f = (lane >> 1) & 7;              // ((row + lane % 16) >> 1) & 7
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                p.at[s] = (row + (lane & 15)) * 128 + (((s * 4 + q) ^ f) << 4);
         } else if constexpr (ESIZE == 2) {
-            // lane i of a group of 16 reads 8 bytes of row k = i / 4 and is
-            // given column i of rows k..k+3
+            // a transposing read: lane i of a group of 16 reads 8 bytes of row
+            // k = i / 4 and is given column i of rows k..k+3
+            const int k = q * 8 + ((lane >> 2) & 3);
+            p.at[0] = k * ROWS * 2 + (((row >> 4) ^ swizzle(k)) << 5) + (lane & 3) * 8;
+        } else {
+            p.at[0] = row + (lane & 15);
+        }
+        return p;
+    }
+    static __device__ __forceinline__ u32x4_t fragment(const char* lds, const Place& p, int i,
+                                                       int s) {
+        if constexpr (K1) {
+            return *(const u32x4_t*)(lds + p.at[s] + i * 2048);
+        } else if constexpr (ESIZE == 2) {
             union {
                 i16x4 h[2];
                 u32x4_t v;
             } u;
+            const char* c = lds + (p.at[0] ^ (i << 5));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = s * 32 + (lane >> 4) * 8 + h * 4 + ((lane >> 2) & 3);
-                const int c = (row >> 4) ^ swizzle(k);
-                const char* p = lds + k * ROWS * 2 + c * 32 + (lane & 3) * 8;
-                u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4)(lds_ptr)p);
-            }
+            for (int h = 0; h < 2; ++h)
+                u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_i16x4)(lds_ptr)(c + (s * 32 + h * 4) * ROWS * 2));
             return u.v;
         } else {
+            const int q = (threadIdx.x & 63) >> 4;
+            const int col = p.at[0] + i * 16;
             u32x4_t v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int k = s * 16 + (lane >> 4) * 4 + e;
-                const int col = row + (lane & 15);
-                const int c = (col >> 3) ^ swizzle(k);
-                v[e] = *(const uint32_t*)(lds + k * ROWS * 4 + c * 32 + (col & 7) * 4);
+                const int k = s * 16 + q * 4 + e;
+                v[e] = *(const uint32_t*)(lds + k * ROWS * 4 + (((col >> 3) ^ swizzle(k)) << 5) +
+                                          (col & 7) * 4);
             }
             return v;
         }
     }
 };
+
+// The barrier between stages.  A direct load to LDS is counted as a memory
+// load, which a workgroup barrier does not wait for by itself: each wavefront
+// waits for its own loads (and its LDS accesses), then for the others.
+__device__ __forceinline__ void stage_barrier() {
+    __builtin_amdgcn_s_waitcnt(0x0070);             // vmcnt(0) lgkmcnt(0)
+    __syncthreads();
+}
 
 // D += P Q^T for 16 rows of P and of Q over 64 bytes of k.
 template <int ESIZE>

@@ -32,6 +32,14 @@ __device__ __forceinline__ float act_slope(float z) {
     return 1.0f;
 }
 
+template <int ACT>
+__device__ __forceinline__ f32x4 act4(f32x4 z) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        z[i] = act<ACT>(z[i]);
+    return z;
+}
+
 // The activation of an epilogue, chosen at run time: a uniform branch.
 __device__ __forceinline__ float act_any(int32_t a, float z) {
     switch (a) {
@@ -78,9 +86,19 @@ __device__ __forceinline__ void store_results(const GemmTask& t, int64_t m, int6
     };
     if (t.pre)
         put((T*)t.pre + m * t.ldp + n, acc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        acc[i] = act_any(t.act, acc[i]);
+    switch (t.act) {                               // one uniform branch for the four
+    case VPA_ACT_RELU:
+        acc = act4<VPA_ACT_RELU>(acc);
+        break;
+    case VPA_ACT_GELU:
+        acc = act4<VPA_ACT_GELU>(acc);
+        break;
+    case VPA_ACT_SILU:
+        acc = act4<VPA_ACT_SILU>(acc);
+        break;
+    default:
+        break;
+    }
     if (t.residual) {
         const V r = *(const V*)((const T*)t.residual + m * t.ldr + n);
 #pragma unroll
