@@ -15,7 +15,7 @@ template <int ESIZE, bool AK, bool BK, bool DIRECT, int BM, int BN, int WM, int 
 __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint32_t tiles_m,
                                                                 uint32_t tiles_n,
                                                                 int64_t stages_per_slice,
-                                                                bool vec, float* part) {
+                                                                float* part) {
     using T = typename elem<ESIZE>::type;
     constexpr int NT = WM * WN * 64;
     constexpr int IM = BM / WM / 16, JN = BN / WN / 16;
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     block[i][j] = acc[h * 4 + i][g * 4 + j];
-            store_block<T>(t, vec, part, mine, m0 + wm + h * 64, n0 + wn + g * 64, block);
+            store_block<T>(t, part, mine, m0 + wm + h * 64, n0 + wn + g * 64, block);
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
         }
@@ -185,7 +185,7 @@ hipError_t launch_tile(const GemmTask& t, const GemmPlan& p, hipStream_t stream)
     const uint32_t tm = (uint32_t)((t.m + BM - 1) / BM), tn = (uint32_t)((t.n + BN - 1) / BN);
     return launch(gemm_tile_kernel<ESIZE, AK, BK, DIRECT, BM, BN, WM, WN>,
                   dim3(tm * tn, (uint32_t)p.slices), dim3(WM * WN * 64), 0, stream, t, tm, tn,
-                  p.stages_per_slice, p.vec, p.slices > 1 ? (float*)t.ws : nullptr);
+                  p.stages_per_slice, p.slices > 1 ? (float*)t.ws : nullptr);
 }
 
 template <int ESIZE, bool AK, bool BK>

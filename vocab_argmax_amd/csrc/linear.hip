@@ -11,13 +11,13 @@ namespace {
 constexpr int kThreads = 256;
 
 // The slices of a split product, added in order, and its epilogue: 4 results
-// of a row a thread (one where rows are not aligned for 4).
-template <typename T, bool VEC>
+// of a row a thread (one where a row is not a multiple of 4).
+template <typename T, bool FOUR>
 __global__ __launch_bounds__(kThreads) void gemm_join_kernel(GemmTask t, int32_t slices) {
     const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const float* part = (const float*)t.ws;
     const int64_t slice = t.m * t.n;
-    if constexpr (VEC) {
+    if constexpr (FOUR) {
         if (id * 4 >= slice)
             return;
         f32x4 v = *(const f32x4*)(part + id * 4);
@@ -36,24 +36,73 @@ __global__ __launch_bounds__(kThreads) void gemm_join_kernel(GemmTask t, int32_t
     }
 }
 
+// dz and the slices of its column sums: a workgroup takes 512 columns, 8 a
+// lane, and each of its 4 wavefronts every fourth row of its slice of rows.
+constexpr int kDzCols = 512;
+
 template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void dz_kernel(DzTask t, int32_t splits) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= t.cols)
-        return;
+    __shared__ float sums[4][kDzCols];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * kDzCols + lane * 8;
     const int64_t per = (t.rows + splits - 1) / splits;
     const int64_t r0 = per * blockIdx.y, r1 = r0 + per < t.rows ? r0 + per : t.rows;
-    float sum = 0.0f;
-    for (int64_t r = r0; r < r1; ++r) {
-        float d = to_f32(((const T*)t.grad)[r * t.ldg + c]);
-        if constexpr (ACT != VPA_ACT_NONE)
-            d *= act_slope<ACT>(to_f32(((const T*)t.pre)[r * t.ldp + c]));
-        sum += d;
-        if (t.dz)
-            from_f32(((T*)t.dz)[r * t.ldz + c], d);
+    const int n = t.cols - c < 8 ? (int)(t.cols - c) : 8;       // columns of this lane, or < 1
+    float sum[8] = {};
+#pragma unroll 2
+    for (int64_t r = r0 + wave; r < r1; r += 4) {
+        const T* g = (const T*)t.grad + r * t.ldg + c;
+        const T* z = ACT == VPA_ACT_NONE ? nullptr : (const T*)t.pre + r * t.ldp + c;
+        float d[8], p[8];
+        if (n == 8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 v = load4(g + h * 4);
+                const f32x4 q = ACT == VPA_ACT_NONE ? v : load4(z + h * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    d[h * 4 + i] = v[i];
+                    p[h * 4 + i] = q[i];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                d[i] = i < n ? to_f32(g[i]) : 0.0f;
+                p[i] = ACT != VPA_ACT_NONE && i < n ? to_f32(z[i]) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (ACT != VPA_ACT_NONE)
+                d[i] *= act_slope<ACT>(p[i]);
+            sum[i] += d[i];
+        }
+        if (t.dz && n > 0) {
+            T* out = (T*)t.dz + r * t.ldz + c;
+            if (n == 8) {
+                store4(out, f32x4{d[0], d[1], d[2], d[3]});
+                store4(out + 4, f32x4{d[4], d[5], d[6], d[7]});
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < n)
+                        from_f32(out[i], d[i]);
+            }
+        }
     }
-    if (t.part)
-        t.part[(int64_t)blockIdx.y * t.cols + c] = sum;
+    if (!t.part)
+        return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        sums[wave][lane * 8 + i] = sum[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kDzCols; i += kThreads) {
+        const int64_t col = (int64_t)blockIdx.x * kDzCols + i;
+        if (col < t.cols)
+            t.part[(int64_t)blockIdx.y * t.cols + col] =
+                ((sums[0][i] + sums[1][i]) + sums[2][i]) + sums[3][i];
+    }
 }
 
 template <typename T>
@@ -76,14 +125,10 @@ bool direct_operand(int esize, const void* p, int64_t ld, bool k1, int64_t rows)
            (k1 || rows % vec == 0);
 }
 
-bool aligned_for_4(const void* p, int64_t ld, int esize) {
-    return !p || ((uintptr_t)p % (4 * esize) == 0 && ld % 4 == 0);
-}
-
 template <typename T>
 hipError_t launch_dz_typed(const DzTask& t, hipStream_t stream) {
     const int32_t splits = dz_splits(t.rows, t.cols);
-    const dim3 grid((uint32_t)((t.cols + kThreads - 1) / kThreads), (uint32_t)splits);
+    const dim3 grid((uint32_t)((t.cols + kDzCols - 1) / kDzCols), (uint32_t)splits);
     const dim3 block(kThreads);
     hipError_t e;
     switch (t.act) {
@@ -101,7 +146,7 @@ hipError_t launch_dz_typed(const DzTask& t, hipStream_t stream) {
     }
     if (e != hipSuccess || !t.bias)
         return e;
-    return launch(bias_finish_kernel<T>, dim3(grid.x), block, 0, stream, t, t.part ? splits : 0);
+    return launch(bias_finish_kernel<T>, dim3((uint32_t)((t.cols + kThreads - 1) / kThreads)), block, 0, stream, t, t.part ? splits : 0);
 }
 
 }  // namespace
@@ -166,16 +211,11 @@ hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream) {
         return launch_linear_rows(esize, t, stream);
     p.direct = direct_operand(esize, t.a, ak ? t.a_m : t.a_k, ak, t.m_readable) &&
                direct_operand(esize, t.b, bk ? t.b_n : t.b_k, bk, t.n);
-    p.vec = aligned_for_4(t.y, t.ldy, t.out_f32 ? 4 : esize) &&
-            aligned_for_4(t.pre, t.ldp, esize) && aligned_for_4(t.residual, t.ldr, esize);
-    const bool vec = p.vec;
-    if (p.slices > 1)
-        p.vec = t.n % 4 == 0;                       // the slices' rows, not the outputs'
     hipError_t e = esize == 2 ? launch_gemm_tiles_bf16(t, p, stream)
                               : launch_gemm_tiles_f32(t, p, stream);
     if (e != hipSuccess || p.slices == 1)
         return e;
-    const bool join4 = vec && p.vec;
+    const bool join4 = t.n % 4 == 0;
     const int64_t items = t.m * t.n / (join4 ? 4 : 1);
     const dim3 grid((uint32_t)((items + kThreads - 1) / kThreads)), block(kThreads);
     if (esize == 2)
@@ -186,13 +226,16 @@ hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream) {
                  : launch(gemm_join_kernel<float, false>, grid, block, 0, stream, t, p.slices);
 }
 
-int32_t dz_splits(int64_t rows, int64_t) {
-    const int64_t s = (rows + 63) / 64;
-    return (int32_t)(s < 1 ? 1 : s > 64 ? 64 : s);
+// Slices of rows: enough workgroups for 8 a CU, at least 16 rows each.
+int32_t dz_splits(int64_t rows, int64_t cols) {
+    const int64_t tiles = (cols + kDzCols - 1) / kDzCols;
+    int64_t s = (2048 + tiles - 1) / tiles;
+    s = s > (rows + 15) / 16 ? (rows + 15) / 16 : s;
+    return (int32_t)(s < 1 ? 1 : s > 256 ? 256 : s);
 }
 
 int64_t dz_threads(int64_t rows, int64_t cols) {
-    return (cols + kThreads - 1) / kThreads * kThreads * dz_splits(rows, cols);
+    return (cols + kDzCols - 1) / kDzCols * kThreads * dz_splits(rows, cols);
 }
 
 hipError_t launch_dz(int esize, const DzTask& t, hipStream_t stream) {

@@ -69,23 +69,34 @@ __device__ __forceinline__ void store_result(const GemmTask& t, int64_t m, int64
         from_f32(((T*)t.y)[m * t.ldy + n], y);
 }
 
-// Four results of consecutive n: 16- or 8-byte accesses (every row of the
-// outputs and the residual is aligned for them).
+// Four elements at any element address: global memory takes accesses of 8 or
+// 16 bytes at every alignment of the element.
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Loose4 {
+    T e[4];
+};
+template <typename T>
+__device__ __forceinline__ f32x4 load4(const T* p) {
+    const Loose4<T> v = *(const Loose4<T>*)p;
+    return f32x4{to_f32(v.e[0]), to_f32(v.e[1]), to_f32(v.e[2]), to_f32(v.e[3])};
+}
+__device__ __forceinline__ void store4(float* p, f32x4 v) {
+    *(Loose4<float>*)p = Loose4<float>{{v[0], v[1], v[2], v[3]}};
+}
+__device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
+    struct __attribute__((packed, aligned(2))) Loose8 {
+        uint32_t lo, hi;
+    };
+    *(Loose8*)p = Loose8{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+
+// Four results of consecutive n.
 template <typename T>
 __device__ __forceinline__ void store_results(const GemmTask& t, int64_t m, int64_t n, f32x4 acc) {
-    using V = T __attribute__((ext_vector_type(4)));
     if (t.bias)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc[i] += to_f32(((const T*)t.bias)[n + i]);
-    auto put = [](T* p, f32x4 v) {
-        if constexpr (sizeof(T) == 2)
-            *(uint2*)p = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-        else
-            *(f32x4*)p = v;
-    };
+        acc += load4((const T*)t.bias + n);
     if (t.pre)
-        put((T*)t.pre + m * t.ldp + n, acc);
+        store4((T*)t.pre + m * t.ldp + n, acc);
     switch (t.act) {                               // one uniform branch for the four
     case VPA_ACT_RELU:
         acc = act4<VPA_ACT_RELU>(acc);
@@ -99,25 +110,20 @@ __device__ __forceinline__ void store_results(const GemmTask& t, int64_t m, int6
     default:
         break;
     }
-    if (t.residual) {
-        const V r = *(const V*)((const T*)t.residual + m * t.ldr + n);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc[i] += to_f32((T)r[i]);
-    }
+    if (t.residual)
+        acc += load4((const T*)t.residual + m * t.ldr + n);
     if (t.out_f32)
-        *(f32x4*)((float*)t.y + m * t.ldy + n) = acc;
+        store4((float*)t.y + m * t.ldy + n, acc);
     else
-        put((T*)t.y + m * t.ldy + n, acc);
+        store4((T*)t.y + m * t.ldy + n, acc);
 }
 
 // A wavefront's 64 x 64 results from accumulators to memory, through its own
-// 16 KiB of LDS so that a store instruction covers whole rows: 4 rows of 64
-// where `vec` says that rows are aligned for 4 elements, else one row, an
-// element a lane.  Rows of LDS have 16 chunks of 16 bytes, chunk c of row r
+// 16 KiB of LDS so that a store instruction covers whole rows: 4 rows of 64,
+// or at the edge of n one row, an element a lane.  Rows of LDS have 16 chunks of 16 bytes, chunk c of row r
 // at c ^ (r & 15).
 template <typename T>
-__device__ __forceinline__ void store_block(const GemmTask& t, bool vec, float* part, char* lds,
+__device__ __forceinline__ void store_block(const GemmTask& t, float* part, char* lds,
                                             int64_t m0, int64_t n0, const f32x4 (&acc)[4][4]) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -131,7 +137,7 @@ __device__ __forceinline__ void store_block(const GemmTask& t, bool vec, float* 
     // fences keep the compiler to it
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (vec && n0 + 64 <= t.n) {
+    if (n0 + 64 <= t.n) {
 #pragma unroll 1
         for (int r0 = 0; r0 < 64; r0 += 16) {
             f32x4 v[4];
@@ -146,7 +152,7 @@ __device__ __forceinline__ void store_block(const GemmTask& t, bool vec, float* 
                 if (m >= t.m)
                     continue;
                 if (part)
-                    *(f32x4*)(part + m * t.n + n) = v[k];
+                    store4(part + m * t.n + n, v[k]);
                 else
                     store_results<T>(t, m, n, v[k]);
             }

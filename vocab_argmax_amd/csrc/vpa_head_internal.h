@@ -99,14 +99,13 @@ struct GemmTask {
     int32_t act;
     void* ws;                 // gemm_workspace() bytes
 };
-// How a product is cut; everything but `direct` and `vec` follows from sizes.
+// How a product is cut; everything but `direct` follows from sizes.
 struct GemmPlan {
     bool rows_kernel;         // few rows: linear_rows.hip
     int32_t tile;             // 256 or 128: rows and columns of a workgroup's tile
     int32_t slices;           // of k, joined by a second kernel
     int64_t stages_per_slice; // stages of 128 bytes of k
     bool direct;              // operands' strides allow direct loads to LDS
-    bool vec;                 // outputs' and residual's allow 4-element accesses
 };
 GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
 size_t gemm_workspace(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
