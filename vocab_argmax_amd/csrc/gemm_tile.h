@@ -33,12 +33,6 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef i16x4 __attribute__((address_space(3))) * lds_i16x4;
 typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef const __attribute__((address_space(1))) void* global_ptr;
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-
-// 16 bytes at any element address.
-struct __attribute__((packed, aligned(2))) Loose16 {
-    u32x4_t v;
-};
 
 // A pointer that is the same in every lane, as one.
 __device__ __forceinline__ void* uniform(const void* p) {

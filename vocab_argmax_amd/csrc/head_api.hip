@@ -96,27 +96,13 @@ vpa_status check_logprob_task(const char* call, int dt, int64_t ld, const vpa_vo
     return ok();
 }
 
-struct LogprobSizes {
-    int64_t chunks, slots;
-    size_t bytes;
-};
-LogprobSizes logprob_sizes(int esize, int64_t part_width, int64_t parts, int64_t rows,
-                           int32_t n_top) {
-    LogprobSizes s;
-    s.chunks = logprob_chunks(esize, part_width, parts, rows);
-    s.slots = parts * rows;
-    s.bytes = logprob_workspace(s.chunks, parts, rows, n_top);
-    return s;
-}
-
 vpa_status check_tokens(const int32_t* token_ids, int32_t n_tokens) {
     if (n_tokens > 0 && (!token_ids || !aligned(token_ids, 4)))
         return fail(VPA_ERR_INVALID, "token_ids is NULL or not 4-byte aligned");
     return ok();
 }
 
-// Shared checks of the calls that scan logits; launches the chunk kernel's
-// sizes only within one dispatch.
+// Shared checks of the calls that scan logits.
 vpa_status check_logprob_scan(const char* call, int esize, const LogprobTask& t,
                               const void* logits, const void* ws, size_t ws_bytes) {
     if (!logits || !aligned(logits, (size_t)esize))
@@ -125,11 +111,12 @@ vpa_status check_logprob_scan(const char* call, int esize, const LogprobTask& t,
     if (slots > kMaxSize)
         return fail(VPA_ERR_INVALID, "%s: %lld rows over all shards exceed 2^31-1", call,
                     (long long)slots);
-    const LogprobSizes z = logprob_sizes(esize, t.part_width, t.n_parts, t.n_rows, t.n_top);
+    const LogprobCut c = logprob_cut(esize, t.part_width, t.n_parts, t.n_rows);
     vpa_status st;
-    if ((st = check_dispatch(logprob_threads(z.chunks, t.n_parts, t.n_rows), call)) != VPA_OK)
+    if ((st = check_dispatch(logprob_threads(c), call)) != VPA_OK ||
+        (st = check_dispatch(slots * 256, call)) != VPA_OK)
         return st;
-    return check_workspace(call, ws, ws_bytes, z.bytes);
+    return check_workspace(call, ws, ws_bytes, logprob_workspace(c, t.n_top));
 }
 
 vpa_status check_logprob_out(const LogprobOut& o, int32_t n_top) {
@@ -198,8 +185,8 @@ size_t vpa_logprobs_workspace(vpa_vocab v, int32_t n_local_shards, int64_t n_row
     for (int esize = 2; esize <= 4; esize += 2) {
         const int64_t cuts[2][2] = {{v.vocab, 1}, {width, n_local_shards}};
         for (const auto& c : cuts) {
-            const LogprobSizes z = logprob_sizes(esize, c[0], c[1], n_rows, n_top);
-            most = z.bytes > most ? z.bytes : most;
+            const size_t bytes = logprob_workspace(logprob_cut(esize, c[0], c[1], n_rows), n_top);
+            most = bytes > most ? bytes : most;
         }
     }
     return most;
@@ -255,7 +242,7 @@ vpa_status vpa_combine_logprobs(const int32_t* stats, vpa_vocab v, int64_t n_row
     const LogprobOut o = {token_ids, n_tokens, logprobs, lse, row_stats, top_ids, top_logprobs};
     if ((st = check_tokens(token_ids, n_tokens)) != VPA_OK ||
         (st = check_logprob_out(o, n_top)) != VPA_OK ||
-        (st = check_dispatch(n_rows * 64, "vpa_combine_logprobs")) != VPA_OK)
+        (st = check_dispatch(n_rows * 256, "vpa_combine_logprobs")) != VPA_OK)
         return st;
     hipError_t e = launch_logprob_combine(stats, v.n_shards, v.shard_width, (int32_t)v.vocab,
                                           (int32_t)n_rows, n_top, o, (hipStream_t)stream);

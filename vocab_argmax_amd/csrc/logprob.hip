@@ -23,10 +23,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kVecs = 8;                          // 16-byte vectors per thread and chunk
+constexpr int kCandidates = 2048;                 // LDS list of a workgroup's candidates
+constexpr int kMostSegments = 64;                 // of a part of a row
+constexpr int kPartGroups = 1024;                 // workgroups to aim for
 
-constexpr int chunk_cols(int esize) {
-    return kThreads * kVecs * (16 / esize);
+// Columns of a chunk: U 16-byte vectors a thread.
+constexpr int chunk_cols(int esize, int u) {
+    return kThreads * u * (16 / esize);
 }
 
 constexpr float kNegInf = -__builtin_inff();
@@ -35,13 +38,15 @@ constexpr float kNegInf = -__builtin_inff();
 __device__ __forceinline__ uint64_t order_of(float x, int32_t id) {
     return ((uint64_t)key_f32(__builtin_bit_cast(uint32_t, x)) << 32) | (uint32_t)~id;
 }
-__device__ __forceinline__ float value_of(uint64_t order) {
-    const uint32_t key = (uint32_t)(order >> 32);
+__device__ __forceinline__ float value_of_key(uint32_t key) {
     if (key == kKeyNanF32)
         return __builtin_nanf("");
     if (key == kKeyZeroF32)
         return 0.0f;
     return __builtin_bit_cast(float, bits_of_key_f32(key));
+}
+__device__ __forceinline__ float value_of(uint64_t order) {
+    return value_of_key((uint32_t)(order >> 32));
 }
 __device__ __forceinline__ int32_t id_of(uint64_t order) {
     return (int32_t)~(uint32_t)order;
@@ -85,98 +90,263 @@ __device__ __forceinline__ Sums wave_join(Sums v) {
     return v;
 }
 
-// A chunk's partial result in the workspace: Sums of every chunk first, then
-// the chunks' top lists.
-__device__ __forceinline__ Sums* sums_of(void* ws) {
-    return (Sums*)ws;
-}
+// Partial results in the workspace: the Sums of every segment first, then the
+// segments' top lists.
 __host__ __device__ inline size_t sums_bytes(int64_t n) {
     return ((size_t)n * sizeof(Sums) + 255) / 256 * 256;
 }
 
-template <int ESIZE>
-__global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, int32_t chunks,
+// n of a wavefront's 64 keys are at least the result, cut to its upper 16
+// bits: the n-th largest key from below.
+__device__ __forceinline__ uint32_t wave_nth_key(uint32_t key, int n) {
+    uint32_t nth = 0;
+#pragma unroll
+    for (int b = 31; b >= 16; --b) {
+        const uint32_t t = nth | (1u << b);
+        nth = __popcll(__ballot(key >= t)) >= n ? t : nth;
+    }
+    return nth;
+}
+
+// The largest n_top of the n orders order(i) (0: none), by the whole
+// workgroup, in order into out[]; returns how many there are (at most
+// n_top).  Each candidate's place is the number of larger ones.
+__device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int n_top,
+                                                uint64_t* out) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t mine = cand[i];
+        int larger = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j)
+            larger += cand[j] > mine;
+        if (larger < n_top)
+            out[larger] = mine;
+    }
+}
+
+// One segment of a row: its Sums and its first n_top columns.
+//
+// The workgroup walks the segment in chunks of U 16-byte vectors a thread,
+// held in registers as fp32.  Every lane keeps M, s and u of its own columns,
+// joined at the end.  A chunk costs 1.5 instructions an element to unpack
+// and take the maximum and 4 more issue slots' worth for 2^z beside a
+// multiply-add, an add and a multiply-add: for bf16 about 8.5 slots, 0.75 of
+// what the memory's rate allows.
+//
+// Alternatives: T is a lower bound of the n_top-th largest value, from the
+// largest values of the lanes on the first chunk (in each of the W
+// wavefronts with columns at least ceil(n_top / W) lanes reach T, so n_top
+// columns do), then the n_top-th value found so far; columns reaching T go
+// to a list in LDS, and the list is cut to its first n_top by counting for
+// each the larger ones.  Few columns pass T, so the scan costs one maximum
+// and one comparison a vector.  A chunk with a NaN, an infinity or more
+// candidates than the list holds takes n_top maxima over the registers.
+template <int ESIZE, int U>
+__global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, LogprobCut cut,
                                                                 void* ws) {
     using T = typename elem<ESIZE>::type;
     constexpr int VEC = 16 / ESIZE;
-    constexpr int N = kVecs * VEC;
-    __shared__ float lds_m[kWaves];
+    constexpr int N = U * VEC;
+    constexpr int CHUNK = chunk_cols(ESIZE, U);
     __shared__ Sums lds_s[kWaves];
-    __shared__ uint64_t lds_top[2][kWaves];
-    const int32_t chunk = blockIdx.x % chunks;
-    const int32_t rest = blockIdx.x / chunks;
+    __shared__ uint32_t lds_key[kWaves];
+    __shared__ uint64_t lds_best[2][kWaves];
+    __shared__ uint64_t cand[kCandidates];
+    __shared__ uint64_t list[VPA_MAX_TOP];
+    __shared__ uint32_t added[3];
+    const int32_t seg = blockIdx.x % cut.segments;
+    const int32_t rest = blockIdx.x / cut.segments;
     const int32_t row = rest % t.n_rows, part = rest / t.n_rows;
     const int64_t first = t.col0 + part * t.part_stride;
-    const int64_t end = first + t.part_width < t.vocab ? first + t.part_width : t.vocab;
-    const int64_t lo = first + (int64_t)chunk * chunk_cols(ESIZE);
+    const int64_t part_end = first + t.part_width < t.vocab ? first + t.part_width : t.vocab;
+    const int64_t lo = first + (int64_t)seg * cut.chunks_per_segment * CHUNK;
+    const int64_t to = lo + (int64_t)cut.chunks_per_segment * CHUNK;
+    const int64_t hi = to < part_end ? to : part_end;
     const T* x = (const T*)t.logits + (int64_t)row * t.ld - t.col0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 
-    float v[N];
+    Sums r = {kNegInf, 0.0f, 0.0f};
+    int kept = 0;                                   // of cand[]: the best so far, in order
+    float bound = kNegInf;                          // T
+    if (t.n_top && threadIdx.x < 3)
+        added[threadIdx.x] = 0;
+    int turn = 0;                                   // of added[]
+    for (int64_t c0 = lo; c0 < hi; c0 += CHUNK) {
+        float v[N];
+        float g[U];                                 // a vector's maximum
+        const int64_t mine = c0 + threadIdx.x * VEC;
+        if (c0 + CHUNK <= hi) {
+            u32x4_t w[U];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int64_t c = lo + ((i / VEC) * kThreads + threadIdx.x) * VEC + i % VEC;
-        v[i] = c < end ? to_f32(x[c]) : kNegInf;
-    }
-    float mx = kNegInf;
+            for (int i = 0; i < U; ++i)
+                w[i] = __builtin_nontemporal_load(
+                    &((const Loose16*)(x + mine + i * kThreads * VEC))->v);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        mx = fmaxf(mx, v[i]);
-    mx = wave_max(mx);
-    if (lane == 0)
-        lds_m[wave] = mx;
-    __syncthreads();
+            for (int i = 0; i < N; ++i)
+                v[i] = vec_elem<ESIZE>(w[i / VEC], i % VEC);
+        } else {
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i)
-        mx = fmaxf(mx, lds_m[i]);
-    // a chunk of -inf alone: measured from 0, every term is 2^-1e30 = 0
-    const float base = mx == kNegInf ? 0.0f : mx;
-    float s = 0.0f, u = 0.0f;
+            for (int i = 0; i < U; ++i) {
+                const int64_t c = mine + i * kThreads * VEC;
+                u32x4_t w = {0, 0, 0, 0};
+                if (c + VEC <= hi)
+                    w = ((const Loose16*)(x + c))->v;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float z = scaled_distance(v[i], base);
-        const float e = exp2_fast(z);
-        s += e;
-        u += z * e;
-    }
-    s = wave_sum(s);
-    u = wave_sum(u);
-    if (lane == 0)
-        lds_s[wave] = Sums{mx, s, u};
-    __syncthreads();
-    const int64_t slot = blockIdx.x;
-    if (threadIdx.x == 0) {
-        Sums r = lds_s[0];
-        for (int i = 1; i < kWaves; ++i) {
-            r.s += lds_s[i].s;
-            r.u += lds_s[i].u;
+                for (int e = 0; e < VEC; ++e)
+                    v[i * VEC + e] = c + VEC <= hi ? vec_elem<ESIZE>(w, e)
+                                     : c + e < hi  ? to_f32(x[c + e])
+                                                   : kNegInf;
+            }
         }
-        sums_of(ws)[slot] = r;
-    }
-    if (t.n_top == 0)
-        return;
-    uint64_t* tops = (uint64_t*)((char*)ws + sums_bytes((int64_t)chunks * t.n_rows * t.n_parts)) +
-                     slot * t.n_top;
-    uint64_t below = ~0ull;
-    for (int k = 0; k < t.n_top; ++k) {
-        uint64_t best = 0;
+        float mx = kNegInf;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            g[i] = v[i * VEC];
+#pragma unroll
+            for (int e = 1; e < VEC; ++e)
+                g[i] = fmaxf(g[i], v[i * VEC + e]);
+            mx = fmaxf(mx, g[i]);
+        }
+        // the lane's sums so far, measured from the new maximum
+        const float m = fmaxf(r.m, mx);
+        {
+            const float d = r.m == m ? 0.0f : scaled_distance(r.m, m);
+            const float f = exp2_fast(d);
+            r.u = (r.u + d * r.s) * f;
+            r.s *= f;
+            r.m = m;
+        }
+        // z from the rounded m log2(e) is one instruction; what the rounding
+        // took off is put right on the sums
+        const float b = m * kLog2e;
+        float s = 0.0f, u = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int64_t c = lo + ((i / VEC) * kThreads + threadIdx.x) * VEC + i % VEC;
-            const uint64_t o = order_of(v[i], (int32_t)c);
-            if (c < end && o < below && o > best)
-                best = o;
+            const float z = __builtin_fmaf(v[i], kLog2e, -b);
+            const float e = exp2_fast(z);
+            s += e;
+            u = __builtin_fmaf(z, e, u);
         }
-        best = wave_max_u64(best);
-        if (lane == 0)
-            lds_top[k & 1][wave] = best;
-        __syncthreads();
-        for (int i = 0; i < kWaves; ++i)
-            best = lds_top[k & 1][i] > best ? lds_top[k & 1][i] : best;
+        const float off = __builtin_fmaf(m, kLog2e, -b);
+        const float f = exp2_fast(-off);
+        u = __builtin_fmaf(-off, s, u) * f;
+        s *= f;
+        // masked columns (0 * -inf), infinities and NaN, and values whose
+        // product with log2(e) is not finite: once more, with care
+        const bool odd = !(fabsf(u) < __builtin_inff());
+        if (__ballot(odd)) {
+            if (odd) {
+                const float base = m == kNegInf ? 0.0f : m;
+                s = u = 0.0f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float z = scaled_distance(v[i], base);
+                    const float e = exp2_fast(z);
+                    s += e;
+                    u += z * e;
+                }
+            }
+        }
+        r.s += s;
+        r.u += u;
+        if (t.n_top == 0)
+            continue;
+
+        // NaN and +inf make the lane's s NaN
+        const bool strange = __syncthreads_or(s != s);
+        bool slow = strange;
+        int total = kept;
+        if (!strange) {
+            if (c0 == lo) {
+                const int64_t lanes = (hi - lo + VEC - 1) / VEC;    // with columns
+                const int waves = lanes >= kThreads ? kWaves : (int)((lanes + 63) / 64);
+                const uint32_t nth = wave_nth_key(key_f32(__builtin_bit_cast(uint32_t, mx)),
+                                                  (t.n_top + waves - 1) / waves);
+                if (lane == 0)
+                    lds_key[wave] = nth;
+                __syncthreads();
+                uint32_t least = lds_key[0];
+                for (int i = 1; i < waves; ++i)
+                    least = lds_key[i] < least ? lds_key[i] : least;
+                bound = value_of_key(least);
+            }
+            if (__ballot(mx >= bound)) {
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    if (!__ballot(g[i] >= bound))
+                        continue;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const int64_t c = mine + i * kThreads * VEC + e;
+                        if (v[i * VEC + e] >= bound && c < hi) {
+                            const uint32_t at = kept + atomicAdd(&added[turn], 1u);
+                            if (at < kCandidates)
+                                cand[at] = order_of(v[i * VEC + e], (int32_t)c);
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            total = kept + (int)added[turn];
+            slow = total > kCandidates;
+        }
+        // the counter after next was last read before the barrier above
         if (threadIdx.x == 0)
-            tops[k] = best;
-        below = best;
+            added[turn == 0 ? 2 : turn - 1] = 0;
+        turn = turn == 2 ? 0 : turn + 1;
+        if (!slow && total == kept)
+            continue;
+        if (!slow) {
+            rank_candidates(cand, total, t.n_top, list);
+        } else {
+            // the best of the kept ones and of every column, n_top times
+            uint64_t below = ~0ull;
+            total = 0;
+            for (int k = 0; k < t.n_top; ++k) {
+                uint64_t best = 0;
+                if ((int)threadIdx.x < kept && cand[threadIdx.x] < below)
+                    best = cand[threadIdx.x];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int64_t c = mine + (i / VEC) * kThreads * VEC + i % VEC;
+                    const uint64_t o = order_of(v[i], (int32_t)c);
+                    if (c < hi && o < below && o > best)
+                        best = o;
+                }
+                best = wave_max_u64(best);
+                if (lane == 0)
+                    lds_best[k & 1][wave] = best;
+                __syncthreads();
+                for (int i = 0; i < kWaves; ++i)
+                    best = lds_best[k & 1][i] > best ? lds_best[k & 1][i] : best;
+                if (threadIdx.x == 0)
+                    list[k] = best;
+                total += best != 0;
+                below = best;
+            }
+        }
+        __syncthreads();
+        kept = total < t.n_top ? total : t.n_top;
+        if ((int)threadIdx.x < kept)
+            cand[threadIdx.x] = list[threadIdx.x];
+        // later columns have larger ids: they have to be above the last value
+        if (kept == t.n_top) {
+            const uint32_t key = (uint32_t)(list[kept - 1] >> 32);
+            bound = key >= kKeyNanF32 ? __builtin_nanf("") : value_of_key(key + 1);
+        }
     }
+    r = wave_join(r);
+    if (lane == 0)
+        lds_s[wave] = r;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kWaves; ++i)
+            join(r, lds_s[i]);
+        ((Sums*)ws)[blockIdx.x] = r;
+    }
+    uint64_t* tops = (uint64_t*)((char*)ws + sums_bytes(cut.total)) + (int64_t)blockIdx.x * t.n_top;
+    if ((int)threadIdx.x < t.n_top)
+        tops[threadIdx.x] = (int)threadIdx.x < kept ? cand[threadIdx.x] : 0;
 }
 
 // A row's max and ln s from its joined sums; no finite column: (-inf, 0).
@@ -204,7 +374,7 @@ __device__ __forceinline__ void write_row(const Sums& r, const RowScale& sc, int
         o.row_stats[3 * row + 1] = sc.log_sum;
         o.row_stats[3 * row + 2] = sc.empty ? 0.0f : (log2f(r.s) - r.u / r.s) * kLn2;
     }
-    for (int j = threadIdx.x; j < o.n_tokens; j += 64) {
+    for (int j = threadIdx.x; j < o.n_tokens; j += kThreads) {
         const int32_t id = o.token_ids[row * o.n_tokens + j];
         float lp = __builtin_nanf("");
         if (id == -1)
@@ -215,47 +385,103 @@ __device__ __forceinline__ void write_row(const Sums& r, const RowScale& sc, int
     }
 }
 
-// The n_top largest of n orders, one after the other, by one wavefront.
+// The n_top largest of n orders (0: none), by the whole workgroup: take(k,
+// order) is called for the k-th by one thread.  `lists` orders each begin at
+// a multiple of n_top, largest first: the largest last order of a list is
+// reached by n_top orders, and those go to LDS to be ranked.  Where they do
+// not fit, the largest is taken n_top times.
 template <typename Order, typename Take>
-__device__ __forceinline__ void select_top(int64_t n, int32_t n_top, Order order, Take take) {
+__device__ __forceinline__ void select_top(int64_t lists, int32_t n_top, uint64_t* cand,
+                                           uint64_t* list, Order order, Take take) {
+    __shared__ uint64_t best_of[2][kWaves];
+    __shared__ uint32_t count;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n = lists * n_top;
+    uint64_t least = 0;
+    for (int64_t i = threadIdx.x; i < lists; i += kThreads) {
+        const uint64_t o = order(i * n_top + n_top - 1);
+        least = o > least ? o : least;
+    }
+    least = wave_max_u64(least);
+    if (lane == 0)
+        best_of[0][wave] = least;
+    if (threadIdx.x == 0)
+        count = 0;
+    __syncthreads();
+    for (int i = 0; i < kWaves; ++i)
+        least = best_of[0][i] > least ? best_of[0][i] : least;
+    least = least ? least : 1;                      // empty places are not candidates
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t o = order(i);
+        if (o >= least) {
+            const uint32_t at = atomicAdd(&count, 1u);
+            if (at < kCandidates)
+                cand[at] = o;
+        }
+    }
+    if ((int)threadIdx.x < n_top)
+        list[threadIdx.x] = 0;
+    __syncthreads();
+    if (count <= kCandidates) {
+        rank_candidates(cand, (int)count, n_top, list);
+        __syncthreads();
+        if ((int)threadIdx.x < n_top)
+            take((int)threadIdx.x, list[threadIdx.x]);
+        return;
+    }
     uint64_t below = ~0ull;
     for (int k = 0; k < n_top; ++k) {
         uint64_t best = 0;
-        for (int64_t i = threadIdx.x; i < n; i += 64) {
+        for (int64_t i = threadIdx.x; i < n; i += kThreads) {
             const uint64_t o = order(i);
             if (o < below && o > best)
                 best = o;
         }
         best = wave_max_u64(best);
+        if (lane == 0)
+            best_of[(k + 1) & 1][wave] = best;
+        __syncthreads();
+        for (int i = 0; i < kWaves; ++i)
+            best = best_of[(k + 1) & 1][i] > best ? best_of[(k + 1) & 1][i] : best;
         if (threadIdx.x == 0)
             take(k, best);
         below = best;
     }
 }
 
-// One wavefront per (part, row): joins the chunks.
-__device__ __forceinline__ Sums join_chunks(const void* ws, int64_t first, int32_t chunks) {
+// Joins sums(0) ... sums(n - 1); every thread holds the result.
+template <typename Get>
+__device__ __forceinline__ Sums join_all(int64_t n, Get sums) {
+    __shared__ Sums lds[kWaves];
     Sums r = {kNegInf, 0.0f, 0.0f};
-    for (int32_t c = threadIdx.x; c < chunks; c += 64)
-        join(r, ((const Sums*)ws)[first + c]);
-    return wave_join(r);
+    for (int64_t i = threadIdx.x; i < n; i += kThreads)
+        join(r, sums(i));
+    r = wave_join(r);
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = r;
+    __syncthreads();
+    r = lds[0];
+    for (int i = 1; i < kWaves; ++i)
+        join(r, lds[i]);
+    return r;
 }
 
 template <int ESIZE>
-__global__ __launch_bounds__(64) void logprob_finish_kernel(LogprobTask t, int32_t chunks,
-                                                            const void* ws, LogprobOut o) {
+__global__ __launch_bounds__(kThreads) void logprob_finish_kernel(LogprobTask t, LogprobCut cut,
+                                                                  const void* ws, LogprobOut o) {
     using T = typename elem<ESIZE>::type;
+    __shared__ uint64_t cand[kCandidates], list[VPA_MAX_TOP];
     const int64_t row = blockIdx.x;
-    const Sums r = join_chunks(ws, row * chunks, chunks);
+    const Sums* sums = (const Sums*)ws + row * cut.segments;
+    const Sums r = join_all(cut.segments, [&](int64_t i) { return sums[i]; });
     const T* x = (const T*)t.logits + row * t.ld - t.col0;
     const RowScale sc = scale_of(r);
     write_row(r, sc, row, t.vocab, o, [&](int, int32_t id) { return to_f32(x[id]); });
     if (t.n_top == 0)
         return;
-    const uint64_t* tops =
-        (const uint64_t*)((const char*)ws + sums_bytes((int64_t)chunks * t.n_rows * t.n_parts)) +
-        row * chunks * t.n_top;
-    select_top((int64_t)chunks * t.n_top, t.n_top, [&](int64_t i) { return tops[i]; },
+    const uint64_t* tops = (const uint64_t*)((const char*)ws + sums_bytes(cut.total)) +
+                           row * cut.segments * t.n_top;
+    select_top(cut.segments, t.n_top, cand, list, [&](int64_t i) { return tops[i]; },
                [&](int k, uint64_t best) {
                    o.top_ids[row * t.n_top + k] = id_of(best);
                    o.top_logprobs[row * t.n_top + k] = sc.logprob(value_of(best));
@@ -263,15 +489,18 @@ __global__ __launch_bounds__(64) void logprob_finish_kernel(LogprobTask t, int32
 }
 
 template <int ESIZE>
-__global__ __launch_bounds__(64) void logprob_record_kernel(LogprobTask t, int32_t chunks,
-                                                            const void* ws,
-                                                            const int32_t* token_ids,
-                                                            int32_t n_tokens, int32_t* stats) {
+__global__ __launch_bounds__(kThreads) void logprob_record_kernel(LogprobTask t, LogprobCut cut,
+                                                                  const void* ws,
+                                                                  const int32_t* token_ids,
+                                                                  int32_t n_tokens,
+                                                                  int32_t* stats) {
     using T = typename elem<ESIZE>::type;
+    __shared__ uint64_t cand[kCandidates], list[VPA_MAX_TOP];
     const int64_t slot = blockIdx.x;
     const int64_t row = slot % t.n_rows, part = slot / t.n_rows;
     int32_t* rec = stats + slot * (3 + n_tokens + 2 * t.n_top);
-    const Sums r = join_chunks(ws, slot * chunks, chunks);
+    const Sums* sums = (const Sums*)ws + slot * cut.segments;
+    const Sums r = join_all(cut.segments, [&](int64_t i) { return sums[i]; });
     if (threadIdx.x == 0) {
         rec[0] = __builtin_bit_cast(int32_t, r.m);
         rec[1] = __builtin_bit_cast(int32_t, r.s);
@@ -280,17 +509,16 @@ __global__ __launch_bounds__(64) void logprob_record_kernel(LogprobTask t, int32
     const int64_t first = t.col0 + part * t.part_stride;
     const int64_t end = first + t.part_width < t.vocab ? first + t.part_width : t.vocab;
     const T* x = (const T*)t.logits + row * t.ld - t.col0;
-    for (int j = threadIdx.x; j < n_tokens; j += 64) {
+    for (int j = threadIdx.x; j < n_tokens; j += kThreads) {
         const int32_t id = token_ids[row * n_tokens + j];
         const float v = id >= first && id < end ? to_f32(x[id]) : 0.0f;
         rec[3 + j] = __builtin_bit_cast(int32_t, v);
     }
     if (t.n_top == 0)
         return;
-    const uint64_t* tops =
-        (const uint64_t*)((const char*)ws + sums_bytes((int64_t)chunks * t.n_rows * t.n_parts)) +
-        slot * chunks * t.n_top;
-    select_top((int64_t)chunks * t.n_top, t.n_top, [&](int64_t i) { return tops[i]; },
+    const uint64_t* tops = (const uint64_t*)((const char*)ws + sums_bytes(cut.total)) +
+                           slot * cut.segments * t.n_top;
+    select_top(cut.segments, t.n_top, cand, list, [&](int64_t i) { return tops[i]; },
                [&](int k, uint64_t best) {
                    int32_t* p = rec + 3 + n_tokens + 2 * k;
                    p[0] = best ? __builtin_bit_cast(int32_t, value_of(best))
@@ -299,28 +527,29 @@ __global__ __launch_bounds__(64) void logprob_record_kernel(LogprobTask t, int32
                });
 }
 
-__global__ __launch_bounds__(64) void logprob_combine_kernel(const int32_t* stats,
-                                                             int32_t n_shards,
-                                                             int64_t shard_width, int32_t vocab,
-                                                             int32_t n_rows, int32_t n_top,
-                                                             LogprobOut o) {
+__global__ __launch_bounds__(kThreads) void logprob_combine_kernel(const int32_t* stats,
+                                                                   int32_t n_shards,
+                                                                   int64_t shard_width,
+                                                                   int32_t vocab, int32_t n_rows,
+                                                                   int32_t n_top, LogprobOut o) {
+    __shared__ uint64_t cand[kCandidates], list[VPA_MAX_TOP];
     const int64_t row = blockIdx.x;
     const int64_t words = 3 + o.n_tokens + 2 * (int64_t)n_top;
     const int32_t* rec = stats + row * words;
     const int64_t step = n_rows * words;           // from shard to shard
-    Sums r = {kNegInf, 0.0f, 0.0f};
-    for (int32_t s = threadIdx.x; s < n_shards; s += 64) {
+    const Sums r = join_all(n_shards, [&](int64_t s) {
         const int32_t* p = rec + s * step;
-        join(r, Sums{__builtin_bit_cast(float, p[0]), __builtin_bit_cast(float, p[1]),
-                     __builtin_bit_cast(float, p[2])});
-    }
-    r = wave_join(r);
+        return Sums{__builtin_bit_cast(float, p[0]), __builtin_bit_cast(float, p[1]),
+                    __builtin_bit_cast(float, p[2])};
+    });
     const RowScale sc = scale_of(r);
     write_row(r, sc, row, vocab, o, [&](int j, int32_t id) {
         return __builtin_bit_cast(float, rec[(id / shard_width) * step + 3 + j]);
     });
+    if (n_top == 0)
+        return;
     const int32_t* top0 = rec + 3 + o.n_tokens;
-    select_top((int64_t)n_shards * n_top, n_top,
+    select_top(n_shards, n_top, cand, list,
                [&](int64_t i) {
                    const int32_t* p = top0 + (i / n_top) * step + 2 * (i % n_top);
                    return p[1] == VPA_EMPTY_ID
@@ -333,25 +562,28 @@ __global__ __launch_bounds__(64) void logprob_combine_kernel(const int32_t* stat
                });
 }
 
+constexpr int kGradVecs = 4;                       // 16-byte vectors a thread
+
 // grad_c = sum_j g_j [c = t_j] - p_c (G + gH (log p_c + H)), G = sum_j g_j.
 // A workgroup writes one chunk of a row without the given tokens' own terms,
 // then the few elements that have them, from logits read before the chunk
 // was written (the gradient may replace the logits).  Equal tokens all write
 // the same sum.
-template <int ESIZE>
+template <int ESIZE, bool ENTROPY>
 __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradTask t,
                                                                 int32_t chunks) {
     using T = typename elem<ESIZE>::type;
     constexpr int VEC = 16 / ESIZE;
+    constexpr int CHUNK = chunk_cols(ESIZE, kGradVecs);
     const int64_t row = blockIdx.x / chunks;
-    const int64_t lo = (int64_t)(blockIdx.x % chunks) * chunk_cols(ESIZE);
-    const int64_t hi = lo + chunk_cols(ESIZE) < t.grad_cols ? lo + chunk_cols(ESIZE) : t.grad_cols;
+    const int64_t lo = (int64_t)(blockIdx.x % chunks) * CHUNK;
+    const int64_t hi = lo + CHUNK < t.grad_cols ? lo + CHUNK : t.grad_cols;
     const T* x = (const T*)t.logits + row * t.ld;
     T* d = (T*)t.grad + row * t.grad_ld;
     const float max = t.row_stats[3 * row], log_sum = t.row_stats[3 * row + 1];
     const float h = t.row_stats[3 * row + 2];
     const bool empty = max == kNegInf && log_sum == 0.0f;
-    const float gh = t.grad_entropy ? t.grad_entropy[row] : 0.0f;
+    const float gh = ENTROPY ? t.grad_entropy[row] : 0.0f;
     const int32_t* tok = t.token_ids + row * t.n_tokens;
     const float* g = t.grad_logprobs + row * t.n_tokens;
     float sum = 0.0f;
@@ -361,7 +593,8 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradTask 
     auto slope = [&](float v) {
         const float lp = (v - max) - log_sum;
         const float p = exp2f(lp * kLog2e);        // keeps p below 2^-126
-        return empty || p == 0.0f ? 0.0f : -p * (sum + gh * (lp + h));
+        const float w = ENTROPY ? __builtin_fmaf(gh, lp + h, sum) : sum;
+        return empty || p == 0.0f ? 0.0f : -p * w;
     };
     // this workgroup's given token, one a thread
     const int32_t mine = threadIdx.x < (uint32_t)t.n_tokens ? tok[threadIdx.x] : -1;
@@ -369,11 +602,34 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradTask 
     const bool here = mine >= 0 && mine < t.vocab && at >= lo && at < hi && at < t.cols;
     const float own = here ? to_f32(x[at]) : 0.0f;
     __syncthreads();
+    u32x4_t w[kGradVecs];
 #pragma unroll
-    for (int i = 0; i < kVecs * VEC; ++i) {
-        const int64_t c = lo + ((i / VEC) * kThreads + threadIdx.x) * VEC + i % VEC;
-        if (c < hi)
-            from_f32(d[c], c < t.cols ? slope(to_f32(x[c])) : 0.0f);
+    for (int i = 0; i < kGradVecs; ++i) {
+        const int64_t c = lo + (i * kThreads + threadIdx.x) * VEC;
+        if (c + VEC <= t.cols)
+            w[i] = ((const Loose16*)(x + c))->v;
+    }
+#pragma unroll
+    for (int i = 0; i < kGradVecs; ++i) {
+        const int64_t c = lo + (i * kThreads + threadIdx.x) * VEC;
+        if (c + VEC <= t.cols) {
+            u32x4_t o;
+            if constexpr (ESIZE == 2) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[e] = pack_bf16(slope(vec_elem<2>(w[i], 2 * e)),
+                                     slope(vec_elem<2>(w[i], 2 * e + 1)));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[e] = __builtin_bit_cast(uint32_t, slope(vec_elem<4>(w[i], e)));
+            }
+            ((Loose16*)(d + c))->v = o;
+        } else {
+            for (int e = 0; e < VEC; ++e)
+                if (c + e < hi)
+                    from_f32(d[c + e], c + e < t.cols ? slope(to_f32(x[c + e])) : 0.0f);
+        }
     }
     __syncthreads();
     if (here) {
@@ -386,63 +642,83 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradTask 
 
 }  // namespace
 
-int32_t logprob_chunks(int esize, int64_t part_width, int64_t, int64_t) {
-    return (int32_t)((part_width + chunk_cols(esize) - 1) / chunk_cols(esize));
+// Chunks of 8 vectors a thread where that still gives every CU 4 workgroups,
+// else of 2 (a decode batch: more, shorter workgroups); a part is cut into
+// segments of whole chunks until there are 4 workgroups a CU.
+LogprobCut logprob_cut(int esize, int64_t part_width, int64_t n_parts, int64_t n_rows) {
+    LogprobCut c;
+    const int64_t rows = n_parts * n_rows;
+    c.vecs = rows * ((part_width + chunk_cols(esize, 8) - 1) / chunk_cols(esize, 8)) >= 1024 ? 8 : 2;
+    const int64_t chunks = (part_width + chunk_cols(esize, c.vecs) - 1) / chunk_cols(esize, c.vecs);
+    int64_t want = (kPartGroups + rows - 1) / rows;
+    want = want > chunks ? chunks : want;
+    want = want > kMostSegments ? kMostSegments : want;
+    c.chunks_per_segment = (int32_t)((chunks + want - 1) / want);
+    c.segments = (int32_t)((chunks + c.chunks_per_segment - 1) / c.chunks_per_segment);
+    c.total = rows * c.segments;
+    return c;
 }
 
-size_t logprob_workspace(int64_t n_chunks, int64_t n_parts, int64_t n_rows, int32_t n_top) {
-    const int64_t n = n_chunks * n_parts * n_rows;
-    return sums_bytes(n) + ((size_t)n * n_top * 8 + 255) / 256 * 256;
+size_t logprob_workspace(const LogprobCut& c, int32_t n_top) {
+    return sums_bytes(c.total) + ((size_t)c.total * n_top * 8 + 255) / 256 * 256;
 }
 
-int64_t logprob_threads(int64_t n_chunks, int64_t n_parts, int64_t n_rows) {
-    return n_chunks * n_parts * n_rows * kThreads;
+int64_t logprob_threads(const LogprobCut& c) {
+    return c.total * kThreads;
 }
 
 hipError_t launch_logprob_parts(int esize, const LogprobTask& t, void* ws, hipStream_t stream) {
-    const int32_t chunks = logprob_chunks(esize, t.part_width, t.n_parts, t.n_rows);
-    const dim3 grid((uint32_t)((int64_t)chunks * t.n_rows * t.n_parts));
-    return esize == 2
-               ? launch(logprob_part_kernel<2>, grid, dim3(kThreads), 0, stream, t, chunks, ws)
-               : launch(logprob_part_kernel<4>, grid, dim3(kThreads), 0, stream, t, chunks, ws);
+    const LogprobCut c = logprob_cut(esize, t.part_width, t.n_parts, t.n_rows);
+    const dim3 grid((uint32_t)c.total), block(kThreads);
+    if (esize == 2)
+        return c.vecs == 8 ? launch(logprob_part_kernel<2, 8>, grid, block, 0, stream, t, c, ws)
+                           : launch(logprob_part_kernel<2, 2>, grid, block, 0, stream, t, c, ws);
+    return c.vecs == 8 ? launch(logprob_part_kernel<4, 8>, grid, block, 0, stream, t, c, ws)
+                       : launch(logprob_part_kernel<4, 2>, grid, block, 0, stream, t, c, ws);
 }
 
 hipError_t launch_logprob_finish(int esize, const LogprobTask& t, const void* ws,
                                  const LogprobOut& o, hipStream_t stream) {
-    const int32_t chunks = logprob_chunks(esize, t.part_width, t.n_parts, t.n_rows);
-    const dim3 grid((uint32_t)t.n_rows);
-    return esize == 2
-               ? launch(logprob_finish_kernel<2>, grid, dim3(64), 0, stream, t, chunks, ws, o)
-               : launch(logprob_finish_kernel<4>, grid, dim3(64), 0, stream, t, chunks, ws, o);
+    const LogprobCut c = logprob_cut(esize, t.part_width, t.n_parts, t.n_rows);
+    const dim3 grid((uint32_t)t.n_rows), block(kThreads);
+    return esize == 2 ? launch(logprob_finish_kernel<2>, grid, block, 0, stream, t, c, ws, o)
+                      : launch(logprob_finish_kernel<4>, grid, block, 0, stream, t, c, ws, o);
 }
 
 hipError_t launch_logprob_records(int esize, const LogprobTask& t, const void* ws,
                                   const int32_t* token_ids, int32_t n_tokens, int32_t* stats,
                                   hipStream_t stream) {
-    const int32_t chunks = logprob_chunks(esize, t.part_width, t.n_parts, t.n_rows);
-    const dim3 grid((uint32_t)((int64_t)t.n_rows * t.n_parts));
-    return esize == 2 ? launch(logprob_record_kernel<2>, grid, dim3(64), 0, stream, t, chunks, ws,
+    const LogprobCut c = logprob_cut(esize, t.part_width, t.n_parts, t.n_rows);
+    const dim3 grid((uint32_t)((int64_t)t.n_rows * t.n_parts)), block(kThreads);
+    return esize == 2 ? launch(logprob_record_kernel<2>, grid, block, 0, stream, t, c, ws,
                                token_ids, n_tokens, stats)
-                      : launch(logprob_record_kernel<4>, grid, dim3(64), 0, stream, t, chunks, ws,
+                      : launch(logprob_record_kernel<4>, grid, block, 0, stream, t, c, ws,
                                token_ids, n_tokens, stats);
 }
 
 hipError_t launch_logprob_combine(const int32_t* stats, int32_t n_shards, int64_t shard_width,
                                   int32_t vocab, int32_t n_rows, int32_t n_top,
                                   const LogprobOut& o, hipStream_t stream) {
-    return launch(logprob_combine_kernel, dim3((uint32_t)n_rows), dim3(64), 0, stream, stats,
+    return launch(logprob_combine_kernel, dim3((uint32_t)n_rows), dim3(kThreads), 0, stream, stats,
                   n_shards, shard_width, vocab, n_rows, n_top, o);
 }
 
 int64_t logprob_grad_threads(int esize, int64_t grad_cols, int64_t n_rows) {
-    return (grad_cols + chunk_cols(esize) - 1) / chunk_cols(esize) * n_rows * kThreads;
+    const int64_t chunk = chunk_cols(esize, kGradVecs);
+    return (grad_cols + chunk - 1) / chunk * n_rows * kThreads;
 }
 
 hipError_t launch_logprob_grad(int esize, const LogprobGradTask& t, hipStream_t stream) {
-    const int32_t chunks = (int32_t)((t.grad_cols + chunk_cols(esize) - 1) / chunk_cols(esize));
-    const dim3 grid((uint32_t)((int64_t)chunks * t.n_rows));
-    return esize == 2 ? launch(logprob_grad_kernel<2>, grid, dim3(kThreads), 0, stream, t, chunks)
-                      : launch(logprob_grad_kernel<4>, grid, dim3(kThreads), 0, stream, t, chunks);
+    const int64_t chunk = chunk_cols(esize, kGradVecs);
+    const int32_t chunks = (int32_t)((t.grad_cols + chunk - 1) / chunk);
+    const dim3 grid((uint32_t)((int64_t)chunks * t.n_rows)), block(kThreads);
+    if (esize == 2)
+        return t.grad_entropy
+                   ? launch(logprob_grad_kernel<2, true>, grid, block, 0, stream, t, chunks)
+                   : launch(logprob_grad_kernel<2, false>, grid, block, 0, stream, t, chunks);
+    return t.grad_entropy
+               ? launch(logprob_grad_kernel<4, true>, grid, block, 0, stream, t, chunks)
+               : launch(logprob_grad_kernel<4, false>, grid, block, 0, stream, t, chunks);
 }
 
 }  // namespace vpa

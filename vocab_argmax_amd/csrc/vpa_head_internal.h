@@ -27,11 +27,16 @@ struct LogprobTask {
     int32_t n_top;
 };
 
-// Chunks that a part is cut into, and the bytes of the chunks' partial
-// results (256-byte multiple).
-int32_t logprob_chunks(int esize, int64_t part_width, int64_t n_parts, int64_t n_rows);
-size_t logprob_workspace(int64_t n_chunks, int64_t n_parts, int64_t n_rows, int32_t n_top);
-int64_t logprob_threads(int64_t n_chunks, int64_t n_parts, int64_t n_rows);
+// How a launch is cut: one workgroup per (part, row, segment of columns).
+struct LogprobCut {
+    int32_t vecs;             // 16-byte vectors of a thread and chunk
+    int32_t segments;         // of a part of a row
+    int32_t chunks_per_segment;
+    int64_t total;            // workgroups, and partial results
+};
+LogprobCut logprob_cut(int esize, int64_t part_width, int64_t n_parts, int64_t n_rows);
+size_t logprob_workspace(const LogprobCut& c, int32_t n_top);
+int64_t logprob_threads(const LogprobCut& c);
 
 struct LogprobOut {
     const int32_t* token_ids;
@@ -43,12 +48,12 @@ struct LogprobOut {
     float* top_logprobs;
 };
 
-// Partial results of every chunk into `ws`.
+// Partial results of every segment into `ws`.
 hipError_t launch_logprob_parts(int esize, const LogprobTask& t, void* ws, hipStream_t stream);
-// Chunk results of one part per row -> the outputs.
+// Segment results of one part per row -> the outputs.
 hipError_t launch_logprob_finish(int esize, const LogprobTask& t, const void* ws,
                                  const LogprobOut& o, hipStream_t stream);
-// Chunk results -> one record per (part, row).
+// Segment results -> one record per (part, row).
 hipError_t launch_logprob_records(int esize, const LogprobTask& t, const void* ws,
                                   const int32_t* token_ids, int32_t n_tokens, int32_t* stats,
                                   hipStream_t stream);

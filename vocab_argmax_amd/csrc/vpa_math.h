@@ -45,6 +45,23 @@ __device__ __forceinline__ void from_f32(float& d, float f) {
     d = f;
 }
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// 16 bytes at any element address: global memory takes such accesses at every
+// alignment of the element.
+struct __attribute__((packed, aligned(2))) Loose16 {
+    u32x4_t v;
+};
+
+// Element e of a 16-byte vector as fp32.
+template <int ESIZE>
+__device__ __forceinline__ float vec_elem(u32x4_t v, int e) {
+    if constexpr (ESIZE == 4)
+        return __builtin_bit_cast(float, (uint32_t)v[e]);
+    const uint32_t w = v[e / 2];
+    return __builtin_bit_cast(float, e % 2 ? w & 0xFFFF0000u : w << 16);
+}
+
 // 2^x by the hardware instruction: within 1 ulp, results below 2^-126 are 0.
 __device__ __forceinline__ float exp2_fast(float x) {
     return __builtin_amdgcn_exp2f(x);
