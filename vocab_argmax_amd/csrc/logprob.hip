@@ -25,7 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kCandidates = 2048;                 // LDS list of a workgroup's candidates
 constexpr int kMostSegments = 64;                 // of a part of a row
-constexpr int kPartGroups = 1024;                 // workgroups to aim for
+constexpr int kPartGroups = 2048;                 // workgroups to aim for
 
 // Columns of a chunk: U 16-byte vectors a thread.
 constexpr int chunk_cols(int esize, int u) {
@@ -127,11 +127,10 @@ __device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int
 // One segment of a row: its Sums and its first n_top columns.
 //
 // The workgroup walks the segment in chunks of U 16-byte vectors a thread,
-// held in registers as fp32.  Every lane keeps M, s and u of its own columns,
-// joined at the end.  A chunk costs 1.5 instructions an element to unpack
-// and take the maximum and 4 more issue slots' worth for 2^z beside a
-// multiply-add, an add and a multiply-add: for bf16 about 8.5 slots, 0.75 of
-// what the memory's rate allows.
+// held in registers.  Every lane keeps M, s and u of its own columns, joined
+// at the end.  For bf16 an element costs 2.5 instructions to unpack (twice)
+// and take the maximum, 4 slots for 2^z, a multiply-add, an add and a
+// multiply-add: 9.5 slots, less than the time that its bytes take.
 //
 // Alternatives: T is a lower bound of the n_top-th largest value, from the
 // largest values of the lanes on the first chunk (in each of the W
@@ -141,6 +140,12 @@ __device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int
 // each the larger ones.  Few columns pass T, so the scan costs one maximum
 // and one comparison a vector.  A chunk with a NaN, an infinity or more
 // candidates than the list holds takes n_top maxima over the registers.
+template <int ESIZE>
+__device__ __forceinline__ u32x4_t all_neg_inf() {
+    constexpr uint32_t w = ESIZE == 2 ? 0xFF80FF80u : 0xFF800000u;
+    return u32x4_t{w, w, w, w};
+}
+
 template <int ESIZE, int U>
 __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, LogprobCut cut,
                                                                 void* ws) {
@@ -159,10 +164,15 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
     const int32_t row = rest % t.n_rows, part = rest / t.n_rows;
     const int64_t first = t.col0 + part * t.part_stride;
     const int64_t part_end = first + t.part_width < t.vocab ? first + t.part_width : t.vocab;
-    const int64_t lo = first + (int64_t)seg * cut.chunks_per_segment * CHUNK;
-    const int64_t to = lo + (int64_t)cut.chunks_per_segment * CHUNK;
-    const int64_t hi = to < part_end ? to : part_end;
     const T* x = (const T*)t.logits + (int64_t)row * t.ld - t.col0;
+    // chunks start at a 16-byte aligned column, up to VEC - 1 before the part
+    const int back = (int)(((uintptr_t)(x + first) & 15) / ESIZE);
+    const int64_t from = first - back + (int64_t)seg * cut.chunks_per_segment * CHUNK;
+    const int64_t to = from + (int64_t)cut.chunks_per_segment * CHUNK;
+    // columns stay below 2^24 (but a part may begin past the vocabulary)
+    const int begin = (int)(from < part_end ? from : part_end);
+    const int hi = (int)(to < part_end ? to : part_end);
+    const int lo = begin < first ? (int)first : begin;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 
     Sums r = {kNegInf, 0.0f, 0.0f};
@@ -171,42 +181,55 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
     if (t.n_top && threadIdx.x < 3)
         added[threadIdx.x] = 0;
     int turn = 0;                                   // of added[]
-    for (int64_t c0 = lo; c0 < hi; c0 += CHUNK) {
-        float v[N];
+    for (int c0 = begin; c0 < hi; c0 += CHUNK) {
+        u32x4_t w[U];                               // columns mine + i * kThreads * VEC + e
         float g[U];                                 // a vector's maximum
-        const int64_t mine = c0 + threadIdx.x * VEC;
-        if (c0 + CHUNK <= hi) {
-            u32x4_t w[U];
+        const int mine = c0 + threadIdx.x * VEC;
+        auto column = [&](int i) { return mine + (i / VEC) * kThreads * VEC + i % VEC; };
+        auto value = [&](int i) { return vec_elem<ESIZE>(w[i / VEC], i % VEC); };
+        if (c0 >= lo && c0 + CHUNK <= hi) {
 #pragma unroll
             for (int i = 0; i < U; ++i)
-                w[i] = __builtin_nontemporal_load(
-                    &((const Loose16*)(x + mine + i * kThreads * VEC))->v);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                v[i] = vec_elem<ESIZE>(w[i / VEC], i % VEC);
+                w[i] = __builtin_nontemporal_load((const u32x4_t*)(x + column(i * VEC)));
         } else {
+            // the segment's ends: columns outside hold -inf
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const int64_t c = mine + i * kThreads * VEC;
-                u32x4_t w = {0, 0, 0, 0};
-                if (c + VEC <= hi)
-                    w = ((const Loose16*)(x + c))->v;
+                const int c = column(i * VEC);
+                w[i] = all_neg_inf<ESIZE>();
+                if (c >= lo && c + VEC <= hi) {
+                    w[i] = *(const u32x4_t*)(x + c);
+                } else if (c + VEC > lo && c < hi) {
+                    union {
+                        T e[VEC];
+                        u32x4_t v;
+                    } part;
+                    part.v = w[i];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    v[i * VEC + e] = c + VEC <= hi ? vec_elem<ESIZE>(w, e)
-                                     : c + e < hi  ? to_f32(x[c + e])
-                                                   : kNegInf;
+                    for (int e = 0; e < VEC; ++e)
+                        if (c + e >= lo && c + e < hi)
+                            part.e[e] = x[c + e];
+                    w[i] = part.v;
+                }
             }
         }
         float mx = kNegInf;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            g[i] = v[i * VEC];
+            g[i] = value(i * VEC);
 #pragma unroll
             for (int e = 1; e < VEC; ++e)
-                g[i] = fmaxf(g[i], v[i * VEC + e]);
+                g[i] = fmaxf(g[i], value(i * VEC + e));
             mx = fmaxf(mx, g[i]);
         }
+        // values are unpacked anew in every use below: held as fp32, 64 of
+        // them would cost half the wavefronts
+        auto anew = [&] {
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                asm volatile("" : "+v"(w[i]));
+        };
+        anew();
         // the lane's sums so far, measured from the new maximum
         const float m = fmaxf(r.m, mx);
         {
@@ -221,11 +244,15 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
         const float b = m * kLog2e;
         float s = 0.0f, u = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float z = __builtin_fmaf(v[i], kLog2e, -b);
-            const float e = exp2_fast(z);
-            s += e;
-            u = __builtin_fmaf(z, e, u);
+        for (int i = 0; i < U; ++i) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float z = __builtin_fmaf(value(i * VEC + e), kLog2e, -b);
+                const float p = exp2_fast(z);
+                s += p;
+                u = __builtin_fmaf(z, p, u);
+            }
+            __builtin_amdgcn_sched_barrier(0);      // registers for one vector at a time
         }
         const float off = __builtin_fmaf(m, kLog2e, -b);
         const float f = exp2_fast(-off);
@@ -235,15 +262,20 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
         // product with log2(e) is not finite: once more, with care
         const bool odd = !(fabsf(u) < __builtin_inff());
         if (__ballot(odd)) {
+            anew();
             if (odd) {
                 const float base = m == kNegInf ? 0.0f : m;
                 s = u = 0.0f;
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float z = scaled_distance(v[i], base);
-                    const float e = exp2_fast(z);
-                    s += e;
-                    u += z * e;
+                for (int i = 0; i < U; ++i) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float z = scaled_distance(value(i * VEC + e), base);
+                        const float p = exp2_fast(z);
+                        s += p;
+                        u += z * p;
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
@@ -257,9 +289,9 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
         bool slow = strange;
         int total = kept;
         if (!strange) {
-            if (c0 == lo) {
-                const int64_t lanes = (hi - lo + VEC - 1) / VEC;    // with columns
-                const int waves = lanes >= kThreads ? kWaves : (int)((lanes + 63) / 64);
+            if (c0 == begin) {
+                const int lanes = (hi - begin + VEC - 1) / VEC;    // with columns
+                const int waves = lanes >= kThreads ? kWaves : (lanes + 63) / 64;
                 const uint32_t nth = wave_nth_key(key_f32(__builtin_bit_cast(uint32_t, mx)),
                                                   (t.n_top + waves - 1) / waves);
                 if (lane == 0)
@@ -271,17 +303,18 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
                 bound = value_of_key(least);
             }
             if (__ballot(mx >= bound)) {
+                anew();
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
                     if (!__ballot(g[i] >= bound))
                         continue;
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        const int64_t c = mine + i * kThreads * VEC + e;
-                        if (v[i * VEC + e] >= bound && c < hi) {
+                        const int c = column(i * VEC + e);
+                        if (value(i * VEC + e) >= bound && c >= lo && c < hi) {
                             const uint32_t at = kept + atomicAdd(&added[turn], 1u);
                             if (at < kCandidates)
-                                cand[at] = order_of(v[i * VEC + e], (int32_t)c);
+                                cand[at] = order_of(value(i * VEC + e), c);
                         }
                     }
                 }
@@ -306,12 +339,17 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
                 uint64_t best = 0;
                 if ((int)threadIdx.x < kept && cand[threadIdx.x] < below)
                     best = cand[threadIdx.x];
+                anew();                             // nor keep their orders around the loop
+                int at = mine;
+                asm volatile("" : "+v"(at));
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const int64_t c = mine + (i / VEC) * kThreads * VEC + i % VEC;
-                    const uint64_t o = order_of(v[i], (int32_t)c);
-                    if (c < hi && o < below && o > best)
+                    const int c = at + column(i) - mine;
+                    const uint64_t o = order_of(value(i), c);
+                    if (c >= lo && c < hi && o < below && o > best)
                         best = o;
+                    if (i % VEC == VEC - 1)
+                        __builtin_amdgcn_sched_barrier(0);
                 }
                 best = wave_max_u64(best);
                 if (lane == 0)
@@ -642,14 +680,17 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradTask 
 
 }  // namespace
 
-// Chunks of 8 vectors a thread where that still gives every CU 4 workgroups,
-// else of 2 (a decode batch: more, shorter workgroups); a part is cut into
-// segments of whole chunks until there are 4 workgroups a CU.
+// Chunks of 8 vectors a thread where that still gives every CU 4 workgroups
+// and fills at least half of them, else of 2 (a decode batch, a small
+// vocabulary); a part is cut into segments of whole chunks until there are
+// kPartGroups workgroups.
 LogprobCut logprob_cut(int esize, int64_t part_width, int64_t n_parts, int64_t n_rows) {
     LogprobCut c;
     const int64_t rows = n_parts * n_rows;
-    c.vecs = rows * ((part_width + chunk_cols(esize, 8) - 1) / chunk_cols(esize, 8)) >= 1024 ? 8 : 2;
-    const int64_t chunks = (part_width + chunk_cols(esize, c.vecs) - 1) / chunk_cols(esize, c.vecs);
+    const int64_t width = part_width + 16 / esize - 1;       // with the columns before it
+    const int64_t big = chunk_cols(esize, 8);
+    c.vecs = 2 * width > big && rows * ((width + big - 1) / big) >= 1024 ? 8 : 2;
+    const int64_t chunks = (width + chunk_cols(esize, c.vecs) - 1) / chunk_cols(esize, c.vecs);
     int64_t want = (kPartGroups + rows - 1) / rows;
     want = want > chunks ? chunks : want;
     want = want > kMostSegments ? kMostSegments : want;
