@@ -219,10 +219,8 @@ vpa_status vpa_logprob_stats(const void* logits, vpa_dtype dtype, int64_t ld, vp
     if (!stats || !aligned(stats, 4))
         return fail(VPA_ERR_INVALID, "stats is NULL or not 4-byte aligned");
     t.logits = logits;
-    hipError_t e = launch_logprob_parts(esize, t, workspace, (hipStream_t)stream);
-    if (e == hipSuccess)
-        e = launch_logprob_records(esize, t, workspace, token_ids, n_tokens, stats,
-                                   (hipStream_t)stream);
+    hipError_t e = launch_logprob_records(esize, t, workspace, token_ids, n_tokens, stats,
+                                          (hipStream_t)stream);
     return e == hipSuccess ? ok() : hip_fail(e, "vpa_logprob_stats launch");
 }
 
@@ -270,9 +268,7 @@ vpa_status vpa_token_logprobs(const void* logits, vpa_dtype dtype, int64_t ld, v
         (st = check_logprob_out(o, n_top)) != VPA_OK)
         return st;
     t.logits = logits;
-    hipError_t e = launch_logprob_parts(esize, t, workspace, (hipStream_t)stream);
-    if (e == hipSuccess)
-        e = launch_logprob_finish(esize, t, workspace, o, (hipStream_t)stream);
+    hipError_t e = launch_token_logprobs(esize, t, workspace, o, (hipStream_t)stream);
     return e == hipSuccess ? ok() : hip_fail(e, "vpa_token_logprobs launch");
 }
 

@@ -25,7 +25,6 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kCandidates = 2048;                 // LDS list of a workgroup's candidates
 constexpr int kMostSegments = 64;                 // of a part of a row
-constexpr int kPartGroups = 2048;                 // workgroups to aim for
 
 // Columns of a chunk: U 16-byte vectors a thread.
 constexpr int chunk_cols(int esize, int u) {
@@ -80,13 +79,41 @@ __device__ __forceinline__ void join(Sums& a, const Sums& b) {
     a.s = a.s * fa + b.s * fb;
     a.m = m;
 }
+// One step of a join with the partner lane of a DPP move (vpa_device.h); rows
+// outside ROW_MASK join the empty set.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ void join_step(Sums& v) {
+    const auto move = [](float x, float none) {
+        return __builtin_bit_cast(
+            float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none),
+                                               __builtin_bit_cast(int, x), CTRL, ROW_MASK, 0xF,
+                                               false));
+    };
+    join(v, Sums{move(v.m, kNegInf), move(v.s, 0.0f), move(v.u, 0.0f)});
+}
+__device__ __forceinline__ float lane63(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
+// Over the wavefront; every lane holds the result.
 __device__ __forceinline__ Sums wave_join(Sums v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-        const Sums o = {__shfl_xor(v.m, off, 64), __shfl_xor(v.s, off, 64),
-                        __shfl_xor(v.u, off, 64)};
-        join(v, o);
-    }
+    join_step<dpp::kSwap1, 0xF>(v);
+    join_step<dpp::kSwap2, 0xF>(v);
+    join_step<dpp::kHalfMirror, 0xF>(v);
+    join_step<dpp::kMirror, 0xF>(v);
+    join_step<dpp::kBcast15, 0xA>(v);
+    join_step<dpp::kBcast31, 0xC>(v);
+    return Sums{lane63(v.m), lane63(v.s), lane63(v.u)};
+}
+// Over the workgroup, through `lds`; every thread holds the result.
+__device__ __forceinline__ Sums block_join(Sums v, Sums* lds) {
+    v = wave_join(v);
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    static_assert(kWaves == 4, "two steps of the first four lanes");
+    v = lds[threadIdx.x & 3];
+    join_step<dpp::kSwap1, 0xF>(v);
+    join_step<dpp::kSwap2, 0xF>(v);
     return v;
 }
 
@@ -94,6 +121,42 @@ __device__ __forceinline__ Sums wave_join(Sums v) {
 // segments' top lists.
 __host__ __device__ inline size_t sums_bytes(int64_t n) {
     return ((size_t)n * sizeof(Sums) + 255) / 256 * 256;
+}
+
+// A row's max and ln s from its joined sums; no finite column: (-inf, 0).
+struct RowScale {
+    float max, log_sum;
+    bool empty;
+    __device__ __forceinline__ float logprob(float x) const {
+        return empty ? kNegInf : (x - max) - log_sum;
+    }
+};
+__device__ __forceinline__ RowScale scale_of(const Sums& r) {
+    const bool empty = r.m == kNegInf && r.s == 0.0f;
+    return RowScale{r.m, empty ? 0.0f : log2f(r.s) * kLn2, empty};
+}
+
+// Writes the outputs of one row other than its alternatives; `logit(j, id)`
+// is the logit of given token j.
+template <typename Logit>
+__device__ __forceinline__ void write_row(const Sums& r, const RowScale& sc, int64_t row,
+                                          int32_t vocab, const LogprobOut& o, Logit logit) {
+    if (threadIdx.x == 0) {
+        if (o.lse)
+            o.lse[row] = sc.max + sc.log_sum;
+        o.row_stats[3 * row] = sc.max;
+        o.row_stats[3 * row + 1] = sc.log_sum;
+        o.row_stats[3 * row + 2] = sc.empty ? 0.0f : (log2f(r.s) - r.u / r.s) * kLn2;
+    }
+    for (int j = threadIdx.x; j < o.n_tokens; j += kThreads) {
+        const int32_t id = o.token_ids[row * o.n_tokens + j];
+        float lp = __builtin_nanf("");
+        if (id == -1)
+            lp = 0.0f;
+        else if (id >= 0 && id < vocab)
+            lp = sc.logprob(logit(j, id));
+        o.logprobs[row * o.n_tokens + j] = lp;
+    }
 }
 
 // n of a wavefront's 64 keys are at least the result, cut to its upper 16
@@ -116,7 +179,7 @@ __device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint64_t mine = cand[i];
         int larger = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < n; ++j)
             larger += cand[j] > mine;
         if (larger < n_top)
@@ -148,7 +211,7 @@ __device__ __forceinline__ u32x4_t all_neg_inf() {
 
 template <int ESIZE, int U>
 __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, LogprobCut cut,
-                                                                void* ws) {
+                                                                LogprobOut o, void* ws) {
     using T = typename elem<ESIZE>::type;
     constexpr int VEC = 16 / ESIZE;
     constexpr int N = U * VEC;
@@ -187,7 +250,10 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
         const int mine = c0 + threadIdx.x * VEC;
         auto column = [&](int i) { return mine + (i / VEC) * kThreads * VEC + i % VEC; };
         auto value = [&](int i) { return vec_elem<ESIZE>(w[i / VEC], i % VEC); };
-        if (c0 >= lo && c0 + CHUNK <= hi) {
+        const bool whole = c0 >= lo && c0 + CHUNK <= hi;
+        // whether vector i has columns of the segment
+        auto has = [&](int i) { return column(i * VEC) + VEC > lo && column(i * VEC) < hi; };
+        if (whole) {
 #pragma unroll
             for (int i = 0; i < U; ++i)
                 w[i] = __builtin_nontemporal_load((const u32x4_t*)(x + column(i * VEC)));
@@ -199,7 +265,7 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
                 w[i] = all_neg_inf<ESIZE>();
                 if (c >= lo && c + VEC <= hi) {
                     w[i] = *(const u32x4_t*)(x + c);
-                } else if (c + VEC > lo && c < hi) {
+                } else if (has(i)) {
                     union {
                         T e[VEC];
                         u32x4_t v;
@@ -245,12 +311,14 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
         float s = 0.0f, u = 0.0f;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
+            if (whole || has(i)) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float z = __builtin_fmaf(value(i * VEC + e), kLog2e, -b);
-                const float p = exp2_fast(z);
-                s += p;
-                u = __builtin_fmaf(z, p, u);
+                for (int e = 0; e < VEC; ++e) {
+                    const float z = __builtin_fmaf(value(i * VEC + e), kLog2e, -b);
+                    const float p = exp2_fast(z);
+                    s += p;
+                    u = __builtin_fmaf(z, p, u);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);      // registers for one vector at a time
         }
@@ -268,12 +336,14 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
                 s = u = 0.0f;
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
+                    if (whole || has(i)) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float z = scaled_distance(value(i * VEC + e), base);
-                        const float p = exp2_fast(z);
-                        s += p;
-                        u += z * p;
+                        for (int e = 0; e < VEC; ++e) {
+                            const float z = scaled_distance(value(i * VEC + e), base);
+                            const float p = exp2_fast(z);
+                            s += p;
+                            u += z * p;
+                        }
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -284,11 +354,7 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
         if (t.n_top == 0)
             continue;
 
-        // NaN and +inf make the lane's s NaN
-        const bool strange = __syncthreads_or(s != s);
-        bool slow = strange;
-        int total = kept;
-        if (!strange) {
+        {
             if (c0 == begin) {
                 const int lanes = (hi - begin + VEC - 1) / VEC;    // with columns
                 const int waves = lanes >= kThreads ? kWaves : (lanes + 63) / 64;
@@ -302,7 +368,10 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
                     least = lds_key[i] < least ? lds_key[i] : least;
                 bound = value_of_key(least);
             }
-            if (__ballot(mx >= bound)) {
+            // NaN and +inf make the lane's s NaN: such a chunk is not listed
+            if (s != s)
+                atomicAdd(&added[turn], (uint32_t)kCandidates);
+            else if (__ballot(mx >= bound)) {
                 anew();
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
@@ -320,9 +389,9 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
                 }
             }
             __syncthreads();
-            total = kept + (int)added[turn];
-            slow = total > kCandidates;
         }
+        int total = kept + (int)added[turn];
+        const bool slow = total >= kCandidates;
         // the counter after next was last read before the barrier above
         if (threadIdx.x == 0)
             added[turn == 0 ? 2 : turn - 1] = 0;
@@ -373,61 +442,30 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
             bound = key >= kKeyNanF32 ? __builtin_nanf("") : value_of_key(key + 1);
         }
     }
-    r = wave_join(r);
-    if (lane == 0)
-        lds_s[wave] = r;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kWaves; ++i)
-            join(r, lds_s[i]);
-        ((Sums*)ws)[blockIdx.x] = r;
+    r = block_join(r, lds_s);
+    const uint64_t top = (int)threadIdx.x < kept ? cand[threadIdx.x] : 0;
+    if (o.row_stats) {                              // the segment is the row
+        const RowScale sc = scale_of(r);
+        write_row(r, sc, row, t.vocab, o, [&](int, int32_t id) { return to_f32(x[id]); });
+        if ((int)threadIdx.x < t.n_top) {
+            o.top_ids[(int64_t)row * t.n_top + threadIdx.x] = id_of(top);
+            o.top_logprobs[(int64_t)row * t.n_top + threadIdx.x] = sc.logprob(value_of(top));
+        }
+        return;
     }
+    if (threadIdx.x == 0)
+        ((Sums*)ws)[blockIdx.x] = r;
     uint64_t* tops = (uint64_t*)((char*)ws + sums_bytes(cut.total)) + (int64_t)blockIdx.x * t.n_top;
     if ((int)threadIdx.x < t.n_top)
-        tops[threadIdx.x] = (int)threadIdx.x < kept ? cand[threadIdx.x] : 0;
-}
-
-// A row's max and ln s from its joined sums; no finite column: (-inf, 0).
-struct RowScale {
-    float max, log_sum;
-    bool empty;
-    __device__ __forceinline__ float logprob(float x) const {
-        return empty ? kNegInf : (x - max) - log_sum;
-    }
-};
-__device__ __forceinline__ RowScale scale_of(const Sums& r) {
-    const bool empty = r.m == kNegInf && r.s == 0.0f;
-    return RowScale{r.m, empty ? 0.0f : log2f(r.s) * kLn2, empty};
-}
-
-// Writes the outputs of one row other than its alternatives; `logit(j, id)`
-// is the logit of given token j.
-template <typename Logit>
-__device__ __forceinline__ void write_row(const Sums& r, const RowScale& sc, int64_t row,
-                                          int32_t vocab, const LogprobOut& o, Logit logit) {
-    if (threadIdx.x == 0) {
-        if (o.lse)
-            o.lse[row] = sc.max + sc.log_sum;
-        o.row_stats[3 * row] = sc.max;
-        o.row_stats[3 * row + 1] = sc.log_sum;
-        o.row_stats[3 * row + 2] = sc.empty ? 0.0f : (log2f(r.s) - r.u / r.s) * kLn2;
-    }
-    for (int j = threadIdx.x; j < o.n_tokens; j += kThreads) {
-        const int32_t id = o.token_ids[row * o.n_tokens + j];
-        float lp = __builtin_nanf("");
-        if (id == -1)
-            lp = 0.0f;
-        else if (id >= 0 && id < vocab)
-            lp = sc.logprob(logit(j, id));
-        o.logprobs[row * o.n_tokens + j] = lp;
-    }
+        tops[threadIdx.x] = top;
 }
 
 // The n_top largest of n orders (0: none), by the whole workgroup: take(k,
-// order) is called for the k-th by one thread.  `lists` orders each begin at
-// a multiple of n_top, largest first: the largest last order of a list is
-// reached by n_top orders, and those go to LDS to be ranked.  Where they do
-// not fit, the largest is taken n_top times.
+// order) is called for the k-th by one thread.  Lists of n_top orders begin at
+// multiples of n_top, largest first.  With j = ceil(n_top / lists), the
+// ceil(n_top / j)-th largest of the lists' j-th orders is reached by n_top
+// orders; the orders whose keys reach its key go to LDS to be ranked.  Where
+// they do not fit, the largest is taken n_top times.
 template <typename Order, typename Take>
 __device__ __forceinline__ void select_top(int64_t lists, int32_t n_top, uint64_t* cand,
                                            uint64_t* list, Order order, Take take) {
@@ -435,20 +473,15 @@ __device__ __forceinline__ void select_top(int64_t lists, int32_t n_top, uint64_
     __shared__ uint32_t count;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t n = lists * n_top;
-    uint64_t least = 0;
-    for (int64_t i = threadIdx.x; i < lists; i += kThreads) {
-        const uint64_t o = order(i * n_top + n_top - 1);
-        least = o > least ? o : least;
-    }
-    least = wave_max_u64(least);
-    if (lane == 0)
-        best_of[0][wave] = least;
+    const int some = lists < 64 ? (int)lists : 64;  // lists, one a lane
+    const int j = (n_top + some - 1) / some;
+    const uint64_t jth = lane < some ? order((int64_t)lane * n_top + j - 1) : 0;
+    const uint32_t key = wave_nth_key((uint32_t)(jth >> 32), (n_top + j - 1) / j);
+    // (empty places are not candidates)
+    const uint64_t least = key ? (uint64_t)key << 32 : 1;
     if (threadIdx.x == 0)
         count = 0;
     __syncthreads();
-    for (int i = 0; i < kWaves; ++i)
-        least = best_of[0][i] > least ? best_of[0][i] : least;
-    least = least ? least : 1;                      // empty places are not candidates
     for (int64_t i = threadIdx.x; i < n; i += kThreads) {
         const uint64_t o = order(i);
         if (o >= least) {
@@ -477,10 +510,10 @@ __device__ __forceinline__ void select_top(int64_t lists, int32_t n_top, uint64_
         }
         best = wave_max_u64(best);
         if (lane == 0)
-            best_of[(k + 1) & 1][wave] = best;
+            best_of[k & 1][wave] = best;
         __syncthreads();
         for (int i = 0; i < kWaves; ++i)
-            best = best_of[(k + 1) & 1][i] > best ? best_of[(k + 1) & 1][i] : best;
+            best = best_of[k & 1][i] > best ? best_of[k & 1][i] : best;
         if (threadIdx.x == 0)
             take(k, best);
         below = best;
@@ -494,14 +527,7 @@ __device__ __forceinline__ Sums join_all(int64_t n, Get sums) {
     Sums r = {kNegInf, 0.0f, 0.0f};
     for (int64_t i = threadIdx.x; i < n; i += kThreads)
         join(r, sums(i));
-    r = wave_join(r);
-    if ((threadIdx.x & 63) == 0)
-        lds[threadIdx.x >> 6] = r;
-    __syncthreads();
-    r = lds[0];
-    for (int i = 1; i < kWaves; ++i)
-        join(r, lds[i]);
-    return r;
+    return block_join(r, lds);
 }
 
 template <int ESIZE>
@@ -682,8 +708,8 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradTask 
 
 // Chunks of 8 vectors a thread where that still gives every CU 4 workgroups
 // and fills at least half of them, else of 2 (a decode batch, a small
-// vocabulary); a part is cut into segments of whole chunks until there are
-// kPartGroups workgroups.
+// vocabulary); a part is cut into segments of whole chunks until there are 4
+// workgroups a CU, or 8 of the smaller ones.
 LogprobCut logprob_cut(int esize, int64_t part_width, int64_t n_parts, int64_t n_rows) {
     LogprobCut c;
     const int64_t rows = n_parts * n_rows;
@@ -691,7 +717,8 @@ LogprobCut logprob_cut(int esize, int64_t part_width, int64_t n_parts, int64_t n
     const int64_t big = chunk_cols(esize, 8);
     c.vecs = 2 * width > big && rows * ((width + big - 1) / big) >= 1024 ? 8 : 2;
     const int64_t chunks = (width + chunk_cols(esize, c.vecs) - 1) / chunk_cols(esize, c.vecs);
-    int64_t want = (kPartGroups + rows - 1) / rows;
+    const int64_t groups = c.vecs == 8 ? 1024 : 2048;
+    int64_t want = (groups + rows - 1) / rows;
     want = want > chunks ? chunks : want;
     want = want > kMostSegments ? kMostSegments : want;
     c.chunks_per_segment = (int32_t)((chunks + want - 1) / want);
@@ -708,28 +735,40 @@ int64_t logprob_threads(const LogprobCut& c) {
     return c.total * kThreads;
 }
 
-hipError_t launch_logprob_parts(int esize, const LogprobTask& t, void* ws, hipStream_t stream) {
-    const LogprobCut c = logprob_cut(esize, t.part_width, t.n_parts, t.n_rows);
+namespace {
+
+hipError_t launch_parts(int esize, const LogprobTask& t, const LogprobCut& c, const LogprobOut& o,
+                        void* ws, hipStream_t stream) {
     const dim3 grid((uint32_t)c.total), block(kThreads);
     if (esize == 2)
-        return c.vecs == 8 ? launch(logprob_part_kernel<2, 8>, grid, block, 0, stream, t, c, ws)
-                           : launch(logprob_part_kernel<2, 2>, grid, block, 0, stream, t, c, ws);
-    return c.vecs == 8 ? launch(logprob_part_kernel<4, 8>, grid, block, 0, stream, t, c, ws)
-                       : launch(logprob_part_kernel<4, 2>, grid, block, 0, stream, t, c, ws);
+        return c.vecs == 8 ? launch(logprob_part_kernel<2, 8>, grid, block, 0, stream, t, c, o, ws)
+                           : launch(logprob_part_kernel<2, 2>, grid, block, 0, stream, t, c, o, ws);
+    return c.vecs == 8 ? launch(logprob_part_kernel<4, 8>, grid, block, 0, stream, t, c, o, ws)
+                       : launch(logprob_part_kernel<4, 2>, grid, block, 0, stream, t, c, o, ws);
 }
 
-hipError_t launch_logprob_finish(int esize, const LogprobTask& t, const void* ws,
-                                 const LogprobOut& o, hipStream_t stream) {
+}  // namespace
+
+hipError_t launch_token_logprobs(int esize, const LogprobTask& t, void* ws, const LogprobOut& o,
+                                 hipStream_t stream) {
     const LogprobCut c = logprob_cut(esize, t.part_width, t.n_parts, t.n_rows);
+    if (c.segments == 1)
+        return launch_parts(esize, t, c, o, ws, stream);
+    hipError_t e = launch_parts(esize, t, c, LogprobOut{}, ws, stream);
+    if (e != hipSuccess)
+        return e;
     const dim3 grid((uint32_t)t.n_rows), block(kThreads);
     return esize == 2 ? launch(logprob_finish_kernel<2>, grid, block, 0, stream, t, c, ws, o)
                       : launch(logprob_finish_kernel<4>, grid, block, 0, stream, t, c, ws, o);
 }
 
-hipError_t launch_logprob_records(int esize, const LogprobTask& t, const void* ws,
+hipError_t launch_logprob_records(int esize, const LogprobTask& t, void* ws,
                                   const int32_t* token_ids, int32_t n_tokens, int32_t* stats,
                                   hipStream_t stream) {
     const LogprobCut c = logprob_cut(esize, t.part_width, t.n_parts, t.n_rows);
+    hipError_t e = launch_parts(esize, t, c, LogprobOut{}, ws, stream);
+    if (e != hipSuccess)
+        return e;
     const dim3 grid((uint32_t)((int64_t)t.n_rows * t.n_parts)), block(kThreads);
     return esize == 2 ? launch(logprob_record_kernel<2>, grid, block, 0, stream, t, c, ws,
                                token_ids, n_tokens, stats)

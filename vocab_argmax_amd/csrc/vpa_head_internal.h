@@ -48,13 +48,12 @@ struct LogprobOut {
     float* top_logprobs;
 };
 
-// Partial results of every segment into `ws`.
-hipError_t launch_logprob_parts(int esize, const LogprobTask& t, void* ws, hipStream_t stream);
-// Segment results of one part per row -> the outputs.
-hipError_t launch_logprob_finish(int esize, const LogprobTask& t, const void* ws,
-                                 const LogprobOut& o, hipStream_t stream);
-// Segment results -> one record per (part, row).
-hipError_t launch_logprob_records(int esize, const LogprobTask& t, const void* ws,
+// The outputs of whole rows (one part): one launch where a row is one segment,
+// else the segments' partial results into `ws` and a second one.
+hipError_t launch_token_logprobs(int esize, const LogprobTask& t, void* ws, const LogprobOut& o,
+                                 hipStream_t stream);
+// One record per (part, row), through partial results in `ws`.
+hipError_t launch_logprob_records(int esize, const LogprobTask& t, void* ws,
                                   const int32_t* token_ids, int32_t n_tokens, int32_t* stats,
                                   hipStream_t stream);
 // Records of every shard -> the outputs.
