@@ -36,8 +36,8 @@ extern "C" {
  *
  * For a row x of V logits, lse = log sum_c exp(x_c), p_c = exp(x_c - lse),
  * entropy = -sum_c p_c log p_c (a term with p_c = 0 is 0), and the log
- * probability of token t is x_t - lse, computed as (x_t - max x) - log sum_c
- * exp(x_c - max x).
+ * probability of token t is x_t - lse, computed as (x_t - M) - log sum_c
+ * exp(x_c - M) for a logit M near the largest.
  *
  *  - A masked column holds -inf: its p is 0 and its log probability -inf.
  *  - A row whose valid columns are all -inf (the mask leaves nothing) has
@@ -61,7 +61,7 @@ size_t vpa_logprobs_workspace(vpa_vocab v, int32_t n_local_shards, int64_t n_row
 
 /* int32 words of one (shard, row) record of vpa_logprob_stats:
  * 3 + n_tokens + 2*n_top, or -1 if the counts are invalid.  A record holds
- *   [0] the fp32 bits of M, the shard's maximum (-inf: none),
+ *   [0] the fp32 bits of M, a logit near the shard's maximum (-inf: none),
  *   [1] of sum 2^z over the shard's columns, z = (x - M) log2(e),
  *   [2] of sum z 2^z,
  *   [3, 3+n_tokens) of the row's given tokens' logits (tokens of other
@@ -88,10 +88,10 @@ vpa_status vpa_logprob_stats(const void* logits, vpa_dtype dtype, int64_t ld, vp
  *  stats         int32 [S][n_rows][words].
  *  logprobs      out, float [n_rows][n_tokens]; NULL iff n_tokens = 0.
  *  lse           out, float [n_rows], or NULL.
- *  row_stats     out, float [n_rows][3]: the row's maximum M, log sum
- *                exp(x - M) and the entropy.  M and the log of the sum stay
- *                apart for the backward pass: lse = M + log sum has lost the
- *                second where M is large.
+ *  row_stats     out, float [n_rows][3]: a logit M near the row's maximum,
+ *                log sum exp(x - M) and the entropy.  M and the log of the sum
+ *                stay apart for the backward pass: lse = M + log sum has lost
+ *                the second where M is large.
  *  top_ids       out, int32 [n_rows][n_top]; NULL iff n_top = 0.
  *  top_logprobs  out, float [n_rows][n_top]; NULL iff n_top = 0. */
 vpa_status vpa_combine_logprobs(const int32_t* stats, vpa_vocab v, int64_t n_rows,

@@ -1,7 +1,7 @@
 // logprob.hip -- log probabilities of given tokens with entropy and the top
 // alternatives, over one or several vocabulary shards, and their gradient.
 //
-// A set of columns is described by M = max x, s = sum 2^z and u = sum z 2^z
+// A set of columns is described by a logit M near its maximum, s = sum 2^z and u = sum z 2^z
 // with z = (x - M) log2(e), and two sets join as
 //   M = max(Ma, Mb),  s = sum_i s_i 2^di,  u = sum_i (u_i + di s_i) 2^di,
 //   di = (Mi - M) log2(e),
@@ -191,9 +191,11 @@ __device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int
 //
 // The workgroup walks the segment in chunks of U 16-byte vectors a thread,
 // held in registers.  Every lane keeps M, s and u of its own columns, joined
-// at the end.  For bf16 an element costs 2.5 instructions to unpack (twice)
-// and take the maximum, 4 slots for 2^z, a multiply-add, an add and a
-// multiply-add: 9.5 slots, less than the time that its bytes take.
+// at the end; M is its first chunk's maximum, so that later chunks are one
+// pass: for bf16 an element costs 1.5 instructions to unpack it and take the
+// maximum, 2 slots for 2^z, a multiply-add, an add and a multiply-add, 6.5
+// slots.  M need only be near the row's maximum: s and u are exact for any M
+// that keeps 2^z within fp32, and a chunk that does not is done with care.
 //
 // Alternatives: T is a lower bound of the n_top-th largest value, from the
 // largest values of the lanes on the first chunk (in each of the W
@@ -203,6 +205,26 @@ __device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int
 // each the larger ones.  Few columns pass T, so the scan costs one maximum
 // and one comparison a vector.  A chunk with a NaN, an infinity or more
 // candidates than the list holds takes n_top maxima over the registers.
+// The largest of three (a NaN among them: any of them or NaN): one
+// instruction, where fmaxf would first quiet inputs that come from bit
+// operations.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+    return d;
+}
+
+// z = (x - M) log2(e) as one multiply-add, x log2(e) - b with b = M log2(e)
+// rounded: what the rounding took off is put right on a chunk's sums.
+struct LaneScale {
+    float b, off, fix;
+    __device__ __forceinline__ void set(float m) {
+        b = m * kLog2e;
+        off = __builtin_fmaf(m, kLog2e, -b);
+        fix = exp2_fast(-off);
+    }
+};
+
 template <int ESIZE>
 __device__ __forceinline__ u32x4_t all_neg_inf() {
     constexpr uint32_t w = ESIZE == 2 ? 0xFF80FF80u : 0xFF800000u;
@@ -238,7 +260,10 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
     const int lo = begin < first ? (int)first : begin;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 
+    // The lane's sums, measured from the maximum of its first chunk with a
+    // finite column.
     Sums r = {kNegInf, 0.0f, 0.0f};
+    LaneScale scale = {0.0f, 0.0f, 1.0f};
     int kept = 0;                                   // of cand[]: the best so far, in order
     float bound = kNegInf;                          // T
     if (t.n_top && threadIdx.x < 3)
@@ -279,42 +304,39 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
                 }
             }
         }
-        float mx = kNegInf;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            g[i] = value(i * VEC);
-#pragma unroll
-            for (int e = 1; e < VEC; ++e)
-                g[i] = fmaxf(g[i], value(i * VEC + e));
-            mx = fmaxf(mx, g[i]);
-        }
-        // values are unpacked anew in every use below: held as fp32, 64 of
-        // them would cost half the wavefronts
+        // values are unpacked anew in every use: held as fp32, 64 of them
+        // would cost half the wavefronts
         auto anew = [&] {
 #pragma unroll
             for (int i = 0; i < U; ++i)
                 asm volatile("" : "+v"(w[i]));
         };
-        anew();
-        // the lane's sums so far, measured from the new maximum
-        const float m = fmaxf(r.m, mx);
-        {
-            const float d = r.m == m ? 0.0f : scaled_distance(r.m, m);
-            const float f = exp2_fast(d);
-            r.u = (r.u + d * r.s) * f;
-            r.s *= f;
-            r.m = m;
+        // the largest of vector i
+        auto largest = [&](int i) {
+            float v = max3(value(i * VEC), value(i * VEC + 1), value(i * VEC + 2));
+#pragma unroll
+            for (int e = 3; e + 1 < VEC; e += 2)
+                v = max3(v, value(i * VEC + e), value(i * VEC + e + 1));
+            return max3(v, value(i * VEC + VEC - 1), value(i * VEC + VEC - 1));
+        };
+        if (__ballot(r.m == kNegInf)) {
+            float v = kNegInf;
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                v = fmaxf(v, largest(i));
+            if (r.m == kNegInf)
+                scale.set(r.m = v);
+            anew();
         }
-        // z from the rounded m log2(e) is one instruction; what the rounding
-        // took off is put right on the sums
-        const float b = m * kLog2e;
-        float s = 0.0f, u = 0.0f;
+        float s = 0.0f, u = 0.0f, mx = kNegInf;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
+            g[i] = largest(i);
+            mx = fmaxf(mx, g[i]);
             if (whole || has(i)) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    const float z = __builtin_fmaf(value(i * VEC + e), kLog2e, -b);
+                    const float z = __builtin_fmaf(value(i * VEC + e), kLog2e, -scale.b);
                     const float p = exp2_fast(z);
                     s += p;
                     u = __builtin_fmaf(z, p, u);
@@ -322,16 +344,23 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
             }
             __builtin_amdgcn_sched_barrier(0);      // registers for one vector at a time
         }
-        const float off = __builtin_fmaf(m, kLog2e, -b);
-        const float f = exp2_fast(-off);
-        u = __builtin_fmaf(-off, s, u) * f;
-        s *= f;
-        // masked columns (0 * -inf), infinities and NaN, and values whose
-        // product with log2(e) is not finite: once more, with care
-        const bool odd = !(fabsf(u) < __builtin_inff());
+        u = __builtin_fmaf(-scale.off, s, u) * scale.fix;
+        s *= scale.fix;
+        // masked columns (0 * -inf), infinities and NaN, values whose product
+        // with log2(e) is not finite or that are far above M: once more, with
+        // care, from the larger of M and the chunk's maximum
+        const bool odd = !(fabsf(u) < __builtin_inff()) || mx > r.m + 40.0f;
         if (__ballot(odd)) {
             anew();
             if (odd) {
+                const float m = fmaxf(r.m, mx);
+                if (m != r.m) {
+                    const float d = scaled_distance(r.m, m);
+                    const float f = exp2_fast(d);
+                    r.u = (r.u + d * r.s) * f;
+                    r.s *= f;
+                    scale.set(r.m = m);
+                }
                 const float base = m == kNegInf ? 0.0f : m;
                 s = u = 0.0f;
 #pragma unroll
