@@ -541,7 +541,8 @@ vpa_status vpa_layer_norm(const void* x, int64_t ldx, vpa_dtype dtype, const voi
 size_t vpa_layer_norm_backward_workspace(int64_t rows, int64_t cols) {
     if (rows < 0 || rows > kMaxSize || cols < 1 || cols > kMaxSize)
         return 0;
-    return round256((size_t)2 * (size_t)norm_splits(rows, cols) * (size_t)cols * 4);
+    const int32_t a = norm_splits(2, rows, cols), b = norm_splits(4, rows, cols);
+    return round256((size_t)2 * (size_t)(a > b ? a : b) * (size_t)cols * 4);
 }
 
 vpa_status vpa_layer_norm_backward(const void* grad, int64_t ldg, const void* x, int64_t ldx,
@@ -570,7 +571,7 @@ vpa_status vpa_layer_norm_backward(const void* grad, int64_t ldg, const void* x,
             return st;
         if (grad_x == grad && grad_x && ldgx != ldg)
             return fail(VPA_ERR_INVALID, "grad_x in grad's place needs ldgx = ldg");
-        // the row sums are taken after grad_x is written
+        // long rows take the sums over rows after grad_x is written
         if (grad_x == grad && grad_x && (grad_weight || grad_bias))
             return fail(VPA_ERR_INVALID,
                         "grad_x in grad's place cannot be joined with grad_weight or grad_bias");
@@ -578,7 +579,7 @@ vpa_status vpa_layer_norm_backward(const void* grad, int64_t ldg, const void* x,
     const bool sums = grad_weight || grad_bias;
     if ((grad_weight && (st = check_vector("grad_weight", grad_weight, we)) != VPA_OK) ||
         (grad_bias && (st = check_vector("grad_bias", grad_bias, we)) != VPA_OK) ||
-        (st = check_dispatch(norm_grad_threads(rows, cols), "vpa_layer_norm_backward")) != VPA_OK)
+        (st = check_dispatch(norm_grad_threads(e, rows, cols), "vpa_layer_norm_backward")) != VPA_OK)
         return st;
     if (sums && (st = check_workspace("vpa_layer_norm_backward", workspace, workspace_bytes,
                                       vpa_layer_norm_backward_workspace(rows, cols))) != VPA_OK)

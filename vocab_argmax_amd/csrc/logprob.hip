@@ -1,8 +1,9 @@
 // logprob.hip -- log probabilities of given tokens with entropy and the top
 // alternatives, over one or several vocabulary shards, and their gradient.
 //
-// A set of columns is described by a logit M near its maximum, s = sum 2^z and u = sum z 2^z
-// with z = (x - M) log2(e), and two sets join as
+// A set of columns is described by a logit M near its maximum and by s = sum
+// 2^z and u = sum z 2^z
+// with z = (x - M) log2(e); two sets join as
 //   M = max(Ma, Mb),  s = sum_i s_i 2^di,  u = sum_i (u_i + di s_i) 2^di,
 //   di = (Mi - M) log2(e),
 // so a row is one pass over its columns, cut into chunks that workgroups

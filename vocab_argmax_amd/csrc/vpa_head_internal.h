@@ -174,10 +174,10 @@ struct NormGradTask {
     int64_t lddx;
     void* dweight;
     void* dbias;
-    float* part;              // [2][norm_splits(rows, cols)][cols]
+    float* part;              // [2][norm_splits(esize, rows, cols)][cols]
 };
-int32_t norm_splits(int64_t rows, int64_t cols);
-int64_t norm_grad_threads(int64_t rows, int64_t cols);
+int32_t norm_splits(int esize, int64_t rows, int64_t cols);
+int64_t norm_grad_threads(int esize, int64_t rows, int64_t cols);
 hipError_t launch_norm_grad(int esize, const NormGradTask& t, hipStream_t stream);
 
 }  // namespace vpa

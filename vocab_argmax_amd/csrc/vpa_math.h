@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "vpa_device.h"
+
 namespace vpa {
 
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -67,36 +69,44 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return __builtin_amdgcn_exp2f(x);
 }
 
-// Sum over the 64 lanes of a wavefront; every lane holds the result.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        v += __shfl_xor(v, off, 64);
-    return v;
+// Sum over the 64 lanes of a wavefront by lane moves (vpa_device.h); every
+// lane holds the result.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float add_move(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                             0, __builtin_bit_cast(int, v), CTRL, ROW_MASK, 0xF,
+                                             false));
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        v = fmaxf(v, __shfl_xor(v, off, 64));
-    return v;
+__device__ __forceinline__ float wave_sum(float v) {
+    v = add_move<dpp::kSwap1, 0xF>(v);
+    v = add_move<dpp::kSwap2, 0xF>(v);
+    v = add_move<dpp::kHalfMirror, 0xF>(v);
+    v = add_move<dpp::kMirror, 0xF>(v);
+    v = add_move<dpp::kBcast15, 0xA>(v);
+    v = add_move<dpp::kBcast31, 0xC>(v);
+    return __builtin_bit_cast(float,
+                              __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
-// Sum over a workgroup of WAVES wavefronts through `lds` (WAVES floats);
-// every thread holds the result.  Callers leave a barrier between two uses
-// of the same lds.
+// Two sums over a workgroup of WAVES wavefronts through `lds`; every thread
+// holds the results.  Callers leave a barrier between two uses of an lds.
 template <int WAVES>
-__device__ __forceinline__ float block_sum(float v, float* lds) {
-    v = wave_sum(v);
-    if constexpr (WAVES == 1)
-        return v;
-    if ((threadIdx.x & 63) == 0)
-        lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float r = 0.0f;
+__device__ __forceinline__ void block_sum2(float& a, float& b, float (&lds)[WAVES][2]) {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (WAVES > 1) {
+        if ((threadIdx.x & 63) == 0) {
+            lds[threadIdx.x >> 6][0] = a;
+            lds[threadIdx.x >> 6][1] = b;
+        }
+        __syncthreads();
+        a = b = 0.0f;
 #pragma unroll
-    for (int i = 0; i < WAVES; ++i)
-        r += lds[i];
-    return r;
+        for (int i = 0; i < WAVES; ++i) {
+            a += lds[i][0];
+            b += lds[i][1];
+        }
+    }
 }
 
 }  // namespace vpa
