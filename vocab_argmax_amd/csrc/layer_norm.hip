@@ -23,10 +23,18 @@ namespace {
 template <typename T, int WAVES, int NV>
 struct RowPart {
     static constexpr int VEC = 16 / (int)sizeof(T);
-    static constexpr int COLS = WAVES * 64 * VEC * NV;
+    // a workgroup of single wavefronts works on 4 rows at a time
+    static constexpr int ROWS = WAVES == 1 ? 4 : 1;
+    static constexpr int THREADS = WAVES * 64 * ROWS;
 
     static __device__ __forceinline__ int column(int i) {
-        return (i * WAVES * 64 + (int)threadIdx.x) * VEC;
+        return (i * WAVES * 64 + (int)threadIdx.x % (WAVES * 64)) * VEC;
+    }
+    static __device__ __forceinline__ int64_t first_row() {
+        return (int64_t)blockIdx.x * ROWS + threadIdx.x / (WAVES * 64);
+    }
+    static __device__ __forceinline__ int64_t row_step() {
+        return (int64_t)gridDim.x * ROWS;
     }
     static __device__ __forceinline__ int count(int i, int cols) {
         const int n = cols - column(i);
@@ -78,18 +86,29 @@ struct RowPart {
     template <typename W>
     static __device__ __forceinline__ void load_weights(const W* w, int cols, float none,
                                                         float (&f)[NV][VEC]) {
+        constexpr int WVEC = 16 / (int)sizeof(W);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            const int c = column(i);
+            if (w && c + VEC <= cols) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int c = column(i) + e;
-                f[i][e] = w && c < cols ? to_f32(w[c]) : none;
+                for (int h = 0; h < VEC / WVEC; ++h) {
+                    const u32x4_t v = ((const Loose16*)(w + c + h * WVEC))->v;
+#pragma unroll
+                    for (int e = 0; e < WVEC; ++e)
+                        f[i][h * WVEC + e] = vec_elem<(int)sizeof(W)>(v, e);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    f[i][e] = w && c + e < cols ? to_f32(w[c + e]) : none;
             }
+        }
     }
 };
 
 template <typename T, typename W, int WAVES, int NV>
-__global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormTask t) {
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(NormTask t) {
     using P = RowPart<T, WAVES, NV>;
     constexpr int VEC = P::VEC, ESIZE = (int)sizeof(T);
     __shared__ float lds[2][2][WAVES][2];
@@ -98,14 +117,15 @@ __global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormTask t) {
     P::load_weights((const W*)t.weight, cols, 1.0f, w);
     P::load_weights((const W*)t.bias, cols, 0.0f, b);
     u32x4_t next[NV];
-    int64_t row = blockIdx.x;
-    P::load((const T*)t.x + row * t.ldx, cols, next);
-    for (int turn = 0; row < t.rows; row += gridDim.x, turn ^= 1) {
+    int64_t row = P::first_row();
+    if (row < t.rows)
+        P::load((const T*)t.x + row * t.ldx, cols, next);
+    for (int turn = 0; row < t.rows; row += P::row_step(), turn ^= 1) {
         u32x4_t v[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             v[i] = next[i];
-        const int64_t after = row + gridDim.x;
+        const int64_t after = row + P::row_step();
         // (y may be x: the next row is read before any of it is written)
         if (after < t.rows)
             P::load((const T*)t.x + after * t.ldx, cols, next);
@@ -144,7 +164,7 @@ __global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormTask t) {
                                       b[i][e]);
             P::store(y, cols, i, f);
         }
-        if (threadIdx.x == 0) {
+        if (P::column(0) == 0) {
             if (t.mean)
                 t.mean[row] = mean0 + delta;
             if (t.rstd)
@@ -154,7 +174,7 @@ __global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormTask t) {
 }
 
 template <typename T, typename W, int WAVES, int NV>
-__global__ __launch_bounds__(WAVES * 64) void norm_grad_kernel(NormGradTask t) {
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_grad_kernel(NormGradTask t) {
     using P = RowPart<T, WAVES, NV>;
     constexpr int VEC = P::VEC, ESIZE = (int)sizeof(T);
     __shared__ float lds[2][WAVES][2];
@@ -169,10 +189,10 @@ __global__ __launch_bounds__(WAVES * 64) void norm_grad_kernel(NormGradTask t) {
         next_mean = t.mean[r];
         next_rstd = t.rstd[r];
     };
-    int64_t row = blockIdx.x;
+    int64_t row = P::first_row();
     if (row < t.rows)
         fetch(row);
-    for (int turn = 0; row < t.rows; row += gridDim.x, turn ^= 1) {
+    for (int turn = 0; row < t.rows; row += P::row_step(), turn ^= 1) {
         u32x4_t g[NV], x[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -180,7 +200,7 @@ __global__ __launch_bounds__(WAVES * 64) void norm_grad_kernel(NormGradTask t) {
             x[i] = next_x[i];
         }
         const float mean = next_mean, rstd = next_rstd;
-        const int64_t after = row + gridDim.x;
+        const int64_t after = row + P::row_step();
         if (after < t.rows)
             fetch(after);
         float a = 0.0f, b = 0.0f;
@@ -216,6 +236,28 @@ __global__ __launch_bounds__(WAVES * 64) void norm_grad_kernel(NormGradTask t) {
     }
     if (!t.part)
         return;
+    if constexpr (P::ROWS > 1) {
+        // the workgroup's rows' sums, added in order
+        static_assert(NV == 1, "a wavefront a row");
+        __shared__ float sums[P::ROWS][2][64 * VEC];
+        const int group = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            sums[group][0][lane * VEC + e] = dw[0][e];
+            sums[group][1][lane * VEC + e] = db[0][e];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * 64 * VEC; i += P::THREADS) {
+            const int c = i % (64 * VEC), which = i / (64 * VEC);
+            float s = 0.0f;
+#pragma unroll
+            for (int r = 0; r < P::ROWS; ++r)
+                s += sums[r][which][c];
+            if (c < cols)
+                t.part[((int64_t)which * gridDim.x + blockIdx.x) * cols + c] = s;
+        }
+        return;
+    }
     // part[0][workgroup][column]: weight's, part[1]: bias's
     float* pw = t.part + (int64_t)blockIdx.x * cols;
     float* pb = pw + (int64_t)gridDim.x * cols;
@@ -380,19 +422,18 @@ hipError_t with_form(NormForm form, F f) {
     return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
 }
 
-// Workgroups of the forward pass: 8 a CU, so that each has several rows for
-// its weights.
-constexpr int64_t kNormGroups = 2048;
-
 template <typename T, typename W>
 hipError_t launch_norm_typed(const NormTask& t, hipStream_t stream) {
     const NormForm form = norm_form((int)sizeof(T), t.cols, false);
     if (form.waves == 0)
         return launch(norm_long_kernel<T, W>, dim3((uint32_t)t.rows), dim3(kLongThreads), 0,
                       stream, t);
-    const dim3 grid((uint32_t)(t.rows < kNormGroups ? t.rows : kNormGroups));
     return with_form<(int)sizeof(T), false>(form, [&](auto waves, auto nv) {
-        return launch(norm_kernel<T, W, waves(), nv()>, grid, dim3(waves() * 64), 0, stream, t);
+        using P = RowPart<T, waves(), nv()>;
+        // 16 wavefronts a CU: each workgroup has several rows for its weights
+        const int64_t most = 4096 * 64 / P::THREADS, need = (t.rows + P::ROWS - 1) / P::ROWS;
+        return launch(norm_kernel<T, W, waves(), nv()>, dim3((uint32_t)(need < most ? need : most)),
+                      dim3(P::THREADS), 0, stream, t);
     });
 }
 
@@ -408,7 +449,7 @@ hipError_t launch_norm_grad_typed(const NormGradTask& task, hipStream_t stream) 
         if (t.rows > 0 || sums)
             e = with_form<(int)sizeof(T), true>(form, [&](auto waves, auto nv) {
                 return launch(norm_grad_kernel<T, W, waves(), nv()>, dim3((uint32_t)splits),
-                              dim3(waves() * 64), 0, stream, t);
+                              dim3(RowPart<T, waves(), nv()>::THREADS), 0, stream, t);
             });
     } else {
         if (t.dx && t.rows > 0)
@@ -438,12 +479,12 @@ hipError_t launch_norm(int esize, const NormTask& t, hipStream_t stream) {
                         : launch_norm_typed<uint16_t, uint16_t>(t, stream);
 }
 
-// Workgroups of the backward pass, each of which leaves a row of sums: 2 a CU
-// (4 of a single wavefront), for long rows slices of 64 rows.
+// Workgroups of the backward pass, each of which leaves a row of sums: 2 a CU,
+// for long rows slices of 64 rows.
 int32_t norm_splits(int esize, int64_t rows, int64_t cols) {
     const NormForm form = norm_form(esize, cols, true);
-    int64_t s = form.waves == 0 ? (rows + 63) / 64 : rows;
-    const int64_t most = form.waves == 0 ? 64 : form.waves == 1 ? 1024 : 512;
+    int64_t s = form.waves == 0 ? (rows + 63) / 64 : form.waves == 1 ? (rows + 3) / 4 : rows;
+    const int64_t most = form.waves == 0 ? 64 : 512;
     s = s > most ? most : s;
     return (int32_t)(s < 1 ? 1 : s);
 }
