@@ -41,6 +41,7 @@ __global__ __launch_bounds__(kWaves * 64) void linear_rows_kernel(GemmTask t, in
     constexpr int KB = 128 / ESIZE;                 // k of a step: 128 bytes of a row
     constexpr int VEC = 16 / ESIZE;
     constexpr int M = MT * 16, N = NW * 16;
+    constexpr int D = MT == 4 ? 1 : 2;
     __shared__ f32x4 sums[kWaves][NW * MT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t block = (int64_t)blockIdx.x * (kWaves / ks) + wave / ks;
@@ -72,8 +73,46 @@ __global__ __launch_bounds__(kWaves * 64) void linear_rows_kernel(GemmTask t, in
                     acc[i][j] = mma<ESIZE>(wv[i][h], xv[j][h], acc[i][j]);
     };
     if (n0 < t.n) {
-#pragma unroll 2
-        for (int64_t s = share; s < whole; s += ks) {
+        // D steps at a time, the next D on their way
+        u32x4_t wn[D][NW][2], xn[D][MT][2];
+        auto fetch = [&](int64_t s) {
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t o = (s + d * ks) * 128 + h * 64 + q * 16;
+#pragma unroll
+                    for (int i = 0; i < NW; ++i)
+                        wn[d][i][h] = ((const Loose16*)(w[i] + o))->v;
+#pragma unroll
+                    for (int j = 0; j < MT; ++j)
+                        xn[d][j][h] = ((const Loose16*)(x[j] + o))->v;
+                }
+        };
+        int64_t s = share;
+        const int64_t last = whole - (int64_t)(D - 1) * ks;     // the last start of D steps, + 1
+        if (s < last)
+            fetch(s);
+        for (; s < last; s += (int64_t)D * ks) {
+            u32x4_t wv[D][NW][2], xv[D][MT][2];
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int i = 0; i < NW; ++i)
+                        wv[d][i][h] = wn[d][i][h];
+#pragma unroll
+                    for (int j = 0; j < MT; ++j)
+                        xv[d][j][h] = xn[d][j][h];
+                }
+            if (s + (int64_t)D * ks < last)
+                fetch(s + (int64_t)D * ks);
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+                multiply(wv[d], xv[d]);
+        }
+        for (; s < whole; s += ks) {
             u32x4_t wv[NW][2], xv[MT][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
