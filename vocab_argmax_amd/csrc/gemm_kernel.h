@@ -180,6 +180,115 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
         }
 }
 
+// Few rows of A (BM = 32 or 64), k contiguous in both: bound by reading B, so
+// the tile is 128 rows of B by all of A's, and STAGES - 1 stages are on their
+// way at a time.  (4 of them for 32 rows, 3 for 64: two workgroups a CU then
+// have about 100 or 64 KiB of B in flight, where the memory's latency at its
+// rate is about 55 KiB a CU; two stages of a 128 x 128 tile, 32 KiB, reached
+// 3.6 TB/s.)
+template <int ESIZE, int BM, int STAGES>
+__global__ __launch_bounds__(256) void gemm_few_rows_kernel(GemmTask t, int64_t stages_per_slice,
+                                                            float* part) {
+    using T = typename elem<ESIZE>::type;
+    constexpr int BN = 128, NT = 256;
+    constexpr int IM = BM / 16, JN = 2;             // a wavefront: BM x 32 results
+    using LA = TileLoader<ESIZE, true, true, BM, NT>;
+    using LB = TileLoader<ESIZE, true, true, BN, NT>;
+    constexpr int BYTES = LA::BYTES + LB::BYTES, LOADS = LA::LOADS + LB::LOADS;
+    __shared__ __align__(1024) char lds[STAGES * BYTES];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n0 = (int64_t)blockIdx.x * BN;
+    LA la;
+    LB lb;
+    la.init(t.a, t.a_m, 0, t.m);
+    lb.init(t.b, t.b_n, n0, t.n);
+    const typename LA::Place pa = LA::place(0);
+    const typename LB::Place pb = LB::place(wave * 32);
+    const typename LA::Direct da = la.direct();
+    const typename LB::Direct db = lb.direct();
+    const int64_t whole = t.k / LA::KB, all = (t.k + LA::KB - 1) / LA::KB;
+    const int64_t s0 = blockIdx.y * stages_per_slice;
+    const int64_t end = s0 + stages_per_slice < all ? s0 + stages_per_slice : all;
+    const int64_t s1 = end < whole ? end : whole;
+    f32x4 acc[IM][JN] = {};
+    auto stage = [&](int64_t s) {
+        char* p = lds + (s - s0) % STAGES * BYTES;
+        la.load(da, s, p);
+        lb.load(db, s, p + LA::BYTES);
+    };
+    auto multiply = [&](const char* p) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            u32x4_t av[IM], bv[JN];
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+                bv[j] = LB::fragment(p + LA::BYTES, pb, j, s);
+#pragma unroll
+            for (int i = 0; i < IM; ++i)
+                av[i] = LA::fragment(p, pa, i, s);
+#pragma unroll
+            for (int i = 0; i < IM; ++i)
+#pragma unroll
+                for (int j = 0; j < JN; ++j)
+                    acc[i][j] = mma<ESIZE>(bv[j], av[i], acc[i][j]);
+        }
+    };
+    // a stage that k ends in comes first
+    if (end > whole) {
+        la.load_tail(whole, t.k, lds);
+        lb.load_tail(whole, t.k, lds + LA::BYTES);
+        stage_barrier();
+        multiply(lds);
+        stage_barrier();
+    }
+    for (int64_t s = s0; s < s0 + STAGES - 1 && s < s1; ++s)
+        stage(s);
+    for (int64_t s = s0; s < s1; ++s) {
+        // stage s has landed when only the later ones are outstanding
+        if (s + STAGES - 1 <= s1)
+            wait_loads<(STAGES - 2) * LOADS>();
+        else
+            wait_loads<0>();
+        // every wavefront's has, and all have read the stage before
+        bare_barrier();
+        if (s + STAGES - 1 < s1)
+            stage(s + STAGES - 1);
+        multiply(lds + (s - s0) % STAGES * BYTES);
+    }
+    // the tile through LDS, 4 results of a row a thread
+    constexpr int LD = BN + 4;
+    static_assert(BM * LD * 4 <= STAGES * BYTES, "the results fit");
+    float* c = (float*)lds;
+    stage_barrier();
+#pragma unroll
+    for (int i = 0; i < IM; ++i)
+#pragma unroll
+        for (int j = 0; j < JN; ++j)
+            *(f32x4*)(c + (i * 16 + (lane & 15)) * LD + wave * 32 + j * 16 + (lane >> 4) * 4) =
+                acc[i][j];
+    __syncthreads();
+    const int64_t n = n0 + (threadIdx.x & 31) * 4;
+    for (int m = threadIdx.x >> 5; m < BM && m < t.m; m += NT / 32) {
+        const f32x4 v = *(const f32x4*)(c + m * LD + (threadIdx.x & 31) * 4);
+        float* p = part ? part + ((int64_t)blockIdx.y * t.m + m) * t.n + n : nullptr;
+        if (n + 4 <= t.n) {
+            if (part)
+                store4(p, v);
+            else
+                store_results<T>(t, m, n, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < t.n) {
+                    if (part)
+                        p[e] = v[e];
+                    else
+                        store_result<T>(t, m, n + e, v[e]);
+                }
+        }
+    }
+}
+
 template <int ESIZE, bool AK, bool BK, bool DIRECT, int BM, int BN, int WM, int WN>
 hipError_t launch_tile(const GemmTask& t, const GemmPlan& p, hipStream_t stream) {
     const uint32_t tm = (uint32_t)((t.m + BM - 1) / BM), tn = (uint32_t)((t.n + BN - 1) / BN);
@@ -192,6 +301,15 @@ template <int ESIZE, bool AK, bool BK>
 hipError_t launch_layout(const GemmTask& t, const GemmPlan& p, hipStream_t stream) {
     if (!p.direct)
         return launch_tile<ESIZE, AK, BK, false, 128, 128, 2, 2>(t, p, stream);
+    if constexpr (AK && BK)
+        if (p.tile <= 64) {
+            const dim3 grid((uint32_t)((t.n + 127) / 128), (uint32_t)p.slices), block(256);
+            float* part = p.slices > 1 ? (float*)t.ws : nullptr;
+            return p.tile == 32 ? launch(gemm_few_rows_kernel<ESIZE, 32, 4>, grid, block, 0,
+                                         stream, t, p.stages_per_slice, part)
+                                : launch(gemm_few_rows_kernel<ESIZE, 64, 3>, grid, block, 0,
+                                         stream, t, p.stages_per_slice, part);
+        }
     if constexpr (ESIZE == 2)
         if (p.tile == 256)
             return launch_tile<ESIZE, AK, BK, true, 256, 256, 2, 4>(t, p, stream);

@@ -245,6 +245,22 @@ __device__ __forceinline__ void stage_barrier() {
     __syncthreads();
 }
 
+// A barrier that leaves memory loads outstanding: LDS accesses are done before
+// it, and the compiler moves none across it.
+__device__ __forceinline__ void bare_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);             // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Waits until at most N memory loads of this wavefront are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N < 64, "six bits of vmcnt");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | 0x0F70);
+}
+
 // D += P Q^T for 16 rows of P and of Q over 64 bytes of k.
 template <int ESIZE>
 __device__ __forceinline__ f32x4 mma(u32x4_t p, u32x4_t q, f32x4 d) {

@@ -159,12 +159,24 @@ hipError_t launch_dz_typed(const DzTask& t, hipStream_t stream) {
 GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1) {
     GemmPlan p{};
     p.slices = 1;
-    if (a_k1 && b_k1 && m <= kRowsKernelMost) {
-        p.rows_kernel = true;
-        return p;
-    }
     // (no k: one slice of no stages, which stores zeros)
     const int64_t stages = k > 0 ? (k * esize + 127) / 128 : 1;
+    p.stages_per_slice = stages;
+    if (a_k1 && b_k1 && m <= 64) {
+        const int64_t tiles = (n + 127) / 128;
+        if (m <= kRowsKernelMost && tiles < 512) {
+            p.rows_kernel = true;
+            return p;
+        }
+        // workgroups for two a CU, of at least 8 stages
+        p.tile = m <= 32 ? 32 : 64;
+        int64_t s = (512 + tiles - 1) / tiles;
+        s = s > stages / 8 ? stages / 8 : s;
+        s = s < 1 ? 1 : s;
+        p.stages_per_slice = (stages + s - 1) / s;
+        p.slices = (int32_t)((stages + p.stages_per_slice - 1) / p.stages_per_slice);
+        return p;
+    }
     double best = 0;
     for (int32_t tile = esize == 2 ? 256 : 128; tile >= 128; tile /= 2) {
         const double stage_us = esize == 4 ? 7.0 : tile == 256 ? 1.6 : 1.1;
@@ -197,7 +209,7 @@ size_t gemm_workspace(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, boo
 int64_t gemm_threads(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1) {
     const GemmPlan p = plan_gemm(esize, m, n, k, a_k1, b_k1);
     if (p.rows_kernel)
-        return linear_rows_threads(m, n);
+        return linear_rows_threads(n);
     // a product that is not direct takes 128-tiles whatever the plan says
     const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128) * p.slices * 256;
     const int64_t join = p.slices > 1 ? (m * n + kThreads - 1) / kThreads * kThreads : 0;

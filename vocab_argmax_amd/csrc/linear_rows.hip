@@ -1,20 +1,21 @@
-// linear_rows.hip -- y = residual + act(x W^T + bias) for at most 64 rows of x:
-// a decode batch, down to a single token.
+// linear_rows.hip -- y = residual + act(x W^T + bias) for at most 16 rows of
+// x: a small decode batch, down to a single token.
 //
 // Every element of W is used a few times at most, so the kernel is bound by
-// reading W once from memory.  A wavefront takes 16 * NW rows of W and a
+// reading W once from memory.  A wavefront takes 16 rows of W and a
 // share of k; W goes straight from memory into the matrix instruction's
-// operand registers, and x, which all wavefronts share, comes from the
-// caches.  Where W has too few rows to fill the chip with wavefronts, KS of
-// a workgroup's 8 wavefronts split the k of one block of rows and join their
-// sums in LDS, in order: one launch, no workspace.
+// operand registers, D steps of 128 bytes a row at a time, and x, which all
+// wavefronts share, comes from the caches.  Where W has too few rows to fill
+// the chip with wavefronts, KS wavefronts of a workgroup split the k of one
+// block of rows and join their sums in LDS, in order: one launch, no
+// workspace.
+#include <type_traits>
+
 #include "gemm_tile.h"
 #include "linear_common.h"
 
 namespace vpa {
 namespace {
-
-constexpr int kWaves = 8;
 
 // 16 bytes of row `p` at element e, 0 past n.
 template <int ESIZE>
@@ -35,177 +36,109 @@ __device__ __forceinline__ u32x4_t load16(const char* p, int64_t e, int64_t n) {
     return u.v;
 }
 
-template <int ESIZE, int MT, int NW>
-__global__ __launch_bounds__(kWaves * 64) void linear_rows_kernel(GemmTask t, int32_t ks) {
+template <int ESIZE, int D, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void linear_rows_kernel(GemmTask t, int32_t ks) {
     using T = typename elem<ESIZE>::type;
     constexpr int KB = 128 / ESIZE;                 // k of a step: 128 bytes of a row
     constexpr int VEC = 16 / ESIZE;
-    constexpr int M = MT * 16, N = NW * 16;
-    constexpr int D = MT == 4 ? 1 : 2;
-    __shared__ f32x4 sums[kWaves][NW * MT][64];
+    __shared__ f32x4 sums[WAVES][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t block = (int64_t)blockIdx.x * (kWaves / ks) + wave / ks;
+    const int64_t block = (int64_t)blockIdx.x * (WAVES / ks) + wave / ks;
     const int share = wave % ks;
-    const int64_t n0 = block * N;
+    const int64_t n0 = block * 16;
     const int r = lane & 15, q = lane >> 4;
-    const char* w[NW];
-    const char* x[MT];
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        // rows past the end repeat the last one: their sums are not stored
-        const int64_t n = n0 + i * 16 + r < t.n ? n0 + i * 16 + r : t.n - 1;
-        w[i] = (const char*)t.b + n * t.b_n * ESIZE;
-    }
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        const int64_t m = j * 16 + r < t.m ? j * 16 + r : t.m - 1;
-        x[j] = (const char*)t.a + m * t.a_m * ESIZE;
-    }
-    f32x4 acc[NW][MT] = {};
+    // rows past the end repeat the last one: their sums are not stored
+    const char* w = (const char*)t.b + (n0 + r < t.n ? n0 + r : t.n - 1) * t.b_n * ESIZE;
+    const char* x = (const char*)t.a + (r < t.m ? r : t.m - 1) * t.a_m * ESIZE;
+    f32x4 acc = {};
     const int64_t whole = t.k / KB, steps = (t.k + KB - 1) / KB;
-    auto multiply = [&](const u32x4_t (&wv)[NW][2], const u32x4_t (&xv)[MT][2]) {
+    // COUNT whole steps from s
+    auto run = [&](int64_t s, auto count) {
+        constexpr int COUNT = count();
+        u32x4_t wv[COUNT][2], xv[COUNT][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < NW; ++i)
-#pragma unroll
-                for (int j = 0; j < MT; ++j)
-                    acc[i][j] = mma<ESIZE>(wv[i][h], xv[j][h], acc[i][j]);
-    };
-    if (n0 < t.n) {
-        // D steps at a time, the next D on their way
-        u32x4_t wn[D][NW][2], xn[D][MT][2];
-        auto fetch = [&](int64_t s) {
-#pragma unroll
-            for (int d = 0; d < D; ++d)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t o = (s + d * ks) * 128 + h * 64 + q * 16;
-#pragma unroll
-                    for (int i = 0; i < NW; ++i)
-                        wn[d][i][h] = ((const Loose16*)(w[i] + o))->v;
-#pragma unroll
-                    for (int j = 0; j < MT; ++j)
-                        xn[d][j][h] = ((const Loose16*)(x[j] + o))->v;
-                }
-        };
-        int64_t s = share;
-        const int64_t last = whole - (int64_t)(D - 1) * ks;     // the last start of D steps, + 1
-        if (s < last)
-            fetch(s);
-        for (; s < last; s += (int64_t)D * ks) {
-            u32x4_t wv[D][NW][2], xv[D][MT][2];
-#pragma unroll
-            for (int d = 0; d < D; ++d)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int i = 0; i < NW; ++i)
-                        wv[d][i][h] = wn[d][i][h];
-#pragma unroll
-                    for (int j = 0; j < MT; ++j)
-                        xv[d][j][h] = xn[d][j][h];
-                }
-            if (s + (int64_t)D * ks < last)
-                fetch(s + (int64_t)D * ks);
-#pragma unroll
-            for (int d = 0; d < D; ++d)
-                multiply(wv[d], xv[d]);
-        }
-        for (; s < whole; s += ks) {
-            u32x4_t wv[NW][2], xv[MT][2];
+        for (int d = 0; d < COUNT; ++d)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t o = s * 128 + h * 64 + q * 16;
-#pragma unroll
-                for (int i = 0; i < NW; ++i)
-                    wv[i][h] = ((const Loose16*)(w[i] + o))->v;
-#pragma unroll
-                for (int j = 0; j < MT; ++j)
-                    xv[j][h] = ((const Loose16*)(x[j] + o))->v;
+                const int64_t o = (s + d) * 128 + h * 64 + q * 16;
+                wv[d][h] = __builtin_nontemporal_load(&((const Loose16*)(w + o))->v);
+                xv[d][h] = ((const Loose16*)(x + o))->v;
             }
-            multiply(wv, xv);
-        }
-        if (whole < steps && share == whole % ks) {
-            u32x4_t wv[NW][2], xv[MT][2];
+        __builtin_amdgcn_sched_barrier(0);          // all loads before the first wait
+#pragma unroll
+        for (int d = 0; d < COUNT; ++d)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                acc = mma<ESIZE>(wv[d][h], xv[d][h], acc);
+    };
+    if (n0 < t.n) {
+        const int64_t batches = whole / D;
+        for (int64_t b = share; b < batches; b += ks)
+            run(b * D, std::integral_constant<int, D>{});
+        for (int64_t s = batches * D + share; s < whole; s += ks)
+            run(s, std::integral_constant<int, 1>{});
+        if (whole < steps && share == ks - 1) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int64_t e = whole * KB + (h * 4 + q) * VEC;
-#pragma unroll
-                for (int i = 0; i < NW; ++i)
-                    wv[i][h] = load16<ESIZE>(w[i], e, t.k);
-#pragma unroll
-                for (int j = 0; j < MT; ++j)
-                    xv[j][h] = load16<ESIZE>(x[j], e, t.k);
+                acc = mma<ESIZE>(load16<ESIZE>(w, e, t.k), load16<ESIZE>(x, e, t.k), acc);
             }
-            multiply(wv, xv);
         }
     }
-#pragma unroll
-    for (int i = 0; i < NW; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-            sums[wave][i * MT + j][lane] = acc[i][j];
+    sums[wave][lane] = acc;
     __syncthreads();
-    // results of the workgroup's blocks, n fastest; in a 16 x 16 piece n is
-    // (lane / 16) * 4 + e and m is lane % 16
-    const int blocks = kWaves / ks;
-    for (int id = threadIdx.x; id < blocks * M * N; id += kWaves * 64) {
-        const int b = id / (M * N), rest = id % (M * N);
-        const int m = rest / N, n = rest % N;
-        const int64_t col = ((int64_t)blockIdx.x * blocks + b) * N + n;
+    // results of the workgroup's blocks, n fastest; in a block n is (lane /
+    // 16) * 4 + e and m is lane % 16
+    const int blocks = WAVES / ks;
+    for (int id = threadIdx.x; id < blocks * 256; id += WAVES * 64) {
+        const int b = id / 256, m = id % 256 / 16, n = id % 16;
+        const int64_t col = ((int64_t)blockIdx.x * blocks + b) * 16 + n;
         if (m >= t.m || col >= t.n)
             continue;
-        const int piece = (n >> 4) * MT + (m >> 4), at = (m & 15) + ((n & 15) >> 2) * 16;
-        float v = sums[b * ks][piece][at][n & 3];
+        const int at = m + (n >> 2) * 16;
+        float v = sums[b * ks][at][n & 3];
         for (int s = 1; s < ks; ++s)
-            v += sums[b * ks + s][piece][at][n & 3];
+            v += sums[b * ks + s][at][n & 3];
         store_result<T>(t, m, col, v);
     }
 }
 
-// Rows of W per wavefront and wavefronts that share a block's k: 32 rows
-// where that still leaves 8 wavefronts a CU, else 16, and k is split until
-// there are as many.
+// Wavefronts that share a block's k, until there are 8 wavefronts a CU, and
+// wavefronts of a workgroup.
 struct RowsPlan {
-    int32_t nw, ks;
+    int32_t ks, waves;
     int64_t groups;
 };
 RowsPlan plan_rows(int64_t n) {
     RowsPlan p;
-    p.nw = n >= 32 * 2048 ? 2 : 1;
-    const int64_t blocks = (n + 16 * p.nw - 1) / (16 * p.nw);
+    const int64_t blocks = (n + 15) / 16;
     p.ks = 1;
-    while (p.ks < kWaves && blocks * p.ks < 2048)
+    while (p.ks < 8 && blocks * p.ks < 2048)
         p.ks *= 2;
-    const int64_t per = kWaves / p.ks;
+    p.waves = p.ks < 4 ? 4 : p.ks;
+    const int64_t per = p.waves / p.ks;
     p.groups = (blocks + per - 1) / per;
     return p;
 }
 
-template <int ESIZE, int MT>
-hipError_t launch_rows(const GemmTask& t, hipStream_t stream) {
-    const RowsPlan p = plan_rows(t.n);
-    const dim3 grid((uint32_t)p.groups), block(kWaves * 64);
-    return p.nw == 2 ? launch(linear_rows_kernel<ESIZE, MT, 2>, grid, block, 0, stream, t, p.ks)
-                     : launch(linear_rows_kernel<ESIZE, MT, 1>, grid, block, 0, stream, t, p.ks);
-}
-
 template <int ESIZE>
-hipError_t launch_rows_any(const GemmTask& t, hipStream_t stream) {
-    if (t.m <= 16)
-        return launch_rows<ESIZE, 1>(t, stream);
-    return t.m <= 32 ? launch_rows<ESIZE, 2>(t, stream) : launch_rows<ESIZE, 4>(t, stream);
+hipError_t launch_rows(const GemmTask& t, hipStream_t stream) {
+    constexpr int D = 8;
+    const RowsPlan p = plan_rows(t.n);
+    const dim3 grid((uint32_t)p.groups), block(p.waves * 64);
+    return p.waves == 8 ? launch(linear_rows_kernel<ESIZE, D, 8>, grid, block, 0, stream, t, p.ks)
+                        : launch(linear_rows_kernel<ESIZE, D, 4>, grid, block, 0, stream, t, p.ks);
 }
 
 }  // namespace
 
-int64_t linear_rows_threads(int64_t, int64_t n) {
-    return plan_rows(n).groups * kWaves * 64;
+int64_t linear_rows_threads(int64_t n) {
+    const RowsPlan p = plan_rows(n);
+    return p.groups * p.waves * 64;
 }
 
 hipError_t launch_linear_rows(int esize, const GemmTask& t, hipStream_t stream) {
-    return esize == 2 ? launch_rows_any<2>(t, stream) : launch_rows_any<4>(t, stream);
+    return esize == 2 ? launch_rows<2>(t, stream) : launch_rows<4>(t, stream);
 }
 
 }  // namespace vpa

@@ -106,7 +106,8 @@ struct GemmTask {
 // How a product is cut; everything but `direct` follows from sizes.
 struct GemmPlan {
     bool rows_kernel;         // few rows: linear_rows.hip
-    int32_t tile;             // 256 or 128: rows and columns of a workgroup's tile
+    int32_t tile;             // 256 or 128: rows and columns of a workgroup's tile; 64 or
+                              // 32: the rows, of 128 columns
     int32_t slices;           // of k, joined by a second kernel
     int64_t stages_per_slice; // stages of 128 bytes of k
     bool direct;              // operands' strides allow direct loads to LDS
@@ -120,8 +121,8 @@ hipError_t launch_gemm_tiles_bf16(const GemmTask& t, const GemmPlan& p, hipStrea
 hipError_t launch_gemm_tiles_f32(const GemmTask& t, const GemmPlan& p, hipStream_t stream);
 
 // The product for few rows of A (linear_rows.hip), k contiguous in both.
-constexpr int kRowsKernelMost = 64;
-int64_t linear_rows_threads(int64_t m, int64_t n);
+constexpr int kRowsKernelMost = 16;
+int64_t linear_rows_threads(int64_t n);
 hipError_t launch_linear_rows(int esize, const GemmTask& t, hipStream_t stream);
 
 // dz = grad * act'(pre) (of the operands' type, skipped if dz is null), and
