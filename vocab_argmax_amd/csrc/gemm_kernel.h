@@ -190,8 +190,8 @@ template <int ESIZE, int BM, int STAGES>
 __global__ __launch_bounds__(256) void gemm_few_rows_kernel(GemmTask t, int64_t stages_per_slice,
                                                             float* part) {
     using T = typename elem<ESIZE>::type;
-    constexpr int BN = 128, NT = 256;
-    constexpr int IM = BM / 16, JN = 2;             // a wavefront: BM x 32 results
+    constexpr int BN = kFewRowsCols, NT = 256;
+    constexpr int IM = BM / 16, JN = BN / 64;       // a wavefront: BM x BN / 4 results
     using LA = TileLoader<ESIZE, true, true, BM, NT>;
     using LB = TileLoader<ESIZE, true, true, BN, NT>;
     constexpr int BYTES = LA::BYTES + LB::BYTES, LOADS = LA::LOADS + LB::LOADS;
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(256) void gemm_few_rows_kernel(GemmTask t, int64_t 
     la.init(t.a, t.a_m, 0, t.m);
     lb.init(t.b, t.b_n, n0, t.n);
     const typename LA::Place pa = LA::place(0);
-    const typename LB::Place pb = LB::place(wave * 32);
+    const typename LB::Place pb = LB::place(wave * (BN / 4));
     const typename LA::Direct da = la.direct();
     const typename LB::Direct db = lb.direct();
     const int64_t whole = t.k / LA::KB, all = (t.k + LA::KB - 1) / LA::KB;
@@ -264,12 +264,13 @@ __global__ __launch_bounds__(256) void gemm_few_rows_kernel(GemmTask t, int64_t 
     for (int i = 0; i < IM; ++i)
 #pragma unroll
         for (int j = 0; j < JN; ++j)
-            *(f32x4*)(c + (i * 16 + (lane & 15)) * LD + wave * 32 + j * 16 + (lane >> 4) * 4) =
+            *(f32x4*)(c + (i * 16 + (lane & 15)) * LD + wave * (BN / 4) + j * 16 + (lane >> 4) * 4) =
                 acc[i][j];
     __syncthreads();
-    const int64_t n = n0 + (threadIdx.x & 31) * 4;
-    for (int m = threadIdx.x >> 5; m < BM && m < t.m; m += NT / 32) {
-        const f32x4 v = *(const f32x4*)(c + m * LD + (threadIdx.x & 31) * 4);
+    constexpr int ACROSS = BN / 4;                  // threads of a row
+    const int64_t n = n0 + threadIdx.x % ACROSS * 4;
+    for (int m = threadIdx.x / ACROSS; m < BM && m < t.m; m += NT / ACROSS) {
+        const f32x4 v = *(const f32x4*)(c + m * LD + threadIdx.x % ACROSS * 4);
         float* p = part ? part + ((int64_t)blockIdx.y * t.m + m) * t.n + n : nullptr;
         if (n + 4 <= t.n) {
             if (part)
@@ -303,11 +304,12 @@ hipError_t launch_layout(const GemmTask& t, const GemmPlan& p, hipStream_t strea
         return launch_tile<ESIZE, AK, BK, false, 128, 128, 2, 2>(t, p, stream);
     if constexpr (AK && BK)
         if (p.tile <= 64) {
-            const dim3 grid((uint32_t)((t.n + 127) / 128), (uint32_t)p.slices), block(256);
+            const dim3 grid((uint32_t)((t.n + kFewRowsCols - 1) / kFewRowsCols), (uint32_t)p.slices);
+            const dim3 block(256);
             float* part = p.slices > 1 ? (float*)t.ws : nullptr;
-            return p.tile == 32 ? launch(gemm_few_rows_kernel<ESIZE, 32, 4>, grid, block, 0,
+            return p.tile == 32 ? launch(gemm_few_rows_kernel<ESIZE, 32, 6>, grid, block, 0,
                                          stream, t, p.stages_per_slice, part)
-                                : launch(gemm_few_rows_kernel<ESIZE, 64, 3>, grid, block, 0,
+                                : launch(gemm_few_rows_kernel<ESIZE, 64, 5>, grid, block, 0,
                                          stream, t, p.stages_per_slice, part);
         }
     if constexpr (ESIZE == 2)

@@ -163,7 +163,7 @@ GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b
     const int64_t stages = k > 0 ? (k * esize + 127) / 128 : 1;
     p.stages_per_slice = stages;
     if (a_k1 && b_k1 && m <= 64) {
-        const int64_t tiles = (n + 127) / 128;
+        const int64_t tiles = (n + kFewRowsCols - 1) / kFewRowsCols;
         if (m <= kRowsKernelMost && tiles < 512) {
             p.rows_kernel = true;
             return p;

@@ -103,11 +103,12 @@ struct GemmTask {
     int32_t act;
     void* ws;                 // gemm_workspace() bytes
 };
+constexpr int kFewRowsCols = 64;  // columns of a tile of few rows
 // How a product is cut; everything but `direct` follows from sizes.
 struct GemmPlan {
     bool rows_kernel;         // few rows: linear_rows.hip
     int32_t tile;             // 256 or 128: rows and columns of a workgroup's tile; 64 or
-                              // 32: the rows, of 128 columns
+                              // 32: the rows, of kFewRowsCols columns
     int32_t slices;           // of k, joined by a second kernel
     int64_t stages_per_slice; // stages of 128 bytes of k
     bool direct;              // operands' strides allow direct loads to LDS
