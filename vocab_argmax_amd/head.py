@@ -13,12 +13,11 @@ examples/draft_head.py for a training step).
 """
 import ctypes
 import functools
-from typing import NamedTuple, Optional
 
 import torch
 
-from . import (VPA_BF16, VPA_F32, Vocab, _check, _dtype_code, _logits_ld, _on, _out_tensor,
-               _stream, _stream_arg, _vocab, _vp, lib)
+from . import (VPA_BF16, VPA_F32, VPA_OK, Vocab, VpaError, _out_tensor, _raw_stream, _stream_arg,
+               _vocab, _vp, last_error, lib)
 
 MAX_TOP = 64             # VPA_MAX_TOP
 MAX_ROW_TOKENS = 64      # VPA_MAX_ROW_TOKENS
@@ -86,7 +85,8 @@ def head_lib():
 def head_call():
     """The launch entry points of include/vpa_head.h, bound to the loaded
     libvpa.so (csrc/headcall.c); they take their C arguments in order."""
-    head_lib()
+    if _bound_to is None or _bound_to is not lib():
+        head_lib()
     return _call_mod
 
 
@@ -111,91 +111,164 @@ def _norm_grad_workspace(rows, cols):
     return int(head_lib().vpa_layer_norm_backward_workspace(rows, cols))
 
 
+# The checks below are on the path of calls that take a few microseconds on the
+# GPU, so each attribute of a tensor is read once and views are made when they
+# are asked for.
+
 def _workspace(workspace, need, device):
-    """A caller's workspace (a contiguous device tensor of at least `need`
-    bytes) or a new one; None if none is needed."""
+    """A caller's workspace (a contiguous device tensor) or a new one of
+    `need` bytes, None if that is 0 -> (tensor kept alive, address, bytes)."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        if not need:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
     if not workspace.is_contiguous() or workspace.device != device:
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _bytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
-
-
-def _matrix(t, name, device, dtype, shape):
+def _matrix(t, name, device, dtype, rows, cols):
     """A 2-D operand with contiguous columns -> its row stride."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(rows, cols)}")
+    stride = t.stride()
+    if cols > 1 and stride[1] != 1:
         raise ValueError(f"{name}'s columns must be contiguous (stride 1)")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return stride[0] if rows > 1 else cols
 
 
 def _rows_of(t, name):
     """The 2-D first operand of a call -> (rows, cols, row stride, dtype code)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
+        code = VPA_BF16
+    elif dtype is torch.float32:
+        code = VPA_F32
+    else:
+        raise TypeError(f"{name} must be bfloat16 or float32, not {dtype}")
+    rows, cols = shape
+    stride = t.stride()
+    if cols > 1 and stride[1] != 1:
         raise ValueError(f"{name}'s columns must be contiguous (stride 1)")
-    return (t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1],
-            VPA_BF16 if t.dtype == torch.bfloat16 else VPA_F32)
+    return rows, cols, stride[0] if rows > 1 else cols, code
+
+
+def _launch(fn, stream, device, *args):
+    """Calls the entry point with `device` current, on the given stream or the
+    device's current one, and raises what it reports."""
+    index = device.index
+    if stream is None:
+        handle = _raw_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+    else:
+        handle = stream.cuda_stream
+    if index is None or torch._C._cuda_getDevice() == index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status != VPA_OK:
+        raise VpaError(status, last_error())
 
 
 # ---------------------------------------------------------------------------
 # token log probabilities
 # ---------------------------------------------------------------------------
 
-class TokenLogprobs(NamedTuple):
-    """Results of token_logprobs / combine_logprobs for N rows."""
-    logprobs: Optional[torch.Tensor]      # float32, the shape of token_ids
-    lse: torch.Tensor                     # float32 [N]: log sum exp of the row
-    entropy: torch.Tensor                 # float32 [N], nats (a column of row_stats)
-    top_ids: Optional[torch.Tensor]       # int32 [N, n_top]
-    top_logprobs: Optional[torch.Tensor]  # float32 [N, n_top]
-    row_stats: torch.Tensor               # float32 [N, 3]: max, log of the scaled sum, entropy
+class TokenLogprobs:
+    """Results of token_logprobs / combine_logprobs for N rows, as views of one
+    allocation that are made when first asked for:
+
+    logprobs      float32, the shape of token_ids (None without tokens)
+    lse           float32 [N]: log sum exp of the row
+    entropy       float32 [N], in nats (a column of row_stats)
+    top_ids       int32 [N, n_top] (None for n_top = 0)
+    top_logprobs  float32 [N, n_top] (None for n_top = 0)
+    row_stats     float32 [N, 3], what the backward pass takes: a logit near the
+                  maximum, the log of the sum scaled by it, the entropy
+    """
+    __slots__ = ("_buf", "_n", "_tokens", "_top", "_made")
+
+    def __init__(self, buf, n, token_shape, n_top):
+        self._buf, self._n, self._tokens, self._top, self._made = buf, n, token_shape, n_top, {}
+
+    def _view(self, name, shape, strides, at, dtype=None):
+        v = self._made.get(name)
+        if v is None:
+            v = (self._buf if dtype is None else self._buf.view(dtype)).as_strided(
+                shape, strides, at)
+            self._made[name] = v
+        return v
+
+    # the buffer: row_stats, lse, logprobs, top_ids, top_logprobs
+    @property
+    def row_stats(self):
+        return self._view("row_stats", (self._n, 3), (3, 1), 0)
+
+    @property
+    def entropy(self):
+        return self._view("entropy", (self._n,), (3,), 2)
+
+    @property
+    def lse(self):
+        return self._view("lse", (self._n,), (1,), 3 * self._n)
+
+    @property
+    def logprobs(self):
+        shape = self._tokens
+        if shape is None:
+            return None
+        return self._view("logprobs", shape, (1,) if len(shape) == 1 else (shape[1], 1),
+                          4 * self._n)
+
+    def _tops_at(self):
+        shape = self._tokens
+        count = 0 if shape is None else 1 if len(shape) == 1 else shape[1]
+        return (4 + count) * self._n
+
+    @property
+    def top_ids(self):
+        return self._view("top_ids", (self._n, self._top), (self._top, 1), self._tops_at(),
+                          torch.int32) if self._top else None
+
+    @property
+    def top_logprobs(self):
+        return self._view("top_logprobs", (self._n, self._top), (self._top, 1),
+                          self._tops_at() + self._n * self._top) if self._top else None
 
 
 def _tokens(token_ids, n, device):
-    """token_ids int32 [N] or [N, T] -> T (0 for None)."""
+    """token_ids int32 [N] or [N, T] -> (T, shape): (0, None) for None or T = 0."""
     if token_ids is None:
-        return 0
-    if token_ids.dtype != torch.int32 or not token_ids.is_contiguous():
+        return 0, None
+    if token_ids.dtype is not torch.int32 or not token_ids.is_contiguous():
         raise ValueError("token_ids must be a contiguous int32 tensor")
     if token_ids.device != device:
         raise ValueError(f"token_ids is on {token_ids.device}, logits on {device}")
-    if token_ids.dim() not in (1, 2) or token_ids.shape[0] != n:
-        raise ValueError(f"token_ids has shape {tuple(token_ids.shape)}, expected ({n},) or "
-                         f"({n}, tokens)")
-    return 1 if token_ids.dim() == 1 else token_ids.shape[1]
+    shape = token_ids.shape
+    if len(shape) not in (1, 2) or shape[0] != n:
+        raise ValueError(f"token_ids has shape {tuple(shape)}, expected ({n},) or ({n}, tokens)")
+    count = 1 if len(shape) == 1 else shape[1]
+    return count, shape if count else None
 
 
-def _logprob_outputs(n, token_ids, n_tokens, n_top, device):
-    """All outputs as views of one allocation; -> (TokenLogprobs, addresses)."""
-    words = n * (4 + n_tokens + 2 * n_top)
-    buf = torch.empty(words, dtype=torch.float32, device=device)
-    stats = buf.as_strided((n, 3), (3, 1), 0)
-    lse = buf.as_strided((n,), (1,), 3 * n)
-    lp = ids = tops = None
-    at = 4 * n
-    if n_tokens:
-        lp = buf.as_strided(token_ids.shape, token_ids.stride(), at)
-        at += n * n_tokens
-    if n_top:
-        ids = buf.view(torch.int32).as_strided((n, n_top), (n_top, 1), at)
-        tops = buf.as_strided((n, n_top), (n_top, 1), at + n * n_top)
-    out = TokenLogprobs(lp, lse, buf.as_strided((n,), (3,), 2), ids, tops, stats)
-    return out, (_vp(lp), lse.data_ptr(), stats.data_ptr(), _vp(ids), _vp(tops))
+def _output_addresses(base, n, n_tokens, n_top):
+    """logprobs, lse, row_stats, top_ids, top_logprobs in a buffer at `base`."""
+    tops = base + 4 * n * (4 + n_tokens)
+    return (base + 16 * n if n_tokens else None, base + 12 * n, base, tops if n_top else None,
+            tops + 4 * n * n_top if n_top else None)
 
 
 @_stream_arg
@@ -210,17 +283,26 @@ def token_logprobs(logits, vocab, shard_width, n_shards, token_ids=None, n_top=0
     gives NaN.  Alternatives come by value, the lower id first among equals.
     Masked columns hold -inf.  workspace: optional device tensor of at least
     logprobs_workspace() bytes."""
-    ld = _logits_ld(logits)
-    n, dev = logits.shape[0], logits.device
-    n_tokens = _tokens(token_ids, n, dev)
+    n, _, ld, code = _rows_of(logits, "logits")
+    dev = logits.device
+    n_tokens, shape = _tokens(token_ids, n, dev)
     fn = head_call().vpa_token_logprobs
-    need = _logprobs_workspace(vocab, shard_width, n_shards, n_shards, n, n_top)
-    ws = _workspace(workspace, need, dev)
-    out, ptrs = _logprob_outputs(n, token_ids, n_tokens, max(n_top, 0), dev)
-    _check(_on(dev, fn, logits.data_ptr(), _dtype_code(logits), ld, vocab, shard_width, n_shards,
-               n, _vp(token_ids), n_tokens, n_top, _vp(ws), _bytes(ws), *ptrs,
-               _stream(stream, dev)))
-    return out
+    words = n * (4 + n_tokens + 2 * max(n_top, 0))
+    if workspace is None:
+        # one allocation: the workspace after the outputs, at 256 bytes
+        need = _logprobs_workspace(vocab, shard_width, n_shards, n_shards, n, n_top)
+        words = (words + 63) // 64 * 64
+        buf = torch.empty(words + need // 4, dtype=torch.float32, device=dev)
+        base = buf.data_ptr()
+        ws = base + 4 * words
+    else:
+        _, ws, need = _workspace(workspace, 0, dev)
+        buf = torch.empty(words, dtype=torch.float32, device=dev)
+        base = buf.data_ptr()
+    _launch(fn, stream, dev, logits.data_ptr(), code, ld, vocab, shard_width, n_shards, n,
+            token_ids.data_ptr() if n_tokens else None, n_tokens, n_top, ws, need,
+            *_output_addresses(base, n, n_tokens, n_top))
+    return TokenLogprobs(buf, n, shape, n_top)
 
 
 def logprobs_workspace(vocab, shard_width, n_shards, n_rows, n_top=0, n_local=None) -> int:
@@ -236,40 +318,42 @@ def logprob_stats(logits, vocab, shard_width, n_shards, token_ids=None, n_top=0,
     ranks hold one shard each: int32 [n_local][N][words].  Gathered in rank
     order along dim 0 they go to combine_logprobs.  logits [N, ld]: column 0
     is global column first_shard * W; token_ids are global."""
-    ld = _logits_ld(logits)
-    n, dev = logits.shape[0], logits.device
+    n, _, ld, code = _rows_of(logits, "logits")
+    dev = logits.device
     if n_local is None:
         n_local = n_shards - first_shard
-    n_tokens = _tokens(token_ids, n, dev)
+    n_tokens, _ = _tokens(token_ids, n, dev)
     words = head_lib().vpa_logprob_words(n_tokens, n_top)
     if words < 0:
         raise ValueError(f"at most {MAX_ROW_TOKENS} tokens and {MAX_TOP} alternatives a row")
-    ws = _workspace(workspace, _logprobs_workspace(vocab, shard_width, n_shards, n_local, n,
-                                                   n_top), dev)
+    _ws, ws, ws_bytes = _workspace(workspace, _logprobs_workspace(vocab, shard_width, n_shards,
+                                                                  n_local, n, n_top), dev)
     out = torch.empty((max(n_local, 0), n, words), dtype=torch.int32, device=dev)
-    _check(_on(dev, head_call().vpa_logprob_stats, logits.data_ptr(), _dtype_code(logits), ld,
-               vocab, shard_width, n_shards, first_shard, n_local, n, _vp(token_ids), n_tokens,
-               n_top, _vp(ws), _bytes(ws), out.data_ptr(), _stream(stream, dev)))
+    _launch(head_call().vpa_logprob_stats, stream, dev, logits.data_ptr(), code, ld, vocab,
+            shard_width, n_shards, first_shard, n_local, n,
+            token_ids.data_ptr() if n_tokens else None, n_tokens, n_top, ws, ws_bytes,
+            out.data_ptr())
     return out
 
 
 @_stream_arg
 def combine_logprobs(stats, vocab, shard_width, token_ids=None, n_top=0, *, stream=None):
     """All shards' records int32 [S][N][words] -> TokenLogprobs."""
-    if stats.dtype != torch.int32 or stats.dim() != 3 or not stats.is_contiguous():
+    if stats.dtype is not torch.int32 or stats.dim() != 3 or not stats.is_contiguous():
         raise ValueError("stats must be a contiguous int32 [shards][rows][words] tensor")
     if not stats.is_cuda:
         raise ValueError("stats must be a device tensor")
     s, n, words = stats.shape
     dev = stats.device
-    n_tokens = _tokens(token_ids, n, dev)
+    n_tokens, shape = _tokens(token_ids, n, dev)
     if words != head_lib().vpa_logprob_words(n_tokens, n_top):
         raise ValueError(f"records of {words} words do not hold {n_tokens} tokens and {n_top} "
                          "alternatives")
-    out, ptrs = _logprob_outputs(n, token_ids, n_tokens, n_top, dev)
-    _check(_on(dev, head_call().vpa_combine_logprobs, stats.data_ptr(), vocab, shard_width, s, n,
-               _vp(token_ids), n_tokens, n_top, *ptrs, _stream(stream, dev)))
-    return out
+    buf = torch.empty(n * (4 + n_tokens + 2 * n_top), dtype=torch.float32, device=dev)
+    _launch(head_call().vpa_combine_logprobs, stream, dev, stats.data_ptr(), vocab, shard_width, s,
+            n, token_ids.data_ptr() if n_tokens else None, n_tokens, n_top,
+            *_output_addresses(buf.data_ptr(), n, n_tokens, n_top))
+    return TokenLogprobs(buf, n, shape, n_top)
 
 
 @_stream_arg
@@ -281,11 +365,11 @@ def token_logprobs_backward(logits, vocab, shard_width, n_shards, token_ids, row
     entropy (float32 [N]).  row_stats: the forward call's.  Columns past the
     vocabulary get 0.  out: the gradient's tensor; it may be the logits
     themselves, which are then replaced."""
-    ld = _logits_ld(logits)
-    n, dev = logits.shape[0], logits.device
+    n, cols, ld, code = _rows_of(logits, "logits")
+    dev = logits.device
     if n_local is None:
         n_local = n_shards - first_shard
-    n_tokens = _tokens(token_ids, n, dev)
+    n_tokens, _ = _tokens(token_ids, n, dev)
     if (grad_logprobs is None) != (token_ids is None):
         raise ValueError("grad_logprobs goes with token_ids")
     for name, t, count in (("grad_logprobs", grad_logprobs, n * n_tokens),
@@ -293,13 +377,15 @@ def token_logprobs_backward(logits, vocab, shard_width, n_shards, token_ids, row
         if t is not None:
             _out_tensor(t, name, torch.float32, count, dev)
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-    gld = _matrix(out, "out", dev, logits.dtype, logits.shape)
-    _check(_on(dev, head_call().vpa_token_logprobs_backward, logits.data_ptr(),
-               _dtype_code(logits), ld, vocab, shard_width, n_shards, first_shard, n_local, n,
-               _vp(token_ids) if n_tokens else None, n_tokens, row_stats.data_ptr(),
-               _vp(grad_logprobs) if n_tokens else None, _vp(grad_entropy), out.data_ptr(), gld,
-               out.shape[1], _stream(stream, dev)))
+        out = torch.empty((n, cols), dtype=logits.dtype, device=dev)
+        gld = cols
+    else:
+        gld = _matrix(out, "out", dev, logits.dtype, n, cols)
+    _launch(head_call().vpa_token_logprobs_backward, stream, dev, logits.data_ptr(), code, ld,
+            vocab, shard_width, n_shards, first_shard, n_local, n,
+            token_ids.data_ptr() if n_tokens else None, n_tokens, row_stats.data_ptr(),
+            grad_logprobs.data_ptr() if n_tokens else None, _vp(grad_entropy), out.data_ptr(), gld,
+            cols)
     return out
 
 
@@ -327,28 +413,34 @@ def head_linear(x, weight, bias=None, activation="none", residual=None, out=None
     float32); out may be the residual itself, or one shard's columns of a
     wider logits tensor."""
     rows, inner, ldx, code = _rows_of(x, "x")
-    dev = x.device
+    dev, dtype = x.device, x.dtype
     if weight.dim() != 2:
         raise ValueError("weight must be 2-D [outer, inner]")
     outer = weight.shape[0]
-    ldw = _matrix(weight, "weight", dev, x.dtype, (outer, inner))
+    ldw = _matrix(weight, "weight", dev, dtype, outer, inner)
     if bias is not None:
-        _out_tensor(bias, "bias", x.dtype, outer, dev)
-    ldr = 0 if residual is None else _matrix(residual, "residual", dev, x.dtype, (rows, outer))
+        _out_tensor(bias, "bias", dtype, outer, dev)
+    ldr = 0 if residual is None else _matrix(residual, "residual", dev, dtype, rows, outer)
     if out is None:
-        out = torch.empty((rows, outer), dtype=out_dtype or x.dtype, device=dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    if out.dtype not in (x.dtype, torch.float32):
-        raise TypeError(f"the output must be {x.dtype} or float32, not {out.dtype}")
-    ldy = _matrix(out, "out", dev, out.dtype, (rows, outer))
-    pre = torch.empty((rows, outer), dtype=x.dtype, device=dev) if with_pre else None
+        out = torch.empty((rows, outer), dtype=out_dtype or dtype, device=dev)
+        ldy = outer
+    else:
+        if out_dtype is not None and out.dtype is not out_dtype:
+            raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        ldy = _matrix(out, "out", dev, out.dtype, rows, outer)
+    out_type = out.dtype
+    if out_type is dtype:
+        out_code = code
+    elif out_type is torch.float32:
+        out_code = VPA_F32
+    else:
+        raise TypeError(f"the output must be {dtype} or float32, not {out_type}")
+    pre = torch.empty((rows, outer), dtype=dtype, device=dev) if with_pre else None
     fn = head_call().vpa_head_linear
-    ws = _workspace(workspace, _linear_workspace(code, rows, outer, inner), dev)
-    _check(_on(dev, fn, x.data_ptr(), ldx, weight.data_ptr(), ldw, _vp(bias), _vp(residual), ldr,
-               code, rows, outer, inner, _activation(activation), out.data_ptr(), ldy,
-               VPA_F32 if out.dtype == torch.float32 else VPA_BF16, _vp(pre), outer, _vp(ws),
-               _bytes(ws), _stream(stream, dev)))
+    _ws, ws, ws_bytes = _workspace(workspace, _linear_workspace(code, rows, outer, inner), dev)
+    _launch(fn, stream, dev, x.data_ptr(), ldx, weight.data_ptr(), ldw, _vp(bias), _vp(residual),
+            ldr, code, rows, outer, inner, _activation(activation), out.data_ptr(), ldy, out_code,
+            _vp(pre), outer, ws, ws_bytes)
     return (out, pre) if with_pre else out
 
 
@@ -364,19 +456,20 @@ def head_linear_backward(grad, x, weight, pre=None, activation="none", need_x=Tr
     if x.dim() != 2:
         raise ValueError("x must be 2-D [rows, inner]")
     inner = x.shape[1]
-    ldx = _matrix(x, "x", dev, dt, (rows, inner))
-    ldw = _matrix(weight, "weight", dev, dt, (outer, inner))
+    ldx = _matrix(x, "x", dev, dt, rows, inner)
+    ldw = _matrix(weight, "weight", dev, dt, outer, inner)
     if act and pre is None:
         raise ValueError(f"the backward pass of {activation} needs pre")
-    ldp = _matrix(pre, "pre", dev, dt, (rows, outer)) if act else 0
+    ldp = _matrix(pre, "pre", dev, dt, rows, outer) if act else 0
     gx = torch.empty((rows, inner), dtype=dt, device=dev) if need_x else None
     gw = torch.empty((outer, inner), dtype=dt, device=dev) if need_weight else None
     gb = torch.empty(outer, dtype=dt, device=dev) if need_bias else None
     fn = head_call().vpa_head_linear_backward
-    ws = _workspace(workspace, _linear_grad_workspace(code, rows, outer, inner), dev)
-    _check(_on(dev, fn, grad.data_ptr(), ldg, x.data_ptr(), ldx, weight.data_ptr(), ldw,
-               _vp(pre) if act else None, ldp, code, rows, outer, inner, act, _vp(gx), inner,
-               _vp(gw), inner, _vp(gb), _vp(ws), _bytes(ws), _stream(stream, dev)))
+    _ws, ws, ws_bytes = _workspace(workspace, _linear_grad_workspace(code, rows, outer, inner),
+                                   dev)
+    _launch(fn, stream, dev, grad.data_ptr(), ldg, x.data_ptr(), ldx, weight.data_ptr(), ldw,
+            _vp(pre) if act else None, ldp, code, rows, outer, inner, act, _vp(gx), inner, _vp(gw),
+            inner, _vp(gb), ws, ws_bytes)
     return gx, gw, gb
 
 
@@ -384,15 +477,17 @@ def head_linear_backward(grad, x, weight, pre=None, activation="none", need_x=Tr
 # layer norm
 # ---------------------------------------------------------------------------
 
-def _norm_weight(t, name, like, wdtype, cols):
+def _norm_weight(t, name, dtype, device, wdtype, cols):
+    """Checks weight or bias -> its dtype (wdtype, the other's, for None)."""
     if t is None:
         return wdtype
-    if t.dtype not in (like.dtype, torch.float32):
-        raise TypeError(f"{name} must be {like.dtype} or float32, not {t.dtype}")
-    if wdtype is not None and t.dtype != wdtype:
-        raise TypeError(f"weight and bias must have one dtype, not {wdtype} and {t.dtype}")
-    _out_tensor(t, name, t.dtype, cols, like.device)
-    return t.dtype
+    td = t.dtype
+    if td is not dtype and td is not torch.float32:
+        raise TypeError(f"{name} must be {dtype} or float32, not {td}")
+    if wdtype is not None and td is not wdtype:
+        raise TypeError(f"weight and bias must have one dtype, not {wdtype} and {td}")
+    _out_tensor(t, name, td, cols, device)
+    return td
 
 
 @_stream_arg
@@ -402,18 +497,21 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, with_stats=False, 
     the backward pass).  weight, bias [cols]: x's dtype or float32.  out may
     be x itself."""
     rows, cols, ldx, code = _rows_of(x, "x")
-    dev = x.device
-    wdt = _norm_weight(bias, "bias", x, _norm_weight(weight, "weight", x, None, cols), cols)
+    dev, dtype = x.device, x.dtype
+    wdt = _norm_weight(bias, "bias", dtype, dev,
+                       _norm_weight(weight, "weight", dtype, dev, None, cols), cols)
     if out is None:
-        out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
-    ldy = _matrix(out, "out", dev, x.dtype, (rows, cols))
+        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        ldy = cols
+    else:
+        ldy = _matrix(out, "out", dev, dtype, rows, cols)
     mean = rstd = None
     if with_stats:
-        buf = torch.empty(2 * rows, dtype=torch.float32, device=dev)
-        mean, rstd = buf.as_strided((rows,), (1,), 0), buf.as_strided((rows,), (1,), rows)
-    _check(_on(dev, head_call().vpa_layer_norm, x.data_ptr(), ldx, code, _vp(weight), _vp(bias),
-               VPA_F32 if (wdt or x.dtype) == torch.float32 else VPA_BF16, rows, cols, eps,
-               out.data_ptr(), ldy, _vp(mean), _vp(rstd), _stream(stream, dev)))
+        mean = torch.empty(rows, dtype=torch.float32, device=dev)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    _launch(head_call().vpa_layer_norm, stream, dev, x.data_ptr(), ldx, code, _vp(weight),
+            _vp(bias), VPA_F32 if wdt is torch.float32 else code, rows, cols, eps, out.data_ptr(),
+            ldy, _vp(mean), _vp(rstd))
     return (out, mean, rstd) if with_stats else out
 
 
@@ -425,8 +523,8 @@ def layer_norm_backward(grad, x, mean, rstd, weight=None, need_x=True, need_weig
     and grad_bias have weight's dtype (x's where weight is None)."""
     rows, cols, ldg, code = _rows_of(grad, "grad")
     dev, dt = grad.device, grad.dtype
-    ldx = _matrix(x, "x", dev, dt, (rows, cols))
-    wdt = _norm_weight(weight, "weight", grad, None, cols) or dt
+    ldx = _matrix(x, "x", dev, dt, rows, cols)
+    wdt = _norm_weight(weight, "weight", dt, dev, None, cols) or dt
     _out_tensor(mean, "mean", torch.float32, rows, dev)
     _out_tensor(rstd, "rstd", torch.float32, rows, dev)
     gx = torch.empty((rows, cols), dtype=dt, device=dev) if need_x else None
@@ -434,9 +532,8 @@ def layer_norm_backward(grad, x, mean, rstd, weight=None, need_x=True, need_weig
     gb = torch.empty(cols, dtype=wdt, device=dev) if need_bias else None
     fn = head_call().vpa_layer_norm_backward
     need = _norm_grad_workspace(rows, cols) if need_weight or need_bias else 0
-    ws = _workspace(workspace, need, dev)
-    _check(_on(dev, fn, grad.data_ptr(), ldg, x.data_ptr(), ldx, code, _vp(weight),
-               VPA_F32 if wdt == torch.float32 else VPA_BF16, mean.data_ptr(), rstd.data_ptr(),
-               rows, cols, _vp(gx), cols, _vp(gw), _vp(gb), _vp(ws), _bytes(ws),
-               _stream(stream, dev)))
+    _ws, ws, ws_bytes = _workspace(workspace, need, dev)
+    _launch(fn, stream, dev, grad.data_ptr(), ldg, x.data_ptr(), ldx, code, _vp(weight),
+            VPA_F32 if wdt is torch.float32 else code, mean.data_ptr(), rstd.data_ptr(), rows,
+            cols, _vp(gx), cols, _vp(gw), _vp(gb), ws, ws_bytes)
     return gx, gw, gb
