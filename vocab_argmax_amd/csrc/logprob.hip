@@ -201,7 +201,8 @@ __device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int
 // Alternatives: T is a lower bound of the n_top-th largest value, from the
 // largest values of the lanes on the first chunk (in each of the W
 // wavefronts with columns at least ceil(n_top / W) lanes reach T, so n_top
-// columns do), then the n_top-th value found so far; columns reaching T go
+// columns do, unless the mask leaves fewer), then the n_top-th value found so
+// far; columns reaching T go
 // to a list in LDS, and the list is cut to its first n_top by counting for
 // each the larger ones.  Few columns pass T, so the scan costs one maximum
 // and one comparison a vector.  A chunk with a NaN, an infinity or more
@@ -396,21 +397,25 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
                 uint32_t least = lds_key[0];
                 for (int i = 1; i < waves; ++i)
                     least = lds_key[i] < least ? lds_key[i] : least;
-                bound = value_of_key(least);
+                bound = value_of_key(least ? least : 1);        // -inf is below it
             }
+            // The first chunk lists its first n_top columns whatever their
+            // values: where the mask leaves fewer than n_top, the rest are
+            // -inf by the lowest ids.
+            const int head = c0 == begin ? lo + t.n_top : lo;
             // NaN and +inf make the lane's s NaN: such a chunk is not listed
             if (s != s)
                 atomicAdd(&added[turn], (uint32_t)kCandidates);
-            else if (__ballot(mx >= bound)) {
+            else if (__ballot(mx >= bound || mine < head)) {
                 anew();
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
-                    if (!__ballot(g[i] >= bound))
+                    if (!__ballot(g[i] >= bound || column(i * VEC) < head))
                         continue;
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
                         const int c = column(i * VEC + e);
-                        if (value(i * VEC + e) >= bound && c >= lo && c < hi) {
+                        if ((value(i * VEC + e) >= bound || c < head) && c >= lo && c < hi) {
                             const uint32_t at = kept + atomicAdd(&added[turn], 1u);
                             if (at < kCandidates)
                                 cand[at] = order_of(value(i * VEC + e), c);
