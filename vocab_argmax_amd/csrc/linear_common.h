@@ -15,7 +15,7 @@ __device__ __forceinline__ float act(float z) {
     if constexpr (ACT == VPA_ACT_GELU)
         return 0.5f * z * (1.0f + erff(z * 0.70710678118654752440f));
     if constexpr (ACT == VPA_ACT_SILU)
-        return z / (1.0f + exp2_fast(-z * kLog2e));
+        return z * __builtin_amdgcn_rcpf(1.0f + exp2_fast(-z * kLog2e));   // within 1 ulp
     return z;
 }
 template <int ACT>
@@ -26,7 +26,7 @@ __device__ __forceinline__ float act_slope(float z) {
         return 0.5f * (1.0f + erff(z * 0.70710678118654752440f)) +
                z * exp2_fast(-0.5f * kLog2e * z * z) * 0.39894228040143267794f;
     if constexpr (ACT == VPA_ACT_SILU) {
-        const float q = 1.0f / (1.0f + exp2_fast(-z * kLog2e));
+        const float q = __builtin_amdgcn_rcpf(1.0f + exp2_fast(-z * kLog2e));
         return q * (1.0f + z * (1.0f - q));
     }
     return 1.0f;
@@ -90,9 +90,10 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
     *(Loose8*)p = Loose8{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
-// Four results of consecutive n.
+// Four results of consecutive n; `res` holds the residual's, where there is one.
 template <typename T>
-__device__ __forceinline__ void store_results(const GemmTask& t, int64_t m, int64_t n, f32x4 acc) {
+__device__ __forceinline__ void store_results(const GemmTask& t, int64_t m, int64_t n, f32x4 acc,
+                                              f32x4 res) {
     if (t.bias)
         acc += load4((const T*)t.bias + n);
     if (t.pre)
@@ -110,12 +111,17 @@ __device__ __forceinline__ void store_results(const GemmTask& t, int64_t m, int6
     default:
         break;
     }
-    if (t.residual)
-        acc += load4((const T*)t.residual + m * t.ldr + n);
+    acc += res;
     if (t.out_f32)
         store4((float*)t.y + m * t.ldy + n, acc);
     else
         store4((T*)t.y + m * t.ldy + n, acc);
+}
+template <typename T>
+__device__ __forceinline__ void store_results(const GemmTask& t, int64_t m, int64_t n, f32x4 acc) {
+    const f32x4 none = {-0.0f, -0.0f, -0.0f, -0.0f};    // keeps a result's sign of zero
+    store_results<T>(t, m, n, acc,
+                     t.residual ? load4((const T*)t.residual + m * t.ldr + n) : none);
 }
 
 // A wavefront's 64 x 64 results from accumulators to memory, through its own
@@ -138,23 +144,40 @@ __device__ __forceinline__ void store_block(const GemmTask& t, float* part, char
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     if (n0 + 64 <= t.n) {
+        const int64_t n = n0 + (lane & 15) * 4;
+        // the residual of a pass of 4 x 4 rows is on its way during the last
+        const bool res = t.residual && !part;
+        f32x4 next[4];
+        auto fetch = [&](int r0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t m = m0 + r0 + k * 4 + (lane >> 4);
+                next[k] = f32x4{-0.0f, -0.0f, -0.0f, -0.0f};
+                if (res && m < t.m)
+                    next[k] = load4((const T*)t.residual + m * t.ldr + n);
+            }
+        };
+        fetch(0);
 #pragma unroll 1
         for (int r0 = 0; r0 < 64; r0 += 16) {
-            f32x4 v[4];
+            f32x4 v[4], r4[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int r = r0 + k * 4 + (lane >> 4), c = lane & 15;
                 v[k] = *(const f32x4*)(lds + r * 256 + ((c ^ (r & 15)) << 4));
+                r4[k] = next[k];
             }
+            if (r0 < 48)
+                fetch(r0 + 16);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int64_t m = m0 + r0 + k * 4 + (lane >> 4), n = n0 + (lane & 15) * 4;
+                const int64_t m = m0 + r0 + k * 4 + (lane >> 4);
                 if (m >= t.m)
                     continue;
                 if (part)
                     store4(part + m * t.n + n, v[k]);
                 else
-                    store_results<T>(t, m, n, v[k]);
+                    store_results<T>(t, m, n, v[k], r4[k]);
             }
         }
         return;
