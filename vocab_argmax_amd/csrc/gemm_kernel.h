@@ -9,8 +9,8 @@ namespace vpa {
 namespace {
 
 // WM x WN wavefronts, each with BM/WM x BN/WN of the tile in its
-// accumulators.  With part set, blockIdx.y is a slice of k and the raw sums
-// go to part[slice][m][n].
+// accumulators.  With part set, the raw sums of a slice of k go to
+// part[slice][m][n].
 template <int ESIZE, bool AK, bool BK, bool DIRECT, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint32_t tiles_m,
                                                                 uint32_t tiles_n,
@@ -24,8 +24,8 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
     using LB = TileLoader<ESIZE, BK, DIRECT, BN, NT>;
     __shared__ __align__(1024) char lds0[LA::BYTES + LB::BYTES];
     __shared__ __align__(1024) char lds1[LA::BYTES + LB::BYTES];
-    uint32_t tm, tn;
-    tile_of_block(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    uint32_t slice, tm, tn;
+    tile_of_block(blockIdx.x, gridDim.x, tiles_m, tiles_n, slice, tm, tn);
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
@@ -34,7 +34,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
     la.init(t.a, AK ? t.a_m : t.a_k, m0, t.m_readable);
     lb.init(t.b, BK ? t.b_n : t.b_k, n0, t.n);
     const int64_t whole = t.k / LA::KB, all = (t.k + LA::KB - 1) / LA::KB;
-    const int64_t s0 = blockIdx.y * stages_per_slice;
+    const int64_t s0 = slice * stages_per_slice;
     const int64_t end = s0 + stages_per_slice < all ? s0 + stages_per_slice : all;
     const typename LA::Place pa = LA::place(wm);
     const typename LB::Place pb = LB::place(wn);
@@ -161,7 +161,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
     }
     stage_barrier();
     if (part)
-        part += (int64_t)blockIdx.y * t.m * t.n;
+        part += slice * t.m * t.n;
     char* mine = wave * 16384 < LA::BYTES + LB::BYTES
                      ? lds0 + wave * 16384 : lds1 + (wave * 16384 - LA::BYTES - LB::BYTES);
 #pragma unroll
@@ -294,7 +294,7 @@ template <int ESIZE, bool AK, bool BK, bool DIRECT, int BM, int BN, int WM, int 
 hipError_t launch_tile(const GemmTask& t, const GemmPlan& p, hipStream_t stream) {
     const uint32_t tm = (uint32_t)((t.m + BM - 1) / BM), tn = (uint32_t)((t.n + BN - 1) / BN);
     return launch(gemm_tile_kernel<ESIZE, AK, BK, DIRECT, BM, BN, WM, WN>,
-                  dim3(tm * tn, (uint32_t)p.slices), dim3(WM * WN * 64), 0, stream, t, tm, tn,
+                  dim3(tm * tn * (uint32_t)p.slices), dim3(WM * WN * 64), 0, stream, t, tm, tn,
                   p.stages_per_slice, p.slices > 1 ? (float*)t.ws : nullptr);
 }
 

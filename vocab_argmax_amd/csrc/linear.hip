@@ -125,6 +125,11 @@ bool direct_operand(int esize, const void* p, int64_t ld, bool k1, int64_t rows)
            (k1 || rows % vec == 0);
 }
 
+// Stages of 128 bytes of k (no k: one, which stores zeros).
+int64_t stages_of(int esize, int64_t k) {
+    return k > 0 ? (k * esize + 127) / 128 : 1;
+}
+
 template <typename T>
 hipError_t launch_dz_typed(const DzTask& t, hipStream_t stream) {
     const int32_t splits = dz_splits(t.rows, t.cols);
@@ -151,16 +156,54 @@ hipError_t launch_dz_typed(const DzTask& t, hipStream_t stream) {
 
 }  // namespace
 
-// Which tile, and how many slices of k.  A candidate's time is modelled as
-// rounds of workgroups over the CUs times a stage's time, plus what a split
-// costs to write and join; the constants are measured on MI355X (bf16: a
+namespace {
+
+// The best tile and number of slices of k for one launch, and its modelled
+// time in us: rounds of workgroups over the CUs times a stage's time, plus
+// what slices cost to write and join.  The constants are measured (bf16: a
 // 256-tile alone on a CU needs 1.6 us a stage, two 128-tiles on a CU 1.1 us;
 // fp32's matrix instructions take 16 times as long for the same k).
+double plan_tiles(int esize, int64_t m, int64_t n, int64_t k, GemmPlan& p) {
+    const int64_t stages = stages_of(esize, k);
+    double best = 0;
+    for (int32_t tile = esize == 2 ? 256 : 128; tile >= 128; tile /= 2) {
+        const double stage_us = esize == 4 ? 7.0 : tile == 256 ? 1.6 : 1.1;
+        const int64_t at_once = tile == 256 ? 256 : 512;
+        const int64_t tiles = ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
+        for (int32_t s = 1; s <= 16; s *= 2) {
+            const int64_t per = (stages + s - 1) / s, blocks = tiles * s;
+            if (s > 1 && per < 4)
+                break;
+            const double rounds = (double)((blocks + at_once - 1) / at_once);
+            double us = rounds * ((double)per * stage_us + 2.0);
+            if (s > 1)
+                us += 4.0 + (double)s * (double)m * (double)n * 8.0 / 4.0e6;
+            if (best == 0 || us < best) {
+                best = us;
+                p.tile = tile;
+                p.slices = (int32_t)((stages + per - 1) / per);
+                p.stages_per_slice = per;
+            }
+        }
+    }
+    return best;
+}
+
+size_t slices_bytes(const GemmPlan& p, int64_t m, int64_t n) {
+    return p.slices > 1 ? (size_t)p.slices * (size_t)m * (size_t)n * 4 : 0;
+}
+
+}  // namespace
+
+// The 256-tiles of a product seldom fill the last round: 272 of them take as
+// long as 512.  Where the model says so, a first launch takes as many columns
+// (or rows) of tiles as fill whole rounds, and a second one, of smaller tiles
+// or slices of k, the rest: 4096 x 4352 x 4096 192 -> 135 us, 2048 x 50257 x
+// 2048 434 -> 417, its gradient of the weight 653 -> 607.
 GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1) {
     GemmPlan p{};
     p.slices = 1;
-    // (no k: one slice of no stages, which stores zeros)
-    const int64_t stages = k > 0 ? (k * esize + 127) / 128 : 1;
+    const int64_t stages = stages_of(esize, k);
     p.stages_per_slice = stages;
     if (a_k1 && b_k1 && m <= 64) {
         const int64_t tiles = (n + kFewRowsCols - 1) / kFewRowsCols;
@@ -177,25 +220,26 @@ GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b
         p.slices = (int32_t)((stages + p.stages_per_slice - 1) / p.stages_per_slice);
         return p;
     }
-    double best = 0;
-    for (int32_t tile = esize == 2 ? 256 : 128; tile >= 128; tile /= 2) {
-        const double stage_us = esize == 4 ? 7.0 : tile == 256 ? 1.6 : 1.1;
-        const int64_t at_once = tile == 256 ? 256 : 512;
-        const int64_t tiles = ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
-        for (int32_t s = 1; s <= 16; s *= 2) {
-            const int64_t per = (stages + s - 1) / s;
-            if (s > 1 && per < 4)
-                break;
-            const double rounds = (double)((tiles * s + at_once - 1) / at_once);
-            double us = rounds * ((double)per * stage_us + 2.0);
-            if (s > 1)
-                us += 4.0 + (double)s * (double)m * (double)n * 8.0 / 4.0e6;
-            if (best == 0 || us < best) {
-                best = us;
-                p.tile = tile;
-                p.slices = (int32_t)((stages + per - 1) / per);
-                p.stages_per_slice = per;
-            }
+    double best = plan_tiles(esize, m, n, k, p);
+    if (esize != 2)
+        return p;
+    const int64_t tm = (m + 255) / 256, tn = (n + 255) / 256, whole = tm * tn / 256 * 256;
+    for (int axis = 0; axis < 2; ++axis) {
+        const int64_t first = (axis ? whole / tm : whole / tn) * 256;
+        if (first == 0 || first >= (axis ? n : m))
+            continue;
+        GemmPlan f{}, r{};
+        const double us = axis ? plan_tiles(esize, m, first, k, f) +
+                                     plan_tiles(esize, m, n - first, k, r)
+                               : plan_tiles(esize, first, n, k, f) +
+                                     plan_tiles(esize, m - first, n, k, r);
+        if (f.tile == 256 && us + 3.0 < best) {
+            best = us + 3.0;
+            p.first_m = axis ? m : first;
+            p.first_n = axis ? first : n;
+            p.tile = f.tile;
+            p.slices = f.slices;
+            p.stages_per_slice = f.stages_per_slice;
         }
     }
     return p;
@@ -203,26 +247,29 @@ GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b
 
 size_t gemm_workspace(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1) {
     const GemmPlan p = plan_gemm(esize, m, n, k, a_k1, b_k1);
-    return p.slices > 1 ? (size_t)p.slices * (size_t)m * (size_t)n * 4 : 0;
+    if (!p.first_m)
+        return slices_bytes(p, m, n);
+    const int64_t mr = p.first_m < m ? m - p.first_m : m, nr = p.first_n < n ? n - p.first_n : n;
+    GemmPlan r{};
+    plan_tiles(esize, mr, nr, k, r);
+    const size_t first = slices_bytes(p, p.first_m, p.first_n), rest = slices_bytes(r, mr, nr);
+    return first > rest ? first : rest;
 }
 
 int64_t gemm_threads(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1) {
     const GemmPlan p = plan_gemm(esize, m, n, k, a_k1, b_k1);
     if (p.rows_kernel)
         return linear_rows_threads(n);
-    // a product that is not direct takes 128-tiles whatever the plan says
-    const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128) * p.slices * 256;
-    const int64_t join = p.slices > 1 ? (m * n + kThreads - 1) / kThreads * kThreads : 0;
+    // a product that is not direct takes 128-tiles whatever the plan says; the
+    // second of two launches has at most 16 slices
+    const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128) * (p.first_m ? 16 : p.slices) * 256;
+    const int64_t join = p.slices > 1 || p.first_m ? (m * n + kThreads - 1) / kThreads * kThreads : 0;
     return tiles > join ? tiles : join;
 }
 
-hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream) {
-    const bool ak = t.a_k == 1, bk = t.b_k == 1;
-    GemmPlan p = plan_gemm(esize, t.m, t.n, t.k, ak, bk);
-    if (p.rows_kernel)
-        return launch_linear_rows(esize, t, stream);
-    p.direct = direct_operand(esize, t.a, ak ? t.a_m : t.a_k, ak, t.m_readable) &&
-               direct_operand(esize, t.b, bk ? t.b_n : t.b_k, bk, t.n);
+namespace {
+
+hipError_t launch_planned(int esize, const GemmTask& t, const GemmPlan& p, hipStream_t stream) {
     hipError_t e = esize == 2 ? launch_gemm_tiles_bf16(t, p, stream)
                               : launch_gemm_tiles_f32(t, p, stream);
     if (e != hipSuccess || p.slices == 1)
@@ -236,6 +283,39 @@ hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream) {
                               p.slices);
     return join4 ? launch(gemm_join_kernel<float, true>, grid, block, 0, stream, t, p.slices)
                  : launch(gemm_join_kernel<float, false>, grid, block, 0, stream, t, p.slices);
+}
+
+}  // namespace
+
+hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream) {
+    const bool ak = t.a_k == 1, bk = t.b_k == 1;
+    GemmPlan p = plan_gemm(esize, t.m, t.n, t.k, ak, bk);
+    if (p.rows_kernel)
+        return launch_linear_rows(esize, t, stream);
+    p.direct = direct_operand(esize, t.a, ak ? t.a_m : t.a_k, ak, t.m_readable) &&
+               direct_operand(esize, t.b, bk ? t.b_n : t.b_k, bk, t.n);
+    if (!p.first_m)
+        return launch_planned(esize, t, p, stream);
+    GemmTask f = t, r = t;                          // the first part and the rest
+    const int out = t.out_f32 ? 4 : esize;
+    auto past = [](const void* q, int64_t bytes) { return q ? (char*)q + bytes : nullptr; };
+    f.m = p.first_m;
+    f.n = p.first_n;
+    const int64_t dm = f.m < t.m ? f.m : 0, dn = f.n < t.n ? f.n : 0;
+    r.m -= dm;
+    r.m_readable -= dm;
+    r.n -= dn;
+    r.a = past(t.a, dm * t.a_m * esize);
+    r.b = past(t.b, dn * t.b_n * esize);
+    r.bias = past(t.bias, dn * esize);
+    r.residual = past(t.residual, (dm * t.ldr + dn) * esize);
+    r.pre = past(t.pre, (dm * t.ldp + dn) * esize);
+    r.y = past(t.y, (dm * t.ldy + dn) * out);
+    GemmPlan q{};
+    plan_tiles(esize, r.m, r.n, r.k, q);
+    q.direct = p.direct;
+    hipError_t e = launch_planned(esize, f, p, stream);
+    return e != hipSuccess ? e : launch_planned(esize, r, q, stream);
 }
 
 // Slices of rows: enough workgroups for 8 a CU, at least 16 rows each.

@@ -111,6 +111,7 @@ struct GemmPlan {
                               // 32: the rows, of kFewRowsCols columns
     int32_t slices;           // of k, joined by a second kernel
     int64_t stages_per_slice; // stages of 128 bytes of k
+    int64_t first_m, first_n; // the plan is for these, the rest has its own; 0: for all
     bool direct;              // operands' strides allow direct loads to LDS
 };
 GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
