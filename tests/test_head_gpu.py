@@ -618,3 +618,163 @@ def test_offsets_past_32_bits():
     vpa.token_logprobs_backward(x, v, v, 1, tok, r.row_stats, gl, out=x)
     want, tol = grad_oracle(vals, v, tok[rows], gl[rows], None, r.row_stats[rows])
     near(x[rows], want, tol + half(BF) * want.abs() + torch.finfo(F32).tiny, "gradient")
+
+
+# ---------------------------------------------------------------------------
+# the kernels that the sizes above do not reach, workspaces, refusals
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n,k,m", [
+    (9, 72, 32800), (16, 520, 33001),       # few rows of a wide weight
+    (40, 4096, 300), (61, 8200, 130),       # few rows, slices of k
+    (2900, 200, 2901),                      # 256-tiles with ragged edges
+    (4090, 136, 4340), (4340, 136, 4090),   # whole rounds of tiles, and the rest
+    (4096, 1024, 4096), (200, 6000, 260),   # many stages; slices of k of larger tiles
+])
+def test_head_linear_tiles(n, k, m):
+    g = gen(n + 31 * k + 7 * m)
+    x, w = randn(g, n, k, dtype=BF), randn(g, m, k, dtype=BF, scale=k ** -0.5)
+    b, r = randn(g, m, dtype=BF), randn(g, n, m, dtype=BF)
+    z, dz, y, dy = linear_oracle(x, w, b, "gelu", r)
+    got, pre = vpa.head_linear(x, w, b, "gelu", r, with_pre=True)
+    near(got, y, dy + half(BF) * (y.abs() + dy), "y")
+    near(pre, z, dz + half(BF) * (z.abs() + dz), "pre")
+    near(vpa.head_linear(x, w, b, "gelu", r, out_dtype=F32), y, dy + U * y.abs(), "fp32 y")
+    for _ in range(3):
+        assert torch.equal(vpa.head_linear(x, w, b, "gelu", r), got)
+
+
+@pytest.mark.parametrize("n,k,m,pad", [(136, 4088, 4340, 0), (2048, 1024, 4097, 0),
+                                       (1030, 520, 2904, 8), (4096, 256, 264, 0),
+                                       (2000, 1024, 2048, 1)])
+def test_head_linear_backward_tiles(n, k, m, pad):
+    g = gen(n + 31 * k + 7 * m)
+    x, w = randn(g, n, k, dtype=BF), randn(g, m, k, dtype=BF, scale=k ** -0.5)
+    gr = randn(g, n, m, dtype=BF)
+    args = (strided(gr, pad), strided(x, pad), strided(w, pad)) if pad else (gr, x, w)
+    gx, gw, gb = vpa.head_linear_backward(*args)
+    gd, xd, wd = gr.double(), x.double(), w.double()
+    want = gd @ wd
+    tol = (m + 2) * 2 * U * (gd.abs() @ wd.abs())
+    near(gx, want, tol + half(BF) * (want.abs() + tol), "grad_x")
+    want = gd.T @ xd
+    tol = (n + 2) * 2 * U * (gd.abs().T @ xd.abs())
+    near(gw, want, tol + half(BF) * (want.abs() + tol), "grad_weight")
+    want = gd.sum(0)
+    tol = (n + 2) * U * gd.abs().sum(0)
+    near(gb, want, tol + half(BF) * (want.abs() + tol), "grad_bias")
+    for _ in range(3):
+        again = vpa.head_linear_backward(*args)
+        assert all(torch.equal(a, c) for a, c in zip(again, (gx, gw, gb)))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,v,s,top", [(2, 150001, 3, 20), (66, 20011, 2, 64), (700, 3001, 1, 7)])
+def test_masks_that_leave_few_tokens(n, v, s, top, dtype):
+    """Row i keeps i % (top + 3) columns, the first, the last or any; the
+    masked ones are -inf or the type's lowest value."""
+    g = gen(n + v)
+    w = -(-v // s)
+    x = randn(g, n, w * s, dtype=dtype, scale=2.0)
+    order = torch.rand((n, v), generator=g, device=DEV).argsort(1)
+    rank = torch.empty_like(order).scatter_(
+        1, order, torch.arange(v, device=DEV).expand(n, v).contiguous())
+    col = torch.arange(v, device=DEV).expand(n, v)
+    i = torch.arange(n, device=DEV)[:, None]
+    rank = torch.where(i % 3 == 0, col, torch.where(i % 3 == 1, v - 1 - col, rank))
+    low = torch.where(i % 2 == 0, NEG, torch.finfo(dtype).min).to(dtype)
+    x[:, :v] = torch.where(rank < i % (top + 3), x[:, :v], low)
+    tok = torch.randint(0, v, (n, 2), generator=g, device=DEV, dtype=torch.int32)
+    check_logprobs(vpa.token_logprobs(x, v, w, s, tok, top), x, v, tok, top, "masked")
+
+
+def test_workspaces_of_the_caller():
+    g = gen(77)
+    n, k, v = 100, 1000, 30011
+    ins = _step_inputs(n, 1000, 30011, 4)
+    x, nw, nb, w, tok, gl = ins
+    garbage = lambda size: torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+    from vocab_argmax_amd import head
+    logits = vpa.head_linear(x, w)
+    ws = vpa.logprobs_workspace(v, v, 1, n, 20)
+    a, b = vpa.token_logprobs(logits, v, v, 1, tok, 20), vpa.token_logprobs(
+        logits, v, v, 1, tok, 20, workspace=garbage(ws))
+    assert torch.equal(a.logprobs, b.logprobs) and torch.equal(a.top_ids, b.top_ids)
+    x2, w2 = randn(g, 40, 8192, dtype=BF), randn(g, 256, 8192, dtype=BF)
+    ws = head._linear_workspace(vpa.VPA_BF16, 40, 256, 8192)
+    assert ws > 0
+    assert torch.equal(vpa.head_linear(x2, w2), vpa.head_linear(x2, w2, workspace=garbage(ws)))
+    with pytest.raises(vpa.VpaError):
+        vpa.head_linear(x2, w2, workspace=garbage(ws - 1))
+    gr = randn(g, n, v, dtype=BF)
+    ws = head._linear_grad_workspace(vpa.VPA_BF16, n, v, k)
+    got = vpa.head_linear_backward(gr, x, w, workspace=garbage(ws))
+    assert all(torch.equal(p, q) for p, q in zip(got, vpa.head_linear_backward(gr, x, w)))
+    with pytest.raises(vpa.VpaError):
+        vpa.head_linear_backward(gr, x, w, workspace=garbage(1))
+    _, mean, rstd = vpa.layer_norm(x, nw, nb, with_stats=True)
+    ws = head._norm_grad_workspace(n, k)
+    got = vpa.layer_norm_backward(x, x, mean, rstd, nw, workspace=garbage(ws))
+    assert all(torch.equal(p, q) for p, q in zip(got, vpa.layer_norm_backward(x, x, mean, rstd, nw)))
+    with pytest.raises(vpa.VpaError):
+        vpa.layer_norm_backward(x, x, mean, rstd, nw, workspace=garbage(ws - 1))
+    with pytest.raises(ValueError):
+        vpa.head_linear(x2, w2, workspace=torch.empty(1 << 24, dtype=torch.uint8))
+
+
+def test_refusals():
+    """Each is refused before anything is launched."""
+    g = gen(8)
+    x, w = randn(g, 4, 64, dtype=BF), randn(g, 32, 64, dtype=BF)
+    tok = torch.zeros(4, dtype=torch.int32, device=DEV)
+    wide = torch.zeros(4, 200, dtype=BF, device=DEV)
+    r = vpa.token_logprobs(wide, 200, 100, 2, tok)
+    e = torch.zeros(4, device=DEV)
+    bad = [
+        lambda: vpa.token_logprobs(wide[:, :120], 200, 100, 2, tok),     # stride 200, too narrow
+        lambda: vpa.token_logprobs(wide[:, ::2], 100, 100, 1, tok),
+        lambda: vpa.token_logprobs(wide[:1].expand(4, 200), 200, 100, 2, tok),
+        lambda: vpa.token_logprobs(wide, 200, 100, 2, tok.long()),
+        lambda: vpa.token_logprobs(wide, 200, 100, 2, tok[:3]),
+        lambda: vpa.token_logprobs(wide, 200, 100, 2, tok.cpu()),
+        lambda: vpa.token_logprobs(wide, 200, 100, 2, tok, 65),
+        lambda: vpa.token_logprobs(wide, 200, 100, 2, tok, -1),
+        lambda: vpa.token_logprobs(wide, 200, 50, 2, tok),
+        lambda: vpa.token_logprobs(wide.half(), 200, 100, 2, tok),
+        lambda: vpa.token_logprobs(wide, 200, 100, 2,
+                                   torch.zeros(4, 65, dtype=torch.int32, device=DEV)),
+        lambda: vpa.logprob_stats(wide[:, :99], 200, 100, 2, tok, first_shard=1),
+        lambda: vpa.logprob_stats(wide, 200, 100, 2, tok, first_shard=2, n_local=1),
+        lambda: vpa.combine_logprobs(torch.zeros(2, 4, 9, dtype=torch.int32, device=DEV), 200, 100,
+                                     tok),
+        lambda: vpa.token_logprobs_backward(wide, 200, 100, 2, tok, r.row_stats, None),
+        lambda: vpa.token_logprobs_backward(wide[:, :120], 200, 100, 2, tok, r.row_stats, e),
+        lambda: vpa.token_logprobs_backward(wide, 200, 100, 2, tok, r.row_stats[:3], e),
+        lambda: vpa.token_logprobs_backward(wide, 200, 100, 2, tok, r.row_stats, e.to(BF)),
+        lambda: vpa.head_linear(x, w[:, :63]),
+        lambda: vpa.head_linear(x, w.float()),
+        lambda: vpa.head_linear(x, w.T),
+        lambda: vpa.head_linear(x, w.cpu()),
+        lambda: vpa.head_linear(x, w, w[0, :31]),
+        lambda: vpa.head_linear(x, w, activation="tanh"),
+        lambda: vpa.head_linear(x, w, residual=x),
+        lambda: vpa.head_linear(x, w, residual=w[:1, :32].expand(4, 32)),
+        lambda: vpa.head_linear(x, w, out=torch.empty(4, 32, dtype=torch.float16, device=DEV)),
+        lambda: vpa.head_linear(x, w, out_dtype=torch.float16),
+        lambda: vpa.head_linear_backward(wide[:, :32], x, w, activation="silu"),
+        lambda: vpa.head_linear_backward(wide[:, :32], x[:3], w),
+        lambda: vpa.layer_norm(x, e),
+        lambda: vpa.layer_norm(x, w[0], w[0].float()),
+        lambda: vpa.layer_norm(x, w[0].half()),
+        lambda: vpa.layer_norm(x, eps=float("nan")),
+        lambda: vpa.layer_norm(x, eps=-1.0),
+        lambda: vpa.layer_norm(x[0]),
+        lambda: vpa.layer_norm_backward(x, x, e[:3], e),
+        lambda: vpa.layer_norm_backward(x, x.float(), e, e),
+    ]
+    for i, call in enumerate(bad):
+        try:
+            call()
+        except (ValueError, TypeError, vpa.VpaError):
+            continue
+        raise AssertionError(f"call {i} was not refused")

@@ -164,6 +164,14 @@ def _rows_of(t, name):
     return rows, cols, stride[0] if rows > 1 else cols, code
 
 
+def _columns(cols, vocab, shard_width, first_shard, n_local):
+    """Refuses logits narrower than what the shards hold of the vocabulary
+    (their row stride may be wide enough, and the last row not)."""
+    need = min(n_local * shard_width, vocab - first_shard * shard_width)
+    if cols < need:
+        raise ValueError(f"logits has {cols} columns, the shards hold {need}")
+
+
 def _launch(fn, stream, device, *args):
     """Calls the entry point with `device` current, on the given stream or the
     device's current one, and raises what it reports."""
@@ -283,7 +291,9 @@ def token_logprobs(logits, vocab, shard_width, n_shards, token_ids=None, n_top=0
     gives NaN.  Alternatives come by value, the lower id first among equals.
     Masked columns hold -inf.  workspace: optional device tensor of at least
     logprobs_workspace() bytes."""
-    n, _, ld, code = _rows_of(logits, "logits")
+    n, cols, ld, code = _rows_of(logits, "logits")
+    if cols < vocab:
+        raise ValueError(f"logits has {cols} columns, the vocabulary {vocab}")
     dev = logits.device
     n_tokens, shape = _tokens(token_ids, n, dev)
     fn = head_call().vpa_token_logprobs
@@ -318,10 +328,11 @@ def logprob_stats(logits, vocab, shard_width, n_shards, token_ids=None, n_top=0,
     ranks hold one shard each: int32 [n_local][N][words].  Gathered in rank
     order along dim 0 they go to combine_logprobs.  logits [N, ld]: column 0
     is global column first_shard * W; token_ids are global."""
-    n, _, ld, code = _rows_of(logits, "logits")
+    n, cols, ld, code = _rows_of(logits, "logits")
     dev = logits.device
     if n_local is None:
         n_local = n_shards - first_shard
+    _columns(cols, vocab, shard_width, first_shard, n_local)
     n_tokens, _ = _tokens(token_ids, n, dev)
     words = head_lib().vpa_logprob_words(n_tokens, n_top)
     if words < 0:
@@ -369,6 +380,7 @@ def token_logprobs_backward(logits, vocab, shard_width, n_shards, token_ids, row
     dev = logits.device
     if n_local is None:
         n_local = n_shards - first_shard
+    _columns(cols, vocab, shard_width, first_shard, n_local)
     n_tokens, _ = _tokens(token_ids, n, dev)
     if (grad_logprobs is None) != (token_ids is None):
         raise ValueError("grad_logprobs goes with token_ids")
