@@ -181,11 +181,12 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
 }
 
 // Few rows of A (BM = 32 or 64), k contiguous in both: bound by reading B, so
-// the tile is 128 rows of B by all of A's, and STAGES - 1 stages are on their
-// way at a time.  (4 of them for 32 rows, 3 for 64: two workgroups a CU then
-// have about 100 or 64 KiB of B in flight, where the memory's latency at its
-// rate is about 55 KiB a CU; two stages of a 128 x 128 tile, 32 KiB, reached
-// 3.6 TB/s.)
+// the tile is 64 rows of B by all of A's, and STAGES - 1 stages are on their
+// way at a time: 5 for 32 rows, 4 for 64, which with two workgroups a CU is 80
+// or 64 KiB of B in flight (two stages of a 128 x 128 tile, 32 KiB, reached
+// 3.6 TB/s).  B is read once and past the L2 (nt).  32 x 2048 x 151936 to fp32:
+// 118 us, of which reading B alone takes 95 in the same pattern; a weight row
+// more costs nothing until the output shows (1 row 102 us, 64 rows 134).
 template <int ESIZE, int BM, int STAGES>
 __global__ __launch_bounds__(256) void gemm_few_rows_kernel(GemmTask t, int64_t stages_per_slice,
                                                             float* part) {
@@ -211,10 +212,15 @@ __global__ __launch_bounds__(256) void gemm_few_rows_kernel(GemmTask t, int64_t 
     const int64_t end = s0 + stages_per_slice < all ? s0 + stages_per_slice : all;
     const int64_t s1 = end < whole ? end : whole;
     f32x4 acc[IM][JN] = {};
+    // Workgroups begin at different stages: rows a power of two apart would
+    // otherwise be read at one place of each by all workgroups at once, from
+    // few of the memory's channels (32 x 4096 x 151936 258 us, so 231).
+    const int64_t shift = s0 < s1 ? blockIdx.x % (s1 - s0) : 0;
     auto stage = [&](int64_t s) {
         char* p = lds + (s - s0) % STAGES * BYTES;
-        la.load(da, s, p);
-        lb.load(db, s, p + LA::BYTES);
+        const int64_t at = s + shift < s1 ? s + shift : s + shift - (s1 - s0);
+        la.load(da, at, p);
+        lb.template load<true>(db, at, p + LA::BYTES);
     };
     auto multiply = [&](const char* p) {
 #pragma unroll
@@ -274,7 +280,7 @@ __global__ __launch_bounds__(256) void gemm_few_rows_kernel(GemmTask t, int64_t 
         float* p = part ? part + ((int64_t)blockIdx.y * t.m + m) * t.n + n : nullptr;
         if (n + 4 <= t.n) {
             if (part)
-                store4(p, v);
+                keep4(p, v);
             else
                 store_results<T>(t, m, n, v);
         } else {

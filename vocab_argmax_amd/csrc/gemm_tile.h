@@ -114,7 +114,8 @@ struct TileLoader {
         d.size = (uint32_t)(K1 ? (left - 1) * ld + 128 : (KB - 1) * ld + left * ESIZE);
         return d;
     }
-    // a whole stage, straight to LDS
+    // a whole stage, straight to LDS; ONCE for an operand that nothing else reads
+    template <bool ONCE = false>
     __device__ __forceinline__ void load(const Direct& d, int64_t stage, char* lds) const {
 #ifdef __HIP_DEVICE_COMPILE__    // the host pass has no buffer type
         const auto buf = __builtin_amdgcn_make_buffer_rsrc(
@@ -124,7 +125,7 @@ struct TileLoader {
         for (int i = 0; i < LOADS; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_ptr)(lds + i * NT * 16 + wave_base),
                                                      16, d.off[i % PERIOD] + i / PERIOD * d.step,
-                                                     0, 0, 0);
+                                                     0, 0, ONCE ? 2 : 0);   // 2: nt
 #endif
     }
     // a whole stage to registers, and from there to LDS

@@ -74,7 +74,8 @@ struct RowPart {
                 v[e] = __builtin_bit_cast(uint32_t, f[e]);
         }
         if (n == VEC) {
-            ((Loose16*)(row + column(i)))->v = v;
+            // past the L2 (32768 x 4096 forward 105 -> 87 us; loads past it are slower)
+            __builtin_nontemporal_store(v, &((Loose16*)(row + column(i)))->v);
         } else {
 #pragma unroll
             for (int e = 0; e < VEC - 1; ++e)
