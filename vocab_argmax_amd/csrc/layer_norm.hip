@@ -262,15 +262,25 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_grad_kerne
     // part[0][workgroup][column]: weight's, part[1]: bias's
     float* pw = t.part + (int64_t)blockIdx.x * cols;
     float* pb = pw + (int64_t)gridDim.x * cols;
+    typedef float f32x4_loose __attribute__((ext_vector_type(4), aligned(4)));
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
+        for (int e = 0; e < VEC; e += 4) {
             const int c = P::column(i) + e;
-            if (c < cols) {
-                pw[c] = dw[i][e];
-                pb[c] = db[i][e];
+            if (c + 4 <= cols) {
+                *(f32x4_loose*)(pw + c) = f32x4_loose{dw[i][e], dw[i][e + 1], dw[i][e + 2],
+                                                      dw[i][e + 3]};
+                *(f32x4_loose*)(pb + c) = f32x4_loose{db[i][e], db[i][e + 1], db[i][e + 2],
+                                                      db[i][e + 3]};
+                continue;
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c + k < cols) {
+                    pw[c + k] = dw[i][e + k];
+                    pb[c + k] = db[i][e + k];
+                }
         }
 }
 
