@@ -2,6 +2,8 @@
 // launch, instantiated for one element size by gemm_bf16.hip and gemm_f32.hip.
 #pragma once
 
+#include <type_traits>
+
 #include "gemm_tile.h"
 #include "linear_common.h"
 
@@ -64,42 +66,52 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
         lb.load_tail(whole, t.k, lds1 + LA::BYTES);
     }
     if constexpr (DIRECT) {
-        // One stage of the loop: the fragments of its first step are in
-        // registers; while a step's products run, the next step's fragments
-        // are read into the registers that they free.  Before the second
-        // step one barrier says both that the next stage has landed and
-        // that every wavefront has read this stage, whose buffer the stage
-        // after next then fills.
+        // While a step's products run, from fragments in registers, the next
+        // step's fragments are read into the registers that they free.  One
+        // barrier a stage says both that the next stage has landed and that
+        // every wavefront has read this one, whose buffer the stage after
+        // next then fills.  It stands after the first products of a step, so
+        // that nothing waits for the reads issued just before it; half of the
+        // wavefronts, one of the two on a SIMD, issue their loads there and
+        // half a stage later the others, since a wavefront that issues them is
+        // held up by the 64 bytes a clock that the loads can be taken in
+        // (8192^3 800 us with all loads and the barrier before a step, 790
+        // with halves, 775 so; 679 by the library on the same card).
         const typename LA::Direct da = la.direct();
         const typename LB::Direct db = lb.direct();
         auto stage = [&](int64_t s, char* lds) {
             la.load(da, s, lds);
             lb.load(db, s, lds + LA::BYTES);
         };
-        u32x4_t av[IM], bv[JN];
-        auto read_all = [&](const char* lds) {
-#pragma unroll
-            for (int j = 0; j < JN; ++j)
-                bv[j] = LB::fragment(lds + LA::BYTES, pb, j, 0);
-#pragma unroll
-            for (int i = 0; i < IM; ++i)
-                av[i] = LA::fragment(lds, pa, i, 0);
-        };
-        auto step = [&](const char* next, int next_step) {
+        u32x4_t av[IM], bv0[JN], bv1[JN];
+        // multiplies av and bv and reads the next fragments into av and bn,
+        // from iteration FIRST on, which between() precedes
+        auto step = [&](const u32x4_t (&bv)[JN], u32x4_t (&bn)[JN], const char* next,
+                        int next_step, auto first, auto between) {
             const typename LA::Place a = pa.again();
             const typename LB::Place b = pb.again();
+            constexpr int FIRST = first();
 #pragma unroll
             for (int i = 0; i < IM; ++i) {
+                if (i == FIRST)
+                    between();
 #pragma unroll
-                for (int j = 0; j < JN; ++j) {
+                for (int j = 0; j < JN; ++j)
                     acc[i][j] = mma<ESIZE>(bv[j], av[i], acc[i][j]);
-                    if (i == IM - 1)
-                        bv[j] = LB::fragment(next + LA::BYTES, b, j, next_step);
-                }
-                av[i] = LA::fragment(next, a, i, next_step);
+#pragma unroll
+                for (int r = i == FIRST ? 0 : i; r <= i && i >= FIRST; ++r)
+                    av[r] = LA::fragment(next, a, r, next_step);
+                if (i == IM - 1)
+#pragma unroll
+                    for (int j = 0; j < JN; ++j)
+                        bn[j] = LB::fragment(next + LA::BYTES, b, j, next_step);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
+        const std::integral_constant<int, 0> at_once{};
+        const std::integral_constant<int, 1> after_one{};
+        const bool early =
+            (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) < WM * WN / 2;
         if (end > whole) {
             stage_barrier();
             multiply(lds1);
@@ -110,21 +122,34 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
             if (s0 + 1 < s1)
                 stage(s0 + 1, lds1);
             stage_barrier();
-            read_all(lds0);
-            step(lds0, 1);
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+                bv0[j] = LB::fragment(lds0 + LA::BYTES, pb, j, 0);
+#pragma unroll
+            for (int i = 0; i < IM; ++i)
+                av[i] = LA::fragment(lds0, pa, i, 0);
+            step(bv0, bv1, lds0, 1, at_once, [] {});
         }
-        // the loop starts at a barrier, where nothing is outstanding
+        // stage s's second step and stage s + 1's first
         for (int64_t s = s0; s + 1 < s1; ++s) {
             char* now = (s - s0) & 1 ? lds1 : lds0;
             char* next = (s - s0) & 1 ? lds0 : lds1;
-            stage_barrier();
-            if (s + 2 < s1)
+            step(bv1, bv0, next, 0, after_one, [&] {
+                stage_barrier();
+                if (early && s + 2 < s1)
+                    stage(s + 2, now);
+            });
+            if (!early && s + 2 < s1)
                 stage(s + 2, now);
-            step(next, 0);
-            step(next, 1);
+            step(bv0, bv1, next, 1, at_once, [] {});
         }
-        if (s0 < s1)
-            step(lds0, 0);                       // (what it reads is not used)
+        if (s0 < s1) {
+#pragma unroll
+            for (int i = 0; i < IM; ++i)
+#pragma unroll
+                for (int j = 0; j < JN; ++j)
+                    acc[i][j] = mma<ESIZE>(bv1[j], av[i], acc[i][j]);
+        }
     } else {
         u32x4_t va[LA::LOADS], vb[LB::LOADS];
         auto fetch = [&](int64_t s) {
