@@ -778,3 +778,29 @@ def test_refusals():
         except (ValueError, TypeError, vpa.VpaError):
             continue
         raise AssertionError(f"call {i} was not refused")
+
+
+@pytest.mark.parametrize("n,k,m", [(1000, 1027, 2100), (2050, 2047, 1030)])
+def test_rows_that_are_not_aligned(n, k, m):
+    """inner is odd: operands are copied to aligned rows, or not, where the
+    caller's rows are aligned already; the results are the same."""
+    g = gen(n + k)
+    x, w = randn(g, n, k, dtype=BF), randn(g, m, k, dtype=BF, scale=k ** -0.5)
+    gr = randn(g, n, m, dtype=BF)
+    pad = -k % 64
+    xa, wa = strided(x, pad), strided(w, pad)
+    z, dz, y, dy = linear_oracle(x, w, None, "silu", gr)
+    got = vpa.head_linear(x, w, None, "silu", gr)
+    near(got, y, dy + half(BF) * (y.abs() + dy), "y")
+    gd, xd, wd = gr.double(), x.double(), w.double()
+    grads = vpa.head_linear_backward(gr, x, w, need_bias=False)[:2]
+    want = gd @ wd
+    tol = (m + 2) * 2 * U * (gd.abs() @ wd.abs())
+    near(grads[0], want, tol + half(BF) * (want.abs() + tol), "grad_x")
+    want = gd.T @ xd
+    tol = (n + 2) * 2 * U * (gd.abs().T @ xd.abs())
+    near(grads[1], want, tol + half(BF) * (want.abs() + tol), "grad_weight")
+    for a, b in ((xa, wa), (x, wa), (xa, w)):
+        near(vpa.head_linear(a, b, None, "silu", gr), y, dy + half(BF) * (y.abs() + dy), "aligned")
+        other = vpa.head_linear_backward(gr, a, b, need_bias=False)[:2]
+        assert all(torch.equal(p, q) for p, q in zip(other, grads))

@@ -34,7 +34,7 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
     LA la;
     LB lb;
     la.init(t.a, AK ? t.a_m : t.a_k, m0, t.m_readable);
-    lb.init(t.b, BK ? t.b_n : t.b_k, n0, t.n);
+    lb.init(t.b, BK ? t.b_n : t.b_k, n0, t.n_readable);
     const int64_t whole = t.k / LA::KB, all = (t.k + LA::KB - 1) / LA::KB;
     const int64_t s0 = slice * stages_per_slice;
     const int64_t end = s0 + stages_per_slice < all ? s0 + stages_per_slice : all;

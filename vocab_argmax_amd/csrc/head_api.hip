@@ -148,26 +148,89 @@ vpa_status check_act(int32_t act) {
     return ok();
 }
 
-// Workspace of the backward pass: dz, the bias sums' slices, the products'.
-struct LinearGradSizes {
-    size_t dz, part, gemm;
-    size_t total() const { return dz + part + gemm; }
-};
-// dz's row stride: rows begin at cache lines, so that both products load them
+// A row stride at which rows begin at cache lines, so that products load them
 // directly, and no load of 64 bytes touches two lines (2048 x 50257 x 2048,
-// dz included: with rows at multiples of 16 bytes the gradient of x takes
+// dz included: with dz's rows at multiples of 16 bytes the gradient of x takes
 // 518 us and the weight's 617, at multiples of 128 bytes 455 and 594).
-int64_t dz_stride(int esize, int64_t outer) {
+int64_t line_stride(int esize, int64_t n) {
     const int64_t vec = 128 / esize;
-    return (outer + vec - 1) / vec * vec;
+    return (n + vec - 1) / vec * vec;
 }
+size_t line_bytes(int esize, int64_t rows, int64_t cols) {
+    return round256((size_t)rows * (size_t)line_stride(esize, cols) * (size_t)esize);
+}
+bool chunk_rows(int esize, const void* p, int64_t ld) {
+    return ld % (16 / esize) == 0 && aligned(p, 16);
+}
+
+// Where inner is no multiple of 16 bytes, contiguous rows of x and weight are
+// not aligned, and the products would load them through registers.  A large
+// bf16 product copies them to aligned rows first: a pass at about 5 TB/s, a
+// launch, against the products' loss, which is 0.6 of the time of the direct
+// product forward and twice it in the backward pass (2048 x 8192 x 4097
+// forward 200 -> 145 us; the gradients of 2048 x 8192 x 2047 239 -> 113 of x,
+// 237 -> 104 of the weight).  fp32
+// products lose less than a copy takes.
+constexpr double kCopyUsAByte = 2.0 / 5e6, kProductUsAFlop = 1 / 1.1e9;
+bool copy_pays(int esize, int64_t elements, double flops, double loss, double launches) {
+    return esize == 2 && loss * flops * kProductUsAFlop >
+                             (double)elements * esize * kCopyUsAByte + 4.0 * launches;
+}
+bool copies_forward(int esize, int64_t rows, int64_t outer, int64_t inner) {
+    return rows > 64 && inner % (16 / esize) != 0 &&
+           copy_pays(esize, (rows + outer) * inner, 2.0 * rows * outer * inner, 0.6, 2);
+}
+bool copies_backward(int esize, int64_t operand_rows, int64_t inner, double flops) {
+    return inner % (16 / esize) != 0 &&
+           copy_pays(esize, operand_rows * inner, flops, 2.0, 1);
+}
+// `p` in rows of line_stride() at `copy`
+hipError_t copy_rows(int esize, const void* p, int64_t ld, int64_t rows, int64_t cols, void* copy,
+                     hipStream_t stream) {
+    DzTask d{};
+    d.grad = p;
+    d.ldg = ld;
+    d.act = VPA_ACT_NONE;
+    d.rows = rows;
+    d.cols = cols;
+    d.dz = copy;
+    d.ldz = line_stride(esize, cols);
+    return launch_dz(esize, d, stream);
+}
+
+// Workspace of the product: copies of x and weight, its slices of k.
+struct LinearSizes {
+    size_t x, w, gemm;
+    size_t total() const { return x + w + gemm; }
+};
+LinearSizes linear_sizes(int esize, int64_t rows, int64_t outer, int64_t inner) {
+    LinearSizes z{};
+    if (copies_forward(esize, rows, outer, inner)) {
+        z.x = line_bytes(esize, rows, inner);
+        z.w = line_bytes(esize, outer, inner);
+    }
+    z.gemm = round256(gemm_workspace(esize, rows, outer, inner, true, true));
+    return z;
+}
+
+// Workspace of the backward pass: dz, the bias sums' slices, copies of weight
+// (for grad_x) and x (for grad_weight), the products'.
+struct LinearGradSizes {
+    size_t dz, part, w, x, gemm;
+    size_t total() const { return dz + part + w + x + gemm; }
+};
 LinearGradSizes linear_grad_sizes(int esize, int64_t rows, int64_t outer, int64_t inner,
                                   bool dz, bool bias, bool gx, bool gw) {
     LinearGradSizes z{};
+    const double flops = 2.0 * rows * outer * inner;
     if (dz && (gx || gw))
-        z.dz = round256((size_t)rows * (size_t)dz_stride(esize, outer) * (size_t)esize);
+        z.dz = line_bytes(esize, rows, outer);
     if (bias)
         z.part = round256((size_t)dz_splits(rows, outer) * (size_t)outer * 4);
+    if (gx && copies_backward(esize, outer, inner, flops))
+        z.w = line_bytes(esize, outer, inner);
+    if (gw && copies_backward(esize, rows, inner, flops))
+        z.x = line_bytes(esize, rows, inner);
     const size_t wx = gx ? gemm_workspace(esize, rows, inner, outer, true, false) : 0;
     const size_t ww = gw ? gemm_workspace(esize, outer, inner, rows, false, false) : 0;
     z.gemm = round256(wx > ww ? wx : ww);
@@ -335,7 +398,7 @@ size_t vpa_head_linear_workspace(vpa_dtype dtype, int64_t rows, int64_t outer, i
     const int esize = esize_of(dtype_value(&dtype));
     if (!esize || rows < 1 || check_sizes("", rows, outer, inner) != VPA_OK)
         return 0;
-    return round256(gemm_workspace(esize, rows, outer, inner, true, true));
+    return linear_sizes(esize, rows, outer, inner).total();
 }
 
 size_t vpa_head_linear_backward_workspace(vpa_dtype dtype, int64_t rows, int64_t outer,
@@ -373,6 +436,8 @@ vpa_status vpa_head_linear(const void* x, int64_t ldx, const void* weight, int64
         return fail(VPA_ERR_INVALID, "y in the residual's place needs its row stride and type");
     if ((st = check_dispatch(gemm_threads(e, rows, outer, inner, true, true),
                              "vpa_head_linear")) != VPA_OK ||
+        (st = check_dispatch(dz_threads(rows > outer ? rows : outer, inner),
+                             "vpa_head_linear")) != VPA_OK ||
         (st = check_workspace("vpa_head_linear", workspace, workspace_bytes,
                               vpa_head_linear_workspace(dtype, rows, outer, inner))) != VPA_OK)
         return st;
@@ -384,7 +449,7 @@ vpa_status vpa_head_linear(const void* x, int64_t ldx, const void* weight, int64
     t.b_n = ldw;
     t.b_k = 1;
     t.m = t.m_readable = rows;
-    t.n = outer;
+    t.n = t.n_readable = outer;
     t.k = inner;
     t.bias = bias;
     t.residual = residual;
@@ -395,8 +460,24 @@ vpa_status vpa_head_linear(const void* x, int64_t ldx, const void* weight, int64
     t.pre = pre;
     t.ldp = ldp;
     t.act = act;
-    t.ws = workspace;
-    hipError_t he = launch_gemm(e, t, (hipStream_t)stream);
+    const LinearSizes z = linear_sizes(e, rows, outer, inner);
+    char* ws = (char*)workspace;
+    hipError_t he;
+    if (z.x && !chunk_rows(e, x, ldx)) {
+        if ((he = copy_rows(e, x, ldx, rows, inner, ws, (hipStream_t)stream)) != hipSuccess)
+            return hip_fail(he, "vpa_head_linear (x) launch");
+        t.a = ws;
+        t.a_m = line_stride(e, inner);
+    }
+    if (z.w && !chunk_rows(e, weight, ldw)) {
+        if ((he = copy_rows(e, weight, ldw, outer, inner, ws + z.x, (hipStream_t)stream)) !=
+            hipSuccess)
+            return hip_fail(he, "vpa_head_linear (weight) launch");
+        t.b = ws + z.x;
+        t.b_n = line_stride(e, inner);
+    }
+    t.ws = ws ? ws + z.x + z.w : nullptr;
+    he = launch_gemm(e, t, (hipStream_t)stream);
     return he == hipSuccess ? ok() : hip_fail(he, "vpa_head_linear launch");
 }
 
@@ -427,7 +508,7 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
         return st;
     // without an activation dz is grad, unless its rows are not aligned: a
     // copy costs one pass over grad, the products' unaligned loads more
-    const bool copy = has_act || ldg % (16 / e) != 0 || !aligned(grad, 16);
+    const bool copy = has_act || !chunk_rows(e, grad, ldg);
     const LinearGradSizes z = linear_grad_sizes(e, rows, outer, inner, copy,
                                                 grad_bias != nullptr, grad_x != nullptr,
                                                 grad_weight != nullptr);
@@ -435,7 +516,9 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
                                         "vpa_head_linear_backward")) != VPA_OK) ||
         (grad_weight && (st = check_dispatch(gemm_threads(e, outer, inner, rows, false, false),
                                              "vpa_head_linear_backward")) != VPA_OK) ||
-        (st = check_dispatch(dz_threads(rows, outer), "vpa_head_linear_backward")) != VPA_OK)
+        (st = check_dispatch(dz_threads(rows, outer), "vpa_head_linear_backward")) != VPA_OK ||
+        (st = check_dispatch(dz_threads(rows > outer ? rows : outer, inner),
+                             "vpa_head_linear_backward")) != VPA_OK)
         return st;
     if (rows > 0 && (st = check_workspace("vpa_head_linear_backward", workspace, workspace_bytes,
                                           z.total())) != VPA_OK)
@@ -455,7 +538,7 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
         d.rows = rows;
         d.cols = outer;
         d.dz = z.dz ? ws : nullptr;
-        d.ldz = dz_stride(e, outer);
+        d.ldz = line_stride(e, outer);
         d.bias = grad_bias;
         // no rows: the sums have no slices, and the finishing kernel writes 0
         d.part = grad_bias && rows > 0 ? (float*)(ws + z.dz) : nullptr;
@@ -466,7 +549,9 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
             lddz = dz_cols = d.ldz;
         }
     }
-    void* gws = ws ? ws + z.dz + z.part : nullptr;
+    char* wcopy = ws + z.dz + z.part;
+    char* xcopy = wcopy + z.w;
+    void* gws = ws ? xcopy + z.x : nullptr;
     if (grad_x && rows > 0) {
         GemmTask t{};
         t.a = dz;
@@ -476,7 +561,13 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
         t.b_n = 1;
         t.b_k = ldw;
         t.m = t.m_readable = rows;
-        t.n = inner;
+        t.n = t.n_readable = inner;
+        if (z.w && !chunk_rows(e, weight, ldw)) {
+            if ((he = copy_rows(e, weight, ldw, outer, inner, wcopy, s)) != hipSuccess)
+                return hip_fail(he, "vpa_head_linear_backward (weight) launch");
+            t.b = wcopy;
+            t.b_k = t.n_readable = line_stride(e, inner);
+        }
         t.k = outer;
         t.y = grad_x;
         t.ldy = ldgx;
@@ -495,7 +586,13 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
         t.b_k = ldx;
         t.m = outer;
         t.m_readable = dz_cols;
-        t.n = inner;
+        t.n = t.n_readable = inner;
+        if (z.x && !chunk_rows(e, x, ldx)) {
+            if ((he = copy_rows(e, x, ldx, rows, inner, xcopy, s)) != hipSuccess)
+                return hip_fail(he, "vpa_head_linear_backward (x) launch");
+            t.b = xcopy;
+            t.b_k = t.n_readable = line_stride(e, inner);
+        }
         t.k = rows;
         t.y = grad_weight;
         t.ldy = ldgw;

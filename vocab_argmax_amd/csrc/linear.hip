@@ -293,7 +293,7 @@ hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream) {
     if (p.rows_kernel)
         return launch_linear_rows(esize, t, stream);
     p.direct = direct_operand(esize, t.a, ak ? t.a_m : t.a_k, ak, t.m_readable) &&
-               direct_operand(esize, t.b, bk ? t.b_n : t.b_k, bk, t.n);
+               direct_operand(esize, t.b, bk ? t.b_n : t.b_k, bk, t.n_readable);
     if (!p.first_m)
         return launch_planned(esize, t, p, stream);
     GemmTask f = t, r = t;                          // the first part and the rest
@@ -305,6 +305,7 @@ hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream) {
     r.m -= dm;
     r.m_readable -= dm;
     r.n -= dn;
+    r.n_readable -= dn;
     r.a = past(t.a, dm * t.a_m * esize);
     r.b = past(t.b, dn * t.b_n * esize);
     r.bias = past(t.bias, dn * esize);

@@ -92,6 +92,7 @@ struct GemmTask {
     int64_t a_m, a_k, b_n, b_k;
     int64_t m, n, k;
     int64_t m_readable;       // columns of A that may be read where a_m is 1 (>= m)
+    int64_t n_readable;       // columns of B that may be read where b_n is 1 (>= n)
     const void* bias;
     const void* residual;
     int64_t ldr;
