@@ -216,7 +216,7 @@ namespace {
 // The best tile and number of slices of k for one launch, and its modelled
 // time in us: rounds of workgroups over the CUs times a stage's time, plus
 // what slices cost to write and join.  The constants are measured (bf16: a
-// 256-tile alone on a CU needs 1.6 us a stage, two 128-tiles on a CU 1.1 us;
+// 256-tile alone on a CU needs 1.5 to 1.6 us a stage, two 128-tiles on a CU 1.1 us;
 // fp32's matrix instructions take 16 times as long for the same k).
 double plan_tiles(int esize, int64_t m, int64_t n, int64_t k, GemmPlan& p) {
     const int64_t stages = stages_of(esize, k);

@@ -2,8 +2,7 @@
 // alternatives, over one or several vocabulary shards, and their gradient.
 //
 // A set of columns is described by a logit M near its maximum and by s = sum
-// 2^z and u = sum z 2^z
-// with z = (x - M) log2(e); two sets join as
+// 2^z and u = sum z 2^z with z = (x - M) log2(e); two sets join as
 //   M = max(Ma, Mb),  s = sum_i s_i 2^di,  u = sum_i (u_i + di s_i) 2^di,
 //   di = (Mi - M) log2(e),
 // so a row is one pass over its columns, cut into chunks that workgroups
@@ -15,6 +14,12 @@
 // Top alternatives carry the argmax order as one 64-bit number, the value's
 // key (vpa_device.h) above the inverted column id: every comparison is one
 // unsigned compare, and no two columns are equal.
+//
+// Large batches are bound by reading the logits once, small ones by the
+// latency of a chunk and of two launches.  Measured, kernels alone: 1024 x
+// 200064 bf16 with 8 alternatives 77 us, 5.3 TB/s; 2048 x 50257 bf16 44 us
+// (4.7; rows that are not aligned); 512 x 50257 fp32 22 + 4 us; 32 x 151936
+// bf16 with 20 alternatives 11.7 + 5.4 us; one row 6.9 + 4.0 us.
 #include "vpa_device.h"
 #include "vpa_head_internal.h"
 #include "vpa_math.h"
@@ -667,7 +672,8 @@ constexpr int kGradVecs = 4;                       // 16-byte vectors a thread
 // A workgroup writes one chunk of a row without the given tokens' own terms,
 // then the few elements that have them, from logits read before the chunk
 // was written (the gradient may replace the logits).  Equal tokens all write
-// the same sum.
+// the same sum.  Bound by memory: 2048 x 50257 bf16 66 us, 6.2 TB/s of reads
+// and writes.
 template <int ESIZE, bool ENTROPY>
 __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradTask t,
                                                                 int32_t chunks) {
