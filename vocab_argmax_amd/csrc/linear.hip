@@ -266,9 +266,12 @@ GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b
             p.rows_kernel = true;
             return p;
         }
-        // workgroups for two a CU, of at least 8 stages
+        // Slices as long as all workgroups run at once, two a CU, and have at
+        // least 8 stages (32 x 4096 x 32000 bf16, 500 tiles: 59 us in 2 slices,
+        // 44 in one; 32 x 4096 x 25600 51 and 41; 32 x 4096 x 11008, 172 tiles:
+        // 26.6 in 3, 26.1 in 2).
         p.tile = m <= 32 ? 32 : 64;
-        int64_t s = (512 + tiles - 1) / tiles;
+        int64_t s = 512 / tiles;
         s = s > stages / 8 ? stages / 8 : s;
         s = s < 1 ? 1 : s;
         p.stages_per_slice = (stages + s - 1) / s;
