@@ -804,3 +804,60 @@ def test_rows_that_are_not_aligned(n, k, m):
         near(vpa.head_linear(a, b, None, "silu", gr), y, dy + half(BF) * (y.abs() + dy), "aligned")
         other = vpa.head_linear_backward(gr, a, b, need_bias=False)[:2]
         assert all(torch.equal(p, q) for p, q in zip(other, grads))
+
+
+def test_product_offsets_past_32_bits():
+    """Logits, their gradient and a weight of more than 2^32 bytes."""
+    n, k, m = 11000, 64, 200064                          # 2.2e9 logits, 4.4 GB
+    g = gen(21)
+    x, w = randn(g, n, k, dtype=BF), randn(g, m, k, dtype=BF, scale=k ** -0.5)
+    rows = torch.tensor([0, 5367, 5368, 10735, n - 1], device=DEV)
+    y = vpa.head_linear(x, w)
+    _, _, want, dy = linear_oracle(x[rows], w, None, "none", None)
+    near(y[rows], want, dy + half(BF) * (want.abs() + dy), "rows of logits")
+    cols = torch.tensor([0, 1, 99999, m - 1], device=DEV)
+    _, _, want, dy = linear_oracle(x, w[cols], None, "none", None)
+    near(y[:, cols], want, dy + half(BF) * (want.abs() + dy), "columns of logits")
+    gx, gw, gb = vpa.head_linear_backward(y, x, w)
+    gd = y[rows].double()
+    want = gd @ w.double()
+    tol = (m + 2) * 2 * U * (gd.abs() @ w.double().abs())
+    near(gx[rows], want, tol + half(BF) * (want.abs() + tol), "grad_x")
+    gd = y[:, cols].double()
+    want = gd.T @ x.double()
+    tol = (n + 2) * 2 * U * (gd.abs().T @ x.double().abs())
+    near(gw[cols], want, tol + half(BF) * (want.abs() + tol), "grad_weight")
+    want = gd.sum(0)
+    tol = (n + 2) * U * gd.abs().sum(0)
+    near(gb[cols], want, tol + half(BF) * (want.abs() + tol), "grad_bias")
+    del y, gx, gw
+    k, m = 16384, 140000                                 # a weight of 2.3e9 elements
+    w = torch.empty((m, k), dtype=BF, device=DEV)
+    for part in w.split(20000):
+        part.copy_(randn(g, *part.shape, dtype=BF, scale=k ** -0.5))
+    cols = torch.tensor([0, 65535, 131072, 131073, m - 1], device=DEV)
+    for n in (3, 40, 300):
+        x = randn(g, n, k, dtype=BF)
+        _, _, want, dy = linear_oracle(x, w[cols], None, "none", None)
+        near(vpa.head_linear(x, w)[:, cols], want, dy + half(BF) * (want.abs() + dy), f"{n} rows")
+
+
+def test_norm_offsets_past_32_bits():
+    n, c = 540000, 4096                                  # 2.2e9 elements, 4.4 GB
+    g = gen(22)
+    x = torch.zeros((n, c), dtype=BF, device=DEV)
+    rows = torch.tensor([0, 524287, 524288, n - 1], device=DEV)
+    vals = randn(g, 4, c, dtype=BF)
+    x[rows] = vals
+    w, b = randn(g, c), randn(g, c)
+    y, mean, rstd = vpa.layer_norm(x, w, b, with_stats=True)
+    want = vpa.layer_norm(vals, w, b, with_stats=True)
+    for got, exp in ((y, want[0]), (mean, want[1]), (rstd, want[2])):
+        assert torch.equal(got[rows], exp)
+    gx, gw, gb = vpa.layer_norm_backward(x, x, mean, rstd, w)
+    sx, sw, sb = vpa.layer_norm_backward(vals, vals, want[1], want[2], w)
+    assert torch.equal(gx[rows], sx)
+    # the other rows' gradients are 0, so the column sums are of the 4 rows
+    near(gw, sw.double(), 8 * U * (vals.double().abs() * ((vals.double() - want[1][:, None].double())
+                                   * want[2][:, None].double()).abs()).sum(0), "grad_weight")
+    near(gb, sb.double(), 8 * U * vals.double().abs().sum(0), "grad_bias")
