@@ -86,10 +86,14 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
         // half a stage later the others, since a wavefront that issues them is
         // held up by the 64 bytes a clock that the loads can be taken in
         // (8192^3 800 us with all loads and the barrier before a step, 790
-        // with halves, 775 so; 679 by the library on the same card).
+        // with halves, 775 so; 679 by the library on the same card).  A
+        // wavefront that issues loads gives way to the other one on its SIMD
+        // until it has done its first products after the next barrier (757 ->
+        // 747 us on a card where the library needs 672).
         const typename LA::Direct da = la.direct();
         const typename LB::Direct db = lb.direct();
         auto stage = [&](int64_t s, char* lds) {
+            __builtin_amdgcn_s_setprio(0);
             la.load(da, s, lds);
             lb.load(db, s, lds + LA::BYTES);
         };
@@ -108,6 +112,8 @@ __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint
 #pragma unroll
                 for (int j = 0; j < JN; ++j)
                     acc[i][j] = mma<ESIZE>(bv[j], av[i], acc[i][j]);
+                if (i == FIRST)
+                    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int r = i == FIRST ? 0 : i; r <= i && i >= FIRST; ++r)
                     av[r] = LA::fragment(next, a, r, next_step);
