@@ -9,7 +9,7 @@
 // the chip with wavefronts, KS wavefronts of a workgroup split the k of one
 // block of rows and join their sums in LDS, in order: one launch, no
 // workspace.  1 x 4096 x 4096 bf16 8.2 us, 4.1 TB/s (a launch of this size
-// alone takes about 3); with rows at 2 bytes past an aligned address 16.
+// alone takes about 3); with rows at 16 bytes past a line 14, at 2 bytes 16.
 #include <type_traits>
 
 #include "gemm_tile.h"
@@ -43,7 +43,10 @@ __global__ __launch_bounds__(WAVES * 64) void linear_rows_kernel(GemmTask t, int
     constexpr int KB = 128 / ESIZE;                 // k of a step: 128 bytes of a row
     constexpr int VEC = 16 / ESIZE;
     __shared__ f32x4 sums[WAVES][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // The wavefront's number as a scalar: what depends on it has to be branched
+    // over, not masked, since a matrix instruction ignores the mask.
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t block = (int64_t)blockIdx.x * (WAVES / ks) + wave / ks;
     const int share = wave % ks;
     const int64_t n0 = block * 16;
