@@ -262,7 +262,10 @@ GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b
     p.stages_per_slice = stages;
     if (a_k1 && b_k1 && m <= 64) {
         const int64_t tiles = (n + kFewRowsCols - 1) / kFewRowsCols;
-        if (m <= kRowsKernelMost && tiles < 512) {
+        // Wavefronts alone while the ring's tiles do not give every CU one
+        // (K = 4096, 8 rows: n = 8192 17 us against 20 for the ring, 16384 39
+        // and 33, 32000 68 and 44).
+        if (m <= kRowsKernelMost && tiles < 256) {
             p.rows_kernel = true;
             return p;
         }

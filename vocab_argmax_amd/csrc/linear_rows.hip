@@ -5,10 +5,9 @@
 // reading W once from memory.  A wavefront takes 16 rows of W and a
 // share of k; W goes straight from memory into the matrix instruction's
 // operand registers, D steps of 128 bytes a row at a time, and x, which all
-// wavefronts share, comes from the caches.  Where W has too few rows to fill
-// the chip with wavefronts, KS wavefronts of a workgroup split the k of one
-// block of rows and join their sums in LDS, in order: one launch, no
-// workspace.  1 x 4096 x 4096 bf16 8.2 us, 4.1 TB/s (a launch of this size
+// wavefronts share, comes from the caches.  The WAVES wavefronts of a
+// workgroup split the k of one block of rows and join their sums in LDS, in
+// order: one launch, no workspace.  1 x 4096 x 4096 bf16 8.2 us, 4.1 TB/s (a launch of this size
 // alone takes about 3); with rows at 16 bytes past a line 14, at 2 bytes 16.
 #include <type_traits>
 
@@ -38,7 +37,7 @@ __device__ __forceinline__ u32x4_t load16(const char* p, int64_t e, int64_t n) {
 }
 
 template <int ESIZE, int D, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void linear_rows_kernel(GemmTask t, int32_t ks) {
+__global__ __launch_bounds__(WAVES * 64) void linear_rows_kernel(GemmTask t) {
     using T = typename elem<ESIZE>::type;
     constexpr int KB = 128 / ESIZE;                 // k of a step: 128 bytes of a row
     constexpr int VEC = 16 / ESIZE;
@@ -47,9 +46,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_rows_kernel(GemmTask t, int
     // over, not masked, since a matrix instruction ignores the mask.
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t block = (int64_t)blockIdx.x * (WAVES / ks) + wave / ks;
-    const int share = wave % ks;
-    const int64_t n0 = block * 16;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int r = lane & 15, q = lane >> 4;
     // rows past the end repeat the last one: their sums are not stored
     const char* w = (const char*)t.b + (n0 + r < t.n ? n0 + r : t.n - 1) * t.b_n * ESIZE;
@@ -75,70 +72,52 @@ __global__ __launch_bounds__(WAVES * 64) void linear_rows_kernel(GemmTask t, int
             for (int h = 0; h < 2; ++h)
                 acc = mma<ESIZE>(wv[d][h], xv[d][h], acc);
     };
-    if (n0 < t.n) {
-        const int64_t batches = whole / D;
-        for (int64_t b = share; b < batches; b += ks)
-            run(b * D, std::integral_constant<int, D>{});
-        for (int64_t s = batches * D + share; s < whole; s += ks)
-            run(s, std::integral_constant<int, 1>{});
-        if (whole < steps && share == ks - 1) {
+    const int64_t batches = whole / D;
+    for (int64_t b = wave; b < batches; b += WAVES)
+        run(b * D, std::integral_constant<int, D>{});
+    for (int64_t s = batches * D + wave; s < whole; s += WAVES)
+        run(s, std::integral_constant<int, 1>{});
+    if (whole < steps && wave == WAVES - 1) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t e = whole * KB + (h * 4 + q) * VEC;
-                acc = mma<ESIZE>(load16<ESIZE>(w, e, t.k), load16<ESIZE>(x, e, t.k), acc);
-            }
+        for (int h = 0; h < 2; ++h) {
+            const int64_t e = whole * KB + (h * 4 + q) * VEC;
+            acc = mma<ESIZE>(load16<ESIZE>(w, e, t.k), load16<ESIZE>(x, e, t.k), acc);
         }
     }
     sums[wave][lane] = acc;
     __syncthreads();
-    // results of the workgroup's blocks, n fastest; in a block n is (lane /
-    // 16) * 4 + e and m is lane % 16
-    const int blocks = WAVES / ks;
-    for (int id = threadIdx.x; id < blocks * 256; id += WAVES * 64) {
-        const int b = id / 256, m = id % 256 / 16, n = id % 16;
-        const int64_t col = ((int64_t)blockIdx.x * blocks + b) * 16 + n;
-        if (m >= t.m || col >= t.n)
-            continue;
-        const int at = m + (n >> 2) * 16;
-        float v = sums[b * ks][at][n & 3];
-        for (int s = 1; s < ks; ++s)
-            v += sums[b * ks + s][at][n & 3];
-        store_result<T>(t, m, col, v);
-    }
+    // n fastest; in a block n is (lane / 16) * 4 + e and m is lane % 16
+    const int m = threadIdx.x / 16, n = threadIdx.x % 16;
+    if (m >= t.m || n0 + n >= t.n)
+        return;
+    const int at = m + (n >> 2) * 16;
+    float v = sums[0][at][n & 3];
+#pragma unroll
+    for (int s = 1; s < WAVES; ++s)
+        v += sums[s][at][n & 3];
+    store_result<T>(t, m, n0 + n, v);
 }
 
-// Wavefronts that share a block's k, until there are 8 wavefronts a CU, and
-// wavefronts of a workgroup.
-struct RowsPlan {
-    int32_t ks, waves;
-    int64_t groups;
-};
-RowsPlan plan_rows(int64_t n) {
-    RowsPlan p;
-    const int64_t blocks = (n + 15) / 16;
-    p.ks = 1;
-    while (p.ks < 8 && blocks * p.ks < 2048)
-        p.ks *= 2;
-    p.waves = p.ks < 4 ? 4 : p.ks;
-    const int64_t per = p.waves / p.ks;
-    p.groups = (blocks + per - 1) / per;
-    return p;
+// 8 wavefronts a workgroup while each has a CU to itself, which its registers
+// allow, else 4 (K = 4096, one row: n = 4800 14.6 us with 8, 14.4 with 4; 4112
+// of K = 1600 8.9 and 7.6; 4096 of K = 4096 9.3 with 8).
+int rows_waves(int64_t n) {
+    return n <= 16 * 256 ? 8 : 4;
 }
 
 template <int ESIZE>
 hipError_t launch_rows(const GemmTask& t, hipStream_t stream) {
     constexpr int D = 8;
-    const RowsPlan p = plan_rows(t.n);
-    const dim3 grid((uint32_t)p.groups), block(p.waves * 64);
-    return p.waves == 8 ? launch(linear_rows_kernel<ESIZE, D, 8>, grid, block, 0, stream, t, p.ks)
-                        : launch(linear_rows_kernel<ESIZE, D, 4>, grid, block, 0, stream, t, p.ks);
+    const int waves = rows_waves(t.n);
+    const dim3 grid((uint32_t)((t.n + 15) / 16)), block((uint32_t)waves * 64);
+    return waves == 8 ? launch(linear_rows_kernel<ESIZE, D, 8>, grid, block, 0, stream, t)
+                      : launch(linear_rows_kernel<ESIZE, D, 4>, grid, block, 0, stream, t);
 }
 
 }  // namespace
 
 int64_t linear_rows_threads(int64_t n) {
-    const RowsPlan p = plan_rows(n);
-    return p.groups * p.waves * 64;
+    return (n + 15) / 16 * rows_waves(n) * 64;
 }
 
 hipError_t launch_linear_rows(int esize, const GemmTask& t, hipStream_t stream) {
