@@ -14,15 +14,16 @@ namespace {
 // accumulators.  With part set, the raw sums of a slice of k go to
 // part[slice][m][n].
 //
-// Bound by the matrix cores, which are busy for 66 % of the clocks of 8192^3
-// bf16 (778 us, 1413 TFLOP/s at the 2.0 GHz that the card holds; 698 us by the
-// library in turn with it); 4096^3 110 us, with bias, silu and a residual 123.
+// Bound by the matrix cores and the card's power: they are busy for 74 % of the
+// clocks of 8192^3 bf16 (747 us, 1472 TFLOP/s, at the 1.9 GHz that the card
+// then holds; at 66 % it held 2.0; 672 us by the library in turn with it);
+// 4096^3 104 us, with bias, silu and a residual 123.
 // A 256-tile needs 32 KiB of each operand a stage, so that two stages fill
 // 128 of 160 KiB of LDS, and reads 24 KiB of LDS a wavefront and stage; a
 // 256-tile of 4 wavefronts spills (729 TFLOP/s); 128-tiles need 2.2 us for the
 // area and k that a 256-tile takes 1.5 for, but fill the chip with small
-// products.  fp32: 4096^3 949 us, 145
-// TFLOP/s, 96 % of the library's, at the rate of fp32's matrix instruction.
+// products.  fp32: 4096^3 957 us, 144 TFLOP/s, 96 % of the library's, at the
+// rate of fp32's matrix instruction.
 template <int ESIZE, bool AK, bool BK, bool DIRECT, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64) void gemm_tile_kernel(GemmTask t, uint32_t tiles_m,
                                                                 uint32_t tiles_n,
