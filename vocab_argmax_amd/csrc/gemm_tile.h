@@ -60,6 +60,7 @@ struct TileLoader {
     const char* base;            // the tile's first row at k = 0
     int64_t ld;                  // bytes from LDS row to LDS row
     int32_t left;                // rows of the operand from the tile's first (at most ROWS)
+    bool narrow;                 // rows contiguous, and fewer than a chunk
 
     static __device__ __forceinline__ int swizzle(int k) {
         constexpr int n = ROWS * ESIZE / 32;            // 32-byte chunks of a row
@@ -92,6 +93,7 @@ struct TileLoader {
         base = (const char*)p + (K1 ? row0 * stride : row0) * ESIZE;
         ld = stride * ESIZE;
         left = rows - row0 < ROWS ? (int32_t)(rows - row0) : ROWS;
+        narrow = !K1 && rows < VEC;
     }
     __device__ __forceinline__ const char* at_stage(int64_t stage) const {
         return base + stage * (K1 ? 128 : KB * ld);
@@ -162,16 +164,54 @@ struct TileLoader {
                 u.e[e] = ((const T*)p)[e];
         return u.v;
     }
-    // the stage that k ends in: 0 past k
+    // v without its first n elements, 0 after the others (n >= 0)
+    static __device__ __forceinline__ u32x4_t moved_down(u32x4_t v, int n) {
+        const uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+        const int bits = n < VEC ? n * ESIZE * 8 : 128, in = bits & 63;
+        const uint64_t both = lo >> in | (hi << 1) << (63 - in);
+        const uint64_t l = bits < 64 ? both : bits < 128 ? hi >> in : 0;
+        const uint64_t h = bits < 64 ? hi >> in : 0;
+        return u32x4_t{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+    }
+    // The stage that k ends in: 0 past k, and past the operand's contiguous
+    // rows.  A chunk that reaches past an end is the one that stops there,
+    // moved down, so that all loads are under way before the first is waited
+    // for (464 x 785 x 10240 bf16 element by element 47 us, 41 so); what has
+    // fewer elements than a chunk goes one by one.
     __device__ __forceinline__ void load_tail(int64_t stage, int64_t k, char* lds) const {
-        const char* p = at_stage(stage);
-        const int k_left = (int)(k - stage * KB);
+        if (narrow || (K1 && k < VEC)) {
+            const char* p = at_stage(stage);
+            const int k_left = (int)(k - stage * KB);
 #pragma unroll 1
+            for (int i = 0; i < LOADS; ++i) {
+                const int r = lds_row(i), e = element(r, position());
+                const int n = K1 ? k_left - e : (r < k_left ? left - e : 0);
+                *(u32x4_t*)(lds + (i * NT + threadIdx.x) * 16) = part(p + offset(i), n);
+            }
+            return;
+        }
+        u32x4_t v[LOADS];
+        int skip[LOADS];
+#pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int r = lds_row(i), e = element(r, position());
-            const int n = K1 ? k_left - e : (r < k_left ? left - e : 0);
-            *(u32x4_t*)(lds + (i * NT + threadIdx.x) * 16) = part(p + offset(i), n);
+            int64_t row, at;                        // of the chunk that is loaded
+            if constexpr (K1) {
+                const int64_t want = stage * KB + e;
+                at = want < k - VEC ? want : k - VEC;
+                skip[i] = (int)(want - at);
+                row = r < left ? r : left - 1;
+            } else {
+                const int64_t want = stage * KB + r;
+                at = e < left - VEC ? e : left - VEC;
+                skip[i] = want < k ? (int)(e - at) : VEC;
+                row = want < k ? want : k - 1;
+            }
+            v[i] = ((const Loose16*)(base + row * ld + at * ESIZE))->v;
         }
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            *(u32x4_t*)(lds + (i * NT + threadIdx.x) * 16) = moved_down(v[i], skip[i]);
     }
     // Fragments: 16 rows, 64 bytes of k (step 0 or 1 of a stage).  A lane's
     // LDS address is worked out once for the wavefront's first row (a multiple
