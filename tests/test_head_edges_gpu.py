@@ -1,0 +1,46 @@
+"""GPU tests of the head's operators where a size, a mask or a range of values
+ends: thin operands, state carried from chunk to chunk of a long row, very
+confident rows, many short rows.  Tolerances as in test_head_gpu.py: half(t) is
+half a step of type t, U is fp32's, a sum of n terms is off by n U sum |terms|,
+2 U a term on the matrix cores."""
+import math
+
+import pytest
+import torch
+
+import vocab_argmax_amd as vpa
+from test_head_gpu import (ACT, BF, DEV, F32, NEG, U, gen, half, linear_oracle, near, randn, slope)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("n,m,k", [  # rows, outer, inner
+    (40, 50257, 1), (64, 32000, 1), (17, 2000, 2), (1, 513, 1), (40, 1, 5025), (300, 1, 1),
+    (33, 3, 3), (64, 2, 4097), (129, 513, 1)])
+def test_products_of_thin_operands(n, m, k, act, dtype):
+    """Forward and backward within a workspace that ends where it has to."""
+    g = gen(n + 31 * k + 7 * m)
+    x, w = randn(g, n, k, dtype=dtype), randn(g, m, k, dtype=dtype, scale=k ** -0.5)
+    b, gr = randn(g, m, dtype=dtype), randn(g, n, m, dtype=dtype)
+    z, dz, y, dy = linear_oracle(x, w, b, act, gr)
+    got, pre = vpa.head_linear(x, w, b, act, gr, with_pre=True)
+    near(got, y, dy + half(dtype) * (y.abs() + dy), "y")
+    d = gr.double() * slope(act, pre.double())
+    off = 0 * d if act == "none" else gr.double().abs() * 16 * U * (1 + pre.double().abs())
+    rounded = off if act == "none" else off + half(dtype) * (d.abs() + off)
+    code = vpa.VPA_BF16 if dtype is BF else vpa.VPA_F32
+    need = vpa.head_lib().vpa_head_linear_backward_workspace(code, n, m, k)
+    buf = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device=DEV)
+    gx, gw, gb = vpa.head_linear_backward(gr, x, w, pre, act, workspace=buf[:need])
+    assert bool((buf[need:] == 0xA5).all()), "written past the workspace"
+    want = d @ w.double()
+    tol = rounded @ w.double().abs() + (m + 2) * 2 * U * (d.abs() @ w.double().abs())
+    near(gx, want, tol + half(dtype) * (want.abs() + tol), "grad_x")
+    want = d.T @ x.double()
+    tol = rounded.T @ x.double().abs() + (n + 2) * 2 * U * (d.T.abs() @ x.double().abs())
+    near(gw, want, tol + half(dtype) * (want.abs() + tol), "grad_weight")
+    want = d.sum(0)
+    tol = off.sum(0) + (n + 2) * U * d.abs().sum(0)
+    near(gb, want, tol + half(dtype) * (want.abs() + tol), "grad_bias")

@@ -1,0 +1,117 @@
+"""What the head operators launch, on the CPU: a preloaded library
+(launch_record.cc) takes the place of the HIP runtime's kernel launch and
+writes each one down, so that the sizes of a launch and the part of the
+workspace that its arguments give it can be compared with what the call
+checked and asked for.  Pointers passed here are never dereferenced."""
+import json
+import os
+import shutil
+import subprocess
+import sys
+
+import pytest
+
+from vocab_argmax_amd import _build
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(HERE)
+
+# Runs `calls` (name, arguments) with recorded launches -> one list per call:
+# [status, message, launches].
+CHILD = """
+import ctypes, json, sys
+import vocab_argmax_amd as vpa
+here = ctypes.CDLL(None)
+class Launch(ctypes.Structure):
+    _fields_ = [("name", ctypes.c_char * 192), ("grid", ctypes.c_uint32 * 3),
+                ("block", ctypes.c_uint32 * 3), ("m", ctypes.c_int64), ("n", ctypes.c_int64),
+                ("k", ctypes.c_int64), ("slices", ctypes.c_int64), ("part", ctypes.c_uint64),
+                ("part_bytes", ctypes.c_int64)]
+here.launches_get.restype = ctypes.POINTER(Launch)
+lib = vpa.head_lib()
+out = []
+for name, args in json.load(sys.stdin):
+    here.launches_clear()
+    args = [vpa.Vocab(*a) if isinstance(a, list) else a for a in args]
+    r = getattr(lib, name)(*args)
+    got = []
+    for i in range(here.launches_count()):
+        l = here.launches_get(i).contents
+        got.append(dict(name=l.name.decode(), grid=list(l.grid), block=list(l.block), m=l.m, n=l.n,
+                        k=l.k, slices=l.slices, part=l.part, part_bytes=l.part_bytes))
+    out.append([r, vpa.last_error() if r else "", got])
+json.dump(out, sys.stdout)
+"""
+
+P = 0x7F0000010000          # aligned, never dereferenced
+WS = 0x7E0000000000
+F32, BF16 = 0, 1
+OK = 0
+
+
+@pytest.fixture(scope="module")
+def record(tmp_path_factory):
+    if not shutil.which("g++"):
+        pytest.skip("no host C++ compiler")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    so = str(tmp_path_factory.mktemp("record") / "launch_record.so")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-D__HIP_PLATFORM_AMD__",
+                    f"-I{rocm}/include", f"-I{_build.INCLUDE}", f"-I{_build.CSRC}",
+                    os.path.join(HERE, "launch_record.cc"), "-ldl", "-o", so], check=True)
+
+    def run(calls):
+        env = dict(os.environ, LD_PRELOAD=so,
+                   PYTHONPATH=os.pathsep.join([ROOT, os.environ.get("PYTHONPATH", "")]))
+        res = subprocess.run([sys.executable, "-c", CHILD], input=json.dumps(calls), text=True,
+                             capture_output=True, env=env, timeout=600)
+        assert res.returncode == 0, res.stderr[-4000:]
+        return json.loads(res.stdout)
+    return run
+
+
+def linear(rows, outer, inner, dt=BF16, ws_bytes=0, act=0, ldx=None, ldw=None):
+    return ["vpa_head_linear", [P, ldx or inner, P, ldw or inner, None, None, 0, dt, rows, outer,
+                                inner, act, P, outer, dt, None, 0, WS, ws_bytes, None]]
+
+
+def linear_backward(rows, outer, inner, dt=BF16, ws_bytes=0, act=0, ldg=None, ldx=None, ldw=None,
+                    need="xwb"):
+    return ["vpa_head_linear_backward",
+            [P, ldg or outer, P, ldx or inner, P, ldw or inner, P, outer, dt, rows, outer, inner,
+             act, P if "x" in need else None, inner, P if "w" in need else None, inner,
+             P if "b" in need else None, WS, ws_bytes, None]]
+
+
+def work_items(launch):
+    n = 1
+    for g, b in zip(launch["grid"], launch["block"]):
+        n *= g * b
+    return n
+
+
+def products_within(record, sizes, make, workspace):
+    """Every launch of each size's call keeps to the workspace it was given,
+    the size that the library itself asks for."""
+    need = record([[workspace, [dt, *size]] for size, dt in sizes])
+    calls = [make(*size, dt=dt, ws_bytes=n[0], act=act)
+             for (size, dt), n in zip(sizes, need) for act in (0, 3)]
+    for call, (status, message, got) in zip(calls, record(calls)):
+        given = call[1][-2]
+        assert status == OK, (call, message)
+        assert got, call
+        for l in got:
+            assert l["part_bytes"] == 0 or (
+                l["part"] >= WS and l["part"] + l["part_bytes"] <= WS + given), (call, l)
+
+
+THIN = [((rows, outer, inner), dt)
+        for dt in (BF16, F32) for rows in (1, 16, 17, 32, 33, 40, 64, 65, 300)
+        for outer in (1, 2, 3, 8, 513, 32000, 50257, 151936)
+        for inner in (1, 2, 3, 8, 513, 50257) if outer * inner < 1 << 28]
+
+
+def test_products_of_thin_operands_keep_to_their_workspace(record):
+    """A weight or x of one column has a stride of 1 both ways: its layout, and
+    with it the slices of the product, is not to be read from the strides."""
+    products_within(record, THIN, linear_backward, "vpa_head_linear_backward_workspace")
+    products_within(record, THIN, linear, "vpa_head_linear_workspace")

@@ -368,10 +368,10 @@ hipError_t launch_layout(const GemmTask& t, const GemmPlan& p, hipStream_t strea
 
 template <int ESIZE>
 hipError_t launch_tiles(const GemmTask& t, const GemmPlan& p, hipStream_t stream) {
-    if (t.a_k != 1)
+    if (!t.a_k1)
         return launch_layout<ESIZE, false, false>(t, p, stream);
-    return t.b_k != 1 ? launch_layout<ESIZE, true, false>(t, p, stream)
-                      : launch_layout<ESIZE, true, true>(t, p, stream);
+    return t.b_k1 ? launch_layout<ESIZE, true, true>(t, p, stream)
+                  : launch_layout<ESIZE, true, false>(t, p, stream);
 }
 
 }  // namespace

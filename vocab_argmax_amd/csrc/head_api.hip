@@ -448,6 +448,7 @@ vpa_status vpa_head_linear(const void* x, int64_t ldx, const void* weight, int64
     t.b = weight;
     t.b_n = ldw;
     t.b_k = 1;
+    t.a_k1 = t.b_k1 = true;
     t.m = t.m_readable = rows;
     t.n = t.n_readable = outer;
     t.k = inner;
@@ -560,6 +561,7 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
         t.b = weight;
         t.b_n = 1;
         t.b_k = ldw;
+        t.a_k1 = true;
         t.m = t.m_readable = rows;
         t.n = t.n_readable = inner;
         if (z.w && !chunk_rows(e, weight, ldw)) {

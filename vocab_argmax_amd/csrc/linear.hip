@@ -349,7 +349,7 @@ hipError_t launch_planned(int esize, const GemmTask& t, const GemmPlan& p, hipSt
 }  // namespace
 
 hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream) {
-    const bool ak = t.a_k == 1, bk = t.b_k == 1;
+    const bool ak = t.a_k1, bk = t.b_k1;
     GemmPlan p = plan_gemm(esize, t.m, t.n, t.k, ak, bk);
     if (p.rows_kernel)
         return launch_linear_rows(esize, t, stream);

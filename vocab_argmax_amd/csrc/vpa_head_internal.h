@@ -85,14 +85,17 @@ hipError_t launch_logprob_grad(int esize, const LogprobGradTask& t, hipStream_t 
 // C[m][n] = sum_k A(m, k) B(n, k), A(m, k) = a[m*a_m + k*a_k] (one of the two
 // strides is 1), B alike, then the epilogue y = residual + act(C + bias[n]).
 // The layouts used: k contiguous in both (a product with a weight), in A
-// alone (grad_x) and in neither (grad_weight).
+// alone (grad_x) and in neither (grad_weight).  The caller names the layout:
+// strides do not tell it (a matrix of one column has 1 both ways), and the
+// workspace was sized for it.
 struct GemmTask {
     const void* a;
     const void* b;
     int64_t a_m, a_k, b_n, b_k;
+    bool a_k1, b_k1;          // k is contiguous in A, in B
     int64_t m, n, k;
-    int64_t m_readable;       // columns of A that may be read where a_m is 1 (>= m)
-    int64_t n_readable;       // columns of B that may be read where b_n is 1 (>= n)
+    int64_t m_readable;       // columns of A that may be read where k is not contiguous (>= m)
+    int64_t n_readable;       // columns of B, alike (>= n)
     const void* bias;
     const void* residual;
     int64_t ldr;
