@@ -115,3 +115,42 @@ def test_products_of_thin_operands_keep_to_their_workspace(record):
     with it the slices of the product, is not to be read from the strides."""
     products_within(record, THIN, linear_backward, "vpa_head_linear_backward_workspace")
     products_within(record, THIN, linear, "vpa_head_linear_workspace")
+
+
+MOST_ITEMS = (1 << 32) - 1  # of one dispatch
+HUGE = 1 << 50
+
+
+def test_large_products_are_not_refused(record):
+    """Scoring and training batches of a wide vocabulary, two-launch plans
+    among them: every launch fits a dispatch, so every call is taken."""
+    calls = [make(rows, outer, inner, dt=dt, ws_bytes=HUGE)
+             for rows in (16, 64, 4096, 65536, 90000, 131072, 1 << 20) for outer in (50257, 200064)
+             for inner in (64, 2047, 2048) for dt in (BF16, F32)
+             for make in (linear, linear_backward)]
+    calls += [linear(40, 1 << 28, 64, ws_bytes=HUGE), linear(40, 64, 1 << 28, ws_bytes=HUGE)]
+    for call, (status, message, got) in zip(calls, record(calls)):
+        assert status == OK, (call, message)
+        assert max(map(work_items, got)) <= MOST_ITEMS, call
+
+
+def test_products_beyond_a_dispatch_are_refused(record):
+    """A call is refused exactly where one of its launches would not fit."""
+    edge = 1 << 30                      # columns: a workgroup of 256 takes 64 of them
+    calls = [linear(40, edge - 64, 8, ws_bytes=HUGE), linear(40, edge, 8, ws_bytes=HUGE),
+             linear(16, edge - 64, 8, ws_bytes=HUGE), linear(16, edge, 8, ws_bytes=HUGE),
+             linear(1 << 21, 1 << 16, 64, ws_bytes=HUGE), linear(1 << 23, 1 << 16, 64, ws_bytes=HUGE)]
+    for i, (call, (status, message, got)) in enumerate(zip(calls, record(calls))):
+        if i % 2:
+            assert status != OK and "exceed one dispatch" in message and not got, (call, got)
+        else:
+            assert status == OK and max(map(work_items, got)) <= MOST_ITEMS, (call, message, got)
+
+
+ORDINARY = [((rows, outer, inner), dt) for dt in (BF16, F32) for rows in (1, 24, 130, 2048, 4340)
+            for outer in (96, 4090, 8192, 50257) for inner in (200, 4088, 8192)]
+
+
+def test_ordinary_products_keep_to_their_workspace(record):
+    products_within(record, ORDINARY, linear_backward, "vpa_head_linear_backward_workspace")
+    products_within(record, ORDINARY, linear, "vpa_head_linear_workspace")

@@ -434,12 +434,12 @@ vpa_status vpa_head_linear(const void* x, int64_t ldx, const void* weight, int64
         return st;
     if (residual == y && residual && (ldr != ldy || odt != dt))
         return fail(VPA_ERR_INVALID, "y in the residual's place needs its row stride and type");
+    const LinearSizes z = linear_sizes(e, rows, outer, inner);
     if ((st = check_dispatch(gemm_threads(e, rows, outer, inner, true, true),
                              "vpa_head_linear")) != VPA_OK ||
-        (st = check_dispatch(dz_threads(rows > outer ? rows : outer, inner),
-                             "vpa_head_linear")) != VPA_OK ||
-        (st = check_workspace("vpa_head_linear", workspace, workspace_bytes,
-                              vpa_head_linear_workspace(dtype, rows, outer, inner))) != VPA_OK)
+        (z.x && (st = check_dispatch(dz_threads(rows > outer ? rows : outer, inner, false),
+                                     "vpa_head_linear")) != VPA_OK) ||
+        (st = check_workspace("vpa_head_linear", workspace, workspace_bytes, z.total())) != VPA_OK)
         return st;
     GemmTask t{};
     t.a = x;
@@ -461,7 +461,6 @@ vpa_status vpa_head_linear(const void* x, int64_t ldx, const void* weight, int64
     t.pre = pre;
     t.ldp = ldp;
     t.act = act;
-    const LinearSizes z = linear_sizes(e, rows, outer, inner);
     char* ws = (char*)workspace;
     hipError_t he;
     if (z.x && !chunk_rows(e, x, ldx)) {
@@ -517,9 +516,11 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
                                         "vpa_head_linear_backward")) != VPA_OK) ||
         (grad_weight && (st = check_dispatch(gemm_threads(e, outer, inner, rows, false, false),
                                              "vpa_head_linear_backward")) != VPA_OK) ||
-        (st = check_dispatch(dz_threads(rows, outer), "vpa_head_linear_backward")) != VPA_OK ||
-        (st = check_dispatch(dz_threads(rows > outer ? rows : outer, inner),
-                             "vpa_head_linear_backward")) != VPA_OK)
+        ((z.dz || grad_bias) &&
+         (st = check_dispatch(dz_threads(rows, outer, grad_bias != nullptr),
+                              "vpa_head_linear_backward")) != VPA_OK) ||
+        ((z.w || z.x) && (st = check_dispatch(dz_threads(rows > outer ? rows : outer, inner, false),
+                                              "vpa_head_linear_backward")) != VPA_OK))
         return st;
     if (rows > 0 && (st = check_workspace("vpa_head_linear_backward", workspace, workspace_bytes,
                                           z.total())) != VPA_OK)

@@ -306,14 +306,40 @@ GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b
     return p;
 }
 
+namespace {
+
+// The second launch of a plan that has one: m and n become its part's sizes.
+GemmPlan plan_rest(int esize, const GemmPlan& first, int64_t& m, int64_t& n, int64_t k) {
+    m -= first.first_m < m ? first.first_m : 0;
+    n -= first.first_n < n ? first.first_n : 0;
+    GemmPlan r{};
+    plan_tiles(esize, m, n, k, r);
+    return r;
+}
+
+// Most work-items of one of a plan's dispatches, the join among them.
+int64_t planned_threads(const GemmPlan& p, int64_t m, int64_t n) {
+    const auto blocks = [&](int64_t rows, int64_t cols) {
+        return ((m + rows - 1) / rows) * ((n + cols - 1) / cols) * p.slices;
+    };
+    // rows that are not aligned take 128-tiles whatever the plan says
+    int64_t most = blocks(128, 128) * 256;
+    const int64_t own = p.tile <= 64    ? blocks(64, kFewRowsCols) * 256
+                        : p.tile == 256 ? blocks(256, 256) * 512
+                                        : most;
+    most = own > most ? own : most;
+    const int64_t join = p.slices > 1 ? (m * n + kThreads - 1) / kThreads * kThreads : 0;
+    return join > most ? join : most;
+}
+
+}  // namespace
+
 size_t gemm_workspace(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1) {
     const GemmPlan p = plan_gemm(esize, m, n, k, a_k1, b_k1);
     if (!p.first_m)
         return slices_bytes(p, m, n);
-    const int64_t mr = p.first_m < m ? m - p.first_m : m, nr = p.first_n < n ? n - p.first_n : n;
-    GemmPlan r{};
-    plan_tiles(esize, mr, nr, k, r);
-    const size_t first = slices_bytes(p, p.first_m, p.first_n), rest = slices_bytes(r, mr, nr);
+    const GemmPlan q = plan_rest(esize, p, m, n, k);
+    const size_t first = slices_bytes(p, p.first_m, p.first_n), rest = slices_bytes(q, m, n);
     return first > rest ? first : rest;
 }
 
@@ -321,11 +347,12 @@ int64_t gemm_threads(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool
     const GemmPlan p = plan_gemm(esize, m, n, k, a_k1, b_k1);
     if (p.rows_kernel)
         return linear_rows_threads(n);
-    // a product that is not direct takes 128-tiles whatever the plan says; the
-    // second of two launches has at most 16 slices
-    const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128) * (p.first_m ? 16 : p.slices) * 256;
-    const int64_t join = p.slices > 1 || p.first_m ? (m * n + kThreads - 1) / kThreads * kThreads : 0;
-    return tiles > join ? tiles : join;
+    if (!p.first_m)
+        return planned_threads(p, m, n);
+    const GemmPlan q = plan_rest(esize, p, m, n, k);
+    const int64_t first = planned_threads(p, p.first_m, p.first_n);
+    const int64_t rest = planned_threads(q, m, n);
+    return first > rest ? first : rest;
 }
 
 namespace {
@@ -373,8 +400,8 @@ hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream) {
     r.residual = past(t.residual, (dm * t.ldr + dn) * esize);
     r.pre = past(t.pre, (dm * t.ldp + dn) * esize);
     r.y = past(t.y, (dm * t.ldy + dn) * out);
-    GemmPlan q{};
-    plan_tiles(esize, r.m, r.n, r.k, q);
+    int64_t m = t.m, n = t.n;
+    GemmPlan q = plan_rest(esize, p, m, n, t.k);
     q.direct = p.direct;
     hipError_t e = launch_planned(esize, f, p, stream);
     return e != hipSuccess ? e : launch_planned(esize, r, q, stream);
@@ -388,8 +415,8 @@ int32_t dz_splits(int64_t rows, int64_t cols) {
     return (int32_t)(s < 1 ? 1 : s > 256 ? 256 : s);
 }
 
-int64_t dz_threads(int64_t rows, int64_t cols) {
-    const int64_t finish = (cols + 63) / 64 * 64 * kFinishWaves;
+int64_t dz_threads(int64_t rows, int64_t cols, bool bias) {
+    const int64_t finish = bias ? (cols + 63) / 64 * 64 * kFinishWaves : 0;
     const int64_t dz = (cols + kDzCols - 1) / kDzCols * kThreads * dz_splits(rows, cols);
     return dz > finish ? dz : finish;
 }

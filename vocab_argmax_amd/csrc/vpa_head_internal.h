@@ -120,6 +120,7 @@ struct GemmPlan {
 };
 GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
 size_t gemm_workspace(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
+// Most work-items of one of the product's dispatches.
 int64_t gemm_threads(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
 hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream);
 
@@ -146,7 +147,7 @@ struct DzTask {
     float* part;              // [dz_splits(rows, cols)][cols]
 };
 int32_t dz_splits(int64_t rows, int64_t cols);
-int64_t dz_threads(int64_t rows, int64_t cols);
+int64_t dz_threads(int64_t rows, int64_t cols, bool bias);
 hipError_t launch_dz(int esize, const DzTask& t, hipStream_t stream);
 
 // ---- layer norm (layer_norm.hip) ----
