@@ -184,7 +184,9 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
  *
  * y = (x - mean) rstd w + b over the `cols` elements of a row, mean and
  * variance of the row (biased), rstd = 1 / sqrt(variance + eps).  weight and
- * bias are optional.
+ * bias are optional.  Rows that a workgroup's registers hold (to 16384 bf16 or
+ * 8192 fp32 columns, in the backward pass to 8192 of either) may be any
+ * number below 2^31; of longer ones a call takes fewer than 2^22.
  * ------------------------------------------------------------------------ */
 /*  x, y       [rows][cols] of type `dtype`, 1 <= cols < 2^31; y may be x
  *             itself (same pointer and row stride).

@@ -44,3 +44,39 @@ def test_products_of_thin_operands(n, m, k, act, dtype):
     want = d.sum(0)
     tol = off.sum(0) + (n + 2) * U * d.abs().sum(0)
     near(gb, want, tol + half(dtype) * (want.abs() + tol), "grad_bias")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_layer_norm_of_many_short_rows(dtype):
+    """More rows than a dispatch has workgroups of 1024 threads: every row and
+    the sums over all of them, the last rows among them."""
+    n, c = (1 << 22) + 5, 9
+    g = gen(n)
+    x, gr = randn(g, n, c, dtype=dtype), randn(g, n, c, dtype=dtype)
+    w, b = randn(g, c, dtype=dtype), randn(g, c, dtype=dtype)
+    xd, gd, wd = x.double(), gr.double(), w.double()
+    mu = xd.mean(1, keepdim=True)
+    var = (xd - mu).square().mean(1, keepdim=True)
+    rs = 1 / (var + 1e-5).sqrt()
+    k = 33 * U                                           # one term a thread, then the tree
+    dmu = k * xd.abs().mean(1, keepdim=True)
+    drs = k + 0.5 * (dmu * dmu + 2 * U * dmu * rs.reciprocal()) / (var + 1e-5)
+    want = (xd - mu) * rs * wd + b.double()
+    part = ((xd - mu) * rs * wd).abs()
+    tol = rs * dmu * wd.abs() + part * (drs + 4 * U) + U * want.abs()
+    y, mean, rstd = vpa.layer_norm(x, w, b, with_stats=True)
+    near(y, want, tol + half(dtype) * (want.abs() + tol), "y")
+    rs = rstd.double()[:, None]
+    xh = (xd - mean.double()[:, None]) * rs
+    u = gd * wd
+    m1, m2 = u.mean(1, keepdim=True), (u * xh).mean(1, keepdim=True)
+    a1, a2 = u.abs().mean(1, keepdim=True), (u * xh).abs().mean(1, keepdim=True)
+    want = rs * (u - m1 - xh * m2)
+    tol = rs * (8 * U * (u.abs() + a1 + xh.abs() * a2) + k * (a1 + xh.abs() * a2))
+    gx, gw, gb = vpa.layer_norm_backward(gr, x, mean, rstd, w)
+    near(gx, want, tol + half(dtype) * (want.abs() + tol), "grad_x")
+    # a thread's share of the rows one after the other, then a few sums of sums
+    terms = n // 2048 + 64
+    for got, t, what in ((gw, gd * xh, "grad_weight"), (gb, gd, "grad_bias")):
+        tol = (terms + 6) * U * t.abs().sum(0)
+        near(got, t.sum(0), tol + half(dtype) * (t.sum(0).abs() + tol), what)

@@ -154,3 +154,30 @@ ORDINARY = [((rows, outer, inner), dt) for dt in (BF16, F32) for rows in (1, 24,
 def test_ordinary_products_keep_to_their_workspace(record):
     products_within(record, ORDINARY, linear_backward, "vpa_head_linear_backward_workspace")
     products_within(record, ORDINARY, linear, "vpa_head_linear_workspace")
+
+
+def norm(rows, cols, dt=BF16):
+    return ["vpa_layer_norm", [P, cols, dt, P, P, dt, rows, cols, 1e-5, P, cols, P, P, None]]
+
+
+def norm_backward(rows, cols, dt=BF16, need="xwb"):
+    return ["vpa_layer_norm_backward",
+            [P, cols, P, cols, dt, P, dt, P, P, rows, cols, P + 4096 if "x" in need else None, cols,
+             P if "w" in need else None, P if "b" in need else None, WS, HUGE, None]]
+
+
+def test_norms_of_many_rows_are_not_refused(record):
+    """Rows that registers hold are walked by a grid of bounded size: any number
+    of them is taken.  Longer rows are a workgroup each and end at 2^22 - 1."""
+    some = [(1 << 22) - 1, 1 << 22, (1 << 22) + 5, 1 << 26, (1 << 31) - 1]
+    calls = [make(rows, cols, dt=dt) for rows in some for dt in (BF16, F32)
+             for cols in (1, 64, 513, 2048, 2049, 8192 if dt == BF16 else 4096)
+             for make in (norm, norm_backward)]
+    calls += [norm(1 << 23, 16384), norm((1 << 22) - 1, 16385), norm_backward((1 << 22) - 1, 8193),
+              norm_backward(1 << 23, 8193, need="w")]
+    for call, (status, message, got) in zip(calls, record(calls)):
+        assert status == OK and got, (call, message)
+        assert max(map(work_items, got)) <= MOST_ITEMS, call
+    calls = [norm(1 << 22, 16385), norm_backward(1 << 22, 8193), norm(1 << 22, 8193, dt=F32)]
+    for call, (status, message, got) in zip(calls, record(calls)):
+        assert status != OK and "exceed one dispatch" in message and not got, call

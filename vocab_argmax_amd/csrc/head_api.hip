@@ -634,7 +634,7 @@ vpa_status vpa_layer_norm(const void* x, int64_t ldx, vpa_dtype dtype, const voi
         return st;
     if (x == y && ldx != ldy)
         return fail(VPA_ERR_INVALID, "y in x's place needs ldy = ldx");
-    if ((st = check_dispatch(norm_threads(rows, cols), "vpa_layer_norm")) != VPA_OK)
+    if ((st = check_dispatch(norm_threads(e, rows, cols), "vpa_layer_norm")) != VPA_OK)
         return st;
     const NormTask t = {x, ldx, weight, bias, we, rows, cols, eps, y, ldy, mean, rstd};
     hipError_t he = launch_norm(e, t, (hipStream_t)stream);
@@ -682,7 +682,8 @@ vpa_status vpa_layer_norm_backward(const void* grad, int64_t ldg, const void* x,
     const bool sums = grad_weight || grad_bias;
     if ((grad_weight && (st = check_vector("grad_weight", grad_weight, we)) != VPA_OK) ||
         (grad_bias && (st = check_vector("grad_bias", grad_bias, we)) != VPA_OK) ||
-        (st = check_dispatch(norm_grad_threads(e, rows, cols), "vpa_layer_norm_backward")) != VPA_OK)
+        (st = check_dispatch(norm_grad_threads(e, rows, cols, grad_x != nullptr, sums),
+                             "vpa_layer_norm_backward")) != VPA_OK)
         return st;
     if (sums && (st = check_workspace("vpa_layer_norm_backward", workspace, workspace_bytes,
                                       vpa_layer_norm_backward_workspace(rows, cols))) != VPA_OK)

@@ -410,6 +410,9 @@ __global__ __launch_bounds__(kJoinWaves * 64) void norm_join_kernel(NormGradTask
 // of bf16 leave the backward pass's sums no registers.
 struct NormForm {
     int waves, nv;
+    // of a workgroup (as RowPart's): single wavefronts work on 4 rows at a time
+    int rows() const { return waves == 1 ? 4 : 1; }
+    int threads() const { return waves * rows() * 64; }
 };
 NormForm norm_form(int esize, int64_t cols, bool grad) {
     const int64_t vecs = (cols * esize + 15) / 16;      // 16-byte vectors of a row
@@ -420,6 +423,16 @@ NormForm norm_form(int esize, int64_t cols, bool grad) {
     if (vecs <= 1024)
         return {8, 2};
     return vecs <= 2048 && !(grad && esize == 2) ? NormForm{8, 4} : NormForm{0, 0};
+}
+
+// Workgroups of the forward pass: 16 wavefronts a CU, which walk over the rows,
+// so that each has several for its weights; long rows have a workgroup each.
+int64_t norm_blocks(NormForm form, int64_t rows) {
+    if (form.waves == 0)
+        return rows;
+    const int64_t most = 4096 * 64 / form.threads();
+    const int64_t need = (rows + form.rows() - 1) / form.rows();
+    return need < most ? need : most;
 }
 
 // Calls f(WAVES, NV), as types, for the form.
@@ -440,15 +453,12 @@ hipError_t with_form(NormForm form, F f) {
 template <typename T, typename W>
 hipError_t launch_norm_typed(const NormTask& t, hipStream_t stream) {
     const NormForm form = norm_form((int)sizeof(T), t.cols, false);
+    const dim3 grid((uint32_t)norm_blocks(form, t.rows));
     if (form.waves == 0)
-        return launch(norm_long_kernel<T, W>, dim3((uint32_t)t.rows), dim3(kLongThreads), 0,
-                      stream, t);
+        return launch(norm_long_kernel<T, W>, grid, dim3(kLongThreads), 0, stream, t);
     return with_form<(int)sizeof(T), false>(form, [&](auto waves, auto nv) {
-        using P = RowPart<T, waves(), nv()>;
-        // 16 wavefronts a CU: each workgroup has several rows for its weights
-        const int64_t most = 4096 * 64 / P::THREADS, need = (t.rows + P::ROWS - 1) / P::ROWS;
-        return launch(norm_kernel<T, W, waves(), nv()>, dim3((uint32_t)(need < most ? need : most)),
-                      dim3(P::THREADS), 0, stream, t);
+        return launch(norm_kernel<T, W, waves(), nv()>, grid,
+                      dim3(RowPart<T, waves(), nv()>::THREADS), 0, stream, t);
     });
 }
 
@@ -483,8 +493,9 @@ hipError_t launch_norm_grad_typed(const NormGradTask& task, hipStream_t stream) 
 
 }  // namespace
 
-int64_t norm_threads(int64_t rows, int64_t) {
-    return rows * kLongThreads;
+int64_t norm_threads(int esize, int64_t rows, int64_t cols) {
+    const NormForm form = norm_form(esize, cols, false);
+    return norm_blocks(form, rows) * (form.waves == 0 ? kLongThreads : form.threads());
 }
 
 hipError_t launch_norm(int esize, const NormTask& t, hipStream_t stream) {
@@ -504,11 +515,18 @@ int32_t norm_splits(int esize, int64_t rows, int64_t cols) {
     return (int32_t)(s < 1 ? 1 : s);
 }
 
-int64_t norm_grad_threads(int esize, int64_t rows, int64_t cols) {
-    const int64_t a = rows * kLongThreads;
-    const int64_t b = (cols + kThreads - 1) / kThreads * kThreads * norm_splits(esize, rows, cols);
-    const int64_t c = (cols + 63) / 64 * 64 * kJoinWaves * 2;
-    return a > b ? (a > c ? a : c) : (b > c ? b : c);
+int64_t norm_grad_threads(int esize, int64_t rows, int64_t cols, bool dx, bool sums) {
+    const NormForm form = norm_form(esize, cols, true);
+    const int64_t splits = norm_splits(esize, rows, cols);
+    int64_t most = form.waves != 0 ? splits * form.threads() : dx ? rows * kLongThreads : 0;
+    if (sums) {
+        const int64_t columns = form.waves == 0 ? (cols + kThreads - 1) / kThreads * kThreads * splits
+                                                : 0;
+        const int64_t join = (cols + 63) / 64 * 64 * kJoinWaves * 2;
+        most = columns > most ? columns : most;
+        most = join > most ? join : most;
+    }
+    return most;
 }
 
 hipError_t launch_norm_grad(int esize, const NormGradTask& t, hipStream_t stream) {

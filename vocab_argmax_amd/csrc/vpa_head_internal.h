@@ -165,7 +165,7 @@ struct NormTask {
     float* mean;
     float* rstd;
 };
-int64_t norm_threads(int64_t rows, int64_t cols);
+int64_t norm_threads(int esize, int64_t rows, int64_t cols);
 hipError_t launch_norm(int esize, const NormTask& t, hipStream_t stream);
 
 struct NormGradTask {
@@ -185,7 +185,8 @@ struct NormGradTask {
     float* part;              // [2][norm_splits(esize, rows, cols)][cols]
 };
 int32_t norm_splits(int esize, int64_t rows, int64_t cols);
-int64_t norm_grad_threads(int esize, int64_t rows, int64_t cols);
+// Most work-items of one dispatch, for grad_x (dx) and the sums over rows.
+int64_t norm_grad_threads(int esize, int64_t rows, int64_t cols, bool dx, bool sums);
 hipError_t launch_norm_grad(int esize, const NormGradTask& t, hipStream_t stream);
 
 }  // namespace vpa
