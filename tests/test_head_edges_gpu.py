@@ -9,7 +9,8 @@ import pytest
 import torch
 
 import vocab_argmax_amd as vpa
-from test_head_gpu import (ACT, BF, DEV, F32, NEG, U, gen, half, linear_oracle, near, randn, slope)
+from test_head_gpu import (BF, DEV, F32, U, check_logprobs, gen, grad_oracle, half, linear_oracle,
+                           near, randn, slope)
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +81,40 @@ def test_layer_norm_of_many_short_rows(dtype):
     for got, t, what in ((gw, gd * xh, "grad_weight"), (gb, gd, "grad_bias")):
         tol = (terms + 6) * U * t.abs().sum(0)
         near(got, t.sum(0), tol + half(dtype) * (t.sum(0).abs() + tol), what)
+
+
+# ---------------------------------------------------------------------------
+# log probabilities: what a row carries from chunk to chunk
+# ---------------------------------------------------------------------------
+
+# rows, vocab: a workgroup reads a row in several chunks, of 8192 fp32 or 16384
+# bf16 columns (the first two), or of 2048 and 4096 (a few rows of a vocabulary
+# that is cut into the most segments; a batch between the two)
+CHUNKED = [(1500, 20000), (1500, 40000), (3, 1200000), (60, 151936)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,v", CHUNKED)
+def test_finite_rows_far_apart(n, v, dtype):
+    """Sums of many columns beside one that is further away than fp32 can
+    multiply them by: the row is that one token."""
+    x = torch.zeros((n, v), dtype=dtype, device=DEV)
+    x[:, v // 3:] = 39.0
+    x[:, v - 1] = 3.0e38
+    if n > 1:
+        x[1, v - 1] = 39.0
+        x[1, 0] = 1.0e30
+        x[1, v // 2] = -3.0e38
+    tok = torch.full((n,), v - 1, dtype=torch.int32, device=DEV)
+    ge = torch.ones(n, device=DEV)
+    r = vpa.token_logprobs(x, v, v, 1, tok, 2)
+    check_logprobs(r, x, v, tok, 2, "far apart")
+    assert bool((r.entropy == 0).all())
+    w = -(-v // 3)
+    wide = torch.full((n, 3 * w), float("nan"), dtype=dtype, device=DEV)
+    wide[:, :v] = x
+    rec = vpa.logprob_stats(wide, v, w, 3, tok, 2)
+    check_logprobs(vpa.combine_logprobs(rec, v, w, tok, 2), x, v, tok, 2, "far apart, sharded")
+    got = vpa.token_logprobs_backward(x, v, v, 1, tok, r.row_stats, ge, ge)
+    want, tol = grad_oracle(x[:3], v, tok[:3], ge[:3], ge[:3], r.row_stats[:3])
+    near(got[:3], want, tol + half(dtype) * want.abs() + torch.finfo(F32).tiny, "gradient")

@@ -70,11 +70,12 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
 struct Sums {
     float m, s, u;
 };
-// (x - m) log2(e), held above -inf so that its product with 2^z = 0 is 0;
-// a NaN stays.
+// (x - m) log2(e), held at -1000, where 2^z is 0 already: its products with
+// 2^z and with the sum of a set that it moves (d s, before 2^d = 0 takes it
+// away) are finite, whatever the logits; a NaN stays.
 __device__ __forceinline__ float scaled_distance(float x, float m) {
     const float z = (x - m) * kLog2e;
-    return z < -1e30f ? -1e30f : z;
+    return z < -1000.0f ? -1000.0f : z;
 }
 __device__ __forceinline__ void join(Sums& a, const Sums& b) {
     const float m = fmaxf(a.m, b.m);
