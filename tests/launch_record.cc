@@ -22,6 +22,7 @@ struct Launch {
     int64_t m, n, k, slices;
     uint64_t part;
     int64_t part_bytes;
+    int64_t chunks;             // of a segment of a row of log probabilities
 };
 
 std::map<const void*, std::string>& names() {
@@ -90,6 +91,12 @@ hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void** args, si
              arg<vpa::GemmTask>(args, 0).ws);
     else if (is("linear_rows_kernel"))
         gemm(l, arg<vpa::GemmTask>(args, 0), 1, nullptr);
+    else if (is("logprob_part_kernel")) {
+        const auto& cut = arg<vpa::LogprobCut>(args, 1);
+        l.slices = cut.segments;
+        l.chunks = cut.chunks_per_segment;
+        l.k = cut.vecs;
+    }
     launches().push_back(l);
     return hipSuccess;
 }

@@ -9,8 +9,8 @@ import pytest
 import torch
 
 import vocab_argmax_amd as vpa
-from test_head_gpu import (BF, DEV, F32, U, check_logprobs, gen, grad_oracle, half, linear_oracle,
-                           near, randn, slope)
+from test_head_gpu import (BF, DEV, F32, NEG, SUM, U, check_logprobs, gen, grad_oracle, half,
+                           linear_oracle, near, randn, slope)
 
 pytestmark = pytest.mark.gpu
 
@@ -87,14 +87,13 @@ def test_layer_norm_of_many_short_rows(dtype):
 # log probabilities: what a row carries from chunk to chunk
 # ---------------------------------------------------------------------------
 
-# rows, vocab: a workgroup reads a row in several chunks, of 8192 fp32 or 16384
-# bf16 columns (the first two), or of 2048 and 4096 (a few rows of a vocabulary
-# that is cut into the most segments; a batch between the two)
-CHUNKED = [(1500, 20000), (1500, 40000), (3, 1200000), (60, 151936)]
+# rows, vocab, 16-byte vectors of a thread and chunk (bf16, fp32): a workgroup of
+# 256 threads reads a row in several chunks
+CHUNKED = [(1500, 20000, 8, 8), (1500, 40000, 8, 8), (3, 1200000, 2, 2), (60, 151936, 2, 8)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("n,v", CHUNKED)
+@pytest.mark.parametrize("n,v", [c[:2] for c in CHUNKED])
 def test_finite_rows_far_apart(n, v, dtype):
     """Sums of many columns beside one that is further away than fp32 can
     multiply them by: the row is that one token."""
@@ -118,3 +117,67 @@ def test_finite_rows_far_apart(n, v, dtype):
     got = vpa.token_logprobs_backward(x, v, v, 1, tok, r.row_stats, ge, ge)
     want, tol = grad_oracle(x[:3], v, tok[:3], ge[:3], ge[:3], r.row_stats[:3])
     near(got[:3], want, tol + half(dtype) * want.abs() + torch.finfo(F32).tiny, "gradient")
+
+
+def late_rows(x, dtype, chunk):
+    """Rows that go wrong, if they do, in a later chunk than the first."""
+    n, v = x.shape
+    last = (v - 1) // chunk * chunk                      # the first column of the last chunk
+    x[0, :chunk] = NEG                                   # a first chunk of masked columns
+    x[1, :last] = NEG
+    x[2, :chunk] = torch.finfo(dtype).min
+    x[3, last:] = NEG                                    # a last chunk of masked ones
+    x[4, v - 2] = float("nan")
+    x[5, v - 1] = float("inf")
+    x[6, v - 3] = float("nan")
+    x[6, 5] = float("inf")
+    x[7, :chunk] -= 100.0                                # the rest is far above
+    x[8] = torch.linspace(-60, 60, v, device=DEV).to(dtype)      # ascending, with ties in bf16
+    x[9, chunk:] = 6.5                                   # thousands of ties, after the first chunk
+    x[10, :chunk] = 6.5                                  # and before
+    x[11] = torch.where(torch.arange(v, device=DEV) % 2 == 0, -0.0, 0.0).to(dtype)
+    x[12] = NEG                                          # 3 tokens, all late
+    x[12, last:last + 3] = torch.tensor([1.0, 3.0, 3.0], device=DEV).to(dtype)
+    x[13, chunk:] += 41.0                                # rises past any lag of the maximum
+    x[14, chunk:] += 0.9
+    x[15, last] = 3.0e38
+    x[16, last] = -3.0e38
+    x[17] = x[17] * 1e30
+    x[18, 1::2] = NEG
+    x[19, last:] = float("nan")
+    return x
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,v,vecs_bf16,vecs_f32", CHUNKED)
+@pytest.mark.parametrize("top", [0, 3, 64])
+def test_rows_of_several_chunks(n, v, vecs_bf16, vecs_f32, top, dtype):
+    g = gen(v + top)
+    chunk = 256 * (8 * vecs_bf16 if dtype is BF else 4 * vecs_f32)
+    kinds = late_rows(randn(g, 20, v, dtype=dtype, scale=2.0), dtype, chunk)
+    # of a call of 3 rows the kinds come 3 at a time
+    batches = [kinds[i:i + n] for i in range(0, 20, n)] if n < 20 else [kinds]
+    for some in batches:
+        x = torch.cat([some, randn(g, max(0, n - len(some)), v, dtype=dtype, scale=2.0)])
+        tok = torch.randint(0, v, (x.shape[0], 3), generator=g, device=DEV, dtype=torch.int32)
+        tok[:, 1], tok[:, 2] = v - 1, -1
+        r = vpa.token_logprobs(x, v, v, 1, tok, top)
+        few = len(some)
+        check_logprobs(cut_rows(r, few), some, v, tok[:few], top, "chunks")
+        if n > 20:
+            near(r.lse[few:40], x[few:40].double().logsumexp(1), SUM * 16, "the others")
+        w = -(-v // 2)
+        wide = torch.full((x.shape[0], 2 * w), float("nan"), dtype=dtype, device=DEV)
+        wide[:, :v] = x
+        rec = vpa.logprob_stats(wide, v, w, 2, tok, top)
+        check_logprobs(cut_rows(vpa.combine_logprobs(rec, v, w, tok, top), few), some, v, tok[:few],
+                       top, "chunks, sharded")
+
+
+class cut_rows:
+    """The first n rows of a TokenLogprobs."""
+
+    def __init__(self, r, n):
+        for name in ("logprobs", "lse", "entropy", "top_ids", "top_logprobs"):
+            t = getattr(r, name)
+            setattr(self, name, t if t is None else t[:n])

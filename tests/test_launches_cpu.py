@@ -26,7 +26,7 @@ class Launch(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 192), ("grid", ctypes.c_uint32 * 3),
                 ("block", ctypes.c_uint32 * 3), ("m", ctypes.c_int64), ("n", ctypes.c_int64),
                 ("k", ctypes.c_int64), ("slices", ctypes.c_int64), ("part", ctypes.c_uint64),
-                ("part_bytes", ctypes.c_int64)]
+                ("part_bytes", ctypes.c_int64), ("chunks", ctypes.c_int64)]
 here.launches_get.restype = ctypes.POINTER(Launch)
 lib = vpa.head_lib()
 out = []
@@ -38,7 +38,8 @@ for name, args in json.load(sys.stdin):
     for i in range(here.launches_count()):
         l = here.launches_get(i).contents
         got.append(dict(name=l.name.decode(), grid=list(l.grid), block=list(l.block), m=l.m, n=l.n,
-                        k=l.k, slices=l.slices, part=l.part, part_bytes=l.part_bytes))
+                        k=l.k, slices=l.slices, part=l.part, part_bytes=l.part_bytes,
+                        chunks=l.chunks))
     out.append([r, vpa.last_error() if r else "", got])
 json.dump(out, sys.stdout)
 """
@@ -181,3 +182,18 @@ def test_norms_of_many_rows_are_not_refused(record):
     calls = [norm(1 << 22, 16385), norm_backward(1 << 22, 8193), norm(1 << 22, 8193, dt=F32)]
     for call, (status, message, got) in zip(calls, record(calls)):
         assert status != OK and "exceed one dispatch" in message and not got, call
+
+
+def test_cuts_that_the_gpu_tests_mean(record):
+    """test_head_edges_gpu.py is about rows that a workgroup reads in several
+    chunks, by the kernel of 8 vectors a thread and by the one of 2."""
+    from test_head_edges_gpu import CHUNKED
+    def logprobs(n, v, dt):
+        return ["vpa_token_logprobs", [P, dt, v, [v, v, 1], n, P, 1, 5, WS, HUGE, P, P, P, P, P,
+                                       None]]
+    calls = [logprobs(c[0], c[1], dt) for c in CHUNKED for dt in (BF16, F32)]
+    want = [c[2 if dt == BF16 else 3] for c in CHUNKED for dt in (BF16, F32)]
+    for call, vecs, (status, message, got) in zip(calls, want, record(calls)):
+        assert status == OK, message
+        part = [l for l in got if "logprob_part_kernel" in l["name"]]
+        assert len(part) == 1 and part[0]["chunks"] >= 2 and part[0]["k"] == vecs, (call, part)
