@@ -10,7 +10,7 @@ import torch
 
 import vocab_argmax_amd as vpa
 from test_head_gpu import (BF, DEV, F32, NEG, SUM, U, check_logprobs, gen, grad_oracle, half,
-                           linear_oracle, near, randn, slope)
+                           linear_oracle, logprob_oracle, near, randn, slope)
 
 pytestmark = pytest.mark.gpu
 
@@ -181,3 +181,57 @@ class cut_rows:
         for name in ("logprobs", "lse", "entropy", "top_ids", "top_logprobs"):
             t = getattr(r, name)
             setattr(self, name, t if t is None else t[:n])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,v", [(1500, 50257), (1500, 20000), (1, 50257), (33, 151936), (3, 1200000)])
+def test_confident_rows_keep_their_digits(n, v, dtype):
+    """A trained model is sure of most tokens: the log probability of the sure
+    one and the entropy are far below 1, and their error is too, wherever in
+    the row the token stands."""
+    g = gen(v + n)
+    x = -4.0 * torch.rand((n, v), generator=g, device=DEV)
+    i = torch.arange(n, device=DEV)
+    at = (v - 1 - (i * 7919) % v) if n > 1 else torch.tensor([v - 5], device=DEV)
+    gap = 24.0 + (i % 16) if n > 1 else torch.tensor([36.0], device=DEV)
+    x[i, at] = gap.float()
+    x = x.to(dtype)
+    tok = at.to(torch.int32)
+    lp, lse, ent, _, _ = logprob_oracle(x[:64], v, tok[:64], 0)
+    gap = gap[:64].double()
+    # What may be lost: terms of at most e^-gap each that a lane adds to the 1
+    # of the sure token, v / 256 and a few of them, and some steps at 1 in 2^z,
+    # the sum's logarithm and the distance from M.  Of u = sum z 2^z nothing
+    # is lost but a relative (64 + 32) U, M's own term being 0.
+    lost = (v / 256 + 64) * (-gap).exp() + 8 * U
+    r = vpa.token_logprobs(x, v, v, 1, tok)
+    near(r.logprobs[:64], lp, lost, "log probability of the sure token")
+    near(r.entropy[:64], ent, lost + SUM * ent, "entropy")
+    rec = vpa.logprob_stats(x, v, v, 1, tok)
+    r = vpa.combine_logprobs(rec, v, v, tok)
+    near(r.logprobs[:64], lp, lost, "log probability of the sure token, of records")
+    near(r.entropy[:64], ent, lost + SUM * ent, "entropy, of records")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,v", [(1500, 50257), (33, 151936)])
+def test_confident_rows_with_a_rival(n, v, dtype):
+    """Two tokens carry a row, the later one ahead by any distance: what the sum
+    loses to the distance between them has a bound that does not grow with it."""
+    i = torch.arange(n, device=DEV)
+    x = torch.full((n, v), -60.0, device=DEV)
+    x[:, 7] = 0.0
+    at = v - 1 - (i * 7919) % (v // 3)
+    x[i, at] = 0.25 * (i % 160).float()
+    x = x.to(dtype)
+    tok = torch.stack([at, torch.full_like(at, 7)], 1).to(torch.int32)
+    lp, lse, ent, _, _ = logprob_oracle(x, v, tok, 0)
+    r = vpa.token_logprobs(x, v, v, 1, tok)
+    # M is at most 4 behind: x - M is off by half a step there, 4 U, and a step
+    # at 4 log2(e) < 8 is 8 U: log2 s has one of them, z half of one, which 2^z
+    # and the logarithm carry on; 2^z, its scale and the sum of the two add 6 U.
+    # The rest's v terms of e^-60 are nothing.
+    tol = 24 * U + 2 * U * lp.abs()
+    near(r.logprobs, lp, tol, "log probabilities")
+    # u's terms are z 2^z, each 2^z off by the 10 U of before, z below 6
+    near(r.entropy, ent, 24 * U + 2 * 6 * 10 * U * ent.clamp(max=1), "entropy")

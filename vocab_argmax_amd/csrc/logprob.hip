@@ -38,6 +38,7 @@ constexpr int chunk_cols(int esize, int u) {
 }
 
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kLag = 4.0f;                      // most that a chunk's maximum may exceed M by
 
 // (value, id) in the argmax order; 0 is below every real column.
 __device__ __forceinline__ uint64_t order_of(float x, int32_t id) {
@@ -111,9 +112,9 @@ __device__ __forceinline__ Sums wave_join(Sums v) {
     join_step<dpp::kBcast31, 0xC>(v);
     return Sums{lane63(v.m), lane63(v.s), lane63(v.u)};
 }
-// Over the workgroup, through `lds`; every thread holds the result.
+// Over the workgroup, of sums that are the same in all lanes of a wavefront,
+// through `lds`; every thread holds the result.
 __device__ __forceinline__ Sums block_join(Sums v, Sums* lds) {
-    v = wave_join(v);
     if ((threadIdx.x & 63) == 0)
         lds[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -197,12 +198,18 @@ __device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int
 // One segment of a row: its Sums and its first n_top columns.
 //
 // The workgroup walks the segment in chunks of U 16-byte vectors a thread,
-// held in registers.  Every lane keeps M, s and u of its own columns, joined
-// at the end; M is its first chunk's maximum, so that later chunks are one
-// pass: for bf16 an element costs 1.5 instructions to unpack it and take the
-// maximum, 2 slots for 2^z, a multiply-add, an add and a multiply-add, 6.5
-// slots.  M need only be near the row's maximum: s and u are exact for any M
-// that keeps 2^z within fp32, and a chunk that does not is done with care.
+// held in registers.  Every lane keeps s and u of its own columns, measured
+// from an M that its wavefront shares and that follows the maximum: it is the
+// first chunk's, and moves to a later chunk's that is more than kLag above it.
+// s is then at least 1 and 2^z at most e^kLag, so that ln s and u / s lose no
+// digits to a large z: the log probability of a token that the model is sure
+// of is right to a few steps at kLag, and where nothing comes within kLag of
+// it, its row's entropy to a few steps at 1 (with M up to 40 behind both were
+// off by 4e-6).  A later chunk is one pass: for bf16 an element costs 1.5
+// instructions to unpack it and take the maximum, 2 slots for 2^z, a
+// multiply-add, an add and a multiply-add, 6.5 slots; where M moves it is two
+// passes (1024 x 200064 with a sure token in half of the rows: 76.7 us, 81.4
+// with a kLag of 1, 76.1 with one of 40).
 //
 // Alternatives: T is a lower bound of the n_top-th largest value, from the
 // largest values of the lanes on the first chunk (in each of the W
@@ -268,9 +275,7 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
     const int lo = begin < first ? (int)first : begin;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 
-    // The lane's sums, measured from the maximum of its first chunk with a
-    // finite column.
-    Sums r = {kNegInf, 0.0f, 0.0f};
+    Sums r = {kNegInf, 0.0f, 0.0f};                 // M is the wavefront's, s and u the lane's
     LaneScale scale = {0.0f, 0.0f, 1.0f};
     int kept = 0;                                   // of cand[]: the best so far, in order
     float bound = kNegInf;                          // T
@@ -327,13 +332,12 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
                 v = max3(v, value(i * VEC + e), value(i * VEC + e + 1));
             return max3(v, value(i * VEC + VEC - 1), value(i * VEC + VEC - 1));
         };
-        if (__ballot(r.m == kNegInf)) {
+        if (r.m == kNegInf) {
             float v = kNegInf;
 #pragma unroll
             for (int i = 0; i < U; ++i)
                 v = fmaxf(v, largest(i));
-            if (r.m == kNegInf)
-                scale.set(r.m = v);
+            scale.set(r.m = wave_max(v));
             anew();
         }
         float s = 0.0f, u = 0.0f, mx = kNegInf;
@@ -355,35 +359,33 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
         u = __builtin_fmaf(-scale.off, s, u) * scale.fix;
         s *= scale.fix;
         // masked columns (0 * -inf), infinities and NaN, values whose product
-        // with log2(e) is not finite or that are far above M: once more, with
-        // care, from the larger of M and the chunk's maximum
-        const bool odd = !(fabsf(u) < __builtin_inff()) || mx > r.m + 40.0f;
+        // with log2(e) is not finite, a maximum that M has to follow: once
+        // more, with care, from the larger of M and the chunk's maximum
+        const bool odd = !(fabsf(u) < __builtin_inff()) || mx > r.m + kLag;
         if (__ballot(odd)) {
             anew();
-            if (odd) {
-                const float m = fmaxf(r.m, mx);
-                if (m != r.m) {
-                    const float d = scaled_distance(r.m, m);
-                    const float f = exp2_fast(d);
-                    r.u = (r.u + d * r.s) * f;
-                    r.s *= f;
-                    scale.set(r.m = m);
-                }
-                const float base = m == kNegInf ? 0.0f : m;
-                s = u = 0.0f;
+            const float m = fmaxf(r.m, wave_max(mx));
+            if (m != r.m) {
+                const float d = scaled_distance(r.m, m);
+                const float f = exp2_fast(d);
+                r.u = (r.u + d * r.s) * f;
+                r.s *= f;
+                scale.set(r.m = m);
+            }
+            const float base = m == kNegInf ? 0.0f : m;
+            s = u = 0.0f;
 #pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    if (whole || has(i)) {
+            for (int i = 0; i < U; ++i) {
+                if (whole || has(i)) {
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const float z = scaled_distance(value(i * VEC + e), base);
-                            const float p = exp2_fast(z);
-                            s += p;
-                            u += z * p;
-                        }
+                    for (int e = 0; e < VEC; ++e) {
+                        const float z = scaled_distance(value(i * VEC + e), base);
+                        const float p = exp2_fast(z);
+                        s += p;
+                        u = __builtin_fmaf(z, p, u);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         r.s += s;
@@ -483,6 +485,8 @@ __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, L
             bound = key >= kKeyNanF32 ? __builtin_nanf("") : value_of_key(key + 1);
         }
     }
+    r.s = wave_sum(r.s);
+    r.u = wave_sum(r.u);
     r = block_join(r, lds_s);
     const uint64_t top = (int)threadIdx.x < kept ? cand[threadIdx.x] : 0;
     if (o.row_stats) {                              // the segment is the row
@@ -568,7 +572,7 @@ __device__ __forceinline__ Sums join_all(int64_t n, Get sums) {
     Sums r = {kNegInf, 0.0f, 0.0f};
     for (int64_t i = threadIdx.x; i < n; i += kThreads)
         join(r, sums(i));
-    return block_join(r, lds);
+    return block_join(wave_join(r), lds);
 }
 
 template <int ESIZE>

@@ -87,6 +87,23 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __builtin_bit_cast(float,
                               __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
+// The maximum, alike; a NaN counts as nothing.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float max_move(float v) {
+    const int i = __builtin_bit_cast(int, v);
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, ROW_MASK, 0xF,
+                                                                          false)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = max_move<dpp::kSwap1, 0xF>(v);
+    v = max_move<dpp::kSwap2, 0xF>(v);
+    v = max_move<dpp::kHalfMirror, 0xF>(v);
+    v = max_move<dpp::kMirror, 0xF>(v);
+    v = max_move<dpp::kBcast15, 0xA>(v);
+    v = max_move<dpp::kBcast31, 0xC>(v);
+    return __builtin_bit_cast(float,
+                              __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
 
 // Two sums over a workgroup of WAVES wavefronts through `lds`; every thread
 // holds the results.  Callers leave a barrier between two uses of an lds.
