@@ -179,6 +179,18 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
                                     int64_t ldgw, void* grad_bias, void* workspace,
                                     size_t workspace_bytes, void* stream);
 
+/* The same for a gradient of type grad_dtype: `dtype`, or VPA_F32 where
+ * vpa_head_linear stored y in fp32 from bf16 operands.  dz is rounded to
+ * `dtype` for the two products as with an activation; grad_bias sums the fp32
+ * values.  Its workspace is vpa_head_linear_backward's. */
+vpa_status vpa_head_linear_backward_typed(const void* grad, int64_t ldg, vpa_dtype grad_dtype,
+                                          const void* x, int64_t ldx, const void* weight,
+                                          int64_t ldw, const void* pre, int64_t ldp,
+                                          vpa_dtype dtype, int64_t rows, int64_t outer,
+                                          int64_t inner, int32_t act, void* grad_x, int64_t ldgx,
+                                          void* grad_weight, int64_t ldgw, void* grad_bias,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------------
  * Layer norm
  *

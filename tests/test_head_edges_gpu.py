@@ -235,3 +235,64 @@ def test_confident_rows_with_a_rival(n, v, dtype):
     near(r.logprobs, lp, tol, "log probabilities")
     # u's terms are z 2^z, each 2^z off by the 10 U of before, z below 6
     near(r.entropy, ent, 24 * U + 2 * 6 * 10 * U * ent.clamp(max=1), "entropy")
+
+
+# ---------------------------------------------------------------------------
+# the gradient of fp32 results of bf16 operands
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("act", ["none", "silu", "relu"])
+@pytest.mark.parametrize("n,k,m", [(1, 1, 1), (1, 129, 70), (3, 65, 129), (64, 256, 320),
+                                   (100, 130, 1031), (513, 96, 2049), (1030, 520, 2904)])
+def test_backward_for_an_fp32_gradient(n, k, m, act):
+    g = gen(n + 31 * k + 7 * m)
+    x, w = randn(g, n, k, dtype=BF), randn(g, m, k, dtype=BF, scale=k ** -0.5)
+    b, gr = randn(g, m, dtype=BF), randn(g, n, m)
+    y, pre = vpa.head_linear(x, w, b, act, out_dtype=F32, with_pre=True)
+    assert y.dtype is F32 and pre.dtype is BF
+    z = pre.double()
+    dz = gr.double() * slope(act, z)
+    off = 0 * dz if act == "none" else gr.double().abs() * 16 * U * (1 + z.abs())
+    rounded = off + half(BF) * (dz.abs() + off)          # the products' operand is bf16
+    wide = torch.full((n, m + 3), float("nan"), device=DEV)
+    wide[:, 1:m + 1] = gr                                # rows that are not aligned
+    for gg in (gr, wide[:, 1:m + 1]):
+        gx, gw, gb = vpa.head_linear_backward(gg, x, w, pre, act)
+        assert gx.dtype is gw.dtype is gb.dtype is BF
+        want = dz @ w.double()
+        tol = rounded @ w.double().abs() + (m + 2) * 2 * U * (dz.abs() @ w.double().abs())
+        near(gx, want, tol + half(BF) * (want.abs() + tol), "grad_x")
+        want = dz.T @ x.double()
+        tol = rounded.T @ x.double().abs() + (n + 2) * 2 * U * (dz.T.abs() @ x.double().abs())
+        near(gw, want, tol + half(BF) * (want.abs() + tol), "grad_weight")
+        want = dz.sum(0)                                 # of the fp32 values, not of rounded ones
+        tol = off.sum(0) + (n + 2) * U * dz.abs().sum(0)
+        near(gb, want, tol + half(BF) * (want.abs() + tol), "grad_bias")
+    only = vpa.head_linear_backward(gr, x, w, pre, act, need_weight=False, need_x=False)
+    assert only[0] is None and only[1] is None and torch.equal(only[2], gb)
+
+
+def test_fp32_logits_of_bf16_operands_train():
+    """LM head with fp32 logits, their log probabilities and the way back."""
+    n, k, v = 40, 96, 3001
+    g = gen(12)
+    x, w = randn(g, n, k, dtype=BF), randn(g, v, k, dtype=BF, scale=k ** -0.5)
+    tok = torch.randint(0, v, (n,), generator=g, device=DEV, dtype=torch.int32)
+    logits = vpa.head_linear(x, w, out_dtype=F32)
+    r = vpa.token_logprobs(logits, v, v, 1, tok)
+    gl = torch.full((n,), -1.0 / n, device=DEV)
+    d = vpa.token_logprobs_backward(logits, v, v, 1, tok, r.row_stats, gl)
+    gx, gw, _ = vpa.head_linear_backward(d, x, w, need_bias=False)
+    dd = d.double()
+    want = dd @ w.double()
+    tol = (half(BF) + (v + 2) * 2 * U) * (dd.abs() @ w.double().abs())
+    near(gx, want, tol + half(BF) * (want.abs() + tol), "grad_x")
+    want = dd.T @ x.double()
+    tol = (half(BF) + (n + 2) * 2 * U) * (dd.T.abs() @ x.double().abs())
+    near(gw, want, tol + half(BF) * (want.abs() + tol), "grad_weight")
+    empty = vpa.head_linear_backward(d[:0], x[:0], w)
+    assert empty[0].shape == (0, k) and bool((empty[1] == 0).all()) and bool((empty[2] == 0).all())
+    with pytest.raises(TypeError):
+        vpa.head_linear_backward(d.to(BF), x.float(), w.float())
+    with pytest.raises(TypeError):
+        vpa.head_linear_backward(d.half(), x, w)

@@ -237,6 +237,135 @@ LinearGradSizes linear_grad_sizes(int esize, int64_t rows, int64_t outer, int64_
     return z;
 }
 
+// grad of type gdt, everything else of type dt.
+vpa_status linear_backward(const void* grad, int64_t ldg, int gdt, const void* x, int64_t ldx,
+                           const void* weight, int64_t ldw, const void* pre, int64_t ldp, int dt,
+                           int64_t rows, int64_t outer, int64_t inner, int32_t act, void* grad_x,
+                           int64_t ldgx, void* grad_weight, int64_t ldgw, void* grad_bias,
+                           void* workspace, size_t workspace_bytes, hipStream_t s) {
+    vpa_status st;
+    if ((st = check_dtype(dt)) != VPA_OK || (st = check_dtype(gdt)) != VPA_OK ||
+        (st = check_act(act)) != VPA_OK ||
+        (st = check_sizes("vpa_head_linear_backward", rows, outer, inner)) != VPA_OK)
+        return st;
+    if (gdt != dt && gdt != VPA_F32)
+        return fail(VPA_ERR_UNSUPPORTED, "grad_dtype %d: the operands' type or VPA_F32", gdt);
+    const int e = esize_of(dt), ge = esize_of(gdt);
+    const bool has_act = act != VPA_ACT_NONE;
+    if (rows > 0) {
+        if ((st = check_matrix("grad", grad, ge, ldg, outer)) != VPA_OK ||
+            (has_act && (st = check_matrix("pre", pre, e, ldp, outer)) != VPA_OK) ||
+            (grad_x && (st = check_matrix("weight", weight, e, ldw, inner)) != VPA_OK) ||
+            (grad_x && (st = check_matrix("grad_x", grad_x, e, ldgx, inner)) != VPA_OK) ||
+            (grad_weight && (st = check_matrix("x", x, e, ldx, inner)) != VPA_OK))
+            return st;
+    }
+    if ((grad_weight &&
+         (st = check_matrix("grad_weight", grad_weight, e, ldgw, inner)) != VPA_OK) ||
+        (grad_bias && (st = check_vector("grad_bias", grad_bias, e)) != VPA_OK))
+        return st;
+    // without an activation dz is grad, unless it is of another type or its rows
+    // are not aligned: a copy costs one pass over grad, the products' unaligned
+    // loads more
+    const bool copy = has_act || gdt != dt || !chunk_rows(e, grad, ldg);
+    const LinearGradSizes z = linear_grad_sizes(e, rows, outer, inner, copy,
+                                                grad_bias != nullptr, grad_x != nullptr,
+                                                grad_weight != nullptr);
+    if ((grad_x && (st = check_dispatch(gemm_threads(e, rows, inner, outer, true, false),
+                                        "vpa_head_linear_backward")) != VPA_OK) ||
+        (grad_weight && (st = check_dispatch(gemm_threads(e, outer, inner, rows, false, false),
+                                             "vpa_head_linear_backward")) != VPA_OK) ||
+        ((z.dz || grad_bias) &&
+         (st = check_dispatch(dz_threads(rows, outer, grad_bias != nullptr),
+                              "vpa_head_linear_backward")) != VPA_OK) ||
+        ((z.w || z.x) && (st = check_dispatch(dz_threads(rows > outer ? rows : outer, inner, false),
+                                              "vpa_head_linear_backward")) != VPA_OK))
+        return st;
+    if (rows > 0 && (st = check_workspace("vpa_head_linear_backward", workspace, workspace_bytes,
+                                          z.total())) != VPA_OK)
+        return st;
+    char* ws = (char*)workspace;
+    const void* dz = grad;
+    int64_t lddz = ldg, dz_cols = outer;
+    hipError_t he = hipSuccess;
+    if (z.dz || grad_bias) {
+        DzTask d{};
+        d.grad = grad;
+        d.ldg = ldg;
+        d.grad_f32 = gdt == VPA_F32;
+        d.pre = pre;
+        d.ldp = ldp;
+        d.act = act;
+        d.rows = rows;
+        d.cols = outer;
+        d.dz = z.dz ? ws : nullptr;
+        d.ldz = line_stride(e, outer);
+        d.bias = grad_bias;
+        // no rows: the sums have no slices, and the finishing kernel writes 0
+        d.part = grad_bias && rows > 0 ? (float*)(ws + z.dz) : nullptr;
+        if ((he = launch_dz(e, d, s)) != hipSuccess)
+            return hip_fail(he, "vpa_head_linear_backward (dz) launch");
+        if (z.dz) {
+            dz = ws;
+            lddz = dz_cols = d.ldz;
+        }
+    }
+    char* wcopy = ws + z.dz + z.part;
+    char* xcopy = wcopy + z.w;
+    void* gws = ws ? xcopy + z.x : nullptr;
+    if (grad_x && rows > 0) {
+        GemmTask t{};
+        t.a = dz;
+        t.a_m = lddz;
+        t.a_k = 1;
+        t.b = weight;
+        t.b_n = 1;
+        t.b_k = ldw;
+        t.a_k1 = true;
+        t.m = t.m_readable = rows;
+        t.n = t.n_readable = inner;
+        if (z.w && !chunk_rows(e, weight, ldw)) {
+            if ((he = copy_rows(e, weight, ldw, outer, inner, wcopy, s)) != hipSuccess)
+                return hip_fail(he, "vpa_head_linear_backward (weight) launch");
+            t.b = wcopy;
+            t.b_k = t.n_readable = line_stride(e, inner);
+        }
+        t.k = outer;
+        t.y = grad_x;
+        t.ldy = ldgx;
+        t.out_f32 = dt == VPA_F32;
+        t.ws = gws;
+        if ((he = launch_gemm(e, t, s)) != hipSuccess)
+            return hip_fail(he, "vpa_head_linear_backward (grad_x) launch");
+    }
+    if (grad_weight) {
+        GemmTask t{};
+        t.a = dz;
+        t.a_m = 1;
+        t.a_k = lddz;
+        t.b = x;
+        t.b_n = 1;
+        t.b_k = ldx;
+        t.m = outer;
+        t.m_readable = dz_cols;
+        t.n = t.n_readable = inner;
+        if (z.x && !chunk_rows(e, x, ldx)) {
+            if ((he = copy_rows(e, x, ldx, rows, inner, xcopy, s)) != hipSuccess)
+                return hip_fail(he, "vpa_head_linear_backward (x) launch");
+            t.b = xcopy;
+            t.b_k = t.n_readable = line_stride(e, inner);
+        }
+        t.k = rows;
+        t.y = grad_weight;
+        t.ldy = ldgw;
+        t.out_f32 = dt == VPA_F32;
+        t.ws = gws;
+        if ((he = launch_gemm(e, t, s)) != hipSuccess)
+            return hip_fail(he, "vpa_head_linear_backward (grad_weight) launch");
+    }
+    return ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -488,123 +617,21 @@ vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x
                                     int64_t ldgw, void* grad_bias, void* workspace,
                                     size_t workspace_bytes, void* stream) {
     const int dt = dtype_value(&dtype);
-    vpa_status st;
-    if ((st = check_dtype(dt)) != VPA_OK || (st = check_act(act)) != VPA_OK ||
-        (st = check_sizes("vpa_head_linear_backward", rows, outer, inner)) != VPA_OK)
-        return st;
-    const int e = esize_of(dt);
-    const bool has_act = act != VPA_ACT_NONE;
-    if (rows > 0) {
-        if ((st = check_matrix("grad", grad, e, ldg, outer)) != VPA_OK ||
-            (has_act && (st = check_matrix("pre", pre, e, ldp, outer)) != VPA_OK) ||
-            (grad_x && (st = check_matrix("weight", weight, e, ldw, inner)) != VPA_OK) ||
-            (grad_x && (st = check_matrix("grad_x", grad_x, e, ldgx, inner)) != VPA_OK) ||
-            (grad_weight && (st = check_matrix("x", x, e, ldx, inner)) != VPA_OK))
-            return st;
-    }
-    if ((grad_weight &&
-         (st = check_matrix("grad_weight", grad_weight, e, ldgw, inner)) != VPA_OK) ||
-        (grad_bias && (st = check_vector("grad_bias", grad_bias, e)) != VPA_OK))
-        return st;
-    // without an activation dz is grad, unless its rows are not aligned: a
-    // copy costs one pass over grad, the products' unaligned loads more
-    const bool copy = has_act || !chunk_rows(e, grad, ldg);
-    const LinearGradSizes z = linear_grad_sizes(e, rows, outer, inner, copy,
-                                                grad_bias != nullptr, grad_x != nullptr,
-                                                grad_weight != nullptr);
-    if ((grad_x && (st = check_dispatch(gemm_threads(e, rows, inner, outer, true, false),
-                                        "vpa_head_linear_backward")) != VPA_OK) ||
-        (grad_weight && (st = check_dispatch(gemm_threads(e, outer, inner, rows, false, false),
-                                             "vpa_head_linear_backward")) != VPA_OK) ||
-        ((z.dz || grad_bias) &&
-         (st = check_dispatch(dz_threads(rows, outer, grad_bias != nullptr),
-                              "vpa_head_linear_backward")) != VPA_OK) ||
-        ((z.w || z.x) && (st = check_dispatch(dz_threads(rows > outer ? rows : outer, inner, false),
-                                              "vpa_head_linear_backward")) != VPA_OK))
-        return st;
-    if (rows > 0 && (st = check_workspace("vpa_head_linear_backward", workspace, workspace_bytes,
-                                          z.total())) != VPA_OK)
-        return st;
-    hipStream_t s = (hipStream_t)stream;
-    char* ws = (char*)workspace;
-    const void* dz = grad;
-    int64_t lddz = ldg, dz_cols = outer;
-    hipError_t he = hipSuccess;
-    if (z.dz || grad_bias) {
-        DzTask d{};
-        d.grad = grad;
-        d.ldg = ldg;
-        d.pre = pre;
-        d.ldp = ldp;
-        d.act = act;
-        d.rows = rows;
-        d.cols = outer;
-        d.dz = z.dz ? ws : nullptr;
-        d.ldz = line_stride(e, outer);
-        d.bias = grad_bias;
-        // no rows: the sums have no slices, and the finishing kernel writes 0
-        d.part = grad_bias && rows > 0 ? (float*)(ws + z.dz) : nullptr;
-        if ((he = launch_dz(e, d, s)) != hipSuccess)
-            return hip_fail(he, "vpa_head_linear_backward (dz) launch");
-        if (z.dz) {
-            dz = ws;
-            lddz = dz_cols = d.ldz;
-        }
-    }
-    char* wcopy = ws + z.dz + z.part;
-    char* xcopy = wcopy + z.w;
-    void* gws = ws ? xcopy + z.x : nullptr;
-    if (grad_x && rows > 0) {
-        GemmTask t{};
-        t.a = dz;
-        t.a_m = lddz;
-        t.a_k = 1;
-        t.b = weight;
-        t.b_n = 1;
-        t.b_k = ldw;
-        t.a_k1 = true;
-        t.m = t.m_readable = rows;
-        t.n = t.n_readable = inner;
-        if (z.w && !chunk_rows(e, weight, ldw)) {
-            if ((he = copy_rows(e, weight, ldw, outer, inner, wcopy, s)) != hipSuccess)
-                return hip_fail(he, "vpa_head_linear_backward (weight) launch");
-            t.b = wcopy;
-            t.b_k = t.n_readable = line_stride(e, inner);
-        }
-        t.k = outer;
-        t.y = grad_x;
-        t.ldy = ldgx;
-        t.out_f32 = dt == VPA_F32;
-        t.ws = gws;
-        if ((he = launch_gemm(e, t, s)) != hipSuccess)
-            return hip_fail(he, "vpa_head_linear_backward (grad_x) launch");
-    }
-    if (grad_weight) {
-        GemmTask t{};
-        t.a = dz;
-        t.a_m = 1;
-        t.a_k = lddz;
-        t.b = x;
-        t.b_n = 1;
-        t.b_k = ldx;
-        t.m = outer;
-        t.m_readable = dz_cols;
-        t.n = t.n_readable = inner;
-        if (z.x && !chunk_rows(e, x, ldx)) {
-            if ((he = copy_rows(e, x, ldx, rows, inner, xcopy, s)) != hipSuccess)
-                return hip_fail(he, "vpa_head_linear_backward (x) launch");
-            t.b = xcopy;
-            t.b_k = t.n_readable = line_stride(e, inner);
-        }
-        t.k = rows;
-        t.y = grad_weight;
-        t.ldy = ldgw;
-        t.out_f32 = dt == VPA_F32;
-        t.ws = gws;
-        if ((he = launch_gemm(e, t, s)) != hipSuccess)
-            return hip_fail(he, "vpa_head_linear_backward (grad_weight) launch");
-    }
-    return ok();
+    return linear_backward(grad, ldg, dt, x, ldx, weight, ldw, pre, ldp, dt, rows, outer, inner,
+                           act, grad_x, ldgx, grad_weight, ldgw, grad_bias, workspace,
+                           workspace_bytes, (hipStream_t)stream);
+}
+
+vpa_status vpa_head_linear_backward_typed(const void* grad, int64_t ldg, vpa_dtype grad_dtype,
+                                          const void* x, int64_t ldx, const void* weight,
+                                          int64_t ldw, const void* pre, int64_t ldp,
+                                          vpa_dtype dtype, int64_t rows, int64_t outer,
+                                          int64_t inner, int32_t act, void* grad_x, int64_t ldgx,
+                                          void* grad_weight, int64_t ldgw, void* grad_bias,
+                                          void* workspace, size_t workspace_bytes, void* stream) {
+    return linear_backward(grad, ldg, dtype_value(&grad_dtype), x, ldx, weight, ldw, pre, ldp,
+                           dtype_value(&dtype), rows, outer, inner, act, grad_x, ldgx, grad_weight,
+                           ldgw, grad_bias, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
 vpa_status vpa_layer_norm(const void* x, int64_t ldx, vpa_dtype dtype, const void* weight,

@@ -13,6 +13,7 @@ static __typeof__(&vpa_token_logprobs) p_token_logprobs;
 static __typeof__(&vpa_token_logprobs_backward) p_token_logprobs_backward;
 static __typeof__(&vpa_head_linear) p_head_linear;
 static __typeof__(&vpa_head_linear_backward) p_head_linear_backward;
+static __typeof__(&vpa_head_linear_backward_typed) p_head_linear_backward_typed;
 static __typeof__(&vpa_layer_norm) p_layer_norm;
 static __typeof__(&vpa_layer_norm_backward) p_layer_norm_backward;
 
@@ -23,6 +24,7 @@ static const struct entry k_entries[] = {
     {"vpa_token_logprobs_backward", (void**)&p_token_logprobs_backward},
     {"vpa_head_linear", (void**)&p_head_linear},
     {"vpa_head_linear_backward", (void**)&p_head_linear_backward},
+    {"vpa_head_linear_backward_typed", (void**)&p_head_linear_backward_typed},
     {"vpa_layer_norm", (void**)&p_layer_norm},
     {"vpa_layer_norm_backward", (void**)&p_layer_norm_backward},
 };
@@ -125,6 +127,23 @@ static PyObject* py_head_linear_backward(PyObject* self, PyObject* const* args, 
                   inner, act, gx, ldgx, gw, ldgw, gb, ws, ws_bytes, stream));
 }
 
+static PyObject* py_head_linear_backward_typed(PyObject* self, PyObject* const* args,
+                                               Py_ssize_t nargs) {
+    (void)self;
+    void *grad, *x, *w, *pre, *gx, *gw, *gb, *ws, *stream;
+    int64_t ldg, ldx, ldw, ldp, rows, outer, inner, ldgx, ldgw;
+    vpa_dtype gdt, dt;
+    int32_t act;
+    size_t ws_bytes;
+    if (!bound("vpa_head_linear_backward_typed", (const void*)p_head_linear_backward_typed) ||
+        !parse("vpa_head_linear_backward_typed", args, nargs, "pldplplpldllliplplppzp", &grad,
+               &ldg, &gdt, &x, &ldx, &w, &ldw, &pre, &ldp, &dt, &rows, &outer, &inner, &act, &gx,
+               &ldgx, &gw, &ldgw, &gb, &ws, &ws_bytes, &stream))
+        return NULL;
+    RETURN_STATUS(p_head_linear_backward_typed(grad, ldg, gdt, x, ldx, w, ldw, pre, ldp, dt, rows,
+                  outer, inner, act, gx, ldgx, gw, ldgw, gb, ws, ws_bytes, stream));
+}
+
 static PyObject* py_layer_norm(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     (void)self;
     void *x, *w, *b, *y, *mean, *rstd, *stream;
@@ -172,6 +191,7 @@ static PyMethodDef k_methods[] = {
     {"vpa_token_logprobs_backward", FASTCALL(py_token_logprobs_backward), "vpa_token_logprobs_backward (include/vpa_head.h)"},
     {"vpa_head_linear", FASTCALL(py_head_linear), "vpa_head_linear (include/vpa_head.h)"},
     {"vpa_head_linear_backward", FASTCALL(py_head_linear_backward), "vpa_head_linear_backward (include/vpa_head.h)"},
+    {"vpa_head_linear_backward_typed", FASTCALL(py_head_linear_backward_typed), "vpa_head_linear_backward_typed (include/vpa_head.h)"},
     {"vpa_layer_norm", FASTCALL(py_layer_norm), "vpa_layer_norm (include/vpa_head.h)"},
     {"vpa_layer_norm_backward", FASTCALL(py_layer_norm_backward), "vpa_layer_norm_backward (include/vpa_head.h)"},
     {"bind", FASTCALL(py_bind), "bind(name, address): the entry point `name` is at `address`"},

@@ -95,7 +95,7 @@ struct Eight {
 // large copy (93 with a row at a time).
 constexpr int kDzCols = 512, kDzRows = 4;
 
-template <typename T, int ACT>
+template <typename T, typename G, int ACT>
 __global__ __launch_bounds__(kThreads) void dz_kernel(DzTask t, int32_t splits) {
     __shared__ float sums[4][kDzCols];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -105,11 +105,12 @@ __global__ __launch_bounds__(kThreads) void dz_kernel(DzTask t, int32_t splits) 
     const int n = t.cols - c < 8 ? (int)(t.cols - c) : 8;       // columns of this lane, or < 1
     float sum[8] = {};
     for (int64_t r = r0 + wave; r < r1; r += 4 * kDzRows) {
-        Eight<T> g[kDzRows], z[kDzRows];
+        Eight<G> g[kDzRows];
+        Eight<T> z[kDzRows];
 #pragma unroll
         for (int k = 0; k < kDzRows; ++k)
             if (r + 4 * k < r1) {
-                g[k].load((const T*)t.grad + (r + 4 * k) * t.ldg + c, n);
+                g[k].load((const G*)t.grad + (r + 4 * k) * t.ldg + c, n);
                 if constexpr (ACT != VPA_ACT_NONE)
                     z[k].load((const T*)t.pre + (r + 4 * k) * t.ldp + c, n);
             }
@@ -184,7 +185,7 @@ int64_t stages_of(int esize, int64_t k) {
     return k > 0 ? (k * esize + 127) / 128 : 1;
 }
 
-template <typename T>
+template <typename T, typename G>
 hipError_t launch_dz_typed(const DzTask& t, hipStream_t stream) {
     const int32_t splits = dz_splits(t.rows, t.cols);
     const dim3 grid((uint32_t)((t.cols + kDzCols - 1) / kDzCols), (uint32_t)splits);
@@ -192,16 +193,16 @@ hipError_t launch_dz_typed(const DzTask& t, hipStream_t stream) {
     hipError_t e;
     switch (t.act) {
     case VPA_ACT_RELU:
-        e = launch(dz_kernel<T, VPA_ACT_RELU>, grid, block, 0, stream, t, splits);
+        e = launch(dz_kernel<T, G, VPA_ACT_RELU>, grid, block, 0, stream, t, splits);
         break;
     case VPA_ACT_GELU:
-        e = launch(dz_kernel<T, VPA_ACT_GELU>, grid, block, 0, stream, t, splits);
+        e = launch(dz_kernel<T, G, VPA_ACT_GELU>, grid, block, 0, stream, t, splits);
         break;
     case VPA_ACT_SILU:
-        e = launch(dz_kernel<T, VPA_ACT_SILU>, grid, block, 0, stream, t, splits);
+        e = launch(dz_kernel<T, G, VPA_ACT_SILU>, grid, block, 0, stream, t, splits);
         break;
     default:
-        e = launch(dz_kernel<T, VPA_ACT_NONE>, grid, block, 0, stream, t, splits);
+        e = launch(dz_kernel<T, G, VPA_ACT_NONE>, grid, block, 0, stream, t, splits);
     }
     if (e != hipSuccess || !t.bias)
         return e;
@@ -422,7 +423,10 @@ int64_t dz_threads(int64_t rows, int64_t cols, bool bias) {
 }
 
 hipError_t launch_dz(int esize, const DzTask& t, hipStream_t stream) {
-    return esize == 2 ? launch_dz_typed<uint16_t>(t, stream) : launch_dz_typed<float>(t, stream);
+    if (esize == 4)
+        return launch_dz_typed<float, float>(t, stream);
+    return t.grad_f32 ? launch_dz_typed<uint16_t, float>(t, stream)
+                      : launch_dz_typed<uint16_t, uint16_t>(t, stream);
 }
 
 }  // namespace vpa

@@ -135,8 +135,9 @@ hipError_t launch_linear_rows(int esize, const GemmTask& t, hipStream_t stream);
 // dz = grad * act'(pre) (of the operands' type, skipped if dz is null), and
 // the column sums of dz (before rounding) into `bias` (skipped if null).
 struct DzTask {
-    const void* grad;
+    const void* grad;         // of the operands' type or, with grad_f32, fp32
     int64_t ldg;
+    bool grad_f32;
     const void* pre;
     int64_t ldp;
     int32_t act;

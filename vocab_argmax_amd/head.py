@@ -28,7 +28,7 @@ HEAD_SYMBOLS = ("vpa_logprobs_workspace", "vpa_logprob_words", "vpa_head_linear_
                 "vpa_head_linear_backward_workspace", "vpa_layer_norm_backward_workspace",
                 "vpa_logprob_stats", "vpa_combine_logprobs", "vpa_token_logprobs",
                 "vpa_token_logprobs_backward", "vpa_head_linear", "vpa_head_linear_backward",
-                "vpa_layer_norm", "vpa_layer_norm_backward")
+                "vpa_head_linear_backward_typed", "vpa_layer_norm", "vpa_layer_norm_backward")
 
 _bound_to = None
 _call_mod = None
@@ -53,6 +53,8 @@ def _bind(loaded):
                                  dt, vp, i64, vp, sz, vp]),
         "vpa_head_linear_backward": (dt, [vp, i64, vp, i64, vp, i64, vp, i64, dt, i64, i64, i64,
                                           i32, vp, i64, vp, i64, vp, vp, sz, vp]),
+        "vpa_head_linear_backward_typed": (dt, [vp, i64, dt, vp, i64, vp, i64, vp, i64, dt, i64,
+                                                i64, i64, i32, vp, i64, vp, i64, vp, vp, sz, vp]),
         "vpa_layer_norm": (dt, [vp, i64, dt, vp, vp, dt, i64, i64, f32, vp, i64, vp, vp, vp]),
         "vpa_layer_norm_backward": (dt, [vp, i64, vp, i64, dt, vp, dt, vp, vp, i64, i64, vp, i64,
                                          vp, vp, vp, sz, vp]),
@@ -461,10 +463,18 @@ def head_linear_backward(grad, x, weight, pre=None, activation="none", need_x=Tr
                          need_weight=True, need_bias=True, workspace=None, *, stream=None):
     """(grad_x, grad_weight, grad_bias) of head_linear for the gradient of y
     [rows, outer], each None where not needed; the residual's gradient is
-    `grad` itself.  pre: head_linear's, required with an activation."""
-    rows, outer, ldg, code = _rows_of(grad, "grad")
-    dev, dt = grad.device, grad.dtype
+    `grad` itself.  grad has y's dtype: x's, or float32 (fp32 logits of bf16
+    operands); the results have x's.  pre: head_linear's, required with an
+    activation."""
+    rows, outer, ldg, grad_code = _rows_of(grad, "grad")
+    dev, dt = grad.device, x.dtype
     act = _activation(activation)
+    if dt is grad.dtype:
+        code = grad_code
+    elif dt is torch.bfloat16:
+        code = VPA_BF16
+    else:
+        raise TypeError(f"x must be {grad.dtype}, not {dt}")
     if x.dim() != 2:
         raise ValueError("x must be 2-D [rows, inner]")
     inner = x.shape[1]
@@ -476,12 +486,12 @@ def head_linear_backward(grad, x, weight, pre=None, activation="none", need_x=Tr
     gx = torch.empty((rows, inner), dtype=dt, device=dev) if need_x else None
     gw = torch.empty((outer, inner), dtype=dt, device=dev) if need_weight else None
     gb = torch.empty(outer, dtype=dt, device=dev) if need_bias else None
-    fn = head_call().vpa_head_linear_backward
+    fn = head_call().vpa_head_linear_backward_typed
     _ws, ws, ws_bytes = _workspace(workspace, _linear_grad_workspace(code, rows, outer, inner),
                                    dev)
-    _launch(fn, stream, dev, grad.data_ptr(), ldg, x.data_ptr(), ldx, weight.data_ptr(), ldw,
-            _vp(pre) if act else None, ldp, code, rows, outer, inner, act, _vp(gx), inner, _vp(gw),
-            inner, _vp(gb), ws, ws_bytes)
+    _launch(fn, stream, dev, grad.data_ptr(), ldg, grad_code, x.data_ptr(), ldx, weight.data_ptr(),
+            ldw, _vp(pre) if act else None, ldp, code, rows, outer, inner, act, _vp(gx), inner,
+            _vp(gw), inner, _vp(gb), ws, ws_bytes)
     return gx, gw, gb
 
 
