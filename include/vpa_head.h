@@ -146,6 +146,14 @@ size_t vpa_head_linear_workspace(vpa_dtype dtype, int64_t rows, int64_t outer, i
 size_t vpa_head_linear_backward_workspace(vpa_dtype dtype, int64_t rows, int64_t outer,
                                           int64_t inner);
 
+/* What one call of the backward pass needs of it: with_dz is 0 only where act
+ * is VPA_ACT_NONE, the gradient is of type `dtype`, its address is a multiple
+ * of 16 bytes and its row stride too, so that the products read the gradient
+ * itself; need_x, need_weight and need_bias say which outputs are not NULL. */
+size_t vpa_head_linear_backward_need(vpa_dtype dtype, int64_t rows, int64_t outer, int64_t inner,
+                                     int32_t with_dz, int32_t need_x, int32_t need_weight,
+                                     int32_t need_bias);
+
 /*  x, weight, bias, residual  of type `dtype`; bias [outer], residual
  *             [rows][outer], either may be NULL.  outer, inner >= 1, below
  *             2^31; rows below 2^31.

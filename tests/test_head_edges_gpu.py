@@ -296,3 +296,26 @@ def test_fp32_logits_of_bf16_operands_train():
         vpa.head_linear_backward(d.to(BF), x.float(), w.float())
     with pytest.raises(TypeError):
         vpa.head_linear_backward(d.half(), x, w)
+
+
+def test_backward_takes_no_memory_for_what_it_does_not_do():
+    """An aligned gradient without an activation is read in place: no dz."""
+    n, k, v = 1024, 64, 65536
+    g = gen(31)
+    x, w = randn(g, n, k, dtype=BF), randn(g, v, k, dtype=BF, scale=k ** -0.5)
+    gr = randn(g, n, v, dtype=BF)
+
+    def peak(call):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        call()
+        return torch.cuda.max_memory_allocated() - before
+    vpa.head_linear_backward(gr, x, w)
+    results = 2 * (n * k + v * k + v) + (1 << 20)        # and the allocator's rounding
+    dz = 2 * n * v
+    lean = peak(lambda: vpa.head_linear_backward(gr, x, w, need_x=False, need_bias=False))
+    code = vpa.VPA_BF16
+    slices = vpa.head_lib().vpa_head_linear_backward_need(code, n, v, k, 0, 0, 1, 0)
+    assert lean <= results + slices and slices < dz / 2
+    assert peak(lambda: vpa.head_linear_backward(gr, x, w, gr, "silu")) >= dz

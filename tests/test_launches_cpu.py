@@ -197,3 +197,27 @@ def test_cuts_that_the_gpu_tests_mean(record):
         assert status == OK, message
         part = [l for l in got if "logprob_part_kernel" in l["name"]]
         assert len(part) == 1 and part[0]["chunks"] >= 2 and part[0]["k"] == vecs, (call, part)
+
+
+def test_backward_needs_what_it_says(record):
+    """vpa_head_linear_backward_need is what the call checks, to the byte, and
+    every launch keeps to it."""
+    some = [((rows, outer, inner), act, ldg, need, dt)
+            for rows, outer, inner in ((40, 512, 4096), (64, 50257, 2), (300, 4090, 785),
+                                       (2048, 8192, 2047), (4096, 4352, 4096))
+            for act in (0, 3) for ldg in (outer, (outer + 7) // 8 * 8, (outer + 7) // 8 * 8 + 1)
+            for need in ("xwb", "x", "w", "b", "xw") for dt in (BF16, F32)]
+    need = record([["vpa_head_linear_backward_need",
+                    [dt, *size, int(act != 0 or ldg % (8 if dt == BF16 else 4) != 0)] +
+                    [int(c in want) for c in "xwb"]] for size, act, ldg, want, dt in some])
+    exact, short = [], []
+    for (size, act, ldg, want, dt), (n, _, _) in zip(some, need):
+        exact.append(linear_backward(*size, dt=dt, ws_bytes=n, act=act, ldg=ldg, need=want))
+        short.append(linear_backward(*size, dt=dt, ws_bytes=n - 1, act=act, ldg=ldg, need=want))
+    for call, (status, message, got) in zip(exact, record(exact)):
+        assert status == OK and got, (call, message)
+        for l in got:
+            assert l["part_bytes"] == 0 or (
+                l["part"] >= WS and l["part"] + l["part_bytes"] <= WS + call[1][-2]), (call, l)
+    for (n, _, _), call, (status, message, got) in zip(need, short, record(short)):
+        assert n == 0 or (status != OK and "workspace" in message and not got), call

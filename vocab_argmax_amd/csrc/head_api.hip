@@ -538,6 +538,17 @@ size_t vpa_head_linear_backward_workspace(vpa_dtype dtype, int64_t rows, int64_t
     return linear_grad_sizes(esize, rows, outer, inner, true, true, true, true).total();
 }
 
+size_t vpa_head_linear_backward_need(vpa_dtype dtype, int64_t rows, int64_t outer, int64_t inner,
+                                     int32_t with_dz, int32_t need_x, int32_t need_weight,
+                                     int32_t need_bias) {
+    const int esize = esize_of(dtype_value(&dtype));
+    if (!esize || rows < 1 || check_sizes("", rows, outer, inner) != VPA_OK)
+        return 0;
+    return linear_grad_sizes(esize, rows, outer, inner, with_dz != 0, need_bias != 0, need_x != 0,
+                             need_weight != 0)
+        .total();
+}
+
 vpa_status vpa_head_linear(const void* x, int64_t ldx, const void* weight, int64_t ldw,
                            const void* bias, const void* residual, int64_t ldr, vpa_dtype dtype,
                            int64_t rows, int64_t outer, int64_t inner, int32_t act, void* y,

@@ -14,6 +14,7 @@ static __typeof__(&vpa_token_logprobs_backward) p_token_logprobs_backward;
 static __typeof__(&vpa_head_linear) p_head_linear;
 static __typeof__(&vpa_head_linear_backward) p_head_linear_backward;
 static __typeof__(&vpa_head_linear_backward_typed) p_head_linear_backward_typed;
+static __typeof__(&vpa_head_linear_backward_need) p_head_linear_backward_need;
 static __typeof__(&vpa_layer_norm) p_layer_norm;
 static __typeof__(&vpa_layer_norm_backward) p_layer_norm_backward;
 
@@ -25,6 +26,7 @@ static const struct entry k_entries[] = {
     {"vpa_head_linear", (void**)&p_head_linear},
     {"vpa_head_linear_backward", (void**)&p_head_linear_backward},
     {"vpa_head_linear_backward_typed", (void**)&p_head_linear_backward_typed},
+    {"vpa_head_linear_backward_need", (void**)&p_head_linear_backward_need},
     {"vpa_layer_norm", (void**)&p_layer_norm},
     {"vpa_layer_norm_backward", (void**)&p_layer_norm_backward},
 };
@@ -144,6 +146,21 @@ static PyObject* py_head_linear_backward_typed(PyObject* self, PyObject* const* 
                   outer, inner, act, gx, ldgx, gw, ldgw, gb, ws, ws_bytes, stream));
 }
 
+/* Host-only: the bytes of one call's workspace. */
+static PyObject* py_head_linear_backward_need(PyObject* self, PyObject* const* args,
+                                              Py_ssize_t nargs) {
+    (void)self;
+    vpa_dtype dt;
+    int64_t rows, outer, inner;
+    int32_t dz, need_x, need_w, need_b;
+    if (!bound("vpa_head_linear_backward_need", (const void*)p_head_linear_backward_need) ||
+        !parse("vpa_head_linear_backward_need", args, nargs, "dllliiii", &dt, &rows, &outer,
+               &inner, &dz, &need_x, &need_w, &need_b))
+        return NULL;
+    return PyLong_FromSize_t(p_head_linear_backward_need(dt, rows, outer, inner, dz, need_x,
+                                                         need_w, need_b));
+}
+
 static PyObject* py_layer_norm(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     (void)self;
     void *x, *w, *b, *y, *mean, *rstd, *stream;
@@ -192,6 +209,7 @@ static PyMethodDef k_methods[] = {
     {"vpa_head_linear", FASTCALL(py_head_linear), "vpa_head_linear (include/vpa_head.h)"},
     {"vpa_head_linear_backward", FASTCALL(py_head_linear_backward), "vpa_head_linear_backward (include/vpa_head.h)"},
     {"vpa_head_linear_backward_typed", FASTCALL(py_head_linear_backward_typed), "vpa_head_linear_backward_typed (include/vpa_head.h)"},
+    {"vpa_head_linear_backward_need", FASTCALL(py_head_linear_backward_need), "vpa_head_linear_backward_need (include/vpa_head.h)"},
     {"vpa_layer_norm", FASTCALL(py_layer_norm), "vpa_layer_norm (include/vpa_head.h)"},
     {"vpa_layer_norm_backward", FASTCALL(py_layer_norm_backward), "vpa_layer_norm_backward (include/vpa_head.h)"},
     {"bind", FASTCALL(py_bind), "bind(name, address): the entry point `name` is at `address`"},

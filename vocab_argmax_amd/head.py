@@ -23,12 +23,14 @@ MAX_TOP = 64             # VPA_MAX_TOP
 MAX_ROW_TOKENS = 64      # VPA_MAX_ROW_TOKENS
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}   # vpa_act
 
-# Every symbol include/vpa_head.h declares; the first five are host-only.
+# Every symbol include/vpa_head.h declares; the first five are called through
+# ctypes alone, the others through the marshalling module too.
 HEAD_SYMBOLS = ("vpa_logprobs_workspace", "vpa_logprob_words", "vpa_head_linear_workspace",
                 "vpa_head_linear_backward_workspace", "vpa_layer_norm_backward_workspace",
                 "vpa_logprob_stats", "vpa_combine_logprobs", "vpa_token_logprobs",
                 "vpa_token_logprobs_backward", "vpa_head_linear", "vpa_head_linear_backward",
-                "vpa_head_linear_backward_typed", "vpa_layer_norm", "vpa_layer_norm_backward")
+                "vpa_head_linear_backward_typed", "vpa_head_linear_backward_need",
+                "vpa_layer_norm", "vpa_layer_norm_backward")
 
 _bound_to = None
 _call_mod = None
@@ -55,6 +57,7 @@ def _bind(loaded):
                                           i32, vp, i64, vp, i64, vp, vp, sz, vp]),
         "vpa_head_linear_backward_typed": (dt, [vp, i64, dt, vp, i64, vp, i64, vp, i64, dt, i64,
                                                 i64, i64, i32, vp, i64, vp, i64, vp, vp, sz, vp]),
+        "vpa_head_linear_backward_need": (sz, [dt, i64, i64, i64, i32, i32, i32, i32]),
         "vpa_layer_norm": (dt, [vp, i64, dt, vp, vp, dt, i64, i64, f32, vp, i64, vp, vp, vp]),
         "vpa_layer_norm_backward": (dt, [vp, i64, vp, i64, dt, vp, dt, vp, vp, i64, i64, vp, i64,
                                          vp, vp, vp, sz, vp]),
@@ -78,7 +81,7 @@ def head_lib():
         for name in _vpa_head_call.entries():
             _vpa_head_call.bind(name, ctypes.cast(getattr(loaded, name), ctypes.c_void_p).value)
         for fn in (_logprobs_workspace, _linear_workspace, _linear_grad_workspace,
-                   _norm_grad_workspace):
+                   _linear_grad_need, _norm_grad_workspace):
             fn.cache_clear()
         _call_mod, _bound_to = _vpa_head_call, loaded
     return loaded
@@ -106,6 +109,12 @@ def _linear_workspace(code, rows, outer, inner):
 @functools.lru_cache(maxsize=256)
 def _linear_grad_workspace(code, rows, outer, inner):
     return int(head_lib().vpa_head_linear_backward_workspace(code, rows, outer, inner))
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_grad_need(code, rows, outer, inner, dz, need_x, need_weight, need_bias):
+    return int(head_lib().vpa_head_linear_backward_need(code, rows, outer, inner, dz, need_x,
+                                                        need_weight, need_bias))
 
 
 @functools.lru_cache(maxsize=256)
@@ -487,9 +496,14 @@ def head_linear_backward(grad, x, weight, pre=None, activation="none", need_x=Tr
     gw = torch.empty((outer, inner), dtype=dt, device=dev) if need_weight else None
     gb = torch.empty(outer, dtype=dt, device=dev) if need_bias else None
     fn = head_call().vpa_head_linear_backward_typed
-    _ws, ws, ws_bytes = _workspace(workspace, _linear_grad_workspace(code, rows, outer, inner),
+    at = grad.data_ptr()
+    # the products read an aligned gradient itself: no place for dz then
+    dz = bool(act or code != grad_code or at % 16 or ldg % (4 if code == VPA_F32 else 8))
+    _ws, ws, ws_bytes = _workspace(workspace, _linear_grad_need(code, rows, outer, inner, dz,
+                                                                bool(need_x), bool(need_weight),
+                                                                bool(need_bias)),
                                    dev)
-    _launch(fn, stream, dev, grad.data_ptr(), ldg, grad_code, x.data_ptr(), ldx, weight.data_ptr(),
+    _launch(fn, stream, dev, at, ldg, grad_code, x.data_ptr(), ldx, weight.data_ptr(),
             ldw, _vp(pre) if act else None, ldp, code, rows, outer, inner, act, _vp(gx), inner,
             _vp(gw), inner, _vp(gb), ws, ws_bytes)
     return gx, gw, gb
