@@ -319,3 +319,34 @@ def test_backward_takes_no_memory_for_what_it_does_not_do():
     slices = vpa.head_lib().vpa_head_linear_backward_need(code, n, v, k, 0, 0, 1, 0)
     assert lean <= results + slices and slices < dz / 2
     assert peak(lambda: vpa.head_linear_backward(gr, x, w, gr, "silu")) >= dz
+
+
+# ---------------------------------------------------------------------------
+# layer norm at the ends of the range
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("c", [1, 5, 9, 63, 100])
+def test_layer_norm_backward_of_constant_rows_far_from_0(c, dtype):
+    """mean * rstd is past fp32's range, (x - mean) * rstd is 0: the lanes past
+    the row's end have no part in its sums."""
+    g = gen(c)
+    x = torch.full((3, c), 1.5e36, device=DEV).to(dtype)
+    x[1] = -1.5e36
+    x[2] = randn(g, c, dtype=dtype)
+    gr, w = randn(g, 3, c, dtype=dtype), randn(g, c, dtype=dtype)
+    y, mean, rstd = vpa.layer_norm(x, w, None, with_stats=True)
+    assert bool((mean[:2].abs() > 1e36).all()) and bool((rstd[:2] > 300).all())
+    gx, gw, gb = vpa.layer_norm_backward(gr, x, mean, rstd, w)
+    rs = rstd.double()[:, None]
+    xh = (x.double() - mean.double()[:, None]) * rs
+    gd = gr.double()
+    u = gd * w.double()
+    m1, m2 = u.mean(1, keepdim=True), (u * xh).mean(1, keepdim=True)
+    want = rs * (u - m1 - xh * m2)
+    a1, a2 = u.abs().mean(1, keepdim=True), (u * xh).abs().mean(1, keepdim=True)
+    tol = rs * (8 * U + 34 * U) * (u.abs() + a1 + xh.abs() * a2)
+    near(gx, want, tol + half(dtype) * (want.abs() + tol), "grad_x")
+    for got, t, what in ((gw, gd * xh, "grad_weight"), (gb, gd, "grad_bias")):
+        tol = 9 * U * t.abs().sum(0)
+        near(got, t.sum(0), tol + half(dtype) * (t.sum(0).abs() + tol), what)

@@ -64,6 +64,22 @@ struct RowPart {
             }
         }
     }
+    // `value` in every place past the row's end
+    static __device__ __forceinline__ void fill_past(T value, int cols, u32x4_t (&v)[NV]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            union {
+                T e[VEC];
+                u32x4_t v;
+            } u;
+            u.v = v[i];
+            const int n = count(i, cols);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                u.e[e] = e < n ? u.e[e] : value;
+            v[i] = u.v;
+        }
+    }
     static __device__ __forceinline__ void store(T* row, int cols, int i,
                                                  const float (&f)[VEC]) {
         const int n = count(i, cols);
@@ -208,6 +224,14 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_grad_kerne
         const int64_t after = row + P::row_step();
         if (after < t.rows)
             fetch(after);
+        // The xh of the 0 past the row meets grad's 0 there, and has to be finite:
+        // where it is not, which takes elements that hardly differ, the mean
+        // stands for it.
+        if (!(fabsf(mean) * rstd < __builtin_inff())) {
+            T value;
+            from_f32(value, mean);
+            P::fill_past(value, cols, x);
+        }
         float a = 0.0f, b = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
