@@ -179,7 +179,9 @@ vpa_status vpa_head_linear(const void* x, int64_t ldx, const void* weight, int64
  * required for grad_x and x for grad_weight.  rows = 0 clears grad_weight and
  * grad_bias.  For bf16, dz is rounded to bf16 for the two products (their
  * operands' type) where an activation makes it differ from grad; grad_bias
- * sums the unrounded fp32 values. */
+ * sums the unrounded fp32 values.  With that rounding and pre's the gradients
+ * of a silu layer are 0.0024 (relative) off 64 bits, where the rounding of the
+ * results alone is 0.0017; callers who need more pass fp32 operands. */
 vpa_status vpa_head_linear_backward(const void* grad, int64_t ldg, const void* x, int64_t ldx,
                                     const void* weight, int64_t ldw, const void* pre, int64_t ldp,
                                     vpa_dtype dtype, int64_t rows, int64_t outer, int64_t inner,
