@@ -16,10 +16,12 @@
 // unsigned compare, and no two columns are equal.
 //
 // Large batches are bound by reading the logits once, small ones by the
-// latency of a chunk and of two launches.  Measured, kernels alone: 1024 x
-// 200064 bf16 with 8 alternatives 77 us, 5.3 TB/s; 2048 x 50257 bf16 44 us
-// (4.7; rows that are not aligned); 512 x 50257 fp32 22 + 4 us; 32 x 151936
-// bf16 with 20 alternatives 11.7 + 5.4 us; one row 6.9 + 4.0 us.
+// latency of a chunk and of two launches.  Measured, kernels alone in a trace:
+// 1024 x 200064 bf16 with 8 alternatives 78 us, 5.2 TB/s; 2048 x 50257 bf16
+// 44 us (4.9; rows that are not aligned); 512 x 50257 fp32 21 + 4 us; 32 x
+// 151936 bf16 with 20 alternatives 11.0 + 5.4 us; one row 6.9 + 3.6 us.
+// Calls: records of one of 8 shards of 1024 x 200064 26 us, their combination
+// 7 us; of 32 rows with 20 alternatives 13.8 and 7.2 us.
 #include "vpa_device.h"
 #include "vpa_head_internal.h"
 #include "vpa_math.h"
@@ -179,9 +181,9 @@ __device__ __forceinline__ uint32_t wave_nth_key(uint32_t key, int n) {
     return nth;
 }
 
-// The largest n_top of the n orders order(i) (0: none), by the whole
-// workgroup, in order into out[]; returns how many there are (at most
-// n_top).  Each candidate's place is the number of larger ones.
+// The largest n_top of the n orders cand[] (0: none), by the whole workgroup,
+// in order into out[]: each candidate's place is the number of larger ones.
+// Places past n are left as they are.
 __device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int n_top,
                                                 uint64_t* out) {
     for (int i = threadIdx.x; i < n; i += kThreads) {
@@ -193,6 +195,32 @@ __device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int
         if (larger < n_top)
             out[larger] = mine;
     }
+}
+
+// The largest of three (a NaN among them: any of them or NaN): one
+// instruction, where fmaxf would first quiet inputs that come from bit
+// operations.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+    return d;
+}
+
+// z = (x - M) log2(e) as one multiply-add, x log2(e) - b with b = M log2(e)
+// rounded: what the rounding took off is put right on a chunk's sums.
+struct LaneScale {
+    float b, off, fix;
+    __device__ __forceinline__ void set(float m) {
+        b = m * kLog2e;
+        off = __builtin_fmaf(m, kLog2e, -b);
+        fix = exp2_fast(-off);
+    }
+};
+
+template <int ESIZE>
+__device__ __forceinline__ u32x4_t all_neg_inf() {
+    constexpr uint32_t w = ESIZE == 2 ? 0xFF80FF80u : 0xFF800000u;
+    return u32x4_t{w, w, w, w};
 }
 
 // One segment of a row: its Sums and its first n_top columns.
@@ -220,32 +248,6 @@ __device__ __forceinline__ void rank_candidates(const uint64_t* cand, int n, int
 // each the larger ones.  Few columns pass T, so the scan costs one maximum
 // and one comparison a vector.  A chunk with a NaN, an infinity or more
 // candidates than the list holds takes n_top maxima over the registers.
-// The largest of three (a NaN among them: any of them or NaN): one
-// instruction, where fmaxf would first quiet inputs that come from bit
-// operations.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
-    return d;
-}
-
-// z = (x - M) log2(e) as one multiply-add, x log2(e) - b with b = M log2(e)
-// rounded: what the rounding took off is put right on a chunk's sums.
-struct LaneScale {
-    float b, off, fix;
-    __device__ __forceinline__ void set(float m) {
-        b = m * kLog2e;
-        off = __builtin_fmaf(m, kLog2e, -b);
-        fix = exp2_fast(-off);
-    }
-};
-
-template <int ESIZE>
-__device__ __forceinline__ u32x4_t all_neg_inf() {
-    constexpr uint32_t w = ESIZE == 2 ? 0xFF80FF80u : 0xFF800000u;
-    return u32x4_t{w, w, w, w};
-}
-
 template <int ESIZE, int U>
 __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, LogprobCut cut,
                                                                 LogprobOut o, void* ws) {
@@ -677,8 +679,9 @@ constexpr int kGradVecs = 4;                       // 16-byte vectors a thread
 // A workgroup writes one chunk of a row without the given tokens' own terms,
 // then the few elements that have them, from logits read before the chunk
 // was written (the gradient may replace the logits).  Equal tokens all write
-// the same sum.  Bound by memory: 2048 x 50257 bf16 66 us, 6.2 TB/s of reads
-// and writes.
+// the same sum.  Bound by memory: 2048 x 50257 bf16 74 us in a trace, 5.7 TB/s
+// of reads and writes; 77 us a call with other logits each time, 64 with the
+// same ones, which the Infinity Cache then holds in part.
 template <int ESIZE, bool ENTROPY>
 __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradTask t,
                                                                 int32_t chunks) {
@@ -734,7 +737,7 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradTask 
                 for (int e = 0; e < 4; ++e)
                     o[e] = __builtin_bit_cast(uint32_t, slope(vec_elem<4>(w[i], e)));
             }
-            __builtin_nontemporal_store(o, &((Loose16*)(d + c))->v);   // 2048 x 50257 83 -> 66 us
+            __builtin_nontemporal_store(o, &((Loose16*)(d + c))->v);   // past the L2: 83 -> 66 us (same logits)
         } else {
             for (int e = 0; e < VEC; ++e)
                 if (c + e < hi)
