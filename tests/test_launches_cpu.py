@@ -61,7 +61,8 @@ def record(tmp_path_factory):
                     os.path.join(HERE, "launch_record.cc"), "-ldl", "-o", so], check=True)
 
     def run(calls):
-        env = dict(os.environ, LD_PRELOAD=so,
+        first = os.environ.get("LD_PRELOAD")
+        env = dict(os.environ, LD_PRELOAD=f"{so}:{first}" if first else so,
                    PYTHONPATH=os.pathsep.join([ROOT, os.environ.get("PYTHONPATH", "")]))
         res = subprocess.run([sys.executable, "-c", CHILD], input=json.dumps(calls), text=True,
                              capture_output=True, env=env, timeout=600)
