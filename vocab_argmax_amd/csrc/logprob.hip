@@ -243,11 +243,11 @@ __device__ __forceinline__ u32x4_t all_neg_inf() {
 // largest values of the lanes on the first chunk (in each of the W
 // wavefronts with columns at least ceil(n_top / W) lanes reach T, so n_top
 // columns do, unless the mask leaves fewer), then the n_top-th value found so
-// far; columns reaching T go
-// to a list in LDS, and the list is cut to its first n_top by counting for
-// each the larger ones.  Few columns pass T, so the scan costs one maximum
-// and one comparison a vector.  A chunk with a NaN, an infinity or more
-// candidates than the list holds takes n_top maxima over the registers.
+// far; columns reaching T go to a list in LDS, and the list is cut to its first
+// n_top by counting for each the larger ones.  Few columns pass T, so the scan
+// costs one maximum and one comparison a vector.  A chunk with a NaN, an
+// infinity or more candidates than the list holds takes n_top maxima over the
+// registers.
 template <int ESIZE, int U>
 __global__ __launch_bounds__(kThreads) void logprob_part_kernel(LogprobTask t, LogprobCut cut,
                                                                 LogprobOut o, void* ws) {
