@@ -126,4 +126,31 @@ __device__ __forceinline__ void block_sum2(float& a, float& b, float (&lds)[WAVE
     }
 }
 
+// (value, id) in the argmax order; 0 is below every real column.
+__device__ __forceinline__ uint64_t order_of(float x, int32_t id) {
+    return ((uint64_t)key_f32(__builtin_bit_cast(uint32_t, x)) << 32) | (uint32_t)~id;
+}
+__device__ __forceinline__ float value_of_key(uint32_t key) {
+    if (key == kKeyNanF32)
+        return __builtin_nanf("");
+    if (key == kKeyZeroF32)
+        return 0.0f;
+    return __builtin_bit_cast(float, bits_of_key_f32(key));
+}
+__device__ __forceinline__ float value_of(uint64_t order) {
+    return value_of_key((uint32_t)(order >> 32));
+}
+__device__ __forceinline__ int32_t id_of(uint64_t order) {
+    return (int32_t)~(uint32_t)order;
+}
+
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+        const uint64_t o = __shfl_xor((unsigned long long)v, off, 64);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
 }  // namespace vpa
