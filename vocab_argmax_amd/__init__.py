@@ -621,3 +621,10 @@ from .head import (ACTIVATIONS, HEAD_SYMBOLS, MAX_ROW_TOKENS, MAX_TOP,  # noqa: 
                    TokenLogprobs, combine_logprobs, head_call, head_lib, head_linear,
                    head_linear_backward, layer_norm, layer_norm_backward, logprob_stats,
                    logprobs_workspace, token_logprobs, token_logprobs_backward)
+
+# A draft head's training, 8-bit and sampling operators (include/vpa_draft.h).
+from .draft import (DISTILL_STATS, DRAFT_SYMBOLS, FP8, MAX_TEACHER_TOP, SCALE_BLOCK,  # noqa: E402
+                    RmsNorm, RmsNormFp8, distill_loss, distill_loss_and_grad,
+                    distill_loss_backward, distill_workspace, draft_call, draft_lib,
+                    head_linear_fp8, quantize_fp8, rms_norm, rms_norm_backward, rms_norm_fp8,
+                    sampled_verify, sampled_verify_workspace)

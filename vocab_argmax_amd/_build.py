@@ -1,15 +1,15 @@
 """Build libvpa.so (HIP, gfx950) in-tree with hipcc, and the binding's
-CPython marshalling modules _vpa_call and _vpa_head_call with the host C
-compiler.
+CPython marshalling modules _vpa_call, _vpa_head_call and _vpa_draft_call with
+the host C compiler.
 
     python -m vocab_argmax_amd._build          # or: vocab_argmax_amd._build.build()
 
 Sources are compiled in parallel into vocab_argmax_amd/_build/ and linked into
 vocab_argmax_amd/libvpa.so.  Packed-fp32 instructions are disabled for the
 device code.
-_vpa_call (csrc/pycall.c) and _vpa_head_call (csrc/headcall.c) do not link the
-library: the binding hands them the entry points of the libvpa.so it has
-loaded.
+_vpa_call (csrc/pycall.c), _vpa_head_call (csrc/headcall.c) and _vpa_draft_call
+(csrc/draftcall.c) do not link the library: the binding hands them the entry
+points of the libvpa.so it has loaded.
 """
 import os
 import shutil
@@ -25,9 +25,11 @@ OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvpa.so")
 SOURCES = ["api.hip", "block_stats.hip", "chunk_stats.hip", "reduce.hip",
            "head_api.hip", "logprob.hip", "linear.hip", "linear_rows.hip", "gemm_bf16.hip",
-           "gemm_f32.hip", "layer_norm.hip"]
+           "gemm_f32.hip", "layer_norm.hip", "draft_api.hip", "sampled.hip", "distill.hip",
+           "rms_norm.hip", "linear_fp8.hip"]
 ARCH = "gfx950"
-MODULES = {"_vpa_call": "pycall.c", "_vpa_head_call": "headcall.c"}
+MODULES = {"_vpa_call": "pycall.c", "_vpa_head_call": "headcall.c",
+           "_vpa_draft_call": "draftcall.c"}
 
 
 def hipcc() -> str:
