@@ -158,7 +158,10 @@ size_t vpa_sampled_verify_workspace(vpa_vocab v, int64_t n_req, int32_t k) {
     if (check_vocab(v) != VPA_OK || n_req < 1 || k < 0 || k > VPA_MAX_DRAFTS ||
         n_req > kMaxSize / (k + 1))
         return 0;
-    return sample_workspace(sample_cut(v.vocab, n_req, k), n_req, k);
+    // either element type's cut
+    const size_t b2 = sample_workspace(sample_cut(2, v.vocab, n_req, k), n_req, k);
+    const size_t b4 = sample_workspace(sample_cut(4, v.vocab, n_req, k), n_req, k);
+    return b2 > b4 ? b2 : b4;
 }
 
 vpa_status vpa_sampled_verify(const void* logits, vpa_dtype dtype, int64_t ld, vpa_vocab v,
@@ -198,7 +201,7 @@ vpa_status vpa_sampled_verify(const void* logits, vpa_dtype dtype, int64_t ld, v
         return st;
     if (!aligned(temperature, 4))
         return fail(VPA_ERR_INVALID, "temperature not 4-byte aligned");
-    const SampleCut c = sample_cut(v.vocab, n_req, k);
+    const SampleCut c = sample_cut(esize_of(dt), v.vocab, n_req, k);
     if ((st = check_dispatch(sample_threads(c, n_req, k), call)) != VPA_OK ||
         (st = check_workspace(call, workspace, workspace_bytes, sample_workspace(c, n_req, k))) !=
             VPA_OK)

@@ -1,0 +1,240 @@
+// row_scan.h -- one pass over a segment of a row of logits for a sum of
+// exponentials (and, where asked for, the first column in the argmax order), as
+// sampled.hip and distill.hip need it.
+//
+// A workgroup walks its segment in chunks of U 16-byte vectors a thread, held in
+// registers, that begin at aligned columns.  Every lane keeps s = sum 2^z of its
+// own columns, z = (x - M) scale, from an M that its wavefront shares: the first
+// chunk's maximum, moved to a later chunk's where that is more than LAG (of z)
+// above it.  A later chunk is one pass: for bf16 an element costs 1.5
+// instructions to unpack it and take the maximum, a multiply-add, 2 slots for
+// 2^z and an add.
+#pragma once
+
+#include "vpa_math.h"
+
+namespace vpa {
+namespace {
+
+constexpr float kMinusInf = -__builtin_inff();
+
+// The largest of three (a NaN among them: any of them or NaN), one instruction.
+__device__ __forceinline__ float largest3(float a, float b, float c) {
+    float d;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+    return d;
+}
+
+template <int ESIZE>
+__device__ __forceinline__ float vec_largest(u32x4_t w) {
+    constexpr int VEC = 16 / ESIZE;
+    float v = largest3(vec_elem<ESIZE>(w, 0), vec_elem<ESIZE>(w, 1), vec_elem<ESIZE>(w, 2));
+#pragma unroll
+    for (int e = 3; e + 1 < VEC; e += 2)
+        v = largest3(v, vec_elem<ESIZE>(w, e), vec_elem<ESIZE>(w, e + 1));
+    return largest3(v, vec_elem<ESIZE>(w, VEC - 1), vec_elem<ESIZE>(w, VEC - 1));
+}
+
+template <int ESIZE>
+__device__ __forceinline__ u32x4_t vec_minus_inf() {
+    constexpr uint32_t w = ESIZE == 2 ? 0xFF80FF80u : 0xFF800000u;
+    return u32x4_t{w, w, w, w};
+}
+
+// Columns c .. c+VEC-1 of a row, those outside [lo, hi) as -inf.
+template <int ESIZE, typename T>
+__device__ __forceinline__ u32x4_t load_columns(const T* x, int64_t c, int64_t lo, int64_t hi) {
+    constexpr int VEC = 16 / ESIZE;
+    if (c >= lo && c + VEC <= hi)
+        return __builtin_nontemporal_load((const u32x4_t*)(x + c));
+    union {
+        T e[VEC];
+        u32x4_t v;
+    } u;
+    u.v = vec_minus_inf<ESIZE>();
+    if (c + VEC > lo && c < hi) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (c + e >= lo && c + e < hi)
+                u.e[e] = x[c + e];
+    }
+    return u.v;
+}
+
+// Makes element e of vector i (both the same in all lanes) -inf in lane `at`.
+template <int ESIZE, int U>
+__device__ __forceinline__ void mask_element(u32x4_t (&w)[U], int i, int e, int at) {
+    const bool mine = (int)(threadIdx.x & 63) == at;
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+        if (k == i)
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                if (d == e * ESIZE / 4) {
+                    const uint32_t v = ESIZE == 4 ? 0xFF800000u
+                                       : e % 2    ? (w[k][d] & 0x0000FFFFu) | 0xFF800000u
+                                                  : (w[k][d] & 0xFFFF0000u) | 0x0000FF80u;
+                    w[k][d] = mine ? v : w[k][d];
+                }
+}
+
+// z = (x - M) scale as one multiply-add, x scale - b with b = M scale rounded:
+// what the rounding took off is put right on the sum.  Where the products are
+// too large for that (logits of 1e30 and more), `apart` says so.
+struct ScaledFrom {
+    float m, b, fix;
+    bool apart;
+    __device__ __forceinline__ void set(float m_, float scale) {
+        m = m_;
+        b = m * scale;
+        apart = !(fabsf(b) < 1e30f);
+        fix = apart ? 1.0f : exp2_fast(-__builtin_fmaf(m, scale, -b));
+    }
+};
+
+// Sum of 2^z over a chunk in registers.  `base` holds a finite M.
+template <int ESIZE, int U>
+__device__ __forceinline__ float chunk_sum(const u32x4_t (&w)[U], const ScaledFrom& base,
+                                           float scale) {
+    constexpr int VEC = 16 / ESIZE;
+    float s = 0.0f;
+    if (base.apart) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                s += exp2_fast((vec_elem<ESIZE>(w[i], e) - base.m) * scale);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        return s;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            s += exp2_fast(__builtin_fmaf(vec_elem<ESIZE>(w[i], e), scale, -base.b));
+        __builtin_amdgcn_sched_barrier(0);         // registers for one vector at a time
+    }
+    return s * base.fix;
+}
+
+// (m, s) of a set of columns: m near its largest, s = sum 2^((x - m) scale); the
+// empty set is (-inf, 0).  A NaN or +inf among the columns makes s NaN.
+struct ExpSum {
+    float m, s;
+};
+__device__ __forceinline__ ExpSum join(ExpSum a, ExpSum b, float scale) {
+    const float m = fmaxf(a.m, b.m);
+    if (m == kMinusInf)
+        return {m, a.s + b.s};
+    return {m, a.s * exp2_fast((a.m - m) * scale) + b.s * exp2_fast((b.m - m) * scale)};
+}
+// Over the lanes of a wavefront, each with its own m.
+__device__ __forceinline__ ExpSum wave_join(ExpSum v, float scale) {
+    const float m = wave_max(v.m);
+    return {m, wave_sum(m == kMinusInf ? v.s : v.s * exp2_fast((v.m - m) * scale))};
+}
+
+// The scan of columns [lo, hi) of the row x, whose chunks of a workgroup of
+// THREADS begin at column `begin` (aligned, at most VEC - 1 below lo).
+template <int ESIZE, int U, int THREADS, bool BEST>
+struct SegmentScan {
+    using T = typename elem<ESIZE>::type;
+    static constexpr int VEC = 16 / ESIZE;
+    static constexpr int CHUNK = THREADS * U * VEC;
+
+    ScaledFrom base = {kMinusInf, 0.0f, 1.0f, false};
+    float s = 0.0f;                                // the lane's
+    float best = kMinusInf;                        // the lane's largest value
+    int best_at = -1;                              // and its vector's first column
+
+    // `masked` is called with a chunk and its first column before it is summed.
+    // LAG in z.
+    template <typename Mask>
+    __device__ __forceinline__ void run(const T* x, int begin, int lo, int hi, float scale,
+                                        float lag, Mask masked) {
+        for (int c0 = begin; c0 < hi; c0 += CHUNK) {
+            u32x4_t w[U];
+            const int mine = c0 + (int)threadIdx.x * VEC;
+            if (c0 >= lo && c0 + CHUNK <= hi) {
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    w[i] = __builtin_nontemporal_load((const u32x4_t*)(x + mine + i * THREADS * VEC));
+            } else {
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    w[i] = load_columns<ESIZE>(x, mine + i * THREADS * VEC, lo, hi);
+            }
+            masked(w, c0);
+            float mx = kMinusInf;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const float g = vec_largest<ESIZE>(w[i]);
+                if constexpr (BEST) {
+                    if (g > best) {
+                        best = g;
+                        best_at = mine + i * THREADS * VEC;
+                    }
+                }
+                mx = fmaxf(mx, g);
+            }
+            // values are unpacked anew in every use: held as fp32 they would
+            // cost half the wavefronts
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                asm volatile("" : "+v"(w[i]));
+            if (base.m == kMinusInf || __ballot((mx - base.m) * scale > lag)) {
+                const float m = fmaxf(base.m, wave_max(mx));
+                if (m == kMinusInf) {              // nothing but masked columns, or NaN
+                    ScaledFrom zero;
+                    zero.set(0.0f, scale);
+                    s += chunk_sum<ESIZE, U>(w, zero, scale);
+                    continue;
+                }
+                if (base.m != kMinusInf)
+                    s *= exp2_fast((base.m - m) * scale);
+                base.set(m, scale);
+            }
+            s += chunk_sum<ESIZE, U>(w, base, scale);
+        }
+    }
+    // of the wavefront's columns
+    __device__ __forceinline__ ExpSum wave() const {
+        return {base.m, wave_sum(s)};
+    }
+    // The first of the wavefront's columns in the argmax order as one number (0:
+    // no columns).  A wavefront with a NaN or +inf goes through its columns again.
+    __device__ __forceinline__ uint64_t wave_best(const T* x, int begin, int lo, int hi) const {
+        uint64_t order = 0;
+        if (__ballot(!(s < __builtin_inff()))) {
+            for (int c0 = begin; c0 < hi; c0 += THREADS * VEC)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int c = c0 + (int)threadIdx.x * VEC + e;
+                    if (c >= lo && c < hi) {
+                        const uint64_t o = order_of(to_f32(x[c]), c);
+                        order = o > order ? o : order;
+                    }
+                }
+            return wave_max_u64(order);
+        }
+        const float top = wave_max(best);
+        if (top == kMinusInf) {                    // masked: the lowest column
+            const int c = begin + (int)threadIdx.x * VEC;
+            const int first = c > lo ? c : lo;
+            if (c + VEC > lo && first < hi)
+                order = order_of(kMinusInf, first);
+        } else if (best == top) {
+#pragma unroll
+            for (int e = VEC - 1; e >= 0; --e) {
+                const int c = best_at + e;
+                if (c >= lo && c < hi && to_f32(x[c]) == top)
+                    order = order_of(top, c);
+            }
+        }
+        return wave_max_u64(order);
+    }
+};
+
+}  // namespace
+}  // namespace vpa

@@ -29,12 +29,14 @@ struct SampleTask {
     int32_t* num_sampled;
     int32_t* num_rejected;
 };
-// How the launches are cut: segments of a row of logits for its statistics, and
-// segments of the row that a request draws from.
+// How the launches are cut: segments of a row of logits for its statistics, in
+// chunks of `vecs` 16-byte vectors a thread, and segments of the row that a
+// request draws from.
 struct SampleCut {
-    int32_t row_segments, draw_segments;
+    int32_t vecs, row_segments, row_chunks;
+    int32_t draw_segments, draw_cols;
 };
-SampleCut sample_cut(int64_t vocab, int64_t n_req, int32_t k);
+SampleCut sample_cut(int esize, int64_t vocab, int64_t n_req, int32_t k);
 size_t sample_workspace(const SampleCut& c, int64_t n_req, int32_t k);
 // Most work-items of one of the launches.
 int64_t sample_threads(const SampleCut& c, int64_t n_req, int32_t k);
