@@ -11,6 +11,8 @@
 // columns: with sums that are off by 2^-24 one draw in a hundred over a flat
 // row of 2e5 columns would come out a column off.  With e = exp((x - m) / T) and
 // Z its sum, the weights are e - q Z, so nothing is divided.
+#include <type_traits>
+
 #include "row_scan.h"
 #include "vpa_draft_internal.h"
 
@@ -20,6 +22,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMostSegments = 64;
+constexpr int kDrawCols = 1024;                    // columns of a block of the drawn row
 
 // A segment of a row of logits: m near its largest, s = sum exp((x - m) / T), and
 // the first column in the argmax order.  s is NaN where it holds a NaN or +inf;
@@ -37,7 +40,7 @@ struct Draw {
     int32_t kind;              // kDrawn: the token stands; weights e, e without `id`, e - q Z
     int32_t row, q_row, id, pos;
 };
-// Sums over a segment of that row: of e, and of the weights.
+// Sums over a block of that row's columns: of e, and of the weights.
 struct DrawSum {
     double e, w;
 };
@@ -49,12 +52,14 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
     return v;
 }
 
-// 2^z for z <= 1000, 0 below 2^-1000 (a masked column): 2^n (1 + f q(f)) with n
-// the nearest whole number and q the interpolation of (2^f - 1) / f at the 9
-// Chebyshev nodes of [-1/2, 1/2], off by 4e-14 at most.
-__device__ __forceinline__ double exp2_f64(double z) {
-    const double n = __builtin_rint(z);
-    const double f = z - n;
+// 2^(d scale), where d scale lies in [-1000, 1000]: 2^n (1 + f q(f)) with n the
+// nearest whole number, which 1.5 2^52 leaves in the last bits of a sum, and q the
+// interpolation of (2^f - 1) / f at the 9 Chebyshev nodes of [-1/2, 1/2], off by
+// 4e-14 at most.
+__device__ __forceinline__ double exp2_f64(double d, double scale) {
+    constexpr double kWhole = 0x1.8p52;
+    const double t = __builtin_fma(d, scale, kWhole);
+    const double f = __builtin_fma(d, scale, -(t - kWhole));
     double q = 0x1.b63880a30e9ffp-24;
     q = __builtin_fma(q, f, 0x1.63d136366db24p-20);
     q = __builtin_fma(q, f, 0x1.ffcb9515a8016p-17);
@@ -64,7 +69,9 @@ __device__ __forceinline__ double exp2_f64(double z) {
     q = __builtin_fma(q, f, 0x1.c6b08d7047e52p-5);
     q = __builtin_fma(q, f, 0x1.ebfbdff823cedp-3);
     q = __builtin_fma(q, f, 0x1.62e42fefa39efp-1);
-    return z < -1000.0 ? 0.0 : __builtin_amdgcn_ldexp(__builtin_fma(q, f, 1.0), (int)n);
+    const uint64_t bits = __builtin_bit_cast(uint64_t, __builtin_fma(q, f, 1.0));
+    const uint32_t n = (uint32_t)__builtin_bit_cast(uint64_t, t);
+    return __builtin_bit_cast(double, bits + ((uint64_t)(n << 20) << 32));
 }
 
 __device__ __forceinline__ float temperature_of(const SampleTask& t, int32_t req) {
@@ -165,8 +172,8 @@ __global__ __launch_bounds__(kAcceptWaves * 64) void sample_accept_kernel(Sample
                 if (greedy)
                     p = id == id_of(order) ? 1.0 : 0.0;
                 else
-                    p = exp2_f64(((double)to_f32(((const T*)t.logits)[(int64_t)row * t.ld + id]) -
-                                  (double)sum.m) * d.scale) / (double)sum.s;
+                    p = exp2(((double)to_f32(((const T*)t.logits)[(int64_t)row * t.ld + id]) -
+                              (double)sum.m) * d.scale) / (double)sum.s;
                 d.q_row = req * t.k + pos;
                 const double q =
                     t.probs ? (double)to_f32(((const Q*)t.probs)[(int64_t)d.q_row * t.ldq + id]) : 1.0;
@@ -203,177 +210,250 @@ __global__ __launch_bounds__(kAcceptWaves * 64) void sample_accept_kernel(Sample
     }
 }
 
-// The weights of VEC columns of the row that is drawn from.
-template <int ESIZE, int QSIZE>
+// The weights of the columns of the row that is drawn from, by KIND.
+template <int ESIZE, int QSIZE, int KIND>
 struct Weights {
     using T = typename elem<ESIZE>::type;
     using Q = typename elem<QSIZE>::type;
     const T* x;
     const Q* q;
     double scale, m;           // e = 2^((x - m) scale)
+    float least;               // logits below it have e = 0 (2^-1000 and less)
     double z;
-    int32_t kind, id;
+    int32_t id;
 
-    __device__ __forceinline__ Weights(const SampleTask& t, const Draw& d) {
+    __device__ __forceinline__ Weights(const SampleTask& t, const Draw& d, double sum) {
         x = (const T*)t.logits + (int64_t)d.row * t.ld;
         q = (const Q*)t.probs + (int64_t)d.q_row * t.ldq;
         scale = d.scale;
         m = (double)d.m;
-        z = 0.0;
-        kind = d.kind;
+        const double far = m - 1000.0 / scale;
+        least = far > -3e38 ? (float)far : -__FLT_MAX__;
+        z = sum;
         id = d.id;
     }
-    __device__ __forceinline__ double e(T v) const {
-        // (one multiply-add of x scale - m scale loses every digit where m is 1e30)
-        return exp2_f64(((double)to_f32(v) - m) * scale);
-    }
-    __device__ __forceinline__ double of(int c, double e) const {
-        if (kind == kWithout)
-            return c == id ? 0.0 : e;
-        if (kind == kMinus) {
-            const double r = __builtin_fma(-(double)to_f32(q[c]), z, e);
-            return r > 0.0 ? r : 0.0;
+    // N consecutive columns from c: their weights, 0 from `hi` on
+    template <int N>
+    __device__ __forceinline__ void of(int c, int hi, double (&w)[N]) const {
+        struct __attribute__((packed, aligned(sizeof(T)))) Xs {
+            T v[N];
+        } xs;
+        struct __attribute__((packed, aligned(sizeof(Q)))) Qs {
+            Q v[N];
+        } qs = {};
+        if (c + N <= hi) {
+            xs = *(const Xs*)(x + c);
+            if constexpr (KIND == kMinus)
+                qs = *(const Qs*)(q + c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                from_f32(xs.v[i], c + i < hi ? to_f32(x[c + i]) : kMinusInf);
+                if (KIND == kMinus && c + i < hi)
+                    qs.v[i] = q[c + i];
+            }
         }
-        return e;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // (one multiply-add of x scale - m scale loses every digit where m is 1e30)
+            const float v = to_f32(xs.v[i]);
+            w[i] = exp2_f64((double)v - m, scale);
+            w[i] = v >= least ? w[i] : 0.0;
+            if constexpr (KIND == kMinus)
+                w[i] = fmax(__builtin_fma(-(double)to_f32(qs.v[i]), z, w[i]), 0.0);
+            if constexpr (KIND == kWithout)
+                w[i] = c + i == id ? 0.0 : w[i];
+        }
     }
 };
 
-// Sums over the segments of each request's row; a workgroup a segment.  With
-// SECOND, the sums of e - q Z for the requests that need them.
+// Calls f with the kind as a type.
+template <typename F>
+__device__ __forceinline__ void with_kind(int32_t kind, F f) {
+    using std::integral_constant;
+    if (kind == kMinus)
+        f(integral_constant<int, kMinus>{});
+    else if (kind == kWithout)
+        f(integral_constant<int, kWithout>{});
+    else
+        f(integral_constant<int, kPlain>{});
+}
+
+// Sum over a workgroup of kThreads, of each thread's own, in a fixed order.
+__device__ __forceinline__ double block_sum_f64(double v, double (&lds)[kWaves]) {
+    v = wave_sum_f64(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return ((lds[0] + lds[1]) + lds[2]) + lds[3];
+}
+__device__ __forceinline__ double sum_of_e(const DrawSum* sums, int blocks, double (&lds)[kWaves]) {
+    double v = 0.0;
+    for (int i = threadIdx.x; i < blocks; i += kThreads)
+        v += sums[i].e;
+    return block_sum_f64(v, lds);
+}
+
+// Sums of the weights over blocks of kDrawCols columns of each request's row, a
+// wavefront a block at a time; of e alone for the requests that subtract a draft
+// distribution, whose weights are summed by a SECOND launch.
 template <int ESIZE, int QSIZE, bool SECOND>
 __global__ __launch_bounds__(kThreads) void sample_sums_kernel(SampleTask t, SampleCut cut,
                                                                const Draw* draws, DrawSum* sums) {
-    __shared__ double lds[2][kWaves];
-    const int32_t req = blockIdx.x / cut.draw_segments, seg = blockIdx.x % cut.draw_segments;
+    constexpr int VEC = 16 / ESIZE;
+    __shared__ double lds[kWaves];
+    const int32_t req = blockIdx.x / cut.draw_groups, group = blockIdx.x % cut.draw_groups;
     const Draw d = draws[req];
     if (d.kind == kDrawn || (SECOND && d.kind != kMinus))
         return;
-    Weights<ESIZE, QSIZE> w(t, d);
+    DrawSum* mine = sums + (int64_t)req * cut.draw_blocks;
+    const double z = SECOND ? sum_of_e(mine, cut.draw_blocks, lds) : 0.0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if constexpr (SECOND) {
-        const DrawSum* mine = sums + (int64_t)req * cut.draw_segments;
-        w.z = wave_sum_f64(lane < cut.draw_segments ? mine[lane].e : 0.0);
-    } else if (d.kind == kMinus) {
-        w.kind = kPlain;
-    }
-    const int lo = seg * cut.draw_cols;
-    const int hi = lo + cut.draw_cols < t.vocab ? lo + cut.draw_cols : t.vocab;
-    double se = 0.0, sw = 0.0;
-    for (int c = lo + (int)threadIdx.x; c < hi; c += kThreads) {
-        const double e = w.e(w.x[c]);
-        se += e;
-        sw += w.of(c, e);
-    }
-    se = wave_sum_f64(se);
-    sw = wave_sum_f64(sw);
-    if (lane == 0) {
-        lds[0][wave] = se;
-        lds[1][wave] = sw;
-    }
-    __syncthreads();
-    if (threadIdx.x != 0)
-        return;
-    DrawSum* out = sums + blockIdx.x;
-    if constexpr (!SECOND)
-        out->e = ((lds[0][0] + lds[0][1]) + lds[0][2]) + lds[0][3];
-    out->w = ((lds[1][0] + lds[1][1]) + lds[1][2]) + lds[1][3];
+    with_kind(!SECOND && d.kind == kMinus ? (int32_t)kPlain : d.kind, [&](auto kind) {
+        const Weights<ESIZE, QSIZE, kind()> w(t, d, z);
+        for (int b = group * kWaves + wave; b < cut.draw_blocks; b += cut.draw_groups * kWaves) {
+            double s = 0.0;
+#pragma unroll
+            for (int i = 0; i < kDrawCols / 64 / VEC; ++i) {
+                double v[VEC];
+                w.of(b * kDrawCols + (i * 64 + lane) * VEC, t.vocab, v);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k)
+                    s += v[k];
+            }
+            s = wave_sum_f64(s);
+            if (lane != 0)
+                continue;
+            if (!SECOND && d.kind == kMinus)
+                mine[b].e = s;
+            else
+                mine[b].w = s;
+        }
+    });
 }
 
-// The column where the running sum passes the random number: its segment from
-// the segments' sums, then a workgroup's threads sum consecutive columns of it,
-// and the thread that the border lies in goes through its own.
-constexpr int kPickThreads = 1024;
-
-template <int ESIZE, int QSIZE>
-__global__ __launch_bounds__(kPickThreads) void sample_pick_kernel(SampleTask t, SampleCut cut,
-                                                                   const Draw* draws,
-                                                                   const DrawSum* sums) {
-    __shared__ double lds[kPickThreads / 64];
-    __shared__ int32_t passed, last;
-    const int32_t req = blockIdx.x;
-    const Draw d = draws[req];
-    if (d.kind == kDrawn)
-        return;
+// The running sum over a workgroup's threads, each with its own v: what is
+// before the thread's, and the whole.
+__device__ __forceinline__ double block_scan_f64(double v, double& all, double (&lds)[kWaves]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    Weights<ESIZE, QSIZE> w(t, d);
-    const DrawSum* all = sums + (int64_t)req * cut.draw_segments;
-    if (threadIdx.x == 0) {
-        passed = kPickThreads;
-        last = 0;
-    }
-    // every thread goes through the (at most 64) sums in the same order
-    double total = 0.0, plain = 0.0;
-    for (int i = 0; i < cut.draw_segments; ++i) {
-        total += all[i].w;
-        plain += all[i].e;
-    }
-    w.z = wave_sum_f64(lane < cut.draw_segments ? all[lane].e : 0.0);
-    const bool fall_back = !(total > 0.0);
-    if (fall_back) {
-        total = plain;
-        w.kind = kPlain;
-    }
-    const double u = t.sample_u[req];
-    const double target = (u > 0.0 ? u : 0.0) * total;
-    double before = 0.0, run = 0.0;
-    int seg = 0;
-    bool inside = false;
-    for (int i = 0; i < cut.draw_segments && !inside; ++i) {
-        const double s = fall_back ? all[i].e : all[i].w;
-        if (s > 0.0) {                             // the last such one, if none passes
-            seg = i;
-            before = run;
-            inside = run + s > target;
-        }
-        run += s;
-    }
-    const int lo = seg * cut.draw_cols;
-    const int hi = lo + cut.draw_cols < t.vocab ? lo + cut.draw_cols : t.vocab;
-    const int per = (hi - lo + kPickThreads - 1) / kPickThreads;
-    const int c0 = lo + (int)threadIdx.x * per;
-    const int c1 = c0 + per < hi ? c0 + per : hi;
-    double mine = 0.0;
-    int top = -1;                                  // the thread's last column with a weight
-    for (int c = c0; c < c1; ++c) {
-        const double v = w.of(c, w.e(w.x[c]));
-        mine += v;
-        top = v > 0.0 ? c : top;
-    }
-    double upto = mine;
+    double upto = v;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
         const double o = __shfl_up(upto, off, 64);
         upto += lane >= off ? o : 0.0;
     }
+    double before = __shfl_up(upto, 1, 64);
+    before = lane == 0 ? 0.0 : before;
+    __syncthreads();
     if (lane == 63)
         lds[wave] = upto;
     __syncthreads();
-    for (int i = 0; i < wave; ++i)
-        before += lds[i];
-    if (mine > 0.0 && before + upto > target)
-        atomicMin(&passed, (int32_t)threadIdx.x);
-    if (top >= 0)
-        atomicMax(&last, top);
-    __syncthreads();
-    int32_t* out = t.out_tokens + (int64_t)req * (t.k + 1) + d.pos;
-    if (passed == kPickThreads) {
-        if (threadIdx.x == 0)
-            *out = last;
+    all = ((lds[0] + lds[1]) + lds[2]) + lds[3];
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i)
+        before += i < wave ? lds[i] : 0.0;
+    return before;
+}
+
+// The column where the running sum passes the random number: its block from the
+// blocks' sums, then its 4 columns a thread.  Where rounding lets none pass, and
+// for random numbers from 1 on, the last one with a weight.
+template <int ESIZE, int QSIZE>
+__global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleTask t, SampleCut cut,
+                                                               const Draw* draws,
+                                                               const DrawSum* sums) {
+    constexpr int N = kDrawCols / kThreads;
+    __shared__ double lds[kWaves], start;
+    __shared__ int32_t passed, last;
+    const int32_t req = blockIdx.x;
+    const Draw d = draws[req];
+    if (d.kind == kDrawn)
         return;
+    const DrawSum* mine = sums + (int64_t)req * cut.draw_blocks;
+    double total = 0.0, z = 0.0;
+    for (int i = threadIdx.x; i < cut.draw_blocks; i += kThreads) {
+        const DrawSum s = mine[i];
+        total += s.w;
+        z += d.kind == kMinus ? s.e : 0.0;
     }
-    if ((int32_t)threadIdx.x != passed)
-        return;
-    double sum = before + upto - mine;
-    int32_t token = top;
-    for (int c = c0; c < c1; ++c) {
-        const double v = w.of(c, w.e(w.x[c]));
-        sum += v;
-        if (v > 0.0 && sum > target) {
-            token = c;
-            break;
+    total = block_sum_f64(total, lds);
+    if (d.kind == kMinus)
+        z = block_sum_f64(z, lds);
+    int32_t kind = d.kind;
+    if (!(total > 0.0)) {
+        // no weight: p itself, which has the draft's column alone where nothing else is left
+        if (kind != kMinus) {
+            if (threadIdx.x == 0)
+                t.out_tokens[(int64_t)req * (t.k + 1) + d.pos] = d.id;
+            return;
         }
+        kind = kPlain;
+        total = z;
     }
-    *out = token;
+    const bool of_e = kind != d.kind;
+    const double u = t.sample_u[req];
+    const double target = (u > 0.0 ? u : 0.0) * total;
+    // the block
+    if (threadIdx.x == 0) {
+        passed = cut.draw_blocks;
+        last = 0;
+        start = 0.0;
+    }
+    double run = 0.0;
+    for (int b0 = 0; b0 < cut.draw_blocks; b0 += kThreads) {
+        const int b = b0 + (int)threadIdx.x;
+        double v = 0.0, all;
+        if (b < cut.draw_blocks)
+            v = of_e ? mine[b].e : mine[b].w;
+        const double before = run + block_scan_f64(v, all, lds);
+        if (v > 0.0 && before + v > target)
+            atomicMin(&passed, b);
+        if (v > 0.0)
+            atomicMax(&last, b);
+        __syncthreads();
+        // of the block that it passes in or, as yet, of the last one with a weight
+        if (b == (passed < cut.draw_blocks ? passed : last) && v > 0.0)
+            start = before;
+        run += all;
+        __syncthreads();
+        if (passed < cut.draw_blocks)
+            break;
+    }
+    const int block = passed < cut.draw_blocks ? passed : last;
+    const double from = start;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        passed = t.vocab;
+        last = 0;
+    }
+    // the column
+    with_kind(kind, [&](auto k) {
+        const Weights<ESIZE, QSIZE, k()> w(t, d, z);
+        const int c = block * kDrawCols + (int)threadIdx.x * N;
+        double v[N], own = 0.0, all;
+        w.of(c, t.vocab, v);
+        int top = -1;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            own += v[i];
+            top = v[i] > 0.0 ? c + i : top;
+        }
+        double sum = from + block_scan_f64(own, all, lds);
+        int32_t token = t.vocab;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            sum += v[i];
+            token = v[i] > 0.0 && sum > target && token == t.vocab ? c + i : token;
+        }
+        if (token < t.vocab)
+            atomicMin(&passed, token);
+        if (top >= 0)
+            atomicMax(&last, top);
+    });
+    __syncthreads();
+    if (threadIdx.x == 0)
+        t.out_tokens[(int64_t)req * (t.k + 1) + d.pos] = passed < t.vocab ? passed : last;
 }
 
 size_t align16(size_t n) {
@@ -388,7 +468,7 @@ Layout layout_of(const SampleCut& c, int64_t n_req, int32_t k) {
     Layout l;
     l.draws = align16((size_t)n_req * (k + 1) * c.row_segments * sizeof(RowStat));
     l.sums = l.draws + align16((size_t)n_req * sizeof(Draw));
-    l.total = l.sums + (size_t)n_req * c.draw_segments * sizeof(DrawSum);
+    l.total = l.sums + (size_t)n_req * c.draw_blocks * sizeof(DrawSum);
     return l;
 }
 
@@ -396,7 +476,8 @@ Layout layout_of(const SampleCut& c, int64_t n_req, int32_t k) {
 
 // Rows in chunks of 8 vectors a thread where that gives every CU 4 workgroups,
 // else of 2, and segments of whole chunks until there are 4 (8) workgroups a CU.
-// The drawn rows in segments of at least 2048 columns.
+// A drawn row has a wavefront for each block of columns, 16 workgroups a CU at
+// most over all requests.
 SampleCut sample_cut(int esize, int64_t vocab, int64_t n_req, int32_t k) {
     SampleCut c;
     const int64_t rows = n_req * (k + 1), vec = 16 / esize;
@@ -409,12 +490,9 @@ SampleCut sample_cut(int esize, int64_t vocab, int64_t n_req, int32_t k) {
     want = want > kMostSegments ? kMostSegments : want;
     c.row_chunks = (int32_t)((chunks + want - 1) / want);
     c.row_segments = (int32_t)((chunks + c.row_chunks - 1) / c.row_chunks);
-    int64_t segs = (2048 + n_req - 1) / n_req;
-    const int64_t most = (vocab + 2047) / 2048;
-    segs = segs > most ? most : segs;
-    segs = segs > kMostSegments ? kMostSegments : segs;
-    c.draw_cols = (int32_t)(((vocab + segs - 1) / segs + 7) / 8 * 8);
-    c.draw_segments = (int32_t)((vocab + c.draw_cols - 1) / c.draw_cols);
+    c.draw_blocks = (int32_t)((vocab + kDrawCols - 1) / kDrawCols);
+    const int64_t groups = (4096 + n_req - 1) / n_req, enough = (c.draw_blocks + kWaves - 1) / kWaves;
+    c.draw_groups = (int32_t)(groups < enough ? groups : enough);
     return c;
 }
 
@@ -424,8 +502,9 @@ size_t sample_workspace(const SampleCut& c, int64_t n_req, int32_t k) {
 
 int64_t sample_threads(const SampleCut& c, int64_t n_req, int32_t k) {
     const int64_t rows = n_req * (k + 1) * c.row_segments * kThreads;
-    const int64_t sums = n_req * c.draw_segments * kThreads, pick = n_req * kPickThreads;
-    return rows > sums ? (rows > pick ? rows : pick) : (sums > pick ? sums : pick);
+    const int64_t sums = n_req * c.draw_groups * kThreads, accept = n_req * kAcceptWaves * 64;
+    const int64_t most = rows > sums ? rows : sums;
+    return most > accept ? most : accept;
 }
 
 namespace {
@@ -438,7 +517,7 @@ hipError_t launch_typed(const SampleTask& t, void* ws, hipStream_t stream) {
     Draw* draws = (Draw*)((char*)ws + l.draws);
     DrawSum* sums = (DrawSum*)((char*)ws + l.sums);
     const dim3 rows((uint32_t)((int64_t)t.n_req * (t.k + 1) * c.row_segments));
-    const dim3 segs((uint32_t)((int64_t)t.n_req * c.draw_segments)), reqs((uint32_t)t.n_req);
+    const dim3 groups((uint32_t)((int64_t)t.n_req * c.draw_groups)), reqs((uint32_t)t.n_req);
     hipError_t e = c.vecs == 8 ? launch(sample_rows_kernel<ESIZE, 8>, rows, dim3(kThreads), 0,
                                         stream, t, c, stats)
                                : launch(sample_rows_kernel<ESIZE, 2>, rows, dim3(kThreads), 0,
@@ -447,13 +526,13 @@ hipError_t launch_typed(const SampleTask& t, void* ws, hipStream_t stream) {
         e = launch(sample_accept_kernel<ESIZE, QSIZE>, reqs, dim3(kAcceptWaves * 64), 0, stream, t,
                    c, stats, draws);
     if (e == hipSuccess)
-        e = launch(sample_sums_kernel<ESIZE, QSIZE, false>, segs, dim3(kThreads), 0, stream, t, c,
+        e = launch(sample_sums_kernel<ESIZE, QSIZE, false>, groups, dim3(kThreads), 0, stream, t, c,
                    draws, sums);
     if (e == hipSuccess && t.probs)
-        e = launch(sample_sums_kernel<ESIZE, QSIZE, true>, segs, dim3(kThreads), 0, stream, t, c,
+        e = launch(sample_sums_kernel<ESIZE, QSIZE, true>, groups, dim3(kThreads), 0, stream, t, c,
                    draws, sums);
     if (e == hipSuccess)
-        e = launch(sample_pick_kernel<ESIZE, QSIZE>, reqs, dim3(kPickThreads), 0, stream, t, c,
+        e = launch(sample_pick_kernel<ESIZE, QSIZE>, reqs, dim3(kThreads), 0, stream, t, c,
                    draws, sums);
     return e;
 }
