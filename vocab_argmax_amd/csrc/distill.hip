@@ -9,14 +9,21 @@
 // distribution over the others and q_0 their share, the gradient of a column
 // not named is r(c) (q_0 P - p_0) / t: one exponential, and right where q(c)
 // itself is too small for fp32.
+#include <type_traits>
+
+#include "row_scan.h"
 #include "vpa_draft_internal.h"
-#include "vpa_math.h"
 
 namespace vpa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kMostSegments = 64;
 constexpr float kInf = __builtin_inff();
+// most (of z) that a chunk's maximum may exceed M by: further off, ln s is a
+// large number of which the loss needs the last digits
+constexpr float kLag = 6.0f;
 
 // A row's statistics as the backward pass takes them.
 struct DistillStats {
@@ -28,16 +35,15 @@ struct DistillStats {
 };
 static_assert(sizeof(DistillStats) == VPA_DISTILL_STATS * sizeof(float), "as the header says");
 
-// A row's named tokens, one a lane: the id (-1 for none), log probability, and
-// whether the lane is the first with its id.
+// A row's named tokens, one a lane: the id (-1 for none) and log probability.
 struct Named {
     int32_t id;
     float lp;
-    bool first, bad;
+    bool bad;
 };
 __device__ __forceinline__ Named named_of(const DistillTask& t, int64_t row) {
     const int lane = threadIdx.x & 63;
-    Named n{-1, -kInf, false, false};
+    Named n{-1, -kInf, false};
     if (lane < t.n_top) {
         n.id = t.ids[row * t.n_top + lane];
         n.lp = t.logprobs[row * t.n_top + lane];
@@ -45,21 +51,15 @@ __device__ __forceinline__ Named named_of(const DistillTask& t, int64_t row) {
     n.bad = n.id < -1 || n.id >= t.vocab || (n.id >= 0 && !(n.lp < kInf));
     if (n.id < 0 || n.id >= t.vocab)
         n.id = -1;
-    n.first = n.id >= 0;
-    for (int j = 0; j < t.n_top; ++j) {
-        const int32_t other = __builtin_amdgcn_readlane(n.id, j);
-        n.first = n.first && !(j < lane && other == n.id);
-    }
     return n;
 }
-
-// (m, s) of a set of columns; the empty set is (-inf, 0).
-__device__ __forceinline__ void join(float& m, float& s, float om, float os, float scale) {
-    const float mx = fmaxf(m, om);
-    if (mx == -kInf)
-        return;                            // (a NaN in s stays)
-    s = s * exp2_fast((m - mx) * scale) + os * exp2_fast((om - mx) * scale);
-    m = mx;
+// Calls f(lane, id) for each lane of `lanes`, in order.
+template <typename F>
+__device__ __forceinline__ void each_id(uint64_t lanes, int32_t id, F f) {
+    for (; lanes; lanes &= lanes - 1) {
+        const int j = (int)__builtin_ctzll(lanes);
+        f(j, __builtin_amdgcn_readlane(id, j));
+    }
 }
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
@@ -69,56 +69,78 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
     return v;
 }
 
-// The loss and statistics of a row from (m, s) of its columns not named (of all
-// columns without a tail), by one wavefront.
-template <typename T>
-__device__ __forceinline__ void finish_row(const DistillTask& t, int64_t row, const T* x,
-                                           const Named& n, float m_out, float s_out) {
-    const float scale = kLog2e / t.temperature;
-    const float v = n.id >= 0 ? to_f32(x[n.id]) : -kInf;
-    float m = m_out, s = s_out;
-    if (t.tail) {
-        const float add = n.first ? v : -kInf;
-        const float mx = fmaxf(m_out, wave_max(add));
-        const float in = add == -kInf ? 0.0f : exp2_fast((add - mx) * scale);
-        s = wave_sum(in);
-        m = mx;
-        if (mx > -kInf)
-            s += m_out == -kInf ? s_out : s_out * exp2_fast((m_out - mx) * scale);
-        else
-            s += s_out;
-    }
-    // the teacher's few terms in 64 bits: what they leave of 1 may be small
-    const bool has = __ballot(n.id >= 0 || n.bad) != 0;
-    const bool empty = m == -kInf && s == 0.0f;
-    const bool bad = __ballot(n.bad) != 0 || !(s < kInf) || m == kInf;
+// What the teacher says of a row, in every lane of a wavefront but p and lp,
+// which are the lane's: the few terms in 64 bits, since what they leave of 1 may
+// be small.
+struct Teacher {
+    double p, lp;
+    double mass, left;         // sum p, and what it leaves (with a tail)
+    float norm;
+    double log_norm;
+    bool has, bad;
+};
+__device__ __forceinline__ Teacher teacher_of(const DistillTask& t, const Named& n) {
+    Teacher r;
+    r.has = __ballot(n.id >= 0 || n.bad) != 0;
+    r.bad = __ballot(n.bad) != 0;
     const float best = wave_max(n.id >= 0 ? n.lp : -kInf);
-    const float norm = !t.tail && best > -kInf ? best : 0.0f;
-    double log_norm = 0.0;
-    if (!t.tail && best > -kInf)
-        log_norm = log(wave_sum_f64(n.id >= 0 ? exp((double)n.lp - norm) : 0.0));
-    const double lp = ((double)n.lp - norm) - log_norm;
-    const double p = n.id >= 0 ? exp(lp) : 0.0;
-    const double mass = wave_sum_f64(p);
-    const double left = t.tail && mass < 1.0 ? 1.0 - mass : 0.0;
+    r.norm = !t.tail && best > -kInf ? best : 0.0f;
+    r.log_norm = 0.0;
+    const double e = n.id >= 0 ? exp((double)n.lp - r.norm) : 0.0;
+    const double sum = wave_sum_f64(e);
+    r.lp = (double)n.lp - r.norm;
+    r.p = e;
+    r.mass = sum;
+    if (!t.tail && best > -kInf) {
+        r.log_norm = log(sum);
+        r.lp -= r.log_norm;
+        r.p = e / sum;
+        r.mass = 1.0;
+    }
+    r.left = t.tail && r.mass < 1.0 ? 1.0 - r.mass : 0.0;
+    return r;
+}
+
+// The loss and statistics of a row from the sums of its columns not named (of all
+// columns without a tail), by one wavefront; v is the lane's named logit.  Every
+// lane holds the statistics.
+__device__ __forceinline__ DistillStats finish_row(const DistillTask& t, int64_t row, float v,
+                                                   const Named& n, const Teacher& te,
+                                                   ExpSum out) {
+    const float scale = kLog2e / t.temperature;
+    float m = out.m, s = out.s;
+    if (t.tail) {
+        bool first = n.id >= 0;                    // an id that is named twice counts once
+        each_id(__ballot(first), n.id, [&](int j, int32_t id) {
+            first = first && !(id == n.id && j < (int)(threadIdx.x & 63));
+        });
+        const float add = first ? v : -kInf;
+        const float mx = fmaxf(m, wave_max(add));
+        s = wave_sum(add == -kInf ? 0.0f : exp2_fast((add - mx) * scale)) +
+            (mx == -kInf || m == mx ? s : s * exp2_fast((m - mx) * scale));
+        m = mx;
+    }
+    const bool empty = m == -kInf && s == 0.0f;
+    const bool bad = te.bad || !(s < kInf) || m == kInf;
     const double inv_t = 1.0 / (double)t.temperature;
     const double log_s = empty ? 0.0 : log((double)s);
-    const double log_out = s_out > 0.0f ? log((double)s_out) : 0.0;
+    const double log_out = !t.tail ? log_s : out.s > 0.0f ? log((double)out.s) : 0.0;
     // log q of the named column, and of the others together
     const double lq = ((double)v - (double)m) * inv_t - log_s;
-    const double lq0 = s_out > 0.0f ? ((double)m_out - (double)m) * inv_t + log_out - log_s : -INFINITY;
-    double loss = wave_sum_f64(p > 0.0 ? p * (lp - lq) : 0.0);
-    if (left > 0.0)
-        loss += left * (log(left) - lq0);
-    const double all = mass + left;
+    const double lq0 =
+        out.s > 0.0f ? ((double)out.m - (double)m) * inv_t + log_out - log_s : -INFINITY;
+    double loss = wave_sum_f64(te.p > 0.0 ? te.p * (te.lp - lq) : 0.0);
+    if (te.left > 0.0)
+        loss += te.left * (log(te.left) - lq0);
+    const double all = te.mass + te.left;
     DistillStats st;
-    st.m_out = m_out == -kInf ? 0.0f : m_out;      // r of a masked column is 0
+    st.m_out = out.m == -kInf ? 0.0f : out.m;      // r of a masked column is 0
     st.log_out = (float)log_out;
-    st.f_out = (float)(t.tail ? exp(lq0) * all - left : all);
+    st.f_out = (float)(t.tail ? exp(lq0) * all - te.left : all);
     st.m = m;
     st.log_s = (float)log_s;
-    st.norm = norm;
-    st.log_norm = (float)log_norm;
+    st.norm = te.norm;
+    st.log_norm = (float)te.log_norm;
     st.mass = (float)all;
     if (empty) {
         loss = all > 0.0 ? INFINITY : 0.0;
@@ -128,7 +150,7 @@ __device__ __forceinline__ void finish_row(const DistillTask& t, int64_t row, co
         loss = NAN;
         st.f_out = st.mass = NAN;
     }
-    if (!has) {
+    if (!te.has) {
         loss = 0.0;
         st.mass = 0.0f;
     }
@@ -136,53 +158,135 @@ __device__ __forceinline__ void finish_row(const DistillTask& t, int64_t row, co
         t.loss[row] = (float)loss;
         *(DistillStats*)(t.row_stats + row * VPA_DISTILL_STATS) = st;
     }
+    return st;
+}
+template <typename T>
+__device__ __forceinline__ float named_logit(const T* x, const Named& n) {
+    return n.id >= 0 ? to_f32(x[n.id]) : -kInf;
 }
 
-template <int ESIZE>
-__global__ __launch_bounds__(kThreads) void distill_kernel(DistillTask t) {
-    using T = typename elem<ESIZE>::type;
-    __shared__ float lds[4][2];
-    __shared__ int32_t ids[64];
-    const int64_t row = blockIdx.x;
-    const T* x = (const T*)t.logits + row * t.ld;
-    const Named n = named_of(t, row);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (wave == 0)
-        ids[lane] = t.tail ? n.id : -1;
-    __syncthreads();
-    auto value = [&](int c) {
-        for (int j = 0; j < t.n_top; ++j)
-            if (ids[j] == c)
-                return -kInf;
-        return to_f32(x[c]);
-    };
-    const float scale = kLog2e / t.temperature;
-    float m = -kInf;
-    for (int c = threadIdx.x; c < t.vocab; c += kThreads)
-        m = fmaxf(m, value(c));
-    float s = 0.0f;
-    const float base = m == -kInf ? 0.0f : m;
-    for (int c = threadIdx.x; c < t.vocab; c += kThreads)
-        s += exp2_fast((value(c) - base) * scale);
-    const float mx = wave_max(m);
-    s = wave_sum(m == -kInf ? s : s * exp2_fast((m - mx) * scale));
-    if (lane == 0) {
-        lds[wave][0] = mx;
-        lds[wave][1] = s;
-    }
-    __syncthreads();
-    if (wave != 0)
+// Masks the named columns of a chunk: of THREADS threads with U vectors each,
+// from column c0.  A wavefront does those of its own lanes, vector by vector and
+// one at a time.
+template <int ESIZE, int U, int THREADS>
+__device__ __forceinline__ void mask_named(u32x4_t (&w)[U], int c0, int32_t id) {
+    constexpr int VEC = 16 / ESIZE;
+    const int at = id >= 0 ? id - c0 : -1;         // (>= 0: c0 may be below 0)
+    const bool here = at >= 0 && at / VEC % THREADS / 64 == (int)threadIdx.x / 64;
+    if (!__ballot(here && at < THREADS * U * VEC))
         return;
-    m = -kInf;
-    s = 0.0f;
-    for (int i = 0; i < 4; ++i) {
-        if (lds[i][0] == -kInf)
-            s += lds[i][1];
-        else
-            join(m, s, lds[i][0], lds[i][1], scale);
-    }
-    finish_row(t, row, x, n, m, s);
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        each_id(__ballot(here && at / VEC / THREADS == i), at, [&](int, int32_t a) {
+            mask_element<ESIZE>(w[i], a % VEC, a / VEC % 64);
+        });
 }
+
+// How the loss's launch is cut: segments of whole chunks of `vecs` vectors a thread.
+struct Cut {
+    int32_t vecs, segments, chunks;
+};
+
+// A workgroup a segment of a row; with one segment, the whole of it.
+template <int ESIZE, int U>
+__global__ __launch_bounds__(kThreads) void distill_kernel(DistillTask t, Cut cut, ExpSum* sums) {
+    using T = typename elem<ESIZE>::type;
+    using Scan = SegmentScan<ESIZE, U, kThreads, false>;
+    __shared__ ExpSum lds[kWaves];
+    const int64_t row = blockIdx.x / cut.segments;
+    const int32_t seg = blockIdx.x % cut.segments;
+    const T* x = (const T*)t.logits + row * t.ld;
+    const float scale = kLog2e / t.temperature;
+    const Named n = named_of(t, row);
+    const int32_t id = t.tail ? n.id : -1;
+    const int begin = -(int)(((uintptr_t)x & 15) / ESIZE) + seg * cut.chunks * Scan::CHUNK;
+    const int end = begin + cut.chunks * Scan::CHUNK;
+    const int lo = begin < 0 ? 0 : begin, hi = end < t.vocab ? end : t.vocab;
+    Scan scan;
+    scan.run(x, begin, lo, hi, scale, kLag, [&](u32x4_t (&w)[U], int c0) {
+        mask_named<ESIZE, U, kThreads>(w, c0, id);
+    });
+    const ExpSum s = scan.wave();
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x >= 64)
+        return;
+    ExpSum all = lds[0];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i)
+        all = join(all, lds[i], scale);
+    if (cut.segments == 1)
+        finish_row(t, row, named_logit(x, n), n, teacher_of(t, n), all);
+    else if (threadIdx.x == 0)
+        sums[blockIdx.x] = all;
+}
+
+// The segments' sums joined; a wavefront a row.
+template <int ESIZE>
+__global__ __launch_bounds__(64) void distill_finish_kernel(DistillTask t, Cut cut,
+                                                            const ExpSum* sums) {
+    using T = typename elem<ESIZE>::type;
+    const int64_t row = blockIdx.x;
+    ExpSum s = {kMinusInf, 0.0f};
+    if ((int)threadIdx.x < cut.segments)
+        s = sums[row * cut.segments + threadIdx.x];
+    const Named n = named_of(t, row);
+    const float v = named_logit((const T*)t.logits + row * t.ld, n);
+    finish_row(t, row, v, n, teacher_of(t, n), wave_join(s, kLog2e / t.temperature));
+}
+
+// The gradient of a row: of its columns not named, r(c) f with r(c) = 2^z / s_o,
+// and of the lane's named one.
+struct Slope {
+    float scale, f, g;
+    ScaledFrom base;
+    bool zero;
+    __device__ __forceinline__ Slope(const DistillTask& t, int64_t row, const DistillStats& st) {
+        scale = kLog2e / t.temperature;
+        g = t.grad_loss[row] / t.temperature;
+        zero = st.mass == 0.0f;
+        base.set(st.m_out, scale);
+        f = g * st.f_out * (exp2f(-st.log_out * kLog2e) * base.fix);
+    }
+    // 16 bytes of columns
+    template <int ESIZE>
+    __device__ __forceinline__ u32x4_t of(u32x4_t w) const {
+        constexpr int VEC = 16 / ESIZE;
+        u32x4_t o = {0, 0, 0, 0};
+        if (zero)                                  // whatever the logits hold
+            return o;
+        float d[VEC];
+        if (base.apart) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                d[e] = exp2_fast((vec_elem<ESIZE>(w, e) - base.m) * scale) * f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                d[e] = exp2_fast(__builtin_fmaf(vec_elem<ESIZE>(w, e), scale, -base.b)) * f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = ESIZE == 2 ? pack_bf16(d[2 * i % VEC], d[(2 * i + 1) % VEC])
+                              : __builtin_bit_cast(uint32_t, d[i]);
+        return o;
+    }
+    // by a whole wavefront, for the lanes whose tokens are `here`, with logits v;
+    // equal ids get the same sum
+    __device__ __forceinline__ float named(const DistillStats& st, const Named& n, bool here,
+                                           float v) const {
+        const float mine = exp2f(((n.lp - st.norm) - st.log_norm) * kLog2e);
+        float p = 0.0f;
+        each_id(__ballot(here), n.id, [&](int j, int32_t id) {
+            const float other = __builtin_bit_cast(
+                float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), j));
+            p += id == n.id ? other : 0.0f;
+        });
+        const float q = exp2f((v - st.m) * scale - st.log_s * kLog2e);
+        return zero ? 0.0f : g * (q * st.mass - p);
+    }
+};
 
 constexpr int kGradVecs = 4;                       // 16-byte vectors a thread
 constexpr int grad_chunk(int esize) {
@@ -202,78 +306,185 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillTask t, i
     const int64_t hi = lo + CHUNK < t.grad_cols ? lo + CHUNK : t.grad_cols;
     const T* x = (const T*)t.logits + row * t.ld;
     T* d = (T*)t.grad + row * t.grad_ld;
-    const DistillStats st = *(const DistillStats*)(t.row_stats + row * VPA_DISTILL_STATS);
-    const float scale = kLog2e / t.temperature;
-    const float g = t.grad_loss[row] / t.temperature;
-    const bool zero = st.mass == 0.0f;
-    const float f = g * st.f_out;
-    const float log2_out = st.log_out * kLog2e;
-    auto slope = [&](float v) {
-        const float r = exp2f((v - st.m_out) * scale - log2_out);
-        return zero ? 0.0f : r * f;
-    };
-    // this workgroup's named tokens, one a lane of the first wavefront
-    float own = 0.0f;
-    int64_t at = -1;
-    if (threadIdx.x < 64) {
-        const Named n = named_of(t, row);
-        if (n.first && n.id >= lo && n.id < hi) {
-            at = n.id;
-            own = to_f32(x[at]);
-        }
-        float p = 0.0f;
-        for (int j = 0; j < t.n_top; ++j) {
-            const int32_t other = __builtin_amdgcn_readlane(n.id, j);
-            const float lp = __builtin_bit_cast(
-                float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, n.lp), j));
-            p += other == n.id ? exp2f(((lp - st.norm) - st.log_norm) * kLog2e) : 0.0f;
-        }
-        const float q = exp2f((own - st.m) * scale - st.log_s * kLog2e);
-        own = zero ? 0.0f : g * (q * st.mass - p);
-    }
-    __syncthreads();
     u32x4_t w[kGradVecs];
 #pragma unroll
     for (int i = 0; i < kGradVecs; ++i) {
         const int64_t c = lo + (i * kThreads + threadIdx.x) * VEC;
         if (c + VEC <= t.vocab)
             w[i] = ((const Loose16*)(x + c))->v;
+        else
+            w[i] = load_columns<ESIZE>(x, (int)c, 0, t.vocab);
     }
+    const DistillStats st = *(const DistillStats*)(t.row_stats + row * VPA_DISTILL_STATS);
+    const Slope sl(t, row, st);
+    // this workgroup's named columns, one a lane of the first wavefront
+    float own = 0.0f;
+    int64_t at = -1;
+    if (threadIdx.x < 64) {
+        const Named n = named_of(t, row);
+        const bool here = n.id >= lo && n.id < hi;
+        if (__ballot(here)) {
+            own = sl.named(st, n, here, here ? to_f32(x[n.id]) : 0.0f);
+            at = here ? n.id : -1;
+        }
+    }
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kGradVecs; ++i) {
         const int64_t c = lo + (i * kThreads + threadIdx.x) * VEC;
-        if (c + VEC <= t.vocab) {
-            u32x4_t o;
-            if constexpr (ESIZE == 2) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[e] = pack_bf16(slope(vec_elem<2>(w[i], 2 * e)),
-                                     slope(vec_elem<2>(w[i], 2 * e + 1)));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[e] = __builtin_bit_cast(uint32_t, slope(vec_elem<4>(w[i], e)));
-            }
-            __builtin_nontemporal_store(o, &((Loose16*)(d + c))->v);
-        } else {
-            for (int e = 0; e < VEC; ++e)
-                if (c + e < hi)
-                    from_f32(d[c + e], c + e < t.vocab ? slope(to_f32(x[c + e])) : 0.0f);
-        }
+        if (c < t.vocab)
+            store_columns<ESIZE>(d, (int)c, 0, t.vocab, sl.of<ESIZE>(w[i]));
+        if (c + VEC > t.vocab)
+#pragma unroll 1
+            for (int64_t z = c > t.vocab ? c : t.vocab; z < c + VEC && z < hi; ++z)
+                from_f32(d[z], 0.0f);
     }
     __syncthreads();
     if (at >= 0)
         from_f32(d[at], own);
 }
 
-}  // namespace
-
-size_t distill_workspace(int64_t, int64_t) {
-    return 0;
+// Loss and gradient of a row that a workgroup holds in registers, NV vectors a
+// lane: the logits are read once.
+template <int ESIZE, int NV, int THREADS>
+__global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillTask t) {
+    using T = typename elem<ESIZE>::type;
+    constexpr int VEC = 16 / ESIZE;
+    constexpr int ROW_WAVES = THREADS / 64;
+    __shared__ float lds_m[ROW_WAVES], lds_s[ROW_WAVES];
+    __shared__ DistillStats lds_st;
+    __shared__ Teacher lds_te[64];                 // registers are short
+    const int64_t row = blockIdx.x;
+    const T* x = (const T*)t.logits + row * t.ld;
+    T* d = (T*)t.grad + row * t.grad_ld;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const float scale = kLog2e / t.temperature;
+    const int begin = -(int)(((uintptr_t)x & 15) / ESIZE);
+    const int mine = begin + (int)threadIdx.x * VEC;
+    // whether all of the workgroup's i-th vectors are columns of the row
+    const auto whole = [&](int i) {
+        return (i > 0 || begin == 0) && begin + (i + 1) * THREADS * VEC <= t.vocab;
+    };
+    u32x4_t w[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = mine + i * THREADS * VEC;
+        if (whole(i))
+            w[i] = __builtin_nontemporal_load((const u32x4_t*)(x + c));
+        else
+            w[i] = load_columns<ESIZE>(x, c, 0, t.vocab);
+    }
+    const Named n = named_of(t, row);
+    const float v = named_logit(x, n);
+    if (wave == 0)
+        lds_te[lane] = teacher_of(t, n);
+    // the named columns stay out of the sums; their own slopes are stored at the end
+    if (t.tail)
+        mask_named<ESIZE, NV, THREADS>(w, begin, n.id);
+    float m = kMinusInf;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        m = fmaxf(m, vec_largest<ESIZE>(w[i]));
+    m = wave_max(m);
+    if (lane == 0)
+        lds_m[wave] = m;
+    __syncthreads();
+    m = wave_max(lds_m[lane % ROW_WAVES]);
+    ScaledFrom base;
+    base.set(m == kMinusInf ? 0.0f : m, scale);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        asm volatile("" : "+v"(w[i]));
+    const float s = wave_sum(chunk_sum<ESIZE, NV>(w, base, scale));
+    if (lane == 0)
+        lds_s[wave] = s;
+    __syncthreads();
+    if (wave == 0) {
+        const float all = wave_sum(lane < ROW_WAVES ? lds_s[lane] : 0.0f);
+        const DistillStats st = finish_row(t, row, v, n, lds_te[lane], ExpSum{m, all});
+        if (lane == 0)
+            lds_st = st;
+    }
+    __syncthreads();
+    const DistillStats st = lds_st;
+    const Slope sl(t, row, st);
+    float own = 0.0f;
+    if (wave == 0)
+        own = sl.named(st, n, n.id >= 0, v);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        asm volatile("" : "+v"(w[i]));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = mine + i * THREADS * VEC;
+        const u32x4_t o = sl.of<ESIZE>(w[i]);
+        if (whole(i))
+            __builtin_nontemporal_store(o, &((Loose16*)(d + c))->v);   // past the L2
+        else
+            store_columns<ESIZE>(d, c, 0, t.vocab, o);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int64_t c = t.vocab + threadIdx.x; c < t.grad_cols; c += THREADS)
+        from_f32(d[c], 0.0f);
+    __syncthreads();
+    if (wave == 0 && n.id >= 0)
+        from_f32(d[n.id], own);
 }
 
-int64_t distill_threads(int, int64_t, int64_t n_rows) {
-    return n_rows * kThreads;
+// Chunks of 8 vectors a thread where that gives every CU 4 workgroups, else of 2;
+// segments of whole chunks until there are 4 (8) workgroups a CU.
+Cut distill_cut(int esize, int64_t vocab, int64_t n_rows) {
+    Cut c;
+    const int64_t vec = 16 / esize, width = vocab + vec - 1, big = kThreads * 8 * vec;
+    c.vecs = 2 * width > big && n_rows * ((width + big - 1) / big) >= 1024 ? 8 : 2;
+    const int64_t chunk = kThreads * c.vecs * vec, chunks = (width + chunk - 1) / chunk;
+    int64_t want = ((c.vecs == 8 ? 1024 : 2048) + n_rows - 1) / n_rows;
+    want = want > chunks ? chunks : want;
+    want = want > kMostSegments ? kMostSegments : want;
+    c.chunks = (int32_t)((chunks + want - 1) / want);
+    c.segments = (int32_t)((chunks + c.chunks - 1) / c.chunks);
+    return c;
+}
+
+// Threads and vectors a lane that hold a row of `vocab` columns (one vector more
+// for what lies before the first aligned column); 0 where a row is too long.
+struct RowForm {
+    int threads, vectors;
+};
+RowForm row_form(int esize, int64_t vocab) {
+    const int64_t vec = 16 / esize, need = (vocab + vec - 1 + vec - 1) / vec;
+    constexpr RowForm forms[] = {{256, 1}, {256, 4}, {256, 8}, {512, 7},
+                                 {512, 13}, {1024, 10}, {1024, 14}, {1024, 20}};
+    for (const RowForm& f : forms)
+        if (need <= f.threads * f.vectors)
+            return f;
+    return {0, 0};
+}
+
+// Whether a call takes its rows whole.  Rows that fill a CU's registers alone
+// need enough of them to be worth it.
+bool rows_whole(RowForm f, int64_t n_rows) {
+    return f.threads != 0 && (f.threads < 1024 || n_rows >= 128);
+}
+
+
+size_t sums_bytes(const Cut& c, int64_t n_rows) {
+    return c.segments == 1 ? 0 : (size_t)n_rows * c.segments * sizeof(ExpSum);
+}
+
+}  // namespace
+
+size_t distill_workspace(int64_t vocab, int64_t n_rows) {
+    const size_t b2 = sums_bytes(distill_cut(2, vocab, n_rows), n_rows);
+    const size_t b4 = sums_bytes(distill_cut(4, vocab, n_rows), n_rows);
+    return b2 > b4 ? b2 : b4;
+}
+
+int64_t distill_threads(int esize, int64_t vocab, int64_t n_rows) {
+    const int64_t cut = n_rows * distill_cut(esize, vocab, n_rows).segments * kThreads;
+    const RowForm f = row_form(esize, vocab);
+    const int64_t rows = rows_whole(f, n_rows) ? n_rows * f.threads : 0;
+    return cut > rows ? cut : rows;
 }
 
 int64_t distill_grad_threads(int esize, int64_t grad_cols, int64_t n_rows) {
@@ -281,10 +492,46 @@ int64_t distill_grad_threads(int esize, int64_t grad_cols, int64_t n_rows) {
     return (grad_cols + chunk - 1) / chunk * n_rows * kThreads;
 }
 
-hipError_t launch_distill(int esize, const DistillTask& t, void*, hipStream_t stream) {
-    const dim3 grid((uint32_t)t.n_rows), block(kThreads);
-    return esize == 2 ? launch(distill_kernel<2>, grid, block, 0, stream, t)
-                      : launch(distill_kernel<4>, grid, block, 0, stream, t);
+namespace {
+
+template <int ESIZE>
+hipError_t launch_loss(const DistillTask& t, void* ws, hipStream_t stream) {
+    const Cut c = distill_cut(ESIZE, t.vocab, t.n_rows);
+    const dim3 grid((uint32_t)((int64_t)t.n_rows * c.segments)), block(kThreads);
+    ExpSum* sums = (ExpSum*)ws;
+    const hipError_t e =
+        c.vecs == 8 ? launch(distill_kernel<ESIZE, 8>, grid, block, 0, stream, t, c, sums)
+                    : launch(distill_kernel<ESIZE, 2>, grid, block, 0, stream, t, c, sums);
+    if (e != hipSuccess || c.segments == 1)
+        return e;
+    return launch(distill_finish_kernel<ESIZE>, dim3((uint32_t)t.n_rows), dim3(64), 0, stream, t, c,
+                  sums);
+}
+
+template <int ESIZE>
+hipError_t launch_rows(const DistillTask& t, RowForm f, hipStream_t stream) {
+    const dim3 grid((uint32_t)t.n_rows), block((uint32_t)f.threads);
+    if (f.threads == 256) {
+        if (f.vectors == 1)
+            return launch(distill_row_kernel<ESIZE, 1, 256>, grid, block, 0, stream, t);
+        return f.vectors == 4 ? launch(distill_row_kernel<ESIZE, 4, 256>, grid, block, 0, stream, t)
+                              : launch(distill_row_kernel<ESIZE, 8, 256>, grid, block, 0, stream, t);
+    }
+    if (f.threads == 512) {
+        if (f.vectors == 7)
+            return launch(distill_row_kernel<ESIZE, 7, 512>, grid, block, 0, stream, t);
+        return launch(distill_row_kernel<ESIZE, 13, 512>, grid, block, 0, stream, t);
+    }
+    if (f.vectors == 10)
+        return launch(distill_row_kernel<ESIZE, 10, 1024>, grid, block, 0, stream, t);
+    return f.vectors == 14 ? launch(distill_row_kernel<ESIZE, 14, 1024>, grid, block, 0, stream, t)
+                           : launch(distill_row_kernel<ESIZE, 20, 1024>, grid, block, 0, stream, t);
+}
+
+}  // namespace
+
+hipError_t launch_distill(int esize, const DistillTask& t, void* ws, hipStream_t stream) {
+    return esize == 2 ? launch_loss<2>(t, ws, stream) : launch_loss<4>(t, ws, stream);
 }
 
 hipError_t launch_distill_grad(int esize, const DistillTask& t, hipStream_t stream) {
@@ -296,6 +543,9 @@ hipError_t launch_distill_grad(int esize, const DistillTask& t, hipStream_t stre
 }
 
 hipError_t launch_distill_both(int esize, const DistillTask& t, void* ws, hipStream_t stream) {
+    const RowForm f = row_form(esize, t.vocab);
+    if (rows_whole(f, t.n_rows))
+        return esize == 2 ? launch_rows<2>(t, f, stream) : launch_rows<4>(t, f, stream);
     const hipError_t e = launch_distill(esize, t, ws, stream);
     return e != hipSuccess ? e : launch_distill_grad(esize, t, stream);
 }

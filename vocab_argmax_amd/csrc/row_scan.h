@@ -41,41 +41,95 @@ __device__ __forceinline__ u32x4_t vec_minus_inf() {
     return u32x4_t{w, w, w, w};
 }
 
-// Columns c .. c+VEC-1 of a row, those outside [lo, hi) as -inf.
+// 16 bytes as one number, and back.
+struct Bits128 {
+    uint64_t lo, hi;
+    __device__ __forceinline__ explicit Bits128(u32x4_t v)
+        : lo(v[0] | (uint64_t)v[1] << 32), hi(v[2] | (uint64_t)v[3] << 32) {}
+    __device__ __forceinline__ Bits128(uint64_t l, uint64_t h) : lo(l), hi(h) {}
+    __device__ __forceinline__ u32x4_t vec() const {
+        return u32x4_t{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    }
+    // by n bits, 0 <= n <= 128
+    __device__ __forceinline__ Bits128 right(int n) const {
+        const int in = n & 63;
+        const uint64_t both = lo >> in | (hi << 1) << (63 - in);
+        return {n < 64 ? both : n < 128 ? hi >> in : 0, n < 64 ? hi >> in : 0};
+    }
+    __device__ __forceinline__ Bits128 left(int n) const {
+        const int in = n & 63;
+        const uint64_t both = hi << in | (lo >> 1) >> (63 - in);
+        return {n < 64 ? lo << in : 0, n < 64 ? both : n < 128 ? lo << in : 0};
+    }
+};
+
+// Columns c .. c+VEC-1 of a row, those outside [lo, hi) as -inf.  A vector that
+// reaches past an end is the one that stops there, moved: with a load for each
+// element a row's registers would be as many again.
 template <int ESIZE, typename T>
-__device__ __forceinline__ u32x4_t load_columns(const T* x, int64_t c, int64_t lo, int64_t hi) {
+__device__ __forceinline__ u32x4_t load_columns(const T* x, int c, int lo, int hi) {
     constexpr int VEC = 16 / ESIZE;
     if (c >= lo && c + VEC <= hi)
         return __builtin_nontemporal_load((const u32x4_t*)(x + c));
-    union {
-        T e[VEC];
-        u32x4_t v;
-    } u;
-    u.v = vec_minus_inf<ESIZE>();
-    if (c + VEC > lo && c < hi) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            if (c + e >= lo && c + e < hi)
-                u.e[e] = x[c + e];
+    if (c + VEC <= lo || c >= hi)
+        return vec_minus_inf<ESIZE>();
+    Bits128 v(0, 0), in(0, 0);                     // values, and where they are
+    if (hi - lo >= VEC) {
+        const int at = c < lo ? lo : hi - VEC;
+        v = Bits128(((const Loose16*)(x + at))->v);
+        const int n = (c < at ? at - c : c - at) * ESIZE * 8;
+        const Bits128 all(~0ull, ~0ull);
+        v = c < at ? v.left(n) : v.right(n);
+        in = c < at ? all.left(n) : all.right(n);
+        // (both ends in one vector: hi - lo >= VEC leaves one of them to each)
+    } else {
+#pragma unroll 1
+        for (int e = lo > c ? lo - c : 0; e < VEC && c + e < hi; ++e) {
+            uint64_t one;
+            if constexpr (ESIZE == 2)
+                one = x[c + e];
+            else
+                one = __builtin_bit_cast(uint32_t, x[c + e]);
+            const Bits128 put = Bits128(one, 0).left(e * ESIZE * 8);
+            const Bits128 all = Bits128(ESIZE == 2 ? 0xFFFFull : 0xFFFFFFFFull, 0).left(e * ESIZE * 8);
+            v = Bits128(v.lo | put.lo, v.hi | put.hi);
+            in = Bits128(in.lo | all.lo, in.hi | all.hi);
+        }
     }
-    return u.v;
+    const Bits128 none(vec_minus_inf<ESIZE>());
+    return Bits128(v.lo | (none.lo & ~in.lo), v.hi | (none.hi & ~in.hi)).vec();
 }
 
-// Makes element e of vector i (both the same in all lanes) -inf in lane `at`.
-template <int ESIZE, int U>
-__device__ __forceinline__ void mask_element(u32x4_t (&w)[U], int i, int e, int at) {
+// Stores those of columns c .. c+VEC-1 that lie in [lo, hi), past the L2.
+template <int ESIZE, typename T>
+__device__ __forceinline__ void store_columns(T* d, int c, int lo, int hi, u32x4_t o) {
+    constexpr int VEC = 16 / ESIZE;
+    if (c >= lo && c + VEC <= hi) {
+        __builtin_nontemporal_store(o, &((Loose16*)(d + c))->v);
+        return;
+    }
+    const Bits128 v(o);
+#pragma unroll 1
+    for (int e = lo > c ? lo - c : 0; e < VEC && c + e < hi; ++e) {
+        const uint64_t one = v.right(e * ESIZE * 8).lo;
+        if constexpr (ESIZE == 2)
+            d[c + e] = (uint16_t)one;
+        else
+            d[c + e] = __builtin_bit_cast(float, (uint32_t)one);
+    }
+}
+
+// Makes element e (the same in all lanes) of lane `at`'s vector -inf.
+template <int ESIZE>
+__device__ __forceinline__ void mask_element(u32x4_t& w, int e, int at) {
+    const Bits128 one = Bits128(ESIZE == 2 ? 0xFFFFull : 0xFFFFFFFFull, 0).left(e * ESIZE * 8);
+    const u32x4_t m = one.vec(), none = vec_minus_inf<ESIZE>();
     const bool mine = (int)(threadIdx.x & 63) == at;
 #pragma unroll
-    for (int k = 0; k < U; ++k)
-        if (k == i)
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-                if (d == e * ESIZE / 4) {
-                    const uint32_t v = ESIZE == 4 ? 0xFF800000u
-                                       : e % 2    ? (w[k][d] & 0x0000FFFFu) | 0xFF800000u
-                                                  : (w[k][d] & 0xFFFF0000u) | 0x0000FF80u;
-                    w[k][d] = mine ? v : w[k][d];
-                }
+    for (int d = 0; d < 4; ++d) {
+        const uint32_t in = mine ? m[d] : 0;
+        w[d] = (w[d] & ~in) | (none[d] & in);
+    }
 }
 
 // z = (x - M) scale as one multiply-add, x scale - b with b = M scale rounded:
@@ -98,21 +152,18 @@ __device__ __forceinline__ float chunk_sum(const u32x4_t (&w)[U], const ScaledFr
                                            float scale) {
     constexpr int VEC = 16 / ESIZE;
     float s = 0.0f;
-    if (base.apart) {
+    // (one branch around both loops would have all of the values unpacked before it)
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
+    for (int i = 0; i < U; ++i) {
+        if (base.apart) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
                 s += exp2_fast((vec_elem<ESIZE>(w[i], e) - base.m) * scale);
-            __builtin_amdgcn_sched_barrier(0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                s += exp2_fast(__builtin_fmaf(vec_elem<ESIZE>(w[i], e), scale, -base.b));
         }
-        return s;
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            s += exp2_fast(__builtin_fmaf(vec_elem<ESIZE>(w[i], e), scale, -base.b));
         __builtin_amdgcn_sched_barrier(0);         // registers for one vector at a time
     }
     return s * base.fix;
@@ -162,8 +213,11 @@ struct SegmentScan {
                     w[i] = __builtin_nontemporal_load((const u32x4_t*)(x + mine + i * THREADS * VEC));
             } else {
 #pragma unroll
-                for (int i = 0; i < U; ++i)
+                for (int i = 0; i < U; ++i) {
                     w[i] = load_columns<ESIZE>(x, mine + i * THREADS * VEC, lo, hi);
+                    asm volatile("" : "+v"(w[i]));
+                    __builtin_amdgcn_sched_barrier(0);     // registers for one at a time
+                }
             }
             masked(w, c0);
             float mx = kMinusInf;
