@@ -420,7 +420,10 @@ vpa_status vpa_quantize_fp8(const void* x, int64_t ldx, vpa_dtype dtype, int64_t
 size_t vpa_head_linear_fp8_workspace(int64_t rows, int64_t outer, int64_t inner) {
     if (rows < 1 || check_sizes("", rows, outer, inner) != VPA_OK)
         return 0;
-    return fp8_workspace(rows, outer, inner);
+    // for results of either type
+    const size_t a = fp8_workspace(rows, outer, inner, false);
+    const size_t b = fp8_workspace(rows, outer, inner, true);
+    return a > b ? a : b;
 }
 
 vpa_status vpa_head_linear_fp8(const void* x, int64_t ldx, const float* x_scale, int64_t ldxs,
@@ -446,18 +449,22 @@ vpa_status vpa_head_linear_fp8(const void* x, int64_t ldx, const float* x_scale,
         (residual && (st = check_matrix("residual", residual, 2, ldr, outer)) != VPA_OK) ||
         (st = check_matrix("y", y, esize_of(odt), ldy, outer)) != VPA_OK)
         return st;
-    if (ldx % 16 || ldw % 16 || ldx > ((int64_t)1 << 21) || ldw > ((int64_t)1 << 21))
+    const int64_t most = (int64_t)1 << 21;
+    if (ldx % 16 || ldw % 16 || ldx > most || ldw > most || ldxs > most)
         return fail(VPA_ERR_INVALID,
-                    "%s: row strides %lld and %lld: multiples of 16 of at most 2^21 are taken", call,
-                    (long long)ldx, (long long)ldw);
+                    "%s: row strides %lld, %lld (multiples of 16) or %lld (scales) above 2^21", call,
+                    (long long)ldx, (long long)ldw, (long long)ldxs);
     if (y == residual && (ldy != ldr || odt != VPA_BF16))
         return fail(VPA_ERR_INVALID, "%s: y in the residual's place needs its stride and type",
                     call);
-    if ((st = check_dispatch(fp8_threads(rows, outer, inner), call)) != VPA_OK ||
-        (st = check_workspace(call, workspace, workspace_bytes, fp8_workspace(rows, outer, inner))) !=
-            VPA_OK)
+    // results of more than a step of bf16 take exact products
+    const bool exact = odt == VPA_F32;
+    if ((st = check_dispatch(fp8_threads(rows, outer, inner, exact), call)) != VPA_OK ||
+        (st = check_workspace(call, workspace, workspace_bytes,
+                              fp8_workspace(rows, outer, inner, exact))) != VPA_OK)
         return st;
     Fp8Task t{};
+    t.exact = exact;
     GemmTask& g = t.g;
     g.a = x;
     g.a_m = ldx;

@@ -313,8 +313,6 @@ GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b
     return p;
 }
 
-namespace {
-
 // The second launch of a plan that has one: m and n become its part's sizes.
 GemmPlan plan_rest(int esize, const GemmPlan& first, int64_t& m, int64_t& n, int64_t k) {
     m -= first.first_m < m ? first.first_m : 0;
@@ -323,6 +321,8 @@ GemmPlan plan_rest(int esize, const GemmPlan& first, int64_t& m, int64_t& n, int
     plan_tiles(esize, m, n, k, r);
     return r;
 }
+
+namespace {
 
 // Most work-items of one of a plan's dispatches, the join among them.
 int64_t planned_threads(const GemmPlan& p, int64_t m, int64_t n) {
@@ -362,22 +362,23 @@ int64_t gemm_threads(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool
     return first > rest ? first : rest;
 }
 
-namespace {
-
-hipError_t launch_planned(int esize, const GemmTask& t, const GemmPlan& p, hipStream_t stream) {
-    hipError_t e = esize == 2 ? launch_gemm_tiles_bf16(t, p, stream)
-                              : launch_gemm_tiles_f32(t, p, stream);
-    if (e != hipSuccess || p.slices == 1)
-        return e;
+hipError_t launch_gemm_join(int esize, const GemmTask& t, int32_t slices, hipStream_t stream) {
     const bool join4 = t.n % 4 == 0;
     const int64_t items = t.m * t.n / (join4 ? 4 : 1);
     const dim3 grid((uint32_t)((items + kThreads - 1) / kThreads)), block(kThreads);
     if (esize == 2)
-        return join4 ? launch(gemm_join_kernel<uint16_t, true>, grid, block, 0, stream, t, p.slices)
-                     : launch(gemm_join_kernel<uint16_t, false>, grid, block, 0, stream, t,
-                              p.slices);
-    return join4 ? launch(gemm_join_kernel<float, true>, grid, block, 0, stream, t, p.slices)
-                 : launch(gemm_join_kernel<float, false>, grid, block, 0, stream, t, p.slices);
+        return join4 ? launch(gemm_join_kernel<uint16_t, true>, grid, block, 0, stream, t, slices)
+                     : launch(gemm_join_kernel<uint16_t, false>, grid, block, 0, stream, t, slices);
+    return join4 ? launch(gemm_join_kernel<float, true>, grid, block, 0, stream, t, slices)
+                 : launch(gemm_join_kernel<float, false>, grid, block, 0, stream, t, slices);
+}
+
+namespace {
+
+hipError_t launch_planned(int esize, const GemmTask& t, const GemmPlan& p, hipStream_t stream) {
+    const hipError_t e = esize == 2 ? launch_gemm_tiles_bf16(t, p, stream)
+                                    : launch_gemm_tiles_f32(t, p, stream);
+    return e != hipSuccess || p.slices == 1 ? e : launch_gemm_join(esize, t, p.slices, stream);
 }
 
 }  // namespace

@@ -12,6 +12,8 @@
 // lies below 2^-13 of the largest (measured; random normal operands end 1.4e-5
 // off in the 2-norm).  Widened to bf16, which holds every e4m3 value, products
 // are summed in full fp32 at half the rate.
+#include <type_traits>
+
 #include "gemm_tile.h"
 #include "linear_common.h"
 #include "vpa_draft_internal.h"
@@ -32,6 +34,22 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
     return u.v;
 }
 
+// The first n bytes at p (n may be 0 or negative), 0 after them; p at 16 bytes.
+__device__ __forceinline__ u32x4_t first_bytes(const char* p, int64_t n) {
+    if (n >= 16)
+        return *(const u32x4_t*)p;
+    union {
+        uint8_t e[16];
+        u32x4_t v;
+    } u;
+    u.v = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 15; ++i)
+        if (i < n)
+            u.e[i] = ((const uint8_t*)p)[i];
+    return u.v;
+}
+
 // P Q^T for 16 rows of P and of Q over 128 k: bytes q*16.. of both halves.
 __device__ __forceinline__ f32x4 mma_exact(const u32x4_t (&p)[2], const u32x4_t (&q)[2]) {
     f32x4 d = {0, 0, 0, 0};
@@ -44,60 +62,538 @@ __device__ __forceinline__ f32x4 mma_exact(const u32x4_t (&p)[2], const u32x4_t 
     return d;
 }
 
-// 16 bytes at column k of a row of n, 0 past its end.
-__device__ __forceinline__ u32x4_t load16(const uint8_t* row, int64_t k, int64_t n) {
-    if (k + 16 <= n)
-        return *(const u32x4_t*)(row + k);
-    union {
-        uint8_t e[16];
-        u32x4_t v;
-    } u;
-    u.v = u32x4_t{0, 0, 0, 0};
-    for (int i = 0; i < 16; ++i)
-        if (k + i < n)
-            u.e[i] = row[k + i];
-    return u.v;
+// The same by the 8-bit instruction (see above).
+__device__ __forceinline__ f32x4 mma_fast(const u32x4_t (&p)[2], const u32x4_t (&q)[2]) {
+    typedef int i32x8 __attribute__((ext_vector_type(8)));
+    const i32x8 a = {(int)p[0][0], (int)p[0][1], (int)p[0][2], (int)p[0][3],
+                     (int)p[1][0], (int)p[1][1], (int)p[1][2], (int)p[1][3]};
+    const i32x8 b = {(int)q[0][0], (int)q[0][1], (int)q[0][2], (int)q[0][3],
+                     (int)q[1][0], (int)q[1][1], (int)q[1][2], (int)q[1][3]};
+    // e4m3 in both, and no scales of the instruction's own
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0,
+                                                            0);
 }
 
-// A wavefront a 16 x 16 tile.
-__global__ __launch_bounds__(64) void fp8_simple_kernel(Fp8Task f, uint32_t tiles_m) {
-    const GemmTask& t = f.g;
-    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-    const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * 16, n0 = (int64_t)(blockIdx.x / tiles_m) * 16;
-    const int64_t m = m0 + r < t.m ? m0 + r : t.m - 1, n = n0 + r < t.n ? n0 + r : t.n - 1;
-    const uint8_t* x = (const uint8_t*)t.a + m * t.a_m;
-    const uint8_t* w = (const uint8_t*)t.b + n * t.b_n;
-    const float* xs = f.a_scale + m * f.lda_scale;
-    const float* ws = f.b_scale + n0 / kScaleBlock * f.ldb_scale;
-    f32x4 acc = {};
-    for (int64_t b = 0; b * kScaleBlock < t.k; ++b) {
-        const int64_t k = b * kScaleBlock + q * 16;
-        const u32x4_t p[2] = {load16(w, k, t.k), load16(w, k + 64, t.k)};
-        const u32x4_t v[2] = {load16(x, k, t.k), load16(x, k + 64, t.k)};
-        acc += mma_exact(p, v) * (xs[b] * ws[b]);
+// A row's 128 bytes widened, for products with several others.
+struct Wide {
+    bf16x8 v[4];
+    __device__ __forceinline__ Wide() {}
+    __device__ __forceinline__ explicit Wide(const u32x4_t (&p)[2]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = widen(p[e / 2][e % 2 * 2], p[e / 2][e % 2 * 2 + 1]);
     }
-    if (m0 + r >= t.m)
-        return;
+};
+__device__ __forceinline__ f32x4 mma_wide(const Wide& p, const Wide& q) {
+    f32x4 d = {0, 0, 0, 0};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        if (n0 + q * 4 + e < t.n)
-            store_result<uint16_t>(t, m0 + r, n0 + q * 4 + e, acc[e]);
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p.v[e], q.v[e], d, 0, 0, 0);
+    return d;
+}
+
+// Weight scales of a workgroup's columns, one for each block of k: the same in
+// all lanes, read through the scalar cache.
+typedef const float __attribute__((address_space(4))) * scalar_floats;
+__device__ __forceinline__ scalar_floats weight_scales(const Fp8Task& f, int64_t n) {
+    return (scalar_floats)uniform(f.b_scale + n / kScaleBlock * f.ldb_scale);
+}
+
+// x's scales of a tile of ROWS rows for one block of k, straight to LDS: 64 rows
+// a wavefront, by the wavefronts that have them.
+template <int ROWS>
+struct ScaleLoader {
+    const float* base;
+    uint32_t off, size;
+    __device__ __forceinline__ void init(const Fp8Task& f, int64_t row0, int64_t rows, int first) {
+        const int left = rows - row0 < ROWS ? (int)(rows - row0) : ROWS;
+        const int r = first + (int)(threadIdx.x & 63);
+        base = f.a_scale + row0 * f.lda_scale;
+        off = (uint32_t)((r < left ? r : left - 1) * f.lda_scale * 4);
+        size = (uint32_t)((left - 1) * f.lda_scale * 4 + 4);
+    }
+    // to `lds` and the 255 bytes after it
+    __device__ __forceinline__ void load(int64_t block, char* lds) const {
+#ifdef __HIP_DEVICE_COMPILE__
+        const auto buf = __builtin_amdgcn_make_buffer_rsrc(
+            uniform(base + block), 0, __builtin_amdgcn_readfirstlane(size), 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_ptr)lds, 4, off, 0, 0, 0);
+#endif
+    }
+};
+
+// WM x WN wavefronts, each with BM/WM x BN/WN of the tile in its accumulators.
+// With part set, the raw sums of a slice of k go to part[slice][m][n].
+//
+// As in the 16-bit products, a stage is 128 bytes of k, here one block of scales,
+// and two stages lie in LDS.  A wavefront holds the stage's fragments of W, and of
+// x a ring of 4 that are read 4 products ahead, so that the accumulators, which
+// the scaling keeps in ordinary registers, leave room.  The barrier that says that
+// the next stage has landed, and that every wavefront has read this one, stands
+// before the first read from the next.
+template <bool EXACT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uint32_t tiles_m,
+                                                               uint32_t tiles_n,
+                                                               int64_t stages_per_slice,
+                                                               float* part) {
+    constexpr int NT = WM * WN * 64, RING = 4;
+    constexpr int IM = BM / WM / 16, JN = BN / WN / 16;
+    static_assert(IM % RING == 0 && JN == 4, "a ring of fragments, blocks of 64 columns");
+    static_assert(BN / WN <= kScaleBlock && kScaleBlock % (BN / WN) == 0, "one scale of W");
+    using LA = TileLoader<1, true, true, BM, NT>;
+    using LB = TileLoader<1, true, true, BN, NT>;
+    constexpr int SCALES = LA::BYTES + LB::BYTES, STAGE = SCALES + BM * 4;
+    __shared__ __align__(1024) char lds0[STAGE];
+    __shared__ __align__(1024) char lds1[STAGE];
+    const GemmTask& t = f.g;
+    uint32_t slice, tm, tn;
+    tile_of_block(blockIdx.x, gridDim.x, tiles_m, tiles_n, slice, tm, tn);
+    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
+    LA la;
+    LB lb;
+    la.init(t.a, t.a_m, m0, t.m);
+    lb.init(t.b, t.b_n, n0, t.n);
+    ScaleLoader<BM> ls;
+    ls.init(f, m0, t.m, wave * 64 % BM);
+    const int64_t whole = t.k / 128, all = (t.k + 127) / 128;
+    const int64_t s0 = slice * stages_per_slice;
+    const int64_t end = s0 + stages_per_slice < all ? s0 + stages_per_slice : all;
+    const int64_t s1 = end < whole ? end : whole;
+    // (a tile's last columns may have no scales of their own)
+    const scalar_floats ws = weight_scales(f, n0 + wn < t.n ? n0 + wn : t.n - 1);
+    const typename LA::Place pa = LA::place(wm);
+    const typename LB::Place pb = LB::place(wn);
+    const int scale_at = SCALES + (wm + (lane & 15)) * 4;
+    f32x4 acc[IM][JN] = {};
+    const typename LA::Direct da = la.direct();
+    const typename LB::Direct db = lb.direct();
+    auto stage = [&](int64_t s, char* lds) {
+        la.load(da, s, lds);
+        lb.load(db, s, lds + LA::BYTES);
+        if (wave < BM / 64)
+            ls.load(s, lds + SCALES + wave * 256);
+    };
+    u32x4_t av[RING][2], bv[JN][2];
+    float sx[RING];
+    auto read_a = [&](const char* lds, const typename LA::Place& p, int i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            av[i % RING][h] = LA::fragment(lds, p, i, h);
+        sx[i % RING] = *(const float*)(lds + scale_at + i * 64);
+    };
+    auto read_b = [&](const char* lds, const typename LB::Place& p, int j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            bv[j][h] = LB::fragment(lds + LA::BYTES, p, j, h);
+    };
+    Wide wide[EXACT ? JN : 1];
+    auto products = [&](int i, float sw) {
+        f32x4 p[JN];
+        if constexpr (EXACT) {
+            const Wide a(av[i % RING]);
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+                p[j] = mma_wide(wide[j], a);
+        } else {
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+                p[j] = mma_fast(bv[j], av[i % RING]);
+        }
+        const float sc = sx[i % RING] * sw;
+#pragma unroll
+        for (int j = 0; j < JN; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][j][e] = __builtin_fmaf(p[j][e], sc, acc[i][j][e]);
+            // here, not at the end of the stage with all of its products kept
+            asm volatile("" : "+v"(acc[i][j]));
+        }
+    };
+    auto widen_b = [&] {
+        if constexpr (EXACT)
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+                wide[j] = Wide(bv[j]);
+    };
+    // a stage that k ends in comes first, so that the loop has whole ones only
+    if (end > whole) {
+        la.load_tail(whole, t.k, lds1);
+        lb.load_tail(whole, t.k, lds1 + LA::BYTES);
+        if (wave < BM / 64)
+            ls.load(whole, lds1 + SCALES + wave * 256);
+        stage_barrier();
+#pragma unroll
+        for (int j = 0; j < JN; ++j)
+            read_b(lds1, pb, j);
+        widen_b();
+#pragma unroll
+        for (int i = 0; i < IM; ++i) {
+            read_a(lds1, pa, i);
+            products(i, ws[whole]);
+        }
+        stage_barrier();
+    }
+    if (s0 < s1) {
+        stage(s0, lds0);
+        if (s0 + 1 < s1)
+            stage(s0 + 1, lds1);
+        stage_barrier();
+#pragma unroll
+        for (int j = 0; j < JN; ++j)
+            read_b(lds0, pb, j);
+#pragma unroll
+        for (int i = 0; i < RING; ++i)
+            read_a(lds0, pa, i);
+    }
+    const bool early = wave < WM * WN / 2;
+    float sw = s0 < s1 ? ws[s0] : 0.0f;
+    for (int64_t s = s0; s + 1 < s1; ++s) {
+        char* now = (s - s0) & 1 ? lds1 : lds0;
+        char* next = (s - s0) & 1 ? lds0 : lds1;
+        const float sw_next = ws[s + 1];
+        widen_b();
+        const typename LA::Place a = pa.again();
+        const typename LB::Place b = pb.again();
+#pragma unroll
+        for (int i = 0; i < IM; ++i) {
+            products(i, sw);
+            if (i == IM - RING) {
+                // the next stage has landed, and this one has been read
+                stage_barrier();
+                if (early && s + 2 < s1)
+                    stage(s + 2, now);
+            }
+            if (i == IM - RING + 2 && !early && s + 2 < s1)
+                stage(s + 2, now);
+            if (i < IM - RING)
+                read_a(now, a, i + RING);
+            else
+                read_a(next, a, i + RING - IM);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int j = 0; j < JN; ++j)
+            read_b(next, b, j);
+        sw = sw_next;
+    }
+    if (s0 < s1) {
+        const char* now = (s1 - 1 - s0) & 1 ? lds1 : lds0;
+        widen_b();
+#pragma unroll
+        for (int i = 0; i < IM; ++i) {
+            products(i, sw);
+            if (i < IM - RING)
+                read_a(now, pa, i + RING);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    stage_barrier();
+    if (part)
+        part += slice * t.m * t.n;
+    constexpr int SLOTS = (LA::BYTES + LB::BYTES) / 16384;     // wavefronts' blocks in one buffer
+    char* mine = wave < SLOTS ? lds0 + wave * 16384 : lds1 + (wave - SLOTS) * 16384;
+#pragma unroll
+    for (int h = 0; h < IM / 4; ++h) {
+        f32x4 block[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                block[i][j] = acc[h * 4 + i][j];
+        store_block<uint16_t>(t, part, mine, m0 + wm + h * 64, n0 + wn, block);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Few rows of x (BM = 32 or 64): bound by reading W, so the tile is 64 rows of W by
+// all of x's, with STAGES - 1 stages on their way (as in the 16-bit products).
+// Products are exact: the matrix cores and the widening have time to spare.
+template <int BM, int STAGES>
+__global__ __launch_bounds__(256) void fp8_few_rows_kernel(Fp8Task f, int64_t stages_per_slice,
+                                                           float* part) {
+    constexpr int BN = kFewRowsCols, NT = 256, WAVES = 4;
+    constexpr int IM = BM / 16;                     // a wavefront: BM x 16 results
+    using LA = TileLoader<1, true, true, BM, NT>;
+    using LB = TileLoader<1, true, true, BN, NT>;
+    // x's scales: every wavefront loads its own copy, so that each has as many
+    // loads under way
+    constexpr int SCALES = LA::BYTES + LB::BYTES, BYTES = SCALES + WAVES * 256;
+    constexpr int LOADS = LA::LOADS + LB::LOADS + 1;
+    __shared__ __align__(1024) char lds[STAGES * BYTES];
+    const GemmTask& t = f.g;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t n0 = (int64_t)blockIdx.x * BN;
+    LA la;
+    LB lb;
+    la.init(t.a, t.a_m, 0, t.m);
+    lb.init(t.b, t.b_n, n0, t.n);
+    ScaleLoader<BM> ls;
+    ls.init(f, 0, t.m, 0);
+    const scalar_floats ws = weight_scales(f, n0);
+    const typename LA::Place pa = LA::place(0);
+    const typename LB::Place pb = LB::place(wave * 16);
+    const typename LA::Direct da = la.direct();
+    const typename LB::Direct db = lb.direct();
+    const int64_t whole = t.k / 128, all = (t.k + 127) / 128;
+    const int64_t s0 = blockIdx.y * stages_per_slice;
+    const int64_t end = s0 + stages_per_slice < all ? s0 + stages_per_slice : all;
+    const int64_t s1 = end < whole ? end : whole;
+    f32x4 acc[IM] = {};
+    // workgroups begin at different stages (see the 16-bit kernel)
+    const int64_t shift = s0 < s1 ? blockIdx.x % (s1 - s0) : 0;
+    auto at = [&](int64_t s) { return s + shift < s1 ? s + shift : s + shift - (s1 - s0); };
+    auto stage = [&](int64_t s) {
+        char* p = lds + (s - s0) % STAGES * BYTES;
+        la.load(da, at(s), p);
+        lb.template load<true>(db, at(s), p + LA::BYTES);
+        ls.load(at(s), p + SCALES + wave * 256);
+    };
+    auto multiply = [&](const char* p, float sw) {
+        u32x4_t v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            v[h] = LB::fragment(p + LA::BYTES, pb, 0, h);
+        const Wide w(v);
+#pragma unroll
+        for (int i = 0; i < IM; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                v[h] = LA::fragment(p, pa, i, h);
+            const float sc = *(const float*)(p + SCALES + wave * 256 + (i * 16 + (lane & 15)) * 4) * sw;
+            const f32x4 d = mma_wide(w, Wide(v));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][e] = __builtin_fmaf(d[e], sc, acc[i][e]);
+        }
+    };
+    // a stage that k ends in comes first
+    if (end > whole) {
+        la.load_tail(whole, t.k, lds);
+        lb.load_tail(whole, t.k, lds + LA::BYTES);
+        ls.load(whole, lds + SCALES + wave * 256);
+        stage_barrier();
+        multiply(lds, ws[whole]);
+        stage_barrier();
+    }
+    for (int64_t s = s0; s < s0 + STAGES - 1 && s < s1; ++s)
+        stage(s);
+    for (int64_t s = s0; s < s1; ++s) {
+        const float sw = ws[at(s)];
+        // stage s has landed when only the later ones are outstanding
+        if (s + STAGES - 1 <= s1)
+            wait_loads<(STAGES - 2) * LOADS>();
+        else
+            wait_loads<0>();
+        // every wavefront's has, and all have read the stage before
+        bare_barrier();
+        if (s + STAGES - 1 < s1)
+            stage(s + STAGES - 1);
+        multiply(lds + (s - s0) % STAGES * BYTES, sw);
+    }
+    // the tile through LDS, 4 results of a row a thread
+    constexpr int LD = BN + 4;
+    static_assert(BM * LD * 4 <= STAGES * BYTES, "the results fit");
+    float* c = (float*)lds;
+    stage_barrier();
+#pragma unroll
+    for (int i = 0; i < IM; ++i)
+        *(f32x4*)(c + (i * 16 + (lane & 15)) * LD + wave * 16 + (lane >> 4) * 4) = acc[i];
+    __syncthreads();
+    constexpr int ACROSS = BN / 4;                  // threads of a row
+    const int64_t n = n0 + threadIdx.x % ACROSS * 4;
+    for (int m = threadIdx.x / ACROSS; m < BM && m < t.m; m += NT / ACROSS) {
+        const f32x4 v = *(const f32x4*)(c + m * LD + threadIdx.x % ACROSS * 4);
+        float* p = part ? part + ((int64_t)blockIdx.y * t.m + m) * t.n + n : nullptr;
+        if (n + 4 <= t.n) {
+            if (part)
+                keep4(p, v);
+            else
+                store_results<uint16_t>(t, m, n, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < t.n) {
+                    if (part)
+                        p[e] = v[e];
+                    else
+                        store_result<uint16_t>(t, m, n + e, v[e]);
+                }
+        }
+    }
+}
+
+// At most 16 rows of x and too few columns for the ring: a workgroup of WAVES
+// wavefronts takes 16 rows of W, whose k they split and whose sums they join in
+// LDS, in order; W goes straight from memory to the wavefronts' registers, D
+// blocks at a time (as in the 16-bit products).
+template <int D, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void fp8_rows_kernel(Fp8Task f) {
+    __shared__ f32x4 sums[WAVES][64];
+    const GemmTask& t = f.g;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int r = lane & 15, q = lane >> 4;
+    // rows past the end repeat the last one: their sums are not stored
+    const int64_t xr = r < t.m ? r : t.m - 1;
+    const char* w = (const char*)t.b + (n0 + r < t.n ? n0 + r : t.n - 1) * t.b_n;
+    const char* x = (const char*)t.a + xr * t.a_m;
+    const float* xs = f.a_scale + xr * f.lda_scale;
+    const scalar_floats ws = weight_scales(f, n0);
+    f32x4 acc = {};
+    auto add = [&](const u32x4_t (&wv)[2], const u32x4_t (&xv)[2], float sc) {
+        const f32x4 d = mma_exact(wv, xv);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[e] = __builtin_fmaf(d[e], sc, acc[e]);
+    };
+    // COUNT whole blocks from s
+    auto run = [&](int64_t s, auto count) {
+        constexpr int COUNT = count();
+        u32x4_t wv[COUNT][2], xv[COUNT][2];
+        float sx[COUNT];
+#pragma unroll
+        for (int d = 0; d < COUNT; ++d) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t o = (s + d) * 128 + h * 64 + q * 16;
+                wv[d][h] = __builtin_nontemporal_load((const u32x4_t*)(w + o));
+                xv[d][h] = *(const u32x4_t*)(x + o);
+            }
+            sx[d] = xs[s + d];
+        }
+        __builtin_amdgcn_sched_barrier(0);          // all loads before the first wait
+#pragma unroll
+        for (int d = 0; d < COUNT; ++d)
+            add(wv[d], xv[d], sx[d] * ws[s + d]);
+    };
+    const int64_t whole = t.k / 128, batches = whole / D;
+    for (int64_t b = wave; b < batches; b += WAVES)
+        run(b * D, std::integral_constant<int, D>{});
+    for (int64_t s = batches * D + wave; s < whole; s += WAVES)
+        run(s, std::integral_constant<int, 1>{});
+    if (t.k > whole * 128 && wave == WAVES - 1) {
+        u32x4_t wv[2], xv[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t k = whole * 128 + h * 64 + q * 16;
+            wv[h] = first_bytes(w + k, t.k - k);
+            xv[h] = first_bytes(x + k, t.k - k);
+        }
+        add(wv, xv, xs[whole] * ws[whole]);
+    }
+    sums[wave][lane] = acc;
+    __syncthreads();
+    // n fastest; in a block n is (lane / 16) * 4 + e and m is lane % 16
+    const int m = threadIdx.x / 16, n = threadIdx.x % 16;
+    if (m >= t.m || m >= 16 || n0 + n >= t.n)
+        return;
+    const int place = m + (n >> 2) * 16;
+    float v = sums[0][place][n & 3];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i)
+        v += sums[i][place][n & 3];
+    store_result<uint16_t>(t, m, n0 + n, v);
+}
+
+// The plan of a 16-bit product whose rows have as many bytes: stages, tiles and
+// what they cost are alike.  Exact products have 128-tiles alone.
+int64_t as_16_bits(int64_t k) {
+    return (k + 1) / 2;
+}
+GemmPlan plan_fp8(int64_t m, int64_t n, int64_t k, bool exact) {
+    GemmPlan p = plan_gemm(2, m, n, as_16_bits(k), true, true);
+    if (exact && !p.rows_kernel && p.tile == 256) {
+        p = GemmPlan{};
+        p.tile = 128;
+        p.slices = 1;
+        p.stages_per_slice = (k + 127) / 128;
+    }
+    return p;
+}
+size_t slices_bytes(const GemmPlan& p, int64_t m, int64_t n) {
+    return p.slices > 1 ? (size_t)p.slices * (size_t)m * (size_t)n * 4 : 0;
+}
+
+template <bool EXACT, int TILE, int WM, int WN>
+hipError_t launch_tile(const Fp8Task& f, const GemmPlan& p, hipStream_t stream) {
+    const uint32_t tm = (uint32_t)((f.g.m + TILE - 1) / TILE);
+    const uint32_t tn = (uint32_t)((f.g.n + TILE - 1) / TILE);
+    return launch(fp8_tile_kernel<EXACT, TILE, TILE, WM, WN>, dim3(tm * tn * (uint32_t)p.slices),
+                  dim3(WM * WN * 64), 0, stream, f, tm, tn, p.stages_per_slice,
+                  p.slices > 1 ? (float*)f.g.ws : nullptr);
+}
+
+hipError_t launch_planned(const Fp8Task& f, const GemmPlan& p, hipStream_t stream) {
+    hipError_t e;
+    if (p.tile <= 64) {
+        const dim3 grid((uint32_t)((f.g.n + kFewRowsCols - 1) / kFewRowsCols), (uint32_t)p.slices);
+        float* part = p.slices > 1 ? (float*)f.g.ws : nullptr;
+        e = p.tile == 32 ? launch(fp8_few_rows_kernel<32, 6>, grid, dim3(256), 0, stream, f,
+                                  p.stages_per_slice, part)
+                         : launch(fp8_few_rows_kernel<64, 4>, grid, dim3(256), 0, stream, f,
+                                  p.stages_per_slice, part);
+    } else if (f.exact) {
+        e = launch_tile<true, 128, 2, 2>(f, p, stream);
+    } else {
+        e = p.tile == 256 ? launch_tile<false, 256, 2, 4>(f, p, stream)
+                          : launch_tile<false, 128, 2, 2>(f, p, stream);
+    }
+    return e != hipSuccess || p.slices == 1 ? e : launch_gemm_join(2, f.g, p.slices, stream);
 }
 
 }  // namespace
 
-size_t fp8_workspace(int64_t, int64_t, int64_t) {
-    return 0;
+size_t fp8_workspace(int64_t m, int64_t n, int64_t k, bool exact) {
+    const GemmPlan p = plan_fp8(m, n, k, exact);
+    if (!p.first_m)
+        return slices_bytes(p, m, n);
+    const GemmPlan q = plan_rest(2, p, m, n, as_16_bits(k));
+    const size_t first = slices_bytes(p, p.first_m, p.first_n), rest = slices_bytes(q, m, n);
+    return first > rest ? first : rest;
 }
 
-int64_t fp8_threads(int64_t m, int64_t n, int64_t) {
-    return (m + 15) / 16 * ((n + 15) / 16) * 64;
+// The 16-bit plan's launches, in smaller tiles at most.
+int64_t fp8_threads(int64_t m, int64_t n, int64_t k, bool exact) {
+    const int64_t planned = gemm_threads(2, m, n, as_16_bits(k), true, true);
+    const int64_t tiles = (m + 127) / 128 * ((n + 127) / 128) * 256;
+    return exact && m > 64 && tiles > planned ? tiles : planned;
 }
 
-hipError_t launch_fp8(const Fp8Task& t, hipStream_t stream) {
-    const int64_t tm = (t.g.m + 15) / 16, tn = (t.g.n + 15) / 16;
-    return launch(fp8_simple_kernel, dim3((uint32_t)(tm * tn)), dim3(64), 0, stream, t,
-                  (uint32_t)tm);
+hipError_t launch_fp8(const Fp8Task& f, hipStream_t stream) {
+    const GemmTask& t = f.g;
+    const GemmPlan p = plan_fp8(t.m, t.n, t.k, f.exact);
+    if (p.rows_kernel) {
+        const int waves = linear_rows_waves(t.n);
+        const dim3 grid((uint32_t)((t.n + 15) / 16)), block((uint32_t)waves * 64);
+        return waves == 8 ? launch(fp8_rows_kernel<8, 8>, grid, block, 0, stream, f)
+                          : launch(fp8_rows_kernel<8, 4>, grid, block, 0, stream, f);
+    }
+    if (!p.first_m)
+        return launch_planned(f, p, stream);
+    Fp8Task a = f, r = f;                           // the first part and the rest
+    auto past = [](const void* q, int64_t bytes) { return q ? (char*)q + bytes : nullptr; };
+    a.g.m = p.first_m;
+    a.g.n = p.first_n;
+    const int64_t dm = a.g.m < t.m ? a.g.m : 0, dn = a.g.n < t.n ? a.g.n : 0;
+    r.g.m -= dm;
+    r.g.n -= dn;
+    r.g.a = past(t.a, dm * t.a_m);
+    r.g.b = past(t.b, dn * t.b_n);
+    r.g.bias = past(t.bias, dn * 2);
+    r.g.residual = past(t.residual, (dm * t.ldr + dn) * 2);
+    r.g.y = past(t.y, (dm * t.ldy + dn) * (t.out_f32 ? 4 : 2));
+    r.a_scale += dm * f.lda_scale;
+    r.b_scale += dn / kScaleBlock * f.ldb_scale;    // (dn is a multiple of 256)
+    int64_t m = t.m, n = t.n;
+    const GemmPlan q = plan_rest(2, p, m, n, as_16_bits(t.k));
+    const hipError_t e = launch_planned(a, p, stream);
+    return e != hipSuccess ? e : launch_planned(r, q, stream);
 }
 
 }  // namespace vpa

@@ -98,17 +98,21 @@ __global__ __launch_bounds__(WAVES * 64) void linear_rows_kernel(GemmTask t) {
     store_result<T>(t, m, n0 + n, v);
 }
 
+}  // namespace
+
 // 8 wavefronts a workgroup while each has a CU to itself, which its registers
 // allow, else 4 (K = 4096, one row: n = 4800 14.6 us with 8, 14.4 with 4; 4112
 // of K = 1600 8.9 and 7.6; 4096 of K = 4096 9.3 with 8).
-int rows_waves(int64_t n) {
+int linear_rows_waves(int64_t n) {
     return n <= 16 * 256 ? 8 : 4;
 }
+
+namespace {
 
 template <int ESIZE>
 hipError_t launch_rows(const GemmTask& t, hipStream_t stream) {
     constexpr int D = 8;
-    const int waves = rows_waves(t.n);
+    const int waves = linear_rows_waves(t.n);
     const dim3 grid((uint32_t)((t.n + 15) / 16)), block((uint32_t)waves * 64);
     return waves == 8 ? launch(linear_rows_kernel<ESIZE, D, 8>, grid, block, 0, stream, t)
                       : launch(linear_rows_kernel<ESIZE, D, 4>, grid, block, 0, stream, t);
@@ -117,7 +121,7 @@ hipError_t launch_rows(const GemmTask& t, hipStream_t stream) {
 }  // namespace
 
 int64_t linear_rows_threads(int64_t n) {
-    return (n + 15) / 16 * rows_waves(n) * 64;
+    return (n + 15) / 16 * linear_rows_waves(n) * 64;
 }
 
 hipError_t launch_linear_rows(int esize, const GemmTask& t, hipStream_t stream) {

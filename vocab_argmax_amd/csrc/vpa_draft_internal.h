@@ -135,9 +135,10 @@ struct Fp8Task {
     int64_t lda_scale;
     const float* b_scale;
     int64_t ldb_scale;
+    bool exact;                        // products in full fp32
 };
-size_t fp8_workspace(int64_t m, int64_t n, int64_t k);
-int64_t fp8_threads(int64_t m, int64_t n, int64_t k);
+size_t fp8_workspace(int64_t m, int64_t n, int64_t k, bool exact);
+int64_t fp8_threads(int64_t m, int64_t n, int64_t k, bool exact);
 hipError_t launch_fp8(const Fp8Task& t, hipStream_t stream);
 
 }  // namespace vpa

@@ -119,16 +119,20 @@ struct GemmPlan {
     bool direct;              // operands' strides allow direct loads to LDS
 };
 GemmPlan plan_gemm(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
+GemmPlan plan_rest(int esize, const GemmPlan& first, int64_t& m, int64_t& n, int64_t k);
 size_t gemm_workspace(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
 // Most work-items of one of the product's dispatches.
 int64_t gemm_threads(int esize, int64_t m, int64_t n, int64_t k, bool a_k1, bool b_k1);
 hipError_t launch_gemm(int esize, const GemmTask& t, hipStream_t stream);
+// The slices of a split product (in t.ws), added in order, and its epilogue.
+hipError_t launch_gemm_join(int esize, const GemmTask& t, int32_t slices, hipStream_t stream);
 
 hipError_t launch_gemm_tiles_bf16(const GemmTask& t, const GemmPlan& p, hipStream_t stream);
 hipError_t launch_gemm_tiles_f32(const GemmTask& t, const GemmPlan& p, hipStream_t stream);
 
 // The product for few rows of A (linear_rows.hip), k contiguous in both.
 constexpr int kRowsKernelMost = 16;
+int linear_rows_waves(int64_t n);
 int64_t linear_rows_threads(int64_t n);
 hipError_t launch_linear_rows(int esize, const GemmTask& t, hipStream_t stream);
 

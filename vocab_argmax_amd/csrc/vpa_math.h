@@ -21,6 +21,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 template <int ESIZE>
 struct elem;
 template <>
+struct elem<1> {
+    using type = uint8_t;             // e4m3 patterns
+};
+template <>
 struct elem<2> {
     using type = uint16_t;
 };
