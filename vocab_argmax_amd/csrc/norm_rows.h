@@ -69,9 +69,8 @@ struct RowPart {
             v[i] = u.v;
         }
     }
-    static __device__ __forceinline__ void store(T* row, int cols, int i,
-                                                 const float (&f)[VEC]) {
-        const int n = count(i, cols);
+    // rounded to T
+    static __device__ __forceinline__ u32x4_t pack(const float (&f)[VEC]) {
         u32x4_t v;
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -82,15 +81,28 @@ struct RowPart {
             for (int e = 0; e < 4; ++e)
                 v[e] = __builtin_bit_cast(uint32_t, f[e]);
         }
+        return v;
+    }
+    static __device__ __forceinline__ void store_packed(T* row, int cols, int i, u32x4_t v) {
+        const int n = count(i, cols);
         if (n == VEC) {
             // past the L2 (32768 x 4096 forward 105 -> 87 us; loads past it are slower)
             __builtin_nontemporal_store(v, &((Loose16*)(row + column(i)))->v);
         } else {
+            union {
+                T e[VEC];
+                u32x4_t v;
+            } u;
+            u.v = v;
 #pragma unroll
             for (int e = 0; e < VEC - 1; ++e)
                 if (e < n)
-                    from_f32(row[column(i) + e], f[e]);
+                    row[column(i) + e] = u.e[e];
         }
+    }
+    static __device__ __forceinline__ void store(T* row, int cols, int i,
+                                                 const float (&f)[VEC]) {
+        store_packed(row, cols, i, pack(f));
     }
     // weights or biases: `none` where there are none
     template <typename W>

@@ -37,7 +37,238 @@ __device__ __forceinline__ uint32_t pack_fp8(float a, float b) {
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xFFFFu;
 }
 
-// A row to a workgroup, several passes over it.
+// Sum over a workgroup of WAVES wavefronts through `lds`; every thread holds it.
+// Callers leave a barrier between two uses of an lds.
+template <int WAVES>
+__device__ __forceinline__ float block_sum(float a, float (&lds)[WAVES]) {
+    a = wave_sum(a);
+    if constexpr (WAVES > 1) {
+        if ((threadIdx.x & 63) == 0)
+            lds[threadIdx.x >> 6] = a;
+        __syncthreads();
+        a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i)
+            a += lds[i];
+    }
+    return a;
+}
+
+// The largest over aligned groups of LANES (16 or 32) lanes.
+template <int LANES>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    const auto step = [&](uint32_t o) { v = o > v ? o : v; };
+    step(dpp_move<dpp::kSwap1, 0xF>(v));
+    step(dpp_move<dpp::kSwap2, 0xF>(v));
+    step(dpp_move<dpp::kHalfMirror, 0xF>(v));
+    step(dpp_move<dpp::kMirror, 0xF>(v));
+    if constexpr (LANES == 32)
+        step(__shfl_xor(v, 16, 64));
+    return v;
+}
+
+// N bytes at any address.
+template <int N>
+struct __attribute__((packed, aligned(1))) LooseBytes {
+    uint32_t w[N / 4];
+};
+
+// A row in registers: x and the residual of the next one on their way, the weights
+// kept over a workgroup's rows.  With FP8, the 128 columns of a scale lie in 16
+// (bf16) or 32 (fp32) lanes side by side.
+template <typename T, typename W, int WAVES, int NV, bool FP8>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_kernel(RmsTask t) {
+    using P = RowPart<T, WAVES, NV>;
+    constexpr int VEC = P::VEC, ESIZE = (int)sizeof(T), LANES = kScaleBlock / VEC;
+    __shared__ float lds[2][WAVES];
+    const int cols = (int)t.cols;
+    const bool res = t.residual != nullptr;
+    float w[NV][VEC];
+    P::load_weights((const W*)t.weight, cols, 1.0f, w);
+    u32x4_t next[NV], next_r[NV];
+    int64_t row = P::first_row();
+    const auto fetch = [&](int64_t r) {
+        P::load((const T*)t.x + r * t.ldx, cols, next);
+        if (res)
+            P::load((const T*)t.residual + r * t.ldr, cols, next_r);
+    };
+    if (row < t.rows)
+        fetch(row);
+    for (int turn = 0; row < t.rows; row += P::row_step(), turn ^= 1) {
+        u32x4_t v[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            v[i] = next[i];
+        if (res) {
+            T* s = (T*)t.summed + row * t.lds;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float f[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    f[e] = vec_elem<ESIZE>(v[i], e) + vec_elem<ESIZE>(next_r[i], e);
+                v[i] = P::pack(f);
+                P::store_packed(s, cols, i, v[i]);
+            }
+        }
+        const int64_t after = row + P::row_step();
+        // (outputs may take the inputs' places: the next row is another)
+        if (after < t.rows)
+            fetch(after);
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float f = vec_elem<ESIZE>(v[i], e);           // 0 past the row
+                q = __builtin_fmaf(f, f, q);
+            }
+        q = block_sum<WAVES>(q, lds[turn]);
+        const float rstd = 1.0f / sqrtf(q / (float)cols + t.eps);
+        if (t.rstd && P::column(0) == 0)
+            t.rstd[row] = rstd;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                f[e] = vec_elem<ESIZE>(v[i], e) * rstd * w[i][e];
+            if constexpr (!FP8) {
+                P::store((T*)t.y + row * t.ldy, cols, i, f);
+            } else {
+                const int n = P::count(i, cols);
+                uint32_t amax = 0;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const uint32_t b = e < n ? abs_bits(f[e]) : 0;
+                    amax = b > amax ? b : amax;
+                }
+                const BlockScale sc = block_scale(group_max<LANES>(amax));
+                LooseBytes<VEC> o;
+#pragma unroll
+                for (int e = 0; e < VEC; e += 4)
+                    o.w[e / 4] = pack_fp8(f[e] * sc.inverse, f[e + 1] * sc.inverse) |
+                                 pack_fp8(f[e + 2] * sc.inverse, f[e + 3] * sc.inverse) << 16;
+                uint8_t* y = (uint8_t*)t.y + row * t.ldy + P::column(i);
+                if (n == VEC) {
+                    *(LooseBytes<VEC>*)y = o;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC - 1; ++e)
+                        if (e < n)
+                            y[e] = (uint8_t)(o.w[e / 4] >> (e % 4 * 8));
+                }
+                if (n > 0 && P::column(i) % kScaleBlock == 0)
+                    t.scale[row * t.ld_scale + P::column(i) / kScaleBlock] = sc.scale;
+            }
+        }
+    }
+}
+
+// The gradients of a workgroup's rows from one read of grad, s and grad_summed,
+// the weight's in registers until the end (a thread always has the same columns).
+template <typename T, typename W, int WAVES, int NV>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_grad_kernel(RmsGradTask t) {
+    using P = RowPart<T, WAVES, NV>;
+    constexpr int VEC = P::VEC, ESIZE = (int)sizeof(T);
+    __shared__ float lds[2][WAVES];
+    const int cols = (int)t.cols;
+    const bool along = t.grad_summed != nullptr && t.dx != nullptr;
+    float w[NV][VEC], dw[NV][VEC] = {};
+    P::load_weights((const W*)t.weight, cols, 1.0f, w);
+    u32x4_t next_g[NV], next_x[NV], next_s[NV];
+    float next_rstd = 0.0f;
+    const auto fetch = [&](int64_t r) {
+        P::load((const T*)t.grad + r * t.ldg, cols, next_g);
+        P::load((const T*)t.summed + r * t.lds, cols, next_x);
+        if (along)
+            P::load((const T*)t.grad_summed + r * t.ldgs, cols, next_s);
+        next_rstd = t.rstd[r];
+    };
+    int64_t row = P::first_row();
+    if (row < t.rows)
+        fetch(row);
+    for (int turn = 0; row < t.rows; row += P::row_step(), turn ^= 1) {
+        u32x4_t g[NV], x[NV], gs[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            g[i] = next_g[i];
+            x[i] = next_x[i];
+            gs[i] = next_s[i];
+        }
+        const float rstd = next_rstd;
+        const int64_t after = row + P::row_step();
+        // (grad_x may take grad's or grad_summed's place: the next row is another)
+        if (after < t.rows)
+            fetch(after);
+        float b = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float gr = vec_elem<ESIZE>(g[i], e);          // 0 past the row
+                const float xh = vec_elem<ESIZE>(x[i], e) * rstd;
+                b = __builtin_fmaf(gr * w[i][e], xh, b);
+                dw[i][e] = __builtin_fmaf(gr, xh, dw[i][e]);
+            }
+        if (!t.dx)
+            continue;
+        b = block_sum<WAVES>(b, lds[turn]) / (float)cols;
+        T* dx = (T*)t.dx + row * t.lddx;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float xh = vec_elem<ESIZE>(x[i], e) * rstd;
+                f[e] = rstd * (vec_elem<ESIZE>(g[i], e) * w[i][e] - xh * b);
+                if (along)
+                    f[e] += vec_elem<ESIZE>(gs[i], e);
+            }
+            P::store(dx, cols, i, f);
+        }
+    }
+    if (!t.part)
+        return;
+    if constexpr (P::ROWS > 1) {
+        // the workgroup's rows' sums, added in order
+        static_assert(NV == 1, "a wavefront a row");
+        __shared__ float sums[P::ROWS][64 * VEC];
+        const int group = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            sums[group][lane * VEC + e] = dw[0][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < 64 * VEC && c < cols; c += P::THREADS) {
+            float s = 0.0f;
+#pragma unroll
+            for (int r = 0; r < P::ROWS; ++r)
+                s += sums[r][c];
+            t.part[(int64_t)blockIdx.x * cols + c] = s;
+        }
+        return;
+    }
+    float* pw = t.part + (int64_t)blockIdx.x * cols;
+    typedef float f32x4_loose __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+            const int c = P::column(i) + e;
+            if (c + 4 <= cols) {
+                *(f32x4_loose*)(pw + c) = f32x4_loose{dw[i][e], dw[i][e + 1], dw[i][e + 2],
+                                                      dw[i][e + 3]};
+                continue;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c + k < cols)
+                    pw[c + k] = dw[i][e + k];
+        }
+}
+
+// Rows too long for a workgroup's registers: several passes over the row, which the
+// caches hold.
 template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void rms_long_kernel(RmsTask t) {
     __shared__ float lds[kLongWaves][2];
@@ -197,24 +428,40 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(QuantTask t, int64_t bl
 
 template <typename T, typename W>
 hipError_t launch_rms_typed(const RmsTask& t, hipStream_t stream) {
-    return launch(rms_long_kernel<T, W>, dim3((uint32_t)t.rows), dim3(kLongThreads), 0, stream, t);
+    const NormForm form = norm_form((int)sizeof(T), t.cols, false);
+    const dim3 grid((uint32_t)norm_blocks(form, t.rows));
+    if (form.waves == 0)
+        return launch(rms_long_kernel<T, W>, grid, dim3(kLongThreads), 0, stream, t);
+    return with_form<(int)sizeof(T), false>(form, [&](auto waves, auto nv) {
+        const dim3 block(RowPart<T, waves(), nv()>::THREADS);
+        return t.scale ? launch(rms_kernel<T, W, waves(), nv(), true>, grid, block, 0, stream, t)
+                       : launch(rms_kernel<T, W, waves(), nv(), false>, grid, block, 0, stream, t);
+    });
 }
 
 template <typename T, typename W>
-hipError_t launch_rms_grad_typed(const RmsGradTask& t, hipStream_t stream) {
+hipError_t launch_rms_grad_typed(const RmsGradTask& task, hipStream_t stream) {
+    RmsGradTask t = task;
+    t.part = t.dweight && t.rows > 0 ? t.part : nullptr;
     // no rows: no sums, and the joining kernel writes 0
     const int32_t splits = t.rows > 0 ? rms_splits((int)sizeof(T), t.rows, t.cols) : 0;
+    const NormForm form = norm_form((int)sizeof(T), t.cols, true);
     hipError_t e = hipSuccess;
-    if (t.dx)
-        e = launch(rms_long_dx_kernel<T, W>, dim3((uint32_t)t.rows), dim3(kLongThreads), 0, stream,
-                   t);
+    if (t.rows > 0 && form.waves != 0) {
+        e = with_form<(int)sizeof(T), true>(form, [&](auto waves, auto nv) {
+            return launch(rms_grad_kernel<T, W, waves(), nv()>, dim3((uint32_t)splits),
+                          dim3(RowPart<T, waves(), nv()>::THREADS), 0, stream, t);
+        });
+    } else if (t.rows > 0) {
+        if (t.dx)
+            e = launch(rms_long_dx_kernel<T, W>, dim3((uint32_t)t.rows), dim3(kLongThreads), 0,
+                       stream, t);
+        if (e == hipSuccess && t.dweight)
+            e = launch(rms_long_columns_kernel<T>,
+                       dim3((uint32_t)((t.cols + kThreads - 1) / kThreads), (uint32_t)splits),
+                       dim3(kThreads), 0, stream, t, splits);
+    }
     if (e != hipSuccess || !t.dweight)
-        return e;
-    if (splits > 0)
-        e = launch(rms_long_columns_kernel<T>,
-                   dim3((uint32_t)((t.cols + kThreads - 1) / kThreads), (uint32_t)splits),
-                   dim3(kThreads), 0, stream, t, splits);
-    if (e != hipSuccess)
         return e;
     return launch(rms_join_kernel<W>, dim3((uint32_t)((t.cols + 63) / 64)), dim3(kJoinWaves * 64), 0,
                   stream, t, splits);
@@ -222,8 +469,9 @@ hipError_t launch_rms_grad_typed(const RmsGradTask& t, hipStream_t stream) {
 
 }  // namespace
 
-int64_t rms_threads(int, int64_t rows, int64_t) {
-    return rows * kLongThreads;
+int64_t rms_threads(int esize, int64_t rows, int64_t cols) {
+    const NormForm form = norm_form(esize, cols, false);
+    return norm_blocks(form, rows) * (form.waves == 0 ? kLongThreads : form.threads());
 }
 
 hipError_t launch_rms(int esize, const RmsTask& t, hipStream_t stream) {
@@ -233,16 +481,23 @@ hipError_t launch_rms(int esize, const RmsTask& t, hipStream_t stream) {
                         : launch_rms_typed<uint16_t, uint16_t>(t, stream);
 }
 
-int32_t rms_splits(int, int64_t rows, int64_t) {
-    const int64_t s = (rows + 63) / 64;
-    return (int32_t)(s < 1 ? 1 : s > 64 ? 64 : s);
+// Workgroups of the backward pass, each of which leaves a row of sums: 2 a CU, for
+// long rows slices of 64 rows.
+int32_t rms_splits(int esize, int64_t rows, int64_t cols) {
+    const NormForm form = norm_form(esize, cols, true);
+    int64_t s = form.waves == 0 ? (rows + 63) / 64 : form.waves == 1 ? (rows + 3) / 4 : rows;
+    const int64_t most = form.waves == 0 ? 64 : 512;
+    s = s > most ? most : s;
+    return (int32_t)(s < 1 ? 1 : s);
 }
 
 int64_t rms_grad_threads(int esize, int64_t rows, int64_t cols, bool dx, bool sums) {
-    int64_t most = dx ? rows * kLongThreads : 0;
+    const NormForm form = norm_form(esize, cols, true);
+    const int64_t splits = rms_splits(esize, rows, cols);
+    int64_t most = form.waves != 0 ? splits * form.threads() : dx ? rows * kLongThreads : 0;
     if (sums) {
-        const int64_t columns = (cols + kThreads - 1) / kThreads * kThreads *
-                                rms_splits(esize, rows, cols);
+        const int64_t columns =
+            form.waves == 0 ? (cols + kThreads - 1) / kThreads * kThreads * splits : 0;
         const int64_t join = (cols + 63) / 64 * 64 * kJoinWaves;
         most = columns > most ? columns : most;
         most = join > most ? join : most;
