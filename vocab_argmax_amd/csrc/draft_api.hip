@@ -410,7 +410,7 @@ vpa_status vpa_quantize_fp8(const void* x, int64_t ldx, vpa_dtype dtype, int64_t
         (st = check_matrix("y", y, 1, ldy, cols)) != VPA_OK ||
         (st = check_matrix("scale", scale, 4, ld_scale,
                            (cols + kScaleBlock - 1) / kScaleBlock)) != VPA_OK ||
-        (st = check_dispatch(quant_threads(rows, cols, block_rows), call)) != VPA_OK)
+        (st = check_dispatch(quant_threads(esize_of(dt), rows, cols, block_rows), call)) != VPA_OK)
         return st;
     const QuantTask t = {x, ldx, rows, cols, block_rows, y, ldy, scale, ld_scale};
     const hipError_t e = launch_quant(esize_of(dt), t, (hipStream_t)stream);

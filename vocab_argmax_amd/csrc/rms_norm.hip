@@ -393,37 +393,84 @@ __global__ __launch_bounds__(kJoinWaves * 64) void rms_join_kernel(RmsGradTask t
     from_f32(((W*)t.dweight)[c], s);
 }
 
-// A workgroup a block of block_rows x 128.
-template <typename T>
+// A matrix as it is in 8 bits.  LANES lanes side by side hold 128 columns of a row,
+// 16 bytes each; a workgroup takes kThreads / LANES rows of one block of columns at
+// a time, or with SQUARE the 128 rows that share a scale, in registers.
+template <typename T, bool SQUARE>
 __global__ __launch_bounds__(kThreads) void quant_kernel(QuantTask t, int64_t blocks_across) {
-    __shared__ uint32_t lds[4];
-    const int64_t br = blockIdx.x / blocks_across, bc = blockIdx.x % blocks_across;
-    const int64_t r0 = br * t.block_rows, c = bc * kScaleBlock + threadIdx.x % kScaleBlock;
-    const int64_t r1 = r0 + t.block_rows < t.rows ? r0 + t.block_rows : t.rows;
-    const int64_t first = r0 + threadIdx.x / kScaleBlock;
+    constexpr int VEC = 16 / (int)sizeof(T), LANES = kScaleBlock / VEC;
+    constexpr int ROWS = kThreads / LANES, NV = SQUARE ? kScaleBlock / ROWS : 1;
+    __shared__ uint32_t lds[kThreads / 64];
+    const int64_t down = blockIdx.x / blocks_across, across = blockIdx.x % blocks_across;
+    const int64_t r0 = down * (SQUARE ? kScaleBlock : ROWS) + threadIdx.x / LANES;
+    const int64_t c = across * kScaleBlock + threadIdx.x % LANES * VEC;
+    const int n = t.cols - c < VEC ? (int)(t.cols - c) : VEC;   // columns of this lane, or < 1
+    u32x4_t v[NV];
     uint32_t amax = 0;
-    if (c < t.cols)
-        for (int64_t r = first; r < r1; r += kThreads / kScaleBlock) {
-            const uint32_t b = abs_bits(to_f32(((const T*)t.x)[r * t.ldx + c]));
-            amax = b > amax ? b : amax;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t r = r0 + i * ROWS;
+        const T* x = (const T*)t.x + r * t.ldx + c;
+        v[i] = u32x4_t{0, 0, 0, 0};
+        if (r < t.rows && n == VEC) {
+            v[i] = ((const Loose16*)x)->v;
+        } else if (r < t.rows) {
+            union {
+                T e[VEC];
+                u32x4_t v;
+            } u;
+            u.v = v[i];
+#pragma unroll
+            for (int e = 0; e < VEC - 1; ++e)
+                if (e < n)
+                    u.e[e] = x[e];
+            v[i] = u.v;
         }
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-        const uint32_t o = __shfl_xor(amax, off, 64);
-        amax = o > amax ? o : amax;
+        for (int e = 0; e < VEC; ++e) {
+            const uint32_t b = abs_bits(vec_elem<(int)sizeof(T)>(v[i], e));
+            amax = b > amax ? b : amax;
+        }
     }
-    if ((threadIdx.x & 63) == 0)
-        lds[threadIdx.x >> 6] = amax;
-    __syncthreads();
-    for (int i = 0; i < 4; ++i)
-        amax = lds[i] > amax ? lds[i] : amax;
+    amax = group_max<LANES>(amax);
+    if constexpr (SQUARE) {
+#pragma unroll
+        for (int off = LANES; off < 64; off <<= 1) {
+            const uint32_t o = __shfl_xor(amax, off, 64);
+            amax = o > amax ? o : amax;
+        }
+        if ((threadIdx.x & 63) == 0)
+            lds[threadIdx.x >> 6] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kThreads / 64; ++i)
+            amax = lds[i] > amax ? lds[i] : amax;
+    }
     const BlockScale sc = block_scale(amax);
-    if (c < t.cols)
-        for (int64_t r = first; r < r1; r += kThreads / kScaleBlock)
-            ((uint8_t*)t.y)[r * t.ldy + c] =
-                (uint8_t)pack_fp8(to_f32(((const T*)t.x)[r * t.ldx + c]) * sc.inverse, 0.0f);
-    if (threadIdx.x == 0)
-        t.scale[br * t.ld_scale + bc] = sc.scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t r = r0 + i * ROWS;
+        if (r >= t.rows)
+            continue;
+        LooseBytes<VEC> o;
+        const auto f = [&](int e) { return vec_elem<(int)sizeof(T)>(v[i], e) * sc.inverse; };
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4)
+            o.w[e / 4] = pack_fp8(f(e), f(e + 1)) | pack_fp8(f(e + 2), f(e + 3)) << 16;
+        uint8_t* y = (uint8_t*)t.y + r * t.ldy + c;
+        if (n == VEC) {
+            *(LooseBytes<VEC>*)y = o;
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC - 1; ++e)
+                if (e < n)
+                    y[e] = (uint8_t)(o.w[e / 4] >> (e % 4 * 8));
+        }
+        if (!SQUARE && threadIdx.x % LANES == 0)
+            t.scale[r * t.ld_scale + across] = sc.scale;
+    }
+    if (SQUARE && threadIdx.x == 0)
+        t.scale[down * t.ld_scale + across] = sc.scale;
 }
 
 template <typename T, typename W>
@@ -512,16 +559,31 @@ hipError_t launch_rms_grad(int esize, const RmsGradTask& t, hipStream_t stream) 
                         : launch_rms_grad_typed<uint16_t, uint16_t>(t, stream);
 }
 
-int64_t quant_threads(int64_t rows, int64_t cols, int32_t block_rows) {
-    return (rows + block_rows - 1) / block_rows * ((cols + kScaleBlock - 1) / kScaleBlock) *
-           kThreads;
+namespace {
+
+// Workgroups down the rows.
+int64_t quant_down(int esize, int64_t rows, int32_t block_rows) {
+    const int64_t per = block_rows == 1 ? kThreads / (kScaleBlock * esize / 16) : block_rows;
+    return (rows + per - 1) / per;
+}
+
+template <typename T>
+hipError_t launch_quant_typed(const QuantTask& t, hipStream_t stream) {
+    const int64_t across = (t.cols + kScaleBlock - 1) / kScaleBlock;
+    const dim3 grid((uint32_t)(quant_down((int)sizeof(T), t.rows, t.block_rows) * across));
+    return t.block_rows == 1
+               ? launch(quant_kernel<T, false>, grid, dim3(kThreads), 0, stream, t, across)
+               : launch(quant_kernel<T, true>, grid, dim3(kThreads), 0, stream, t, across);
+}
+
+}  // namespace
+
+int64_t quant_threads(int esize, int64_t rows, int64_t cols, int32_t block_rows) {
+    return quant_down(esize, rows, block_rows) * ((cols + kScaleBlock - 1) / kScaleBlock) * kThreads;
 }
 
 hipError_t launch_quant(int esize, const QuantTask& t, hipStream_t stream) {
-    const int64_t across = (t.cols + kScaleBlock - 1) / kScaleBlock;
-    const dim3 grid((uint32_t)((t.rows + t.block_rows - 1) / t.block_rows * across));
-    return esize == 2 ? launch(quant_kernel<uint16_t>, grid, dim3(kThreads), 0, stream, t, across)
-                      : launch(quant_kernel<float>, grid, dim3(kThreads), 0, stream, t, across);
+    return esize == 2 ? launch_quant_typed<uint16_t>(t, stream) : launch_quant_typed<float>(t, stream);
 }
 
 }  // namespace vpa

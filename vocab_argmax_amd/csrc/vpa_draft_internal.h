@@ -122,7 +122,7 @@ struct QuantTask {
     float* scale;
     int64_t ld_scale;
 };
-int64_t quant_threads(int64_t rows, int64_t cols, int32_t block_rows);
+int64_t quant_threads(int esize, int64_t rows, int64_t cols, int32_t block_rows);
 hipError_t launch_quant(int esize, const QuantTask& t, hipStream_t stream);
 
 // ---- products of 8-bit operands (linear_fp8.hip) ----
