@@ -45,11 +45,33 @@ struct DrawSum {
     double e, w;
 };
 
+// v plus its partner's of a DPP move (vpa_device.h); 0 where a lane has none.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double add_move_f64(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROW_MASK, 0xF, false);
+    const uint32_t hi =
+        __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROW_MASK, 0xF, false);
+    return v + __builtin_bit_cast(double, lo | (uint64_t)hi << 32);
+}
+// The running sum over the lanes of a wavefront, the lane's own included.
+__device__ __forceinline__ double wave_scan_f64(double v) {
+    constexpr int kRight = 0x110;                  // row_shr:0
+    v = add_move_f64<kRight + 1, 0xF>(v);
+    v = add_move_f64<kRight + 2, 0xF>(v);
+    v = add_move_f64<kRight + 4, 0xF>(v);
+    v = add_move_f64<kRight + 8, 0xF>(v);
+    v = add_move_f64<dpp::kBcast15, 0xA>(v);
+    return add_move_f64<dpp::kBcast31, 0xC>(v);
+}
+__device__ __forceinline__ double lane63_f64(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, lo | (uint64_t)hi << 32);
+}
 __device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        v += __shfl_xor(v, off, 64);
-    return v;
+    return lane63_f64(wave_scan_f64(v));
 }
 
 // 2^(d scale), where d scale lies in [-1000, 1000]: 2^n (1 + f q(f)) with n the
@@ -72,6 +94,15 @@ __device__ __forceinline__ double exp2_f64(double d, double scale) {
     const uint64_t bits = __builtin_bit_cast(uint64_t, __builtin_fma(q, f, 1.0));
     const uint32_t n = (uint32_t)__builtin_bit_cast(uint64_t, t);
     return __builtin_bit_cast(double, bits + ((uint64_t)(n << 20) << 32));
+}
+
+// The logit below which 2^((x - m) scale) is 0 (2^-1000 and less).
+__device__ __forceinline__ float least_of(double m, double scale) {
+    const double far = m - 1000.0 / scale;
+    return far > -3e38 ? (float)far : -__FLT_MAX__;
+}
+__device__ __forceinline__ double exp2_f64_of(float x, float m, double scale) {
+    return x >= least_of((double)m, scale) ? exp2_f64((double)x - (double)m, scale) : 0.0;
 }
 
 __device__ __forceinline__ float temperature_of(const SampleTask& t, int32_t req) {
@@ -172,8 +203,8 @@ __global__ __launch_bounds__(kAcceptWaves * 64) void sample_accept_kernel(Sample
                 if (greedy)
                     p = id == id_of(order) ? 1.0 : 0.0;
                 else
-                    p = exp2(((double)to_f32(((const T*)t.logits)[(int64_t)row * t.ld + id]) -
-                              (double)sum.m) * d.scale) / (double)sum.s;
+                    p = exp2_f64_of(to_f32(((const T*)t.logits)[(int64_t)row * t.ld + id]), sum.m,
+                                    d.scale) / (double)sum.s;
                 d.q_row = req * t.k + pos;
                 const double q =
                     t.probs ? (double)to_f32(((const Q*)t.probs)[(int64_t)d.q_row * t.ldq + id]) : 1.0;
@@ -210,7 +241,11 @@ __global__ __launch_bounds__(kAcceptWaves * 64) void sample_accept_kernel(Sample
     }
 }
 
-// The weights of the columns of the row that is drawn from, by KIND.
+// The weights of the columns of the row that is drawn from, by KIND, or with kAny
+// by the kind that a call is given: a few columns, for which three copies of the
+// code would take longer to fetch than to run.
+constexpr int kAny = -1;
+
 template <int ESIZE, int QSIZE, int KIND>
 struct Weights {
     using T = typename elem<ESIZE>::type;
@@ -220,15 +255,15 @@ struct Weights {
     double scale, m;           // e = 2^((x - m) scale)
     float least;               // logits below it have e = 0 (2^-1000 and less)
     double z;
-    int32_t id;
+    int32_t id, kind;
 
-    __device__ __forceinline__ Weights(const SampleTask& t, const Draw& d, double sum) {
+    __device__ __forceinline__ Weights(const SampleTask& t, const Draw& d, int32_t k, double sum) {
+        kind = KIND == kAny ? k : KIND;
         x = (const T*)t.logits + (int64_t)d.row * t.ld;
         q = (const Q*)t.probs + (int64_t)d.q_row * t.ldq;
         scale = d.scale;
         m = (double)d.m;
-        const double far = m - 1000.0 / scale;
-        least = far > -3e38 ? (float)far : -__FLT_MAX__;
+        least = least_of(m, scale);
         z = sum;
         id = d.id;
     }
@@ -243,13 +278,13 @@ struct Weights {
         } qs = {};
         if (c + N <= hi) {
             xs = *(const Xs*)(x + c);
-            if constexpr (KIND == kMinus)
+            if (kind == kMinus)
                 qs = *(const Qs*)(q + c);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 from_f32(xs.v[i], c + i < hi ? to_f32(x[c + i]) : kMinusInf);
-                if (KIND == kMinus && c + i < hi)
+                if (kind == kMinus && c + i < hi)
                     qs.v[i] = q[c + i];
             }
         }
@@ -259,9 +294,9 @@ struct Weights {
             const float v = to_f32(xs.v[i]);
             w[i] = exp2_f64((double)v - m, scale);
             w[i] = v >= least ? w[i] : 0.0;
-            if constexpr (KIND == kMinus)
+            if (kind == kMinus)
                 w[i] = fmax(__builtin_fma(-(double)to_f32(qs.v[i]), z, w[i]), 0.0);
-            if constexpr (KIND == kWithout)
+            if (kind == kWithout)
                 w[i] = c + i == id ? 0.0 : w[i];
         }
     }
@@ -311,7 +346,7 @@ __global__ __launch_bounds__(kThreads) void sample_sums_kernel(SampleTask t, Sam
     const double z = SECOND ? sum_of_e(mine, cut.draw_blocks, lds) : 0.0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     with_kind(!SECOND && d.kind == kMinus ? (int32_t)kPlain : d.kind, [&](auto kind) {
-        const Weights<ESIZE, QSIZE, kind()> w(t, d, z);
+        const Weights<ESIZE, QSIZE, kind()> w(t, d, kind(), z);
         for (int b = group * kWaves + wave; b < cut.draw_blocks; b += cut.draw_groups * kWaves) {
             double s = 0.0;
 #pragma unroll
@@ -337,12 +372,7 @@ __global__ __launch_bounds__(kThreads) void sample_sums_kernel(SampleTask t, Sam
 // before the thread's, and the whole.
 __device__ __forceinline__ double block_scan_f64(double v, double& all, double (&lds)[kWaves]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double upto = v;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_up(upto, off, 64);
-        upto += lane >= off ? o : 0.0;
-    }
+    const double upto = wave_scan_f64(v);
     double before = __shfl_up(upto, 1, 64);
     before = lane == 0 ? 0.0 : before;
     __syncthreads();
@@ -356,6 +386,44 @@ __device__ __forceinline__ double block_scan_f64(double v, double& all, double (
     return before;
 }
 
+// The first of a workgroup's items, in the order of its threads, that the running
+// sum passes at; as long as none does, the last one with a weight.  (Atomics on
+// LDS go through a wavefront's lanes one by one.)
+struct PassingWave {
+    double before;
+    int32_t index;
+    int32_t kind;              // 2: passed, 1: has a weight, 0: neither
+};
+template <int WAVES>
+struct Passing {
+    PassingWave* lds;
+    bool passed = false;
+    int32_t index = 0;
+    double before = 0.0;
+    __device__ __forceinline__ explicit Passing(PassingWave* l) : lds(l) {}
+
+    // every thread: whether it passes at item `at`, whether it has a weight and its
+    // last one, and the sum before
+    __device__ __forceinline__ void take(bool passes, bool weight, int32_t at, int32_t top,
+                                         double sum) {
+        const uint64_t p = __ballot(passes), w = __ballot(weight);
+        const int from = p ? (int)__builtin_ctzll(p) : w ? 63 - (int)__builtin_clzll(w) : 0;
+        __syncthreads();
+        if ((int)(threadIdx.x & 63) == from)
+            lds[threadIdx.x >> 6] = PassingWave{sum, p ? at : top, p ? 2 : w ? 1 : 0};
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+            const PassingWave o = lds[i];
+            if (!passed && o.kind != 0) {
+                passed = o.kind == 2;
+                index = o.index;
+                before = o.before;
+            }
+        }
+    }
+};
+
 // The column where the running sum passes the random number: its block from the
 // blocks' sums, then its 4 columns a thread.  Where rounding lets none pass, and
 // for random numbers from 1 on, the last one with a weight.
@@ -364,15 +432,21 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleTask t, Sam
                                                                const Draw* draws,
                                                                const DrawSum* sums) {
     constexpr int N = kDrawCols / kThreads;
-    __shared__ double lds[kWaves], start;
-    __shared__ int32_t passed, last;
+    __shared__ double lds[kWaves];
+    __shared__ PassingWave found[kWaves];
     const int32_t req = blockIdx.x;
+    const DrawSum* mine = sums + (int64_t)req * cut.draw_blocks;
+    // loaded together: a kernel's first loads take a microsecond
     const Draw d = draws[req];
+    const double u = t.sample_u[req];
+    DrawSum first = {0.0, 0.0};
+    if ((int)threadIdx.x < cut.draw_blocks)
+        first = mine[threadIdx.x];
+    __builtin_amdgcn_sched_barrier(0);
     if (d.kind == kDrawn)
         return;
-    const DrawSum* mine = sums + (int64_t)req * cut.draw_blocks;
-    double total = 0.0, z = 0.0;
-    for (int i = threadIdx.x; i < cut.draw_blocks; i += kThreads) {
+    double total = first.w, z = d.kind == kMinus ? first.e : 0.0;
+    for (int i = threadIdx.x + kThreads; i < cut.draw_blocks; i += kThreads) {
         const DrawSum s = mine[i];
         total += s.w;
         z += d.kind == kMinus ? s.e : 0.0;
@@ -392,68 +466,47 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleTask t, Sam
         total = z;
     }
     const bool of_e = kind != d.kind;
-    const double u = t.sample_u[req];
     const double target = (u > 0.0 ? u : 0.0) * total;
     // the block
-    if (threadIdx.x == 0) {
-        passed = cut.draw_blocks;
-        last = 0;
-        start = 0.0;
-    }
+    Passing<kWaves> at(found);
     double run = 0.0;
     for (int b0 = 0; b0 < cut.draw_blocks; b0 += kThreads) {
         const int b = b0 + (int)threadIdx.x;
         double v = 0.0, all;
-        if (b < cut.draw_blocks)
+        if (b0 == 0)
+            v = of_e ? first.e : first.w;
+        else if (b < cut.draw_blocks)
             v = of_e ? mine[b].e : mine[b].w;
         const double before = run + block_scan_f64(v, all, lds);
-        if (v > 0.0 && before + v > target)
-            atomicMin(&passed, b);
-        if (v > 0.0)
-            atomicMax(&last, b);
-        __syncthreads();
-        // of the block that it passes in or, as yet, of the last one with a weight
-        if (b == (passed < cut.draw_blocks ? passed : last) && v > 0.0)
-            start = before;
+        at.take(v > 0.0 && before + v > target, v > 0.0, b, b, before);
         run += all;
-        __syncthreads();
-        if (passed < cut.draw_blocks)
+        if (at.passed)
             break;
     }
-    const int block = passed < cut.draw_blocks ? passed : last;
-    const double from = start;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        passed = t.vocab;
-        last = 0;
-    }
+    const int block = at.index;
+    const double from = at.before;
     // the column
-    with_kind(kind, [&](auto k) {
-        const Weights<ESIZE, QSIZE, k()> w(t, d, z);
-        const int c = block * kDrawCols + (int)threadIdx.x * N;
-        double v[N], own = 0.0, all;
-        w.of(c, t.vocab, v);
-        int top = -1;
+    const Weights<ESIZE, QSIZE, kAny> w(t, d, kind, z);
+    const int c = block * kDrawCols + (int)threadIdx.x * N;
+    double v[N], own = 0.0, all;
+    w.of(c, t.vocab, v);
+    int top = -1;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            own += v[i];
-            top = v[i] > 0.0 ? c + i : top;
-        }
-        double sum = from + block_scan_f64(own, all, lds);
-        int32_t token = t.vocab;
+    for (int i = 0; i < N; ++i) {
+        own += v[i];
+        top = v[i] > 0.0 ? c + i : top;
+    }
+    double sum = from + block_scan_f64(own, all, lds);
+    int32_t token = t.vocab;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            sum += v[i];
-            token = v[i] > 0.0 && sum > target && token == t.vocab ? c + i : token;
-        }
-        if (token < t.vocab)
-            atomicMin(&passed, token);
-        if (top >= 0)
-            atomicMax(&last, top);
-    });
-    __syncthreads();
+    for (int i = 0; i < N; ++i) {
+        sum += v[i];
+        token = v[i] > 0.0 && sum > target && token == t.vocab ? c + i : token;
+    }
+    Passing<kWaves> column(found);
+    column.take(token < t.vocab, top >= 0, token, top, 0.0);
     if (threadIdx.x == 0)
-        t.out_tokens[(int64_t)req * (t.k + 1) + d.pos] = passed < t.vocab ? passed : last;
+        t.out_tokens[(int64_t)req * (t.k + 1) + d.pos] = column.index;
 }
 
 size_t align16(size_t n) {
