@@ -1,11 +1,11 @@
 // sampled.hip -- verification of drafted tokens against the target's
 // probabilities, from given random numbers.
 //
-// Five steps: partial sums of exponentials and the argmax of every row's
-// segments; a request's acceptance tests, which give the row it draws from;
-// that row's exponentials summed in 64 bits by segments; the sums of the
-// weights max(p - q, 0), where a draft distribution is subtracted; the column
-// where the running sum passes the random number.
+// Three or four launches: partial sums of exponentials and the argmax of every
+// row's segments; a request's acceptance tests, which give the row it draws
+// from, and that row's exponentials summed in 64 bits by blocks of columns; the
+// sums of the weights max(p - q, 0), where a draft distribution is subtracted;
+// the column where the running sum passes the random number.
 //
 // The draw is in 64 bits because a border lies between any two of up to 2^24
 // columns: with sums that are off by 2^-24 one draw in a hundred over a flat
@@ -159,25 +159,20 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleTask t, Sam
     stats[blockIdx.x] = RowStat{all.m, all.s, order};
 }
 
-// A workgroup a request, a wavefront a position, until one is not accepted.
-constexpr int kAcceptWaves = 8;
-
+// The acceptance tests of a request by a workgroup, a wavefront a position, until
+// one is not accepted: the row that the request draws from.  `token` is the argmax
+// where that is what it draws, else -1.
 template <int ESIZE, int QSIZE>
-__global__ __launch_bounds__(kAcceptWaves * 64) void sample_accept_kernel(SampleTask t,
-                                                                          SampleCut cut,
-                                                                          const RowStat* stats,
-                                                                          Draw* draws) {
+__device__ __forceinline__ Draw accept_request(const SampleTask& t, const SampleCut& cut,
+                                               const RowStat* stats, int32_t req, int32_t& token) {
     using T = typename elem<ESIZE>::type;
     using Q = typename elem<QSIZE>::type;
-    __shared__ Draw ends[kAcceptWaves];
-    __shared__ int32_t tokens[kAcceptWaves];         // the argmax where it is drawn, else -1
-    __shared__ int32_t at_end[kAcceptWaves];
-    const int32_t req = blockIdx.x;
+    __shared__ Draw ends[kWaves];
+    __shared__ int32_t tokens[kWaves], at_end[kWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float temp = temperature_of(t, req);
     const float scale = is_greedy(temp) ? kLog2e : kLog2e / temp;
-    const int32_t* ids = t.draft_ids + (int64_t)req * t.k;
-    for (int first = 0;; first += kAcceptWaves) {
+    for (int first = 0;; first += kWaves) {
         const int pos = first + wave;
         bool last = true;
         if (pos <= t.k) {
@@ -185,6 +180,16 @@ __global__ __launch_bounds__(kAcceptWaves * 64) void sample_accept_kernel(Sample
             RowStat st = {kMinusInf, 0.0f, 0};
             if (lane < cut.row_segments)
                 st = stats[(int64_t)row * cut.row_segments + lane];
+            // the draft's logit and probability are on their way meanwhile
+            const int32_t id = pos < t.k ? t.draft_ids[(int64_t)req * t.k + pos] : -1;
+            const int32_t q_row = req * t.k + pos;
+            float x = 0.0f, q = 1.0f, u = 0.0f;
+            if (is_draft(t, id)) {
+                x = to_f32(((const T*)t.logits)[(int64_t)row * t.ld + id]);
+                u = t.accept_u[q_row];
+                if (t.probs)
+                    q = to_f32(((const Q*)t.probs)[(int64_t)q_row * t.ldq + id]);
+            }
             const ExpSum sum = wave_join(ExpSum{st.m, st.s}, scale);
             const uint64_t order = wave_max_u64(st.order);
             const bool greedy = is_greedy(temp) || !(fabsf(sum.m) < __builtin_inff()) ||
@@ -197,18 +202,14 @@ __global__ __launch_bounds__(kAcceptWaves * 64) void sample_accept_kernel(Sample
             d.q_row = 0;
             d.id = -1;
             d.pos = pos;
-            const int32_t id = pos < t.k ? ids[pos] : -1;
             if (is_draft(t, id)) {
                 double p;
                 if (greedy)
                     p = id == id_of(order) ? 1.0 : 0.0;
                 else
-                    p = exp2_f64_of(to_f32(((const T*)t.logits)[(int64_t)row * t.ld + id]), sum.m,
-                                    d.scale) / (double)sum.s;
-                d.q_row = req * t.k + pos;
-                const double q =
-                    t.probs ? (double)to_f32(((const Q*)t.probs)[(int64_t)d.q_row * t.ldq + id]) : 1.0;
-                last = !((double)t.accept_u[d.q_row] * q < p);
+                    p = exp2_f64_of(x, sum.m, d.scale) / (double)sum.s;
+                last = !((double)u * (double)q < p);
+                d.q_row = q_row;
                 d.kind = t.probs ? kMinus : kWithout;
                 d.id = id;
             }
@@ -223,21 +224,26 @@ __global__ __launch_bounds__(kAcceptWaves * 64) void sample_accept_kernel(Sample
             at_end[wave] = last;
         __syncthreads();
         int found = 0;
-        while (found < kAcceptWaves && !at_end[found])
+        while (found < kWaves && !at_end[found])
             ++found;
-        if (found < kAcceptWaves) {
-            const Draw d = ends[found];
-            int32_t* out = t.out_tokens + (int64_t)req * (t.k + 1);
-            for (int j = threadIdx.x; j <= t.k; j += kAcceptWaves * 64)
-                out[j] = j < d.pos ? ids[j] : j == d.pos ? tokens[found] : -1;
-            if (threadIdx.x == 0) {
-                t.num_sampled[req] = d.pos + 1;
-                t.num_rejected[req] = t.k - d.pos;
-                draws[req] = d;
-            }
-            return;
+        if (found < kWaves) {
+            token = tokens[found];
+            return ends[found];
         }
         __syncthreads();
+    }
+}
+
+// What is known of a request's outputs before its draw; by a workgroup.
+__device__ __forceinline__ void write_request(const SampleTask& t, int32_t req, const Draw& d,
+                                              int32_t token, Draw* draws) {
+    int32_t* out = t.out_tokens + (int64_t)req * (t.k + 1);
+    for (int j = threadIdx.x; j <= t.k; j += kThreads)
+        out[j] = j < d.pos ? t.draft_ids[(int64_t)req * t.k + j] : j == d.pos ? token : -1;
+    if (threadIdx.x == 0) {
+        t.num_sampled[req] = d.pos + 1;
+        t.num_rejected[req] = t.k - d.pos;
+        draws[req] = d;
     }
 }
 
@@ -267,35 +273,44 @@ struct Weights {
         z = sum;
         id = d.id;
     }
-    // N consecutive columns from c: their weights, 0 from `hi` on
+    // what N consecutive columns hold
     template <int N>
-    __device__ __forceinline__ void of(int c, int hi, double (&w)[N]) const {
-        struct __attribute__((packed, aligned(sizeof(T)))) Xs {
+    struct Columns {
+        struct __attribute__((packed, aligned(sizeof(T)))) {
             T v[N];
-        } xs;
-        struct __attribute__((packed, aligned(sizeof(Q)))) Qs {
+        } x;
+        struct __attribute__((packed, aligned(sizeof(Q)))) {
             Q v[N];
-        } qs = {};
+        } q;
+    };
+    // columns from c on, masked from `hi` on
+    template <int N>
+    __device__ __forceinline__ void load(int c, int hi, Columns<N>& o) const {
         if (c + N <= hi) {
-            xs = *(const Xs*)(x + c);
+            o.x = *(const decltype(o.x)*)(x + c);
             if (kind == kMinus)
-                qs = *(const Qs*)(q + c);
+                o.q = *(const decltype(o.q)*)(q + c);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                from_f32(xs.v[i], c + i < hi ? to_f32(x[c + i]) : kMinusInf);
+                from_f32(o.x.v[i], c + i < hi ? to_f32(x[c + i]) : kMinusInf);
+                o.q.v[i] = 0;
                 if (kind == kMinus && c + i < hi)
-                    qs.v[i] = q[c + i];
+                    o.q.v[i] = q[c + i];
             }
         }
+    }
+    // their weights
+    template <int N>
+    __device__ __forceinline__ void of(int c, const Columns<N>& o, double (&w)[N]) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             // (one multiply-add of x scale - m scale loses every digit where m is 1e30)
-            const float v = to_f32(xs.v[i]);
+            const float v = to_f32(o.x.v[i]);
             w[i] = exp2_f64((double)v - m, scale);
             w[i] = v >= least ? w[i] : 0.0;
             if (kind == kMinus)
-                w[i] = fmax(__builtin_fma(-(double)to_f32(qs.v[i]), z, w[i]), 0.0);
+                w[i] = fmax(__builtin_fma(-(double)to_f32(o.q.v[i]), z, w[i]), 0.0);
             if (kind == kWithout)
                 w[i] = c + i == id ? 0.0 : w[i];
         }
@@ -330,16 +345,47 @@ __device__ __forceinline__ double sum_of_e(const DrawSum* sums, int blocks, doub
     return block_sum_f64(v, lds);
 }
 
+// The acceptance tests alone; a workgroup a request.
+template <int ESIZE, int QSIZE>
+__global__ __launch_bounds__(kThreads) void sample_accept_kernel(SampleTask t, SampleCut cut,
+                                                                 const RowStat* stats,
+                                                                 Draw* draws) {
+    int32_t token;
+    const Draw d = accept_request<ESIZE, QSIZE>(t, cut, stats, blockIdx.x, token);
+    write_request(t, blockIdx.x, d, token, draws);
+}
+
 // Sums of the weights over blocks of kDrawCols columns of each request's row, a
 // wavefront a block at a time; of e alone for the requests that subtract a draft
-// distribution, whose weights are summed by a SECOND launch.
-template <int ESIZE, int QSIZE, bool SECOND>
+// distribution, whose weights are summed by a second launch (kSecond).  With
+// kAccept each of a request's workgroups makes its acceptance tests, and the
+// first writes what they say: up to 64 requests that costs less than a launch
+// (1 x 5 x 151936 19.3 us with a launch of its own, 16.2 so; 24 x 4 31.2 and
+// 29.2), for more of them more (170 x 6 x 200064 138 and 145).
+//
+// Bound by the 64-bit instructions, 16 an element, which take 8 clocks of a SIMD
+// each here: 33 us for 170 x 200064 bf16, whose loads take 14.  (The next block's
+// loads ahead of a block's sums made it no faster.)
+enum SumsStep { kAccept, kFirst, kSecond };
+constexpr int64_t kAcceptInSums = 64;
+
+template <int ESIZE, int QSIZE, int STEP>
 __global__ __launch_bounds__(kThreads) void sample_sums_kernel(SampleTask t, SampleCut cut,
-                                                               const Draw* draws, DrawSum* sums) {
+                                                               const RowStat* stats, Draw* draws,
+                                                               DrawSum* sums) {
     constexpr int VEC = 16 / ESIZE;
+    constexpr bool SECOND = STEP == kSecond;
     __shared__ double lds[kWaves];
     const int32_t req = blockIdx.x / cut.draw_groups, group = blockIdx.x % cut.draw_groups;
-    const Draw d = draws[req];
+    Draw d;
+    if constexpr (STEP == kAccept) {
+        int32_t token;
+        d = accept_request<ESIZE, QSIZE>(t, cut, stats, req, token);
+        if (group == 0)
+            write_request(t, req, d, token, draws);
+    } else {
+        d = draws[req];
+    }
     if (d.kind == kDrawn || (SECOND && d.kind != kMinus))
         return;
     DrawSum* mine = sums + (int64_t)req * cut.draw_blocks;
@@ -351,8 +397,11 @@ __global__ __launch_bounds__(kThreads) void sample_sums_kernel(SampleTask t, Sam
             double s = 0.0;
 #pragma unroll
             for (int i = 0; i < kDrawCols / 64 / VEC; ++i) {
+                const int c = b * kDrawCols + (i * 64 + lane) * VEC;
+                typename Weights<ESIZE, QSIZE, kind()>::template Columns<VEC> columns;
                 double v[VEC];
-                w.of(b * kDrawCols + (i * 64 + lane) * VEC, t.vocab, v);
+                w.load(c, t.vocab, columns);
+                w.of(c, columns, v);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k)
                     s += v[k];
@@ -489,7 +538,9 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleTask t, Sam
     const Weights<ESIZE, QSIZE, kAny> w(t, d, kind, z);
     const int c = block * kDrawCols + (int)threadIdx.x * N;
     double v[N], own = 0.0, all;
-    w.of(c, t.vocab, v);
+    typename Weights<ESIZE, QSIZE, kAny>::template Columns<N> columns;
+    w.load(c, t.vocab, columns);
+    w.of(c, columns, v);
     int top = -1;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -555,9 +606,8 @@ size_t sample_workspace(const SampleCut& c, int64_t n_req, int32_t k) {
 
 int64_t sample_threads(const SampleCut& c, int64_t n_req, int32_t k) {
     const int64_t rows = n_req * (k + 1) * c.row_segments * kThreads;
-    const int64_t sums = n_req * c.draw_groups * kThreads, accept = n_req * kAcceptWaves * 64;
-    const int64_t most = rows > sums ? rows : sums;
-    return most > accept ? most : accept;
+    const int64_t sums = n_req * c.draw_groups * kThreads;
+    return rows > sums ? rows : sums;
 }
 
 namespace {
@@ -575,14 +625,18 @@ hipError_t launch_typed(const SampleTask& t, void* ws, hipStream_t stream) {
                                         stream, t, c, stats)
                                : launch(sample_rows_kernel<ESIZE, 2>, rows, dim3(kThreads), 0,
                                         stream, t, c, stats);
-    if (e == hipSuccess)
-        e = launch(sample_accept_kernel<ESIZE, QSIZE>, reqs, dim3(kAcceptWaves * 64), 0, stream, t,
-                   c, stats, draws);
-    if (e == hipSuccess)
-        e = launch(sample_sums_kernel<ESIZE, QSIZE, false>, groups, dim3(kThreads), 0, stream, t, c,
+    const dim3 block(kThreads);
+    if (e == hipSuccess && t.n_req <= kAcceptInSums) {
+        e = launch(sample_sums_kernel<ESIZE, QSIZE, kAccept>, groups, block, 0, stream, t, c, stats,
                    draws, sums);
+    } else if (e == hipSuccess) {
+        e = launch(sample_accept_kernel<ESIZE, QSIZE>, reqs, block, 0, stream, t, c, stats, draws);
+        if (e == hipSuccess)
+            e = launch(sample_sums_kernel<ESIZE, QSIZE, kFirst>, groups, block, 0, stream, t, c,
+                       stats, draws, sums);
+    }
     if (e == hipSuccess && t.probs)
-        e = launch(sample_sums_kernel<ESIZE, QSIZE, true>, groups, dim3(kThreads), 0, stream, t, c,
+        e = launch(sample_sums_kernel<ESIZE, QSIZE, kSecond>, groups, block, 0, stream, t, c, stats,
                    draws, sums);
     if (e == hipSuccess)
         e = launch(sample_pick_kernel<ESIZE, QSIZE>, reqs, dim3(kThreads), 0, stream, t, c,
