@@ -221,7 +221,7 @@ size_t vpa_head_linear_fp8_workspace(int64_t rows, int64_t outer, int64_t inner)
  *  x        e4m3 [rows][ldx], x_scale float [rows][ldxs] (blocks of 1 x 128).
  *  weight   e4m3 [outer][ldw], w_scale float [ceil(outer/128)][ldws] (128 x 128).
  *           Rows of x and weight begin at multiples of 16 bytes (pointer, and
- *           ldx and ldw, which like ldxs are at most 2^21); what lies past a
+ *           ldx and ldw; all four strides are at most 2^21); what lies past a
  *           row's `inner` values does not matter.
  *  bias, residual  VPA_BF16, [outer] and [rows][outer], either may be NULL.
  *  y        out, of type out_dtype: VPA_BF16 or VPA_F32.  It may be the residual

@@ -450,10 +450,10 @@ vpa_status vpa_head_linear_fp8(const void* x, int64_t ldx, const float* x_scale,
         (st = check_matrix("y", y, esize_of(odt), ldy, outer)) != VPA_OK)
         return st;
     const int64_t most = (int64_t)1 << 21;
-    if (ldx % 16 || ldw % 16 || ldx > most || ldw > most || ldxs > most)
+    if (ldx % 16 || ldw % 16 || ldx > most || ldw > most || ldxs > most || ldws > most)
         return fail(VPA_ERR_INVALID,
-                    "%s: row strides %lld, %lld (multiples of 16) or %lld (scales) above 2^21", call,
-                    (long long)ldx, (long long)ldw, (long long)ldxs);
+                    "%s: row strides %lld, %lld (multiples of 16), %lld or %lld (scales) above 2^21",
+                    call, (long long)ldx, (long long)ldw, (long long)ldxs, (long long)ldws);
     if (y == residual && (ldy != ldr || odt != VPA_BF16))
         return fail(VPA_ERR_INVALID, "%s: y in the residual's place needs its stride and type",
                     call);

@@ -99,18 +99,19 @@ __device__ __forceinline__ scalar_floats weight_scales(const Fp8Task& f, int64_t
     return (scalar_floats)uniform(f.b_scale + n / kScaleBlock * f.ldb_scale);
 }
 
-// x's scales of a tile of ROWS rows for one block of k, straight to LDS: 64 rows
-// a wavefront, by the wavefronts that have them.
-template <int ROWS>
+// The scales of up to 64 rows (of x, or of blocks of W's rows) for one block of k,
+// straight to LDS; rows past the last repeat it.
 struct ScaleLoader {
     const float* base;
     uint32_t off, size;
-    __device__ __forceinline__ void init(const Fp8Task& f, int64_t row0, int64_t rows, int first) {
-        const int left = rows - row0 < ROWS ? (int)(rows - row0) : ROWS;
-        const int r = first + (int)(threadIdx.x & 63);
-        base = f.a_scale + row0 * f.lda_scale;
-        off = (uint32_t)((r < left ? r : left - 1) * f.lda_scale * 4);
-        size = (uint32_t)((left - 1) * f.lda_scale * 4 + 4);
+    // rows `first` and up to 63 more of `rows`; none where first is past them
+    __device__ __forceinline__ void init(const float* p, int64_t ld, int64_t first, int64_t rows) {
+        first = first < rows ? first : rows - 1;
+        const int left = rows - first < 64 ? (int)(rows - first) : 64;
+        const int r = (int)(threadIdx.x & 63);
+        base = p + first * ld;
+        off = (uint32_t)((r < left ? r : left - 1) * ld * 4);
+        size = (uint32_t)((left - 1) * ld * 4 + 4);
     }
     // to `lds` and the 255 bytes after it
     __device__ __forceinline__ void load(int64_t block, char* lds) const {
@@ -142,7 +143,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
     static_assert(BN / WN <= kScaleBlock && kScaleBlock % (BN / WN) == 0, "one scale of W");
     using LA = TileLoader<1, true, true, BM, NT>;
     using LB = TileLoader<1, true, true, BN, NT>;
-    constexpr int SCALES = LA::BYTES + LB::BYTES, STAGE = SCALES + BM * 4;
+    // x's scales, then W's
+    constexpr int SCALES = LA::BYTES + LB::BYTES, XWAVES = BM / 64;
+    constexpr int STAGE = SCALES + (XWAVES + 1) * 256;
+    static_assert(XWAVES < WM * WN, "a wavefront for each 64 scales");
     __shared__ __align__(1024) char lds0[STAGE];
     __shared__ __align__(1024) char lds1[STAGE];
     const GemmTask& t = f.g;
@@ -156,24 +160,27 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
     LB lb;
     la.init(t.a, t.a_m, m0, t.m);
     lb.init(t.b, t.b_n, n0, t.n);
-    ScaleLoader<BM> ls;
-    ls.init(f, m0, t.m, wave * 64 % BM);
+    ScaleLoader ls;
+    if (wave < XWAVES)
+        ls.init(f.a_scale, f.lda_scale, m0 + wave * 64, t.m);
+    else
+        ls.init(f.b_scale, f.ldb_scale, n0 / kScaleBlock, (t.n + kScaleBlock - 1) / kScaleBlock);
     const int64_t whole = t.k / 128, all = (t.k + 127) / 128;
     const int64_t s0 = slice * stages_per_slice;
     const int64_t end = s0 + stages_per_slice < all ? s0 + stages_per_slice : all;
     const int64_t s1 = end < whole ? end : whole;
-    // (a tile's last columns may have no scales of their own)
-    const scalar_floats ws = weight_scales(f, n0 + wn < t.n ? n0 + wn : t.n - 1);
     const typename LA::Place pa = LA::place(wm);
     const typename LB::Place pb = LB::place(wn);
     const int scale_at = SCALES + (wm + (lane & 15)) * 4;
+    const int wscale_at = SCALES + XWAVES * 256 + wn / kScaleBlock * 4;
     f32x4 acc[IM][JN] = {};
     const typename LA::Direct da = la.direct();
     const typename LB::Direct db = lb.direct();
     auto stage = [&](int64_t s, char* lds) {
+        __builtin_amdgcn_s_setprio(0);
         la.load(da, s, lds);
         lb.load(db, s, lds + LA::BYTES);
-        if (wave < BM / 64)
+        if (wave <= XWAVES)
             ls.load(s, lds + SCALES + wave * 256);
     };
     u32x4_t av[RING][2], bv[JN][2];
@@ -190,27 +197,40 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
             bv[j][h] = LB::fragment(lds + LA::BYTES, p, j, h);
     };
     Wide wide[EXACT ? JN : 1];
-    auto products = [&](int i, float sw) {
-        f32x4 p[JN];
-        if constexpr (EXACT) {
-            const Wide a(av[i % RING]);
+    // A product's scaling, 4 multiply-adds, runs in the shadow of the product after
+    // next: row i's follow row i + 1's products one by one, and the last row's the
+    // next stage's first.
+    f32x4 p[2][JN] = {};
+    float scale[2] = {};
+    auto add = [&](int i, int j) {
 #pragma unroll
-            for (int j = 0; j < JN; ++j)
-                p[j] = mma_wide(wide[j], a);
-        } else {
-#pragma unroll
-            for (int j = 0; j < JN; ++j)
-                p[j] = mma_fast(bv[j], av[i % RING]);
-        }
-        const float sc = sx[i % RING] * sw;
+        for (int e = 0; e < 4; ++e)
+            acc[i][j][e] = __builtin_fmaf(p[i % 2][j][e], scale[i % 2], acc[i][j][e]);
+        // here, not at the end of the stage with all of its products kept
+        asm volatile("" : "+v"(acc[i][j]));
+    };
+    static_assert(IM % 2 == 0, "rows take turns");
+    auto products = [&](int i, float sw, auto after) {
+        Wide a;
+        if constexpr (EXACT)
+            a = Wide(av[i % RING]);
+        scale[i % 2] = sx[i % RING] * sw;
 #pragma unroll
         for (int j = 0; j < JN; ++j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[i][j][e] = __builtin_fmaf(p[j][e], sc, acc[i][j][e]);
-            // here, not at the end of the stage with all of its products kept
-            asm volatile("" : "+v"(acc[i][j]));
+            if constexpr (EXACT)
+                p[i % 2][j] = mma_wide(wide[j], a);
+            else
+                p[i % 2][j] = mma_fast(bv[j], av[i % RING]);
+            add((i + IM - 1) % IM, j);
+            after(j);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    const auto nothing = [](int) {};
+    auto finish = [&] {
+#pragma unroll
+        for (int j = 0; j < JN; ++j)
+            add(IM - 1, j);
     };
     auto widen_b = [&] {
         if constexpr (EXACT)
@@ -222,7 +242,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
     if (end > whole) {
         la.load_tail(whole, t.k, lds1);
         lb.load_tail(whole, t.k, lds1 + LA::BYTES);
-        if (wave < BM / 64)
+        if (wave <= XWAVES)
             ls.load(whole, lds1 + SCALES + wave * 256);
         stage_barrier();
 #pragma unroll
@@ -232,7 +252,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
 #pragma unroll
         for (int i = 0; i < IM; ++i) {
             read_a(lds1, pa, i);
-            products(i, ws[whole]);
+            products(i, *(const float*)(lds1 + wscale_at), nothing);
         }
         stage_barrier();
     }
@@ -249,17 +269,24 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
             read_a(lds0, pa, i);
     }
     const bool early = wave < WM * WN / 2;
-    float sw = s0 < s1 ? ws[s0] : 0.0f;
+    // (scalar loads of it would make every wait one for all of LDS's answers)
+    float sw = *(const float*)(lds0 + wscale_at);
     for (int64_t s = s0; s + 1 < s1; ++s) {
         char* now = (s - s0) & 1 ? lds1 : lds0;
         char* next = (s - s0) & 1 ? lds0 : lds1;
-        const float sw_next = ws[s + 1];
+        float sw_next = 0.0f;
         widen_b();
         const typename LA::Place a = pa.again();
         const typename LB::Place b = pb.again();
 #pragma unroll
         for (int i = 0; i < IM; ++i) {
-            products(i, sw);
+            // the last row's products are the last to use a fragment of W
+            products(i, sw, [&](int j) {
+                if (i == IM - 1)
+                    read_b(next, b, j);
+            });
+            if (i == 0)
+                __builtin_amdgcn_s_setprio(1);
             if (i == IM - RING) {
                 // the next stage has landed, and this one has been read
                 stage_barrier();
@@ -272,11 +299,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
                 read_a(now, a, i + RING);
             else
                 read_a(next, a, i + RING - IM);
+            if (i == IM - RING)
+                sw_next = *(const float*)(next + wscale_at);
             __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int j = 0; j < JN; ++j)
-            read_b(next, b, j);
         sw = sw_next;
     }
     if (s0 < s1) {
@@ -284,12 +310,13 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
         widen_b();
 #pragma unroll
         for (int i = 0; i < IM; ++i) {
-            products(i, sw);
+            products(i, sw, nothing);
             if (i < IM - RING)
                 read_a(now, pa, i + RING);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
+    finish();
     stage_barrier();
     if (part)
         part += slice * t.m * t.n;
@@ -332,8 +359,8 @@ __global__ __launch_bounds__(256) void fp8_few_rows_kernel(Fp8Task f, int64_t st
     LB lb;
     la.init(t.a, t.a_m, 0, t.m);
     lb.init(t.b, t.b_n, n0, t.n);
-    ScaleLoader<BM> ls;
-    ls.init(f, 0, t.m, 0);
+    ScaleLoader ls;
+    ls.init(f.a_scale, f.lda_scale, 0, t.m);
     const scalar_floats ws = weight_scales(f, n0);
     const typename LA::Place pa = LA::place(0);
     const typename LB::Place pb = LB::place(wave * 16);
