@@ -126,10 +126,17 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleTask t, Sam
     const int32_t row = blockIdx.x / cut.row_segments, seg = blockIdx.x % cut.row_segments;
     const int32_t req = row / (t.k + 1), pos = row % (t.k + 1);
     // rows after a placeholder are not needed
+    const int32_t* ids = t.draft_ids + (int64_t)req * t.k;
     bool ended = false;
-    for (int j = threadIdx.x; j < pos; j += kThreads)
-        ended |= !is_draft(t, t.draft_ids[(int64_t)req * t.k + j]);
-    if (__syncthreads_or(ended))
+    if (pos <= 16) {                               // the same loads in every lane
+        for (int j = 0; j < pos; ++j)
+            ended |= !is_draft(t, ids[j]);
+    } else {
+        for (int j = threadIdx.x; j < pos; j += kThreads)
+            ended |= !is_draft(t, ids[j]);
+        ended = __syncthreads_or(ended);
+    }
+    if (ended)
         return;
     const T* x = (const T*)t.logits + (int64_t)row * t.ld;
     const float temp = temperature_of(t, req);
@@ -578,16 +585,22 @@ Layout layout_of(const SampleCut& c, int64_t n_req, int32_t k) {
 
 }  // namespace
 
-// Rows in chunks of 8 vectors a thread where that gives every CU 4 workgroups,
-// else of 2, and segments of whole chunks until there are 4 (8) workgroups a CU.
+// Rows in chunks of 8 vectors a thread where that gives every CU 4 workgroups, of
+// 4 where that does, else of 2, and segments of whole chunks until there are 4
+// workgroups a CU (8 of the smaller ones).
 // A drawn row has a wavefront for each block of columns, 16 workgroups a CU at
 // most over all requests.
 SampleCut sample_cut(int esize, int64_t vocab, int64_t n_req, int32_t k) {
     SampleCut c;
     const int64_t rows = n_req * (k + 1), vec = 16 / esize;
     const int64_t width = vocab + vec - 1;         // with the columns before an aligned one
-    const int64_t big = kThreads * 8 * vec;
-    c.vecs = 2 * width > big && rows * ((width + big - 1) / big) >= 1024 ? 8 : 2;
+    c.vecs = 8;
+    while (c.vecs > 2) {
+        const int64_t cols = kThreads * c.vecs * vec;
+        if (2 * width > cols && rows * ((width + cols - 1) / cols) >= 1024)
+            break;
+        c.vecs /= 2;
+    }
     const int64_t chunk = kThreads * c.vecs * vec, chunks = (width + chunk - 1) / chunk;
     int64_t want = ((c.vecs == 8 ? 1024 : 2048) + rows - 1) / rows;
     want = want > chunks ? chunks : want;
@@ -621,10 +634,10 @@ hipError_t launch_typed(const SampleTask& t, void* ws, hipStream_t stream) {
     DrawSum* sums = (DrawSum*)((char*)ws + l.sums);
     const dim3 rows((uint32_t)((int64_t)t.n_req * (t.k + 1) * c.row_segments));
     const dim3 groups((uint32_t)((int64_t)t.n_req * c.draw_groups)), reqs((uint32_t)t.n_req);
-    hipError_t e = c.vecs == 8 ? launch(sample_rows_kernel<ESIZE, 8>, rows, dim3(kThreads), 0,
-                                        stream, t, c, stats)
-                               : launch(sample_rows_kernel<ESIZE, 2>, rows, dim3(kThreads), 0,
-                                        stream, t, c, stats);
+    const auto kernel = c.vecs == 8   ? sample_rows_kernel<ESIZE, 8>
+                        : c.vecs == 4 ? sample_rows_kernel<ESIZE, 4>
+                                      : sample_rows_kernel<ESIZE, 2>;
+    hipError_t e = launch(kernel, rows, dim3(kThreads), 0, stream, t, c, stats);
     const dim3 block(kThreads);
     if (e == hipSuccess && t.n_req <= kAcceptInSums) {
         e = launch(sample_sums_kernel<ESIZE, QSIZE, kAccept>, groups, block, 0, stream, t, c, stats,

@@ -118,6 +118,11 @@ def _fp8_workspace(rows, outer, inner):
     return int(draft_lib().vpa_head_linear_fp8_workspace(rows, outer, inner))
 
 
+def _new(rows, cols, dtype, device):
+    """A new matrix (by strides: 1.3 us, torch.empty 1.6)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
 def _whole_rows(logits, vocab):
     """Logits that hold every shard of a row -> (rows, columns, row stride, dtype code)."""
     n, cols, ld, code = _rows_of(logits, "logits")
@@ -219,7 +224,7 @@ def _teacher(ids, logprobs, n, device):
 def _grad_tensor(out, logits, n, cols, ld):
     """The gradient's tensor -> (tensor, row stride)."""
     if out is None:
-        return torch.empty((n, cols), dtype=logits.dtype, device=logits.device), cols
+        return _new(n, cols, logits.dtype, logits.device), cols
     if out is logits:
         return out, ld
     return out, _matrix(out, "out", logits.device, logits.dtype, n, cols)
@@ -327,15 +332,16 @@ def _summed_tensor(x, residual, summed, rows, cols, device):
         return None, 0, None, 0
     ldr = _matrix(residual, "residual", device, x.dtype, rows, cols)
     if summed is None:
-        return residual.data_ptr(), ldr, torch.empty((rows, cols), dtype=x.dtype, device=device), cols
+        return residual.data_ptr(), ldr, _new(rows, cols, x.dtype, device), cols
     return residual.data_ptr(), ldr, summed, _matrix(summed, "summed", device, x.dtype, rows, cols)
 
 
 def _fp8_rows(rows, cols, device):
     """A new 8-bit matrix whose rows begin at multiples of 16 bytes -> (tensor, row stride)."""
     ld = (cols + 15) // 16 * 16
-    t = torch.empty((rows, ld), dtype=FP8, device=device)
-    return (t if ld == cols else t.as_strided((rows, cols), (ld, 1))), ld
+    if ld == cols:
+        return _new(rows, cols, FP8, device), ld
+    return _new(rows, ld, FP8, device).as_strided((rows, cols), (ld, 1)), ld
 
 
 @_stream_arg
@@ -351,7 +357,7 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, out=None, summed=None, wit
     wdt = _norm_weight(weight, "weight", dtype, dev, None, cols)
     res, ldr, s, lds = _summed_tensor(x, residual, summed, rows, cols, dev)
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        out = _new(rows, cols, dtype, dev)
         ldy = cols
     else:
         ldy = _matrix(out, "out", dev, dtype, rows, cols)
@@ -373,7 +379,7 @@ def rms_norm_fp8(x, weight=None, residual=None, eps=1e-6, summed=None, *, stream
     res, ldr, s, lds = _summed_tensor(x, residual, summed, rows, cols, dev)
     y, ldy = _fp8_rows(rows, cols, dev)
     blocks = (cols + SCALE_BLOCK - 1) // SCALE_BLOCK
-    scale = torch.empty((rows, blocks), dtype=torch.float32, device=dev)
+    scale = _new(rows, blocks, torch.float32, dev)
     _launch(draft_call().vpa_rms_norm_fp8, stream, dev, x.data_ptr(), ldx, code, res, ldr,
             _vp(weight), VPA_F32 if wdt is torch.float32 else code, rows, cols, eps, _vp(s), lds,
             y.data_ptr(), ldy, scale.data_ptr(), blocks)
@@ -399,7 +405,7 @@ def rms_norm_backward(grad, summed, rstd, weight=None, grad_summed=None, need_x=
         raise ValueError("out is grad_x's tensor: it goes with need_x")
     gx, ldgx = None, 0
     if need_x:
-        gx, ldgx = ((torch.empty((rows, cols), dtype=dt, device=dev), cols) if out is None
+        gx, ldgx = ((_new(rows, cols, dt, dev), cols) if out is None
                     else (out, _matrix(out, "out", dev, dt, rows, cols)))
     gw = torch.empty(cols, dtype=wdt, device=dev) if need_weight else None
     fn = draft_call().vpa_rms_norm_backward
@@ -422,8 +428,7 @@ def quantize_fp8(x, block_rows=1, *, stream=None):
     dev = x.device
     y, ldy = _fp8_rows(rows, cols, dev)
     blocks = (cols + SCALE_BLOCK - 1) // SCALE_BLOCK
-    scale = torch.empty(((rows + block_rows - 1) // block_rows, blocks), dtype=torch.float32,
-                        device=dev)
+    scale = _new((rows + block_rows - 1) // block_rows, blocks, torch.float32, dev)
     _launch(draft_call().vpa_quantize_fp8, stream, dev, x.data_ptr(), ldx, code, rows, cols,
             block_rows, y.data_ptr(), ldy, scale.data_ptr(), blocks)
     return y, scale
@@ -466,7 +471,7 @@ def head_linear_fp8(x, x_scale, weight, weight_scale, bias=None, activation="non
         _out_tensor(bias, "bias", torch.bfloat16, outer, dev)
     ldr = 0 if residual is None else _matrix(residual, "residual", dev, torch.bfloat16, rows, outer)
     if out is None:
-        out = torch.empty((rows, outer), dtype=out_dtype or torch.bfloat16, device=dev)
+        out = _new(rows, outer, out_dtype or torch.bfloat16, dev)
         ldy = outer
     else:
         if out_dtype is not None and out.dtype is not out_dtype:
