@@ -182,16 +182,20 @@ __device__ __forceinline__ void mask_named(u32x4_t (&w)[U], int c0, int32_t id) 
         });
 }
 
-// How the loss's launch is cut: segments of whole chunks of `vecs` vectors a thread.
+// How the loss's launch is cut: segments of whole chunks.
 struct Cut {
-    int32_t vecs, segments, chunks;
+    int32_t segments, chunks;
 };
 
-// A workgroup a segment of a row; with one segment, the whole of it.
-template <int ESIZE, int U>
+// A workgroup a segment of a row; with one segment, the whole of it.  A chunk is 2
+// vectors a thread (2048 x 50257 bf16 40.8 us, with 1 40.9, 4 41.5, 8 46.3; 8192 x
+// 16000 57, 61, 58, 77; 64 x 151936 11.2, 11.6, 11.2, 12.1).
+constexpr int kScanVecs = 2;
+
+template <int ESIZE>
 __global__ __launch_bounds__(kThreads) void distill_kernel(DistillTask t, Cut cut, ExpSum* sums) {
     using T = typename elem<ESIZE>::type;
-    using Scan = SegmentScan<ESIZE, U, kThreads, false>;
+    using Scan = SegmentScan<ESIZE, kScanVecs, kThreads, false>;
     __shared__ ExpSum lds[kWaves];
     const int64_t row = blockIdx.x / cut.segments;
     const int32_t seg = blockIdx.x % cut.segments;
@@ -203,8 +207,8 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillTask t, Cut cu
     const int end = begin + cut.chunks * Scan::CHUNK;
     const int lo = begin < 0 ? 0 : begin, hi = end < t.vocab ? end : t.vocab;
     Scan scan;
-    scan.run(x, begin, lo, hi, scale, kLag, [&](u32x4_t (&w)[U], int c0) {
-        mask_named<ESIZE, U, kThreads>(w, c0, id);
+    scan.run(x, begin, lo, hi, scale, kLag, [&](u32x4_t (&w)[kScanVecs], int c0) {
+        mask_named<ESIZE, kScanVecs, kThreads>(w, c0, id);
     });
     const ExpSum s = scan.wave();
     if ((threadIdx.x & 63) == 0)
@@ -431,14 +435,14 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillTask t) {
         from_f32(d[n.id], own);
 }
 
-// Chunks of 8 vectors a thread where that gives every CU 4 workgroups, else of 2;
-// segments of whole chunks until there are 4 (8) workgroups a CU.
+// Segments of whole chunks until there are 8 workgroups a CU (64 x 151936 bf16 11.2
+// us, with 4 a CU 11.9, with 16 11.5); whole rows where those alone are 4 a CU (1024
+// x 200064 fp32 123 us, in two segments 130; the launch that joins them is saved).
 Cut distill_cut(int esize, int64_t vocab, int64_t n_rows) {
     Cut c;
-    const int64_t vec = 16 / esize, width = vocab + vec - 1, big = kThreads * 8 * vec;
-    c.vecs = 2 * width > big && n_rows * ((width + big - 1) / big) >= 1024 ? 8 : 2;
-    const int64_t chunk = kThreads * c.vecs * vec, chunks = (width + chunk - 1) / chunk;
-    int64_t want = ((c.vecs == 8 ? 1024 : 2048) + n_rows - 1) / n_rows;
+    const int64_t vec = 16 / esize, width = vocab + vec - 1;
+    const int64_t chunk = kThreads * kScanVecs * vec, chunks = (width + chunk - 1) / chunk;
+    int64_t want = n_rows >= 1024 ? 1 : (2048 + n_rows - 1) / n_rows;
     want = want > chunks ? chunks : want;
     want = want > kMostSegments ? kMostSegments : want;
     c.chunks = (int32_t)((chunks + want - 1) / want);
@@ -461,12 +465,15 @@ RowForm row_form(int esize, int64_t vocab) {
     return {0, 0};
 }
 
-// Whether a call takes its rows whole.  Rows that fill a CU's registers alone
-// need enough of them to be worth it.
+// Whether a call takes its rows whole: up to 64 KB (32 x 28000 bf16 10.4 us, in two
+// launches 12.1; 8 x 1000 8.3 and 11.0; 8192 x 16000 105 and 178).  Longer ones leave
+// most of the chip idle where they are few: from 64 rows on with 512 threads (50257
+// columns, 16 rows 13.7 and 12.2, 64 14.6 and 15.3, 2048 90 and 121), from 128 on
+// with 1024 (151936 columns, 64 rows 31.7 and 19.0, 128 33.3 and 32.7, 256 42.8 and
+// 51.1, 1024 163 and 168; 100000 columns, 96 rows 21.2 and 19.1, 128 21.5 and 22.4).
 bool rows_whole(RowForm f, int64_t n_rows) {
-    return f.threads != 0 && (f.threads < 1024 || n_rows >= 128);
+    return f.threads != 0 && (f.threads * f.vectors <= 4096 || n_rows >= f.threads / 8);
 }
-
 
 size_t sums_bytes(const Cut& c, int64_t n_rows) {
     return c.segments == 1 ? 0 : (size_t)n_rows * c.segments * sizeof(ExpSum);
@@ -499,9 +506,7 @@ hipError_t launch_loss(const DistillTask& t, void* ws, hipStream_t stream) {
     const Cut c = distill_cut(ESIZE, t.vocab, t.n_rows);
     const dim3 grid((uint32_t)((int64_t)t.n_rows * c.segments)), block(kThreads);
     ExpSum* sums = (ExpSum*)ws;
-    const hipError_t e =
-        c.vecs == 8 ? launch(distill_kernel<ESIZE, 8>, grid, block, 0, stream, t, c, sums)
-                    : launch(distill_kernel<ESIZE, 2>, grid, block, 0, stream, t, c, sums);
+    const hipError_t e = launch(distill_kernel<ESIZE>, grid, block, 0, stream, t, c, sums);
     if (e != hipSuccess || c.segments == 1)
         return e;
     return launch(distill_finish_kernel<ESIZE>, dim3((uint32_t)t.n_rows), dim3(64), 0, stream, t, c,

@@ -203,8 +203,8 @@ vpa_status vpa_sampled_verify(const void* logits, vpa_dtype dtype, int64_t ld, v
         return fail(VPA_ERR_INVALID, "temperature not 4-byte aligned");
     const SampleCut c = sample_cut(esize_of(dt), v.vocab, n_req, k);
     if ((st = check_dispatch(sample_threads(c, n_req, k), call)) != VPA_OK ||
-        (st = check_workspace(call, workspace, workspace_bytes, sample_workspace(c, n_req, k))) !=
-            VPA_OK)
+        (st = check_workspace(call, workspace, workspace_bytes,
+                              vpa_sampled_verify_workspace(v, n_req, k))) != VPA_OK)
         return st;
     SampleTask t{};
     t.logits = logits;

@@ -528,12 +528,19 @@ hipError_t launch_rms(int esize, const RmsTask& t, hipStream_t stream) {
                         : launch_rms_typed<uint16_t, uint16_t>(t, stream);
 }
 
-// Workgroups of the backward pass, each of which leaves a row of sums: 2 a CU, for
-// long rows slices of 64 rows.
+// Workgroups of the backward pass, each of which leaves a row of sums: 2 a CU (8192 x
+// 4096 bf16 53 us, with 1 52, with 4 61); up to 4 of those with one vector a lane,
+// as long as each has 16 rows (16384 x 1600 45 us, with 2 50; 8192 x 1024 fp32, 512
+// of them, 29, with 4 32) or, where they leave half of the lanes idle, 8 (8192 x 513
+// 24, with 2 33).  For long rows slices of 64 rows.
 int32_t rms_splits(int esize, int64_t rows, int64_t cols) {
     const NormForm form = norm_form(esize, cols, true);
     int64_t s = form.waves == 0 ? (rows + 63) / 64 : form.waves == 1 ? (rows + 3) / 4 : rows;
-    const int64_t most = form.waves == 0 ? 64 : 512;
+    int64_t most = form.waves == 0 ? 64 : 512;
+    if (form.nv == 1) {
+        const int64_t each = rows / (cols * esize <= form.threads() * 8 ? 8 : 16);
+        most = each > 1024 ? 1024 : each > most ? each : most;
+    }
     s = s > most ? most : s;
     return (int32_t)(s < 1 ? 1 : s);
 }

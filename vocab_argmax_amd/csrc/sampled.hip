@@ -115,12 +115,16 @@ __device__ __forceinline__ bool is_draft(const SampleTask& t, int32_t id) {
     return id >= 0 && id < t.vocab;
 }
 
-// A workgroup a segment of a row.
-template <int ESIZE, int U>
+// A workgroup a segment of a row.  A chunk is 2 vectors a thread: 170 x 6 x 200064
+// bf16 110 us for the whole call, 117 with 8 and 108-117 with 1; 64 x 4 x 151936 37,
+// 39 and 42; 24 x 4 x 32000 14.5, 17.3 and 15.0.
+constexpr int kRowVecs = 2;
+
+template <int ESIZE>
 __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleTask t, SampleCut cut,
                                                                RowStat* stats) {
     using T = typename elem<ESIZE>::type;
-    using Scan = SegmentScan<ESIZE, U, kThreads, true>;
+    using Scan = SegmentScan<ESIZE, kRowVecs, kThreads, true>;
     __shared__ ExpSum lds_s[kWaves];
     __shared__ uint64_t lds_o[kWaves];
     const int32_t row = blockIdx.x / cut.row_segments, seg = blockIdx.x % cut.row_segments;
@@ -585,24 +589,16 @@ Layout layout_of(const SampleCut& c, int64_t n_req, int32_t k) {
 
 }  // namespace
 
-// Rows in chunks of 8 vectors a thread where that gives every CU 4 workgroups, of
-// 4 where that does, else of 2, and segments of whole chunks until there are 4
-// workgroups a CU (8 of the smaller ones).
+// Rows in segments of whole chunks until there are 4 workgroups a CU (65 x 4 x
+// 151936: 40.7 us with 4, 42.5 with 8, 41.1 with 16; 24 x 4 23.5, 23.7, 27.3).
 // A drawn row has a wavefront for each block of columns, 16 workgroups a CU at
-// most over all requests.
+// most over all requests (64 x 4 x 151936: 43.0 us with 8, 38.6 with 16, 38.2 with 32).
 SampleCut sample_cut(int esize, int64_t vocab, int64_t n_req, int32_t k) {
     SampleCut c;
     const int64_t rows = n_req * (k + 1), vec = 16 / esize;
     const int64_t width = vocab + vec - 1;         // with the columns before an aligned one
-    c.vecs = 8;
-    while (c.vecs > 2) {
-        const int64_t cols = kThreads * c.vecs * vec;
-        if (2 * width > cols && rows * ((width + cols - 1) / cols) >= 1024)
-            break;
-        c.vecs /= 2;
-    }
-    const int64_t chunk = kThreads * c.vecs * vec, chunks = (width + chunk - 1) / chunk;
-    int64_t want = ((c.vecs == 8 ? 1024 : 2048) + rows - 1) / rows;
+    const int64_t chunk = kThreads * kRowVecs * vec, chunks = (width + chunk - 1) / chunk;
+    int64_t want = (1024 + rows - 1) / rows;
     want = want > chunks ? chunks : want;
     want = want > kMostSegments ? kMostSegments : want;
     c.row_chunks = (int32_t)((chunks + want - 1) / want);
@@ -634,11 +630,8 @@ hipError_t launch_typed(const SampleTask& t, void* ws, hipStream_t stream) {
     DrawSum* sums = (DrawSum*)((char*)ws + l.sums);
     const dim3 rows((uint32_t)((int64_t)t.n_req * (t.k + 1) * c.row_segments));
     const dim3 groups((uint32_t)((int64_t)t.n_req * c.draw_groups)), reqs((uint32_t)t.n_req);
-    const auto kernel = c.vecs == 8   ? sample_rows_kernel<ESIZE, 8>
-                        : c.vecs == 4 ? sample_rows_kernel<ESIZE, 4>
-                                      : sample_rows_kernel<ESIZE, 2>;
-    hipError_t e = launch(kernel, rows, dim3(kThreads), 0, stream, t, c, stats);
     const dim3 block(kThreads);
+    hipError_t e = launch(sample_rows_kernel<ESIZE>, rows, block, 0, stream, t, c, stats);
     if (e == hipSuccess && t.n_req <= kAcceptInSums) {
         e = launch(sample_sums_kernel<ESIZE, QSIZE, kAccept>, groups, block, 0, stream, t, c, stats,
                    draws, sums);

@@ -29,11 +29,11 @@ struct SampleTask {
     int32_t* num_sampled;
     int32_t* num_rejected;
 };
-// How the launches are cut: segments of a row of logits for its statistics, in
-// chunks of `vecs` 16-byte vectors a thread; blocks of columns of the row that a
-// request draws from, and workgroups that share them.
+// How the launches are cut: segments of a row of logits for its statistics, of
+// whole chunks; blocks of columns of the row that a request draws from, and
+// workgroups that share them.
 struct SampleCut {
-    int32_t vecs, row_segments, row_chunks;
+    int32_t row_segments, row_chunks;
     int32_t draw_blocks, draw_groups;
 };
 SampleCut sample_cut(int esize, int64_t vocab, int64_t n_req, int32_t k);
