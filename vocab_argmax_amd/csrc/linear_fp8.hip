@@ -123,6 +123,132 @@ struct ScaleLoader {
     }
 };
 
+// What a wavefront of the tile kernel adds to its results: a pass is 32 rows of 64
+// columns, 8 columns of a row a lane, and is loaded while the one before is stored.
+// (4096^3 with a residual 77 us; 92 with store_block, whose passes are 16 rows,
+// and that waits 8 times for memory where this does 4 times: 2048 x 2048 x 8192 44
+// and 60.)
+struct ResidualAhead {
+    u32x4_t v[4];
+    const uint16_t* p;
+    int64_t ld, rows;
+    bool any;
+    // rows m0 and on, columns n0 and on; `none`: sums of a slice take no residual
+    __device__ __forceinline__ void init(const GemmTask& t, int64_t m0, int64_t n0, bool none) {
+        const int lane = threadIdx.x & 63;
+        const int64_t n = n0 + (lane & 7) * 8, m = m0 + (lane >> 3);
+        any = t.residual && !none && n + 8 <= t.n;
+        ld = t.ldr;
+        rows = t.m - m;
+        p = (const uint16_t*)t.residual + m * ld + n;
+    }
+    __device__ __forceinline__ void fetch(int pass) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t row = pass * 32 + k * 8;
+            v[k] = u32x4_t{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};   // -0
+            if (any && row < rows)
+                v[k] = ((const Loose16*)(p + row * ld))->v;
+        }
+    }
+};
+
+// 8 finished results of a row.
+__device__ __forceinline__ void store8(const GemmTask& t, int64_t m, int64_t n, f32x4 (&v)[2],
+                                       u32x4_t res) {
+    if (t.bias)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            v[h] += load4((const uint16_t*)t.bias + n + h * 4);
+    const auto each = [&](auto a) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            v[h] = act4<a()>(v[h]);
+    };
+    using std::integral_constant;
+    if (t.act == VPA_ACT_RELU)
+        each(integral_constant<int, VPA_ACT_RELU>{});
+    else if (t.act == VPA_ACT_GELU)
+        each(integral_constant<int, VPA_ACT_GELU>{});
+    else if (t.act == VPA_ACT_SILU)
+        each(integral_constant<int, VPA_ACT_SILU>{});
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e / 4][e % 4] += vec_elem<2>(res, e);
+    if (t.out_f32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            store4((float*)t.y + m * t.ldy + n + h * 4, v[h]);
+        return;
+    }
+    const u32x4_t o = {pack_bf16(v[0][0], v[0][1]), pack_bf16(v[0][2], v[0][3]),
+                       pack_bf16(v[1][0], v[1][1]), pack_bf16(v[1][2], v[1][3])};
+    __builtin_nontemporal_store(o, &((Loose16*)((uint16_t*)t.y + m * t.ldy + n))->v);
+}
+
+// store_block with 8 results of a row a lane: block `block` of those that a
+// wavefront stores one below the other, the first at row m0.
+__device__ __forceinline__ void store_block8(const GemmTask& t, float* part, char* lds, int64_t m0,
+                                             int64_t n0, int block, int blocks,
+                                             const f32x4 (&acc)[4][4], ResidualAhead& res) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = i * 16 + (lane & 15), c = j * 4 + (lane >> 4);
+            *(f32x4*)(lds + r * 256 + ((c ^ (r & 15)) << 4)) = acc[i][j];
+        }
+    // the wavefront's own LDS, in order (see store_block)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int64_t n = n0 + (lane & 7) * 8;
+    const int left = t.n - n < 8 ? (int)(t.n - n) : 8;          // results of this lane, or < 1
+    if (n0 >= t.n)
+        return;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        u32x4_t now[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            now[k] = res.v[k];
+        const int pass = block * 2 + half;
+        if (pass + 1 < blocks * 2)
+            res.fetch(pass + 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = half * 32 + k * 8 + (lane >> 3), c = (lane & 7) * 2;
+            const int64_t m = m0 + block * 64 + r;
+            f32x4 v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                v[h] = *(const f32x4*)(lds + r * 256 + (((c + h) ^ (r & 15)) << 4));
+            if (m >= t.m)
+                continue;
+            float* p = part ? part + m * t.n + n : nullptr;
+            if (left == 8) {
+                if (part) {
+                    keep4(p, v[0]);
+                    keep4(p + 4, v[1]);
+                } else {
+                    store8(t, m, n, v, now[k]);
+                }
+                continue;
+            }
+            // the lane that n ends in: its results once more, one by one
+#pragma unroll 1
+            for (int e = 0; e < left; ++e) {
+                const float one = *(const float*)(lds + r * 256 +
+                                                  (((c + e / 4) ^ (r & 15)) << 4) + e % 4 * 4);
+                if (part)
+                    p[e] = one;
+                else
+                    store_result<uint16_t>(t, m, n + e, one);
+            }
+        }
+    }
+}
+
 // WM x WN wavefronts, each with BM/WM x BN/WN of the tile in its accumulators.
 // With part set, the raw sums of a slice of k go to part[slice][m][n].
 //
@@ -316,8 +442,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
             __builtin_amdgcn_sched_barrier(0);
         }
     }
+    ResidualAhead res;
+    res.init(t, m0 + wm, n0 + wn, part != nullptr);
+    res.fetch(0);
     finish();
-    stage_barrier();
+    bare_barrier();                                // this stage's fragments have been read
     if (part)
         part += slice * t.m * t.n;
     constexpr int SLOTS = (LA::BYTES + LB::BYTES) / 16384;     // wavefronts' blocks in one buffer
@@ -330,7 +459,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 block[i][j] = acc[h * 4 + i][j];
-        store_block<uint16_t>(t, part, mine, m0 + wm + h * 64, n0 + wn, block);
+        store_block8(t, part, mine, m0 + wm, n0 + wn, h, IM / 4, block, res);
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
     }

@@ -74,36 +74,34 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
     return lane63_f64(wave_scan_f64(v));
 }
 
-// 2^(d scale), where d scale lies in [-1000, 1000]: 2^n (1 + f q(f)) with n the
-// nearest whole number, which 1.5 2^52 leaves in the last bits of a sum, and q the
-// interpolation of (2^f - 1) / f at the 9 Chebyshev nodes of [-1/2, 1/2], off by
-// 4e-14 at most.
-__device__ __forceinline__ double exp2_f64(double d, double scale) {
-    constexpr double kWhole = 0x1.8p52;
-    const double t = __builtin_fma(d, scale, kWhole);
-    const double f = __builtin_fma(d, scale, -(t - kWhole));
-    double q = 0x1.b63880a30e9ffp-24;
-    q = __builtin_fma(q, f, 0x1.63d136366db24p-20);
-    q = __builtin_fma(q, f, 0x1.ffcb9515a8016p-17);
-    q = __builtin_fma(q, f, 0x1.4308ac85aa947p-13);
-    q = __builtin_fma(q, f, 0x1.5d87fe86fe88ep-10);
-    q = __builtin_fma(q, f, 0x1.3b2ab7181b755p-7);
-    q = __builtin_fma(q, f, 0x1.c6b08d7047e52p-5);
-    q = __builtin_fma(q, f, 0x1.ebfbdff823cedp-3);
-    q = __builtin_fma(q, f, 0x1.62e42fefa39efp-1);
-    const uint64_t bits = __builtin_bit_cast(uint64_t, __builtin_fma(q, f, 1.0));
-    const uint32_t n = (uint32_t)__builtin_bit_cast(uint64_t, t);
-    return __builtin_bit_cast(double, bits + ((uint64_t)(n << 20) << 32));
-}
-
-// The logit below which 2^((x - m) scale) is 0 (2^-1000 and less).
-__device__ __forceinline__ float least_of(double m, double scale) {
-    const double far = m - 1000.0 / scale;
-    return far > -3e38 ? (float)far : -__FLT_MAX__;
-}
-__device__ __forceinline__ double exp2_f64_of(float x, float m, double scale) {
-    return x >= least_of((double)m, scale) ? exp2_f64((double)x - (double)m, scale) : 0.0;
-}
+// 2^((x - m) scale) as 2^n (1 + f q(f)): n the nearest whole number, which 1.5 2^52
+// leaves in the last bits of a sum, and q the interpolation of (2^f - 1) / f at the
+// 9 Chebyshev nodes of [-1/2, 1/2], off by 4e-14 at most.  From `least` down (and
+// for -inf) x is taken for one whose power is below every number.
+struct Power {
+    double m, scale, least, top;
+    __device__ __forceinline__ Power(double m_, double scale_)
+        : m(m_), scale(scale_), least(-1100.0 / scale_), top(0x1.b63880a30e9ffp-24) {
+        asm("" : "+v"(top));                       // in registers, not moved there each time
+    }
+    __device__ __forceinline__ double of(float x) const {
+        constexpr double kWhole = 0x1.8p52;
+        // (one multiply-add of x scale - m scale loses every digit where m is 1e30)
+        const double d = fmax((double)x - m, least);
+        const double t = __builtin_fma(d, scale, kWhole);
+        const double f = __builtin_fma(d, scale, -(t - kWhole));
+        double q = __builtin_fma(top, f, 0x1.63d136366db24p-20);
+        q = __builtin_fma(q, f, 0x1.ffcb9515a8016p-17);
+        q = __builtin_fma(q, f, 0x1.4308ac85aa947p-13);
+        q = __builtin_fma(q, f, 0x1.5d87fe86fe88ep-10);
+        q = __builtin_fma(q, f, 0x1.3b2ab7181b755p-7);
+        q = __builtin_fma(q, f, 0x1.c6b08d7047e52p-5);
+        q = __builtin_fma(q, f, 0x1.ebfbdff823cedp-3);
+        q = __builtin_fma(q, f, 0x1.62e42fefa39efp-1);
+        return __builtin_amdgcn_ldexp(__builtin_fma(q, f, 1.0),
+                                      (int)__builtin_bit_cast(uint64_t, t));
+    }
+};
 
 __device__ __forceinline__ float temperature_of(const SampleTask& t, int32_t req) {
     return t.temperature ? t.temperature[req] : 1.0f;
@@ -218,7 +216,7 @@ __device__ __forceinline__ Draw accept_request(const SampleTask& t, const Sample
                 if (greedy)
                     p = id == id_of(order) ? 1.0 : 0.0;
                 else
-                    p = exp2_f64_of(x, sum.m, d.scale) / (double)sum.s;
+                    p = Power((double)sum.m, d.scale).of(x) / (double)sum.s;
                 last = !((double)u * (double)q < p);
                 d.q_row = q_row;
                 d.kind = t.probs ? kMinus : kWithout;
@@ -269,18 +267,15 @@ struct Weights {
     using Q = typename elem<QSIZE>::type;
     const T* x;
     const Q* q;
-    double scale, m;           // e = 2^((x - m) scale)
-    float least;               // logits below it have e = 0 (2^-1000 and less)
+    Power e;
     double z;
     int32_t id, kind;
 
-    __device__ __forceinline__ Weights(const SampleTask& t, const Draw& d, int32_t k, double sum) {
+    __device__ __forceinline__ Weights(const SampleTask& t, const Draw& d, int32_t k, double sum)
+        : e((double)d.m, d.scale) {
         kind = KIND == kAny ? k : KIND;
         x = (const T*)t.logits + (int64_t)d.row * t.ld;
         q = (const Q*)t.probs + (int64_t)d.q_row * t.ldq;
-        scale = d.scale;
-        m = (double)d.m;
-        least = least_of(m, scale);
         z = sum;
         id = d.id;
     }
@@ -316,10 +311,7 @@ struct Weights {
     __device__ __forceinline__ void of(int c, const Columns<N>& o, double (&w)[N]) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            // (one multiply-add of x scale - m scale loses every digit where m is 1e30)
-            const float v = to_f32(o.x.v[i]);
-            w[i] = exp2_f64((double)v - m, scale);
-            w[i] = v >= least ? w[i] : 0.0;
+            w[i] = e.of(to_f32(o.x.v[i]));
             if (kind == kMinus)
                 w[i] = fmax(__builtin_fma(-(double)to_f32(o.q.v[i]), z, w[i]), 0.0);
             if (kind == kWithout)
@@ -371,12 +363,13 @@ __global__ __launch_bounds__(kThreads) void sample_accept_kernel(SampleTask t, S
 // distribution, whose weights are summed by a second launch (kSecond).  With
 // kAccept each of a request's workgroups makes its acceptance tests, and the
 // first writes what they say: up to 64 requests that costs less than a launch
-// (1 x 5 x 151936 19.3 us with a launch of its own, 16.2 so; 24 x 4 31.2 and
-// 29.2), for more of them more (170 x 6 x 200064 138 and 145).
+// (1 x 5 x 151936 15.2 us with a launch of its own, 13.2 so; 24 x 4 25.4 and 24.0;
+// 64 x 4 38.9 and 38.6), for more of them more (170 x 6 x 200064 112 and 118).
 //
-// Bound by the 64-bit instructions, 16 an element, which take 8 clocks of a SIMD
-// each here: 33 us for 170 x 200064 bf16, whose loads take 14.  (The next block's
-// loads ahead of a block's sums made it no faster.)
+// Bound by instructions: 18 an element for e, 24 for e - q Z, most of them 64-bit
+// ones, of 5 clocks of a SIMD each: for 170 x 200064 bf16 20 and 27 us of 30 and
+// 32 (the loads alone take 14 and 28).  The next block's loads ahead of a block's
+// sums made it no faster.
 enum SumsStep { kAccept, kFirst, kSecond };
 constexpr int64_t kAcceptInSums = 64;
 
