@@ -467,7 +467,13 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
 
 // Few rows of x (BM = 32 or 64): bound by reading W, so the tile is 64 rows of W by
 // all of x's, with STAGES - 1 stages on their way (as in the 16-bit products).
-// Products are exact: the matrix cores and the widening have time to spare.
+// Products are exact: the matrix cores and the widening have time to spare (with
+// the 8-bit instruction 64 x 4096 x 11008 took 24 us for 26).
+//
+// Workgroups on a CU beside one another hide more than stages on their way: 32 x
+// 2048 x 151936 62 us (5.1 TB/s) with 4 stages, 3 workgroups a CU, and 73 with 6,
+// two; 64 x 2048 x 151936 79 with 2, 84 with 3, 93 with 4.  64 rows keep 4 stages
+// where no CU gets a second workgroup (64 x 4096 x 4096 13.4 us, with 3 14.0).
 template <int BM, int STAGES>
 __global__ __launch_bounds__(256) void fp8_few_rows_kernel(Fp8Task f, int64_t stages_per_slice,
                                                            float* part) {
@@ -690,10 +696,10 @@ hipError_t launch_planned(const Fp8Task& f, const GemmPlan& p, hipStream_t strea
     if (p.tile <= 64) {
         const dim3 grid((uint32_t)((f.g.n + kFewRowsCols - 1) / kFewRowsCols), (uint32_t)p.slices);
         float* part = p.slices > 1 ? (float*)f.g.ws : nullptr;
-        e = p.tile == 32 ? launch(fp8_few_rows_kernel<32, 6>, grid, dim3(256), 0, stream, f,
-                                  p.stages_per_slice, part)
-                         : launch(fp8_few_rows_kernel<64, 4>, grid, dim3(256), 0, stream, f,
-                                  p.stages_per_slice, part);
+        const auto kernel = p.tile == 32               ? fp8_few_rows_kernel<32, 4>
+                            : grid.x * grid.y > 256u ? fp8_few_rows_kernel<64, 2>
+                                                     : fp8_few_rows_kernel<64, 4>;
+        e = launch(kernel, grid, dim3(256), 0, stream, f, p.stages_per_slice, part);
     } else if (f.exact) {
         e = launch_tile<true, 128, 2, 2>(f, p, stream);
     } else {
