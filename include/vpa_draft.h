@@ -152,8 +152,8 @@ vpa_status vpa_distill_loss_and_grad(const void* logits, vpa_dtype dtype, int64_
  * Root-mean-square norm
  *
  * s = x + residual, rounded to x's type (s = x without a residual);
- * y = s rstd w, rstd = 1 / sqrt(mean of s^2 over the row + eps).  The weight is
- * optional.  1 <= cols < 2^31, fewer than 2^22 rows of those that a workgroup's
+ * y = s rstd w, rstd = 1 / sqrt(mean of s^2 over the row + eps).  The squares are
+ * summed in fp32 (past 1e19 they overflow: rstd is 0).  The weight is optional.  1 <= cols < 2^31, fewer than 2^22 rows of those that a workgroup's
  * registers do not hold (past 16384 bf16 or 8192 fp32 columns; in the backward
  * pass 8192 of either).
  * ------------------------------------------------------------------------ */
@@ -188,7 +188,8 @@ size_t vpa_rms_norm_backward_workspace(int64_t rows, int64_t cols);
  *   grad_x      = grad_summed + rstd (u - xh mean(u xh))   [rows][cols]
  *   grad_weight = sum over rows of grad * xh               [cols], type wdtype
  * grad_x is the gradient of x and of the residual.  Either output may be NULL;
- * grad_x may be grad or grad_summed (same pointer and row stride).  rows = 0
+ * grad_x may be grad_summed, or grad where grad_weight is NULL (same pointer and
+ * row stride).  rows = 0
  * clears grad_weight. */
 vpa_status vpa_rms_norm_backward(const void* grad, int64_t ldg, const void* summed, int64_t lds,
                                  vpa_dtype dtype, const void* weight, vpa_dtype wdtype,

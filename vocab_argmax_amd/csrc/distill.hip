@@ -187,7 +187,8 @@ struct Cut {
     int32_t segments, chunks;
 };
 
-// A workgroup a segment of a row; with one segment, the whole of it.  A chunk is 2
+// A workgroup a segment of a row; with one segment, the whole of it.  Bound by
+// reading: 512 x 50257 fp32 18 us, 1024 x 151936 bf16 54 (5.8-5.9 TB/s).  A chunk is 2
 // vectors a thread (2048 x 50257 bf16 40.8 us, with 1 40.9, 4 41.5, 8 46.3; 8192 x
 // 16000 57, 61, 58, 77; 64 x 151936 11.2, 11.6, 11.2, 12.1).
 constexpr int kScanVecs = 2;
@@ -226,7 +227,8 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillTask t, Cut cu
         sums[blockIdx.x] = all;
 }
 
-// The segments' sums joined; a wavefront a row.
+// The segments' sums joined; a wavefront a row.  Bound by latency, of its loads and
+// of the 64-bit logarithms: 4 us for 512 rows of 4 segments.
 template <int ESIZE>
 __global__ __launch_bounds__(64) void distill_finish_kernel(DistillTask t, Cut cut,
                                                             const ExpSum* sums) {
@@ -299,7 +301,9 @@ constexpr int grad_chunk(int esize) {
 
 // The gradient of one chunk of a row: every column as one that is not named,
 // then the named ones, from logits read before the chunk was written (the
-// gradient may replace the logits).
+// gradient may replace the logits).  A workgroup's stores keep their order, so
+// what the first wavefront stores after the barrier is what stays.  Bound by
+// memory: 1024 x 151936 bf16 107 us, 5.8 TB/s read and written.
 template <int ESIZE>
 __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillTask t, int32_t chunks) {
     using T = typename elem<ESIZE>::type;
@@ -349,7 +353,9 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillTask t, i
 }
 
 // Loss and gradient of a row that a workgroup holds in registers, NV vectors a
-// lane: the logits are read once.
+// lane: the logits are read once.  Bound by memory: 2048 x 50257 bf16 89 us, 4.8
+// TB/s read and written, where a large copy has 4.9; the two passes of rows that
+// are read twice have more bandwidth and a third more bytes (121 us).
 template <int ESIZE, int NV, int THREADS>
 __global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillTask t) {
     using T = typename elem<ESIZE>::type;

@@ -75,7 +75,8 @@ struct __attribute__((packed, aligned(1))) LooseBytes {
 
 // A row in registers: x and the residual of the next one on their way, the weights
 // kept over a workgroup's rows.  With FP8, the 128 columns of a scale lie in 16
-// (bf16) or 32 (fp32) lanes side by side.
+// (bf16) or 32 (fp32) lanes side by side.  Bound by memory: 8192 x 4096 bf16 with
+// a residual 43 us (6.3 TB/s), with y in 8 bits 40 (5.8); 32 rows 4.5, latency.
 template <typename T, typename W, int WAVES, int NV, bool FP8>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_kernel(RmsTask t) {
     using P = RowPart<T, WAVES, NV>;
@@ -167,6 +168,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_kernel(RmsT
 
 // The gradients of a workgroup's rows from one read of grad, s and grad_summed,
 // the weight's in registers until the end (a thread always has the same columns).
+// Bound by memory: 8192 x 4096 bf16 with grad_summed 45 us, 6.2 TB/s.
 template <typename T, typename W, int WAVES, int NV>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_grad_kernel(RmsGradTask t) {
     using P = RowPart<T, WAVES, NV>;
@@ -268,7 +270,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_grad_kernel
 }
 
 // Rows too long for a workgroup's registers: several passes over the row, which the
-// caches hold.
+// caches hold, an element a lane: 4096 x 12288 bf16 backward 284 us, 1.8 TB/s.
 template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void rms_long_kernel(RmsTask t) {
     __shared__ float lds[kLongWaves][2];
@@ -368,7 +370,8 @@ __global__ __launch_bounds__(kThreads) void rms_long_columns_kernel(RmsGradTask 
 }
 
 // The slices' column sums, added in a fixed order: 64 columns a workgroup, 16
-// wavefronts with every sixteenth sum each.
+// wavefronts with every sixteenth sum each.  512 x 4096 sums 4.2 us, a launch and
+// two rounds of loads.
 constexpr int kJoinWaves = 16;
 
 template <typename W>
@@ -395,7 +398,8 @@ __global__ __launch_bounds__(kJoinWaves * 64) void rms_join_kernel(RmsGradTask t
 
 // A matrix as it is in 8 bits.  LANES lanes side by side hold 128 columns of a row,
 // 16 bytes each; a workgroup takes kThreads / LANES rows of one block of columns at
-// a time, or with SQUARE the 128 rows that share a scale, in registers.
+// a time, or with SQUARE the 128 rows that share a scale, in registers.  Bound by
+// memory: 151936 x 2048 bf16 192 us (4.9 TB/s), in blocks of 128 x 128 166 (5.6).
 template <typename T, bool SQUARE>
 __global__ __launch_bounds__(kThreads) void quant_kernel(QuantTask t, int64_t blocks_across) {
     constexpr int VEC = 16 / (int)sizeof(T), LANES = kScaleBlock / VEC;
