@@ -92,6 +92,23 @@ __device__ __forceinline__ f32x4 mma_wide(const Wide& p, const Wide& q) {
     return d;
 }
 
+// A row's 128 bytes as an operand of either product.
+template <bool EXACT>
+struct Operand : Wide {
+    __device__ __forceinline__ explicit Operand(const u32x4_t (&p)[2]) : Wide(p) {}
+};
+template <>
+struct Operand<false> {
+    u32x4_t v[2];
+    __device__ __forceinline__ explicit Operand(const u32x4_t (&p)[2]) : v{p[0], p[1]} {}
+};
+__device__ __forceinline__ f32x4 mma(const Operand<true>& p, const Operand<true>& q) {
+    return mma_wide(p, q);
+}
+__device__ __forceinline__ f32x4 mma(const Operand<false>& p, const Operand<false>& q) {
+    return mma_fast(p.v, q.v);
+}
+
 // Weight scales of a workgroup's columns, one for each block of k: the same in
 // all lanes, read through the scalar cache.
 typedef const float __attribute__((address_space(4))) * scalar_floats;
@@ -262,7 +279,7 @@ __device__ __forceinline__ void store_block8(const GemmTask& t, float* part, cha
 // The 16-bit product of these sizes takes 806 and 104.  The barrier that says that
 // the next stage has landed, and that every wavefront has read this one, stands
 // before the first read from the next.
-template <bool EXACT, int BM, int BN, int WM, int WN>
+template <bool EXACT, int BM, int BN, int WM, int WN, int BUFS>
 __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uint32_t tiles_m,
                                                                uint32_t tiles_n,
                                                                int64_t stages_per_slice,
@@ -273,12 +290,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
     static_assert(BN / WN <= kScaleBlock && kScaleBlock % (BN / WN) == 0, "one scale of W");
     using LA = TileLoader<1, true, true, BM, NT>;
     using LB = TileLoader<1, true, true, BN, NT>;
-    // x's scales, then W's
+    // x's scales, then W's; where stages are counted every wavefront loads some, past
+    // the first of them W's again
     constexpr int SCALES = LA::BYTES + LB::BYTES, XWAVES = BM / 64;
-    constexpr int STAGE = SCALES + (XWAVES + 1) * 256;
+    constexpr int SWAVES = BUFS > 2 ? WM * WN : XWAVES + 1;
+    constexpr int STAGE = (SCALES + SWAVES * 256 + 1023) / 1024 * 1024;
+    constexpr int LOADS = LA::LOADS + LB::LOADS + 1;
     static_assert(XWAVES < WM * WN, "a wavefront for each 64 scales");
-    __shared__ __align__(1024) char lds0[STAGE];
-    __shared__ __align__(1024) char lds1[STAGE];
+    static_assert((BUFS & (BUFS - 1)) == 0, "a mask for stages");
+    __shared__ __align__(1024) char lds[BUFS * STAGE];
     const GemmTask& t = f.g;
     uint32_t slice, tm, tn;
     tile_of_block(blockIdx.x, gridDim.x, tiles_m, tiles_n, slice, tm, tn);
@@ -310,9 +330,24 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
         __builtin_amdgcn_s_setprio(0);
         la.load(da, s, lds);
         lb.load(db, s, lds + LA::BYTES);
-        if (wave <= XWAVES)
+        if (wave < SWAVES)
             ls.load(s, lds + SCALES + wave * 256);
     };
+    const auto buffer = [&](int64_t s) { return lds + ((int)(s - s0) & (BUFS - 1)) * STAGE; };
+    // stage s is in LDS and every wavefront has come here; `more` stages of those
+    // after it may be on their way, if so many there are
+    const auto landed = [&](int64_t s, auto more) {
+        if constexpr (BUFS == 2) {
+            stage_barrier();
+        } else {
+            if (s + more() < s1)
+                wait_loads<more() * LOADS>();
+            else
+                wait_loads<0>();
+            bare_barrier();
+        }
+    };
+    using std::integral_constant;
     u32x4_t av[RING][2], bv[JN][2];
     float sx[RING];
     auto read_a = [&](const char* lds, const typename LA::Place& p, int i) {
@@ -370,40 +405,40 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
     };
     // a stage that k ends in comes first, so that the loop has whole ones only
     if (end > whole) {
-        la.load_tail(whole, t.k, lds1);
-        lb.load_tail(whole, t.k, lds1 + LA::BYTES);
-        if (wave <= XWAVES)
-            ls.load(whole, lds1 + SCALES + wave * 256);
+        la.load_tail(whole, t.k, buffer(s0 + 1));
+        lb.load_tail(whole, t.k, buffer(s0 + 1) + LA::BYTES);
+        if (wave < SWAVES)
+            ls.load(whole, buffer(s0 + 1) + SCALES + wave * 256);
         stage_barrier();
 #pragma unroll
         for (int j = 0; j < JN; ++j)
-            read_b(lds1, pb, j);
+            read_b(buffer(s0 + 1), pb, j);
         widen_b();
 #pragma unroll
         for (int i = 0; i < IM; ++i) {
-            read_a(lds1, pa, i);
-            products(i, *(const float*)(lds1 + wscale_at), nothing);
+            read_a(buffer(s0 + 1), pa, i);
+            products(i, *(const float*)(buffer(s0 + 1) + wscale_at), nothing);
         }
         stage_barrier();
     }
     if (s0 < s1) {
-        stage(s0, lds0);
-        if (s0 + 1 < s1)
-            stage(s0 + 1, lds1);
-        stage_barrier();
+#pragma unroll
+        for (int i = 0; i < BUFS; ++i)
+            if (s0 + i < s1)
+                stage(s0 + i, buffer(s0 + i));
+        landed(s0, integral_constant<int, BUFS - 1>{});
 #pragma unroll
         for (int j = 0; j < JN; ++j)
-            read_b(lds0, pb, j);
+            read_b(buffer(s0), pb, j);
 #pragma unroll
         for (int i = 0; i < RING; ++i)
-            read_a(lds0, pa, i);
+            read_a(buffer(s0), pa, i);
     }
     const bool early = wave < WM * WN / 2;
     // (scalar loads of it would make every wait one for all of LDS's answers)
-    float sw = *(const float*)(lds0 + wscale_at);
+    float sw = *(const float*)(lds + wscale_at);
     for (int64_t s = s0; s + 1 < s1; ++s) {
-        char* now = (s - s0) & 1 ? lds1 : lds0;
-        char* next = (s - s0) & 1 ? lds0 : lds1;
+        char *now = buffer(s), *next = buffer(s + 1);
         float sw_next = 0.0f;
         widen_b();
         const typename LA::Place a = pa.again();
@@ -419,12 +454,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
                 __builtin_amdgcn_s_setprio(1);
             if (i == IM - RING) {
                 // the next stage has landed, and this one has been read
-                stage_barrier();
-                if (early && s + 2 < s1)
-                    stage(s + 2, now);
+                landed(s + 1, integral_constant<int, BUFS - 2>{});
+                if (early && s + BUFS < s1)
+                    stage(s + BUFS, now);
             }
-            if (i == IM - RING + 2 && !early && s + 2 < s1)
-                stage(s + 2, now);
+            if (i == IM - RING + 2 && !early && s + BUFS < s1)
+                stage(s + BUFS, now);
             if (i < IM - RING)
                 read_a(now, a, i + RING);
             else
@@ -436,7 +471,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
         sw = sw_next;
     }
     if (s0 < s1) {
-        const char* now = (s1 - 1 - s0) & 1 ? lds1 : lds0;
+        const char* now = buffer(s1 - 1);
         widen_b();
 #pragma unroll
         for (int i = 0; i < IM; ++i) {
@@ -453,8 +488,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
     bare_barrier();                                // this stage's fragments have been read
     if (part)
         part += slice * t.m * t.n;
-    constexpr int SLOTS = (LA::BYTES + LB::BYTES) / 16384;     // wavefronts' blocks in one buffer
-    char* mine = wave < SLOTS ? lds0 + wave * 16384 : lds1 + (wave - SLOTS) * 16384;
+    static_assert(WM * WN * 16384 <= BUFS * STAGE, "a block of results for each wavefront");
+    char* mine = lds + wave * 16384;
 #pragma unroll
     for (int h = 0; h < IM / 4; ++h) {
         f32x4 block[4][4];
@@ -469,16 +504,17 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
     }
 }
 
-// Few rows of x (BM = 32 or 64): bound by reading W, so the tile is 64 rows of W by
-// all of x's, with STAGES - 1 stages on their way (as in the 16-bit products).
-// Products are exact: the matrix cores and the widening have time to spare (with
-// the 8-bit instruction 64 x 4096 x 11008 took 24 us for 26).
+// Few rows of x: bound by reading W, so the tile is 64 rows of W by 32 or 64 of x,
+// which has as many or (see plan_fp8) a few times those, with STAGES - 1 stages on
+// their way (as in the 16-bit products).  Up to 64 rows products are exact: the
+// matrix cores and the widening have time to spare (with the 8-bit instruction 64 x
+// 4096 x 11008 took 24 us for 26).
 //
 // Workgroups on a CU beside one another hide more than stages on their way: 32 x
 // 2048 x 151936 62 us (5.1 TB/s) with 4 stages, 3 workgroups a CU, and 73 with 6,
 // two; 64 x 2048 x 151936 79 with 2, 84 with 3, 93 with 4.  64 rows keep 4 stages
 // where no CU gets a second workgroup (64 x 4096 x 4096 13.4 us, with 3 14.0).
-template <int BM, int STAGES>
+template <bool EXACT, int BM, int STAGES>
 __global__ __launch_bounds__(256) void fp8_few_rows_kernel(Fp8Task f, int64_t stages_per_slice,
                                                            float* part) {
     constexpr int BN = kFewRowsCols, NT = 256, WAVES = 4;
@@ -493,13 +529,13 @@ __global__ __launch_bounds__(256) void fp8_few_rows_kernel(Fp8Task f, int64_t st
     const GemmTask& t = f.g;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t n0 = (int64_t)blockIdx.x * BN;
+    const int64_t n0 = (int64_t)blockIdx.x * BN, m0 = (int64_t)blockIdx.z * BM;
     LA la;
     LB lb;
-    la.init(t.a, t.a_m, 0, t.m);
+    la.init(t.a, t.a_m, m0, t.m);
     lb.init(t.b, t.b_n, n0, t.n);
     ScaleLoader ls;
-    ls.init(f.a_scale, f.lda_scale, 0, t.m);
+    ls.init(f.a_scale, f.lda_scale, m0, t.m);
     const scalar_floats ws = weight_scales(f, n0);
     const typename LA::Place pa = LA::place(0);
     const typename LB::Place pb = LB::place(wave * 16);
@@ -524,14 +560,14 @@ __global__ __launch_bounds__(256) void fp8_few_rows_kernel(Fp8Task f, int64_t st
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             v[h] = LB::fragment(p + LA::BYTES, pb, 0, h);
-        const Wide w(v);
+        const Operand<EXACT> w(v);
 #pragma unroll
         for (int i = 0; i < IM; ++i) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 v[h] = LA::fragment(p, pa, i, h);
             const float sc = *(const float*)(p + SCALES + wave * 256 + (i * 16 + (lane & 15)) * 4) * sw;
-            const f32x4 d = mma_wide(w, Wide(v));
+            const f32x4 d = mma(w, Operand<EXACT>(v));
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 acc[i][e] = __builtin_fmaf(d[e], sc, acc[i][e]);
@@ -572,8 +608,9 @@ __global__ __launch_bounds__(256) void fp8_few_rows_kernel(Fp8Task f, int64_t st
     __syncthreads();
     constexpr int ACROSS = BN / 4;                  // threads of a row
     const int64_t n = n0 + threadIdx.x % ACROSS * 4;
-    for (int m = threadIdx.x / ACROSS; m < BM && m < t.m; m += NT / ACROSS) {
-        const f32x4 v = *(const f32x4*)(c + m * LD + threadIdx.x % ACROSS * 4);
+    for (int r = threadIdx.x / ACROSS; r < BM && m0 + r < t.m; r += NT / ACROSS) {
+        const int64_t m = m0 + r;
+        const f32x4 v = *(const f32x4*)(c + r * LD + threadIdx.x % ACROSS * 4);
         float* p = part ? part + ((int64_t)blockIdx.y * t.m + m) * t.n + n : nullptr;
         if (n + 4 <= t.n) {
             if (part)
@@ -669,17 +706,39 @@ __global__ __launch_bounds__(WAVES * 64) void fp8_rows_kernel(Fp8Task f) {
     store_result<uint16_t>(t, m, n0 + n, v);
 }
 
-// The plan of a 16-bit product whose rows have as many bytes: stages, tiles and
-// what they cost are alike (of 128-tiles in 1-16 slices and 256-tiles in 1-8 the
-// best one is 0-14 % faster at 15 sizes from 65 to 2048 rows, 17 % at 512 x 8192 x
-// 8192).  Exact products have 128-tiles alone: widening takes the registers of more.
-// They take up to twice the time from 1024 rows on (4096^3 127 us) and a tenth more
-// for 65 to 128 (65 x 4096 x 4096 18.5 and 16.7), the reason for the 8-bit
-// instruction there where the result is rounded to bf16 anyway.
 int64_t as_16_bits(int64_t k) {
     return (k + 1) / 2;
 }
+// A plan of `blocks` tiles, fewer than there are CUs: slices of at least 8 stages
+// until every CU has one.
+GemmPlan plan_a_round(int tile, int64_t blocks, int64_t k) {
+    GemmPlan p{};
+    const int64_t stages = (k + 127) / 128;
+    int64_t s = 256 / blocks;
+    s = s > stages / 8 ? stages / 8 : s;
+    s = s < 1 ? 1 : s;
+    p.tile = tile;
+    p.stages_per_slice = (stages + s - 1) / s;
+    p.slices = (int32_t)((stages + p.stages_per_slice - 1) / p.stages_per_slice);
+    return p;
+}
+// More than 64 rows in 64-tiles while a round of workgroups holds them (128 x 4096 x
+// 4096 15.8 us, in 128-tiles 18.5; 100 x 2048 x 8192 11.8 and 16.5; 256 x 4096 x 4096
+// 19.9 and 22.0; 128 x 8192 x 8192 35.7 and 29.9), then in 128-tiles while a round
+// holds those (512 x 8192 x 8192 61 us, in two slices or two rounds 75; 512 x 4096 x
+// 4096 25.6 in the two slices that fit, 28.7 in one, 26.6 in four).  Else the plan of
+// a 16-bit product whose rows have as many bytes, whose stages, tiles and costs are
+// alike.  Exact products have no 256-tiles: widening takes the registers of more.
+// They take up to twice the time from 1024 rows on (4096^3 122 us, by the 8-bit
+// instruction 64), the reason for it where the result is rounded to bf16 anyway.
 GemmPlan plan_fp8(int64_t m, int64_t n, int64_t k, bool exact) {
+    const auto blocks = [&](int64_t tile) {
+        return ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
+    };
+    if (m > 64 && blocks(64) <= 256)
+        return plan_a_round(64, blocks(64), k);
+    if (m > 64 && blocks(128) <= 256)
+        return plan_a_round(128, blocks(128), k);
     GemmPlan p = plan_gemm(2, m, n, as_16_bits(k), true, true);
     if (exact && !p.rows_kernel && p.tile == 256) {
         p = GemmPlan{};
@@ -689,33 +748,43 @@ GemmPlan plan_fp8(int64_t m, int64_t n, int64_t k, bool exact) {
     }
     return p;
 }
+static_assert(kFewRowsCols == 64, "64-tiles");
 size_t slices_bytes(const GemmPlan& p, int64_t m, int64_t n) {
     return p.slices > 1 ? (size_t)p.slices * (size_t)m * (size_t)n * 4 : 0;
 }
 
-template <bool EXACT, int TILE, int WM, int WN>
+template <bool EXACT, int TILE, int WM, int WN, int BUFS>
 hipError_t launch_tile(const Fp8Task& f, const GemmPlan& p, hipStream_t stream) {
     const uint32_t tm = (uint32_t)((f.g.m + TILE - 1) / TILE);
     const uint32_t tn = (uint32_t)((f.g.n + TILE - 1) / TILE);
-    return launch(fp8_tile_kernel<EXACT, TILE, TILE, WM, WN>, dim3(tm * tn * (uint32_t)p.slices),
+    return launch(fp8_tile_kernel<EXACT, TILE, TILE, WM, WN, BUFS>, dim3(tm * tn * (uint32_t)p.slices),
                   dim3(WM * WN * 64), 0, stream, f, tm, tn, p.stages_per_slice,
                   p.slices > 1 ? (float*)f.g.ws : nullptr);
 }
 
 hipError_t launch_planned(const Fp8Task& f, const GemmPlan& p, hipStream_t stream) {
     hipError_t e;
+    // 128-tiles of which no CU gets a second workgroup have its LDS for 4 stages (512
+    // x 8192 x 8192 61 us, with two 85; 128 x 2048 x 32000 21.8 and 25.8)
+    const bool deep = ((f.g.m + 127) / 128) * ((f.g.n + 127) / 128) * p.slices <= 256;
     if (p.tile <= 64) {
-        const dim3 grid((uint32_t)((f.g.n + kFewRowsCols - 1) / kFewRowsCols), (uint32_t)p.slices);
+        const dim3 grid((uint32_t)((f.g.n + kFewRowsCols - 1) / kFewRowsCols), (uint32_t)p.slices,
+                        (uint32_t)((f.g.m + p.tile - 1) / p.tile));
         float* part = p.slices > 1 ? (float*)f.g.ws : nullptr;
-        const auto kernel = p.tile == 32               ? fp8_few_rows_kernel<32, 4>
-                            : grid.x * grid.y > 256u ? fp8_few_rows_kernel<64, 2>
-                                                     : fp8_few_rows_kernel<64, 4>;
+        const bool one = grid.x * grid.y * grid.z <= 256u;
+        const auto kernel = f.g.m > 64 && !f.exact ? fp8_few_rows_kernel<false, 64, 4>
+                            : p.tile == 32         ? fp8_few_rows_kernel<true, 32, 4>
+                            : one                  ? fp8_few_rows_kernel<true, 64, 4>
+                                                   : fp8_few_rows_kernel<true, 64, 2>;
         e = launch(kernel, grid, dim3(256), 0, stream, f, p.stages_per_slice, part);
     } else if (f.exact) {
-        e = launch_tile<true, 128, 2, 2>(f, p, stream);
+        e = deep ? launch_tile<true, 128, 2, 2, 4>(f, p, stream)
+                 : launch_tile<true, 128, 2, 2, 2>(f, p, stream);
+    } else if (p.tile == 256) {
+        e = launch_tile<false, 256, 2, 4, 2>(f, p, stream);
     } else {
-        e = p.tile == 256 ? launch_tile<false, 256, 2, 4>(f, p, stream)
-                          : launch_tile<false, 128, 2, 2>(f, p, stream);
+        e = deep ? launch_tile<false, 128, 2, 2, 4>(f, p, stream)
+                 : launch_tile<false, 128, 2, 2, 2>(f, p, stream);
     }
     return e != hipSuccess || p.slices == 1 ? e : launch_gemm_join(2, f.g, p.slices, stream);
 }
