@@ -133,15 +133,16 @@ __device__ __forceinline__ void mask_element(u32x4_t& w, int e, int at) {
 }
 
 // z = (x - M) scale as one multiply-add, x scale - b with b = M scale rounded:
-// what the rounding took off is put right on the sum.  Where the products are
-// too large for that (logits of 1e30 and more), `apart` says so.
+// what the rounding took off, 2^-24 of b at most, is put right on the sum.  From
+// 2^20 on, where that would leave a power's range before long (a low temperature,
+// logits of 1e6), `apart` says that the difference comes first.
 struct ScaledFrom {
     float m, b, fix;
     bool apart;
     __device__ __forceinline__ void set(float m_, float scale) {
         m = m_;
         b = m * scale;
-        apart = !(fabsf(b) < 1e30f);
+        apart = !(fabsf(b) < 0x1p20f);
         fix = apart ? 1.0f : exp2_fast(-__builtin_fmaf(m, scale, -b));
     }
 };
