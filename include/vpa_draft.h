@@ -115,7 +115,7 @@ size_t vpa_distill_workspace(vpa_vocab v, int64_t n_rows);
 /*  logits       [n_rows][ld], every shard of a row side by side, ld >= V.
  *  teacher_ids, teacher_logprobs  int32 and float [n_rows][n_top], as
  *               vpa_token_logprobs returns them; 1 <= n_top <= VPA_MAX_TEACHER_TOP.
- *  temperature  finite and > 0.
+ *  temperature  finite, from 2^-100 on.
  *  loss         out, float [n_rows].
  *  row_stats    out, float [n_rows][VPA_DISTILL_STATS], for the backward pass. */
 vpa_status vpa_distill_loss(const void* logits, vpa_dtype dtype, int64_t ld, vpa_vocab v,

@@ -35,9 +35,10 @@ vpa_status check_distill(const char* call, const void* logits, int dt, int64_t l
     if (n_top < 1 || n_top > VPA_MAX_TEACHER_TOP)
         return fail(VPA_ERR_INVALID, "%s: n_top %d outside [1, %d]", call, (int)n_top,
                     VPA_MAX_TEACHER_TOP);
-    if (!(temperature > 0.0f) || !(temperature < INFINITY))
-        return fail(VPA_ERR_INVALID, "%s: temperature %g is not finite and > 0", call,
-                    (double)temperature);
+    // (of less, 1 / t times a difference of logits would leave fp32)
+    if (!(temperature >= 0x1p-100f) || !(temperature < INFINITY))
+        return fail(VPA_ERR_INVALID, "%s: temperature %g is not finite and > 0 (from 2^-100 on)",
+                    call, (double)temperature);
     if (n_rows > 0 && ((st = check_vector("logits", logits, esize_of(dt))) != VPA_OK ||
                        (st = check_vector("teacher_ids", ids, 4)) != VPA_OK ||
                        (st = check_vector("teacher_logprobs", logprobs, 4)) != VPA_OK))
