@@ -142,9 +142,8 @@ struct ScaleLoader {
 
 // What a wavefront of the tile kernel adds to its results: a pass is 32 rows of 64
 // columns, 8 columns of a row a lane, and is loaded while the one before is stored.
-// (4096^3 with a residual 77 us; 92 with store_block, whose passes are 16 rows,
-// and that waits 8 times for memory where this does 4 times: 2048 x 2048 x 8192 44
-// and 60.)
+// (store_block's passes are 16 rows, 8 waits for memory where this has 4: with it
+// 4096^3 with a residual took 92 us and 77 so, 2048 x 2048 x 8192 60 and 44.)
 struct ResidualAhead {
     u32x4_t v[4];
     const uint16_t* p;
@@ -273,10 +272,11 @@ __device__ __forceinline__ void store_block8(const GemmTask& t, float* part, cha
 // and two stages lie in LDS.  A wavefront holds the stage's fragments of W, and of
 // x a ring of 4 that are read 4 products ahead, so that the accumulators, which
 // the scaling keeps in ordinary registers, leave room.
-// 8192^3 515 us, 2130 TFLOP/s, the matrix cores busy half of the clocks: a
-// product's 4 multiply-adds take issue slots beside it, and with them left out the
-// kernel would take a tenth less, without memory's part a fifth.  4096^3 68 us.
-// The 16-bit product of these sizes takes 806 and 104.  The barrier that says that
+// 8192^3 480-490 us, 2240-2290 TFLOP/s, the matrix cores busy half of the clocks: a
+// product's 4 multiply-adds take issue slots beside it (a tenth of the time with
+// everything else left in), and operands come at the rate of LDS and the caches (a
+// fifth).  4096^3 65 us.  The 16-bit product of these sizes takes 790 and 105.
+// The barrier that says that
 // the next stage has landed, and that every wavefront has read this one, stands
 // before the first read from the next.
 template <bool EXACT, int BM, int BN, int WM, int WN, int BUFS>
