@@ -269,7 +269,7 @@ __device__ __forceinline__ void store_block8(const GemmTask& t, float* part, cha
 // With part set, the raw sums of a slice of k go to part[slice][m][n].
 //
 // As in the 16-bit products, a stage is 128 bytes of k, here one block of scales,
-// and two stages lie in LDS.  A wavefront holds the stage's fragments of W, and of
+// and BUFS of them lie in LDS.  A wavefront holds the stage's fragments of W, and of
 // x a ring of 4 that are read 4 products ahead, so that the accumulators, which
 // the scaling keeps in ordinary registers, leave room.
 // 8192^3 480-490 us, 2240-2290 TFLOP/s, the matrix cores busy half of the clocks: a
