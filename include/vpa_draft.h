@@ -171,8 +171,9 @@ vpa_status vpa_rms_norm(const void* x, int64_t ldx, vpa_dtype dtype, const void*
 
 /* The same with y in 8 bits: each block of 128 columns of a row (the last may
  * be shorter) has the scale amax / 448, amax its largest |y| (at least
- * 2^-100), and y / scale rounded to nearest even.  A block that holds a NaN or
- * an infinity has scale NaN, and its elements stand for NaN.
+ * 2^-100), and y / scale, a division rounded to fp32, is rounded to nearest
+ * even.  A block that holds a NaN or an infinity has scale NaN, and its
+ * elements stand for NaN.
  *  y       out, e4m3 [rows][ldy].
  *  scale   out, float [rows][ld_scale], ld_scale >= ceil(cols / 128). */
 vpa_status vpa_rms_norm_fp8(const void* x, int64_t ldx, vpa_dtype dtype, const void* residual,

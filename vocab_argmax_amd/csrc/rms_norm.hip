@@ -15,25 +15,39 @@ constexpr int kThreads = 256;
 constexpr float kFp8Max = 448.0f;
 constexpr uint32_t kAmaxLeast = 0x0D800000u;       // 2^-100
 
-// A block's scale and its inverse from the largest |y| as fp32 bits, which sort
-// as the values do, infinity and NaN last.
-struct BlockScale {
-    float scale, inverse;
+// Quotients by d, those of a division rounded once: a product with a rounded inverse
+// puts one in a thousand ties of e4m3 on the wrong side.  The inverse is in two
+// parts, the second what the first one's rounding left: together they give y / d to
+// 2^-46, so q within its last place, and one step by the remainder, which a
+// multiply-add has exactly, the nearest fp32 value.
+struct Divisor {
+    float d, inverse, rest;
+    __device__ __forceinline__ float quotient(float y) const {
+        const float q = __builtin_fmaf(y, inverse, y * rest);
+        return copysignf(__builtin_fmaf(__builtin_fmaf(-d, q, y), inverse, q), y);
+    }
 };
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
+constexpr Divisor kByFp8Max = {kFp8Max, (float)(1.0 / kFp8Max),
+                               (float)(1.0 / kFp8Max - (double)(float)(1.0 / kFp8Max))};
+
+// A block's scale from the largest |y| as fp32 bits, which sort as the values do,
+// infinity and NaN last.
+__device__ __forceinline__ Divisor block_scale(uint32_t amax_bits) {
     if (amax_bits >= 0x7F800000u)
-        return {__builtin_nanf(""), __builtin_nanf("")};
-    const float amax = __builtin_bit_cast(float, amax_bits < kAmaxLeast ? kAmaxLeast : amax_bits);
-    return {amax / kFp8Max, kFp8Max / amax};
+        return {__builtin_nanf(""), __builtin_nanf(""), 0.0f};
+    const Divisor by = kByFp8Max;
+    const float scale = by.quotient(
+        __builtin_bit_cast(float, amax_bits < kAmaxLeast ? kAmaxLeast : amax_bits));
+    const float inverse = 1.0f / scale;
+    return {scale, inverse, __builtin_fmaf(-scale, inverse, 1.0f) * inverse};
 }
 __device__ __forceinline__ uint32_t abs_bits(float f) {
     return __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu;
 }
-// Two values in 8 bits, to nearest even (NaN stays NaN): bits 0-7 and 8-15.
-// Values above 448 by the inverse's rounding are 448.
+// Two values in 8 bits, to nearest even (NaN stays NaN): bits 0-7 and 8-15.  The
+// instruction makes 448 of everything up to 464 (measured), so quotients that the
+// scale's rounding leaves above 448, by a step or two of fp32, need no clamp.
 __device__ __forceinline__ uint32_t pack_fp8(float a, float b) {
-    a = a > kFp8Max ? kFp8Max : a < -kFp8Max ? -kFp8Max : a;
-    b = b > kFp8Max ? kFp8Max : b < -kFp8Max ? -kFp8Max : b;
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xFFFFu;
 }
 
@@ -144,12 +158,12 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_kernel(RmsT
                     const uint32_t b = e < n ? abs_bits(f[e]) : 0;
                     amax = b > amax ? b : amax;
                 }
-                const BlockScale sc = block_scale(group_max<LANES>(amax));
+                const Divisor sc = block_scale(group_max<LANES>(amax));
                 LooseBytes<VEC> o;
 #pragma unroll
                 for (int e = 0; e < VEC; e += 4)
-                    o.w[e / 4] = pack_fp8(f[e] * sc.inverse, f[e + 1] * sc.inverse) |
-                                 pack_fp8(f[e + 2] * sc.inverse, f[e + 3] * sc.inverse) << 16;
+                    o.w[e / 4] = pack_fp8(sc.quotient(f[e]), sc.quotient(f[e + 1])) |
+                                 pack_fp8(sc.quotient(f[e + 2]), sc.quotient(f[e + 3])) << 16;
                 uint8_t* y = (uint8_t*)t.y + row * t.ldy + P::column(i);
                 if (n == VEC) {
                     *(LooseBytes<VEC>*)y = o;
@@ -160,7 +174,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_kernel(RmsT
                             y[e] = (uint8_t)(o.w[e / 4] >> (e % 4 * 8));
                 }
                 if (n > 0 && P::column(i) % kScaleBlock == 0)
-                    t.scale[row * t.ld_scale + P::column(i) / kScaleBlock] = sc.scale;
+                    t.scale[row * t.ld_scale + P::column(i) / kScaleBlock] = sc.d;
             }
         }
     }
@@ -317,14 +331,14 @@ __global__ __launch_bounds__(kLongThreads) void rms_long_kernel(RmsTask t) {
             const uint32_t o = __shfl_xor(amax, off, 64);
             amax = o > amax ? o : amax;
         }
-        const BlockScale sc = block_scale(amax);
-        const uint32_t p = pack_fp8(v0 * sc.inverse, v1 * sc.inverse);
+        const Divisor sc = block_scale(amax);
+        const uint32_t p = pack_fp8(sc.quotient(v0), sc.quotient(v1));
         if (c < t.cols)
             y[c] = (uint8_t)p;
         if (c + 1 < t.cols)
             y[c + 1] = (uint8_t)(p >> 8);
         if (lane == 0)
-            t.scale[row * t.ld_scale + b] = sc.scale;
+            t.scale[row * t.ld_scale + b] = sc.d;
     }
 }
 
@@ -450,14 +464,14 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(QuantTask t, int64_t bl
         for (int i = 0; i < kThreads / 64; ++i)
             amax = lds[i] > amax ? lds[i] : amax;
     }
-    const BlockScale sc = block_scale(amax);
+    const Divisor sc = block_scale(amax);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t r = r0 + i * ROWS;
         if (r >= t.rows)
             continue;
         LooseBytes<VEC> o;
-        const auto f = [&](int e) { return vec_elem<(int)sizeof(T)>(v[i], e) * sc.inverse; };
+        const auto f = [&](int e) { return sc.quotient(vec_elem<(int)sizeof(T)>(v[i], e)); };
 #pragma unroll
         for (int e = 0; e < VEC; e += 4)
             o.w[e / 4] = pack_fp8(f(e), f(e + 1)) | pack_fp8(f(e + 2), f(e + 3)) << 16;
@@ -471,10 +485,10 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(QuantTask t, int64_t bl
                     y[e] = (uint8_t)(o.w[e / 4] >> (e % 4 * 8));
         }
         if (!SQUARE && threadIdx.x % LANES == 0)
-            t.scale[r * t.ld_scale + across] = sc.scale;
+            t.scale[r * t.ld_scale + across] = sc.d;
     }
     if (SQUARE && threadIdx.x == 0)
-        t.scale[down * t.ld_scale + across] = sc.scale;
+        t.scale[down * t.ld_scale + across] = sc.d;
 }
 
 template <typename T, typename W>
