@@ -210,16 +210,15 @@ vpa_status vpa_quantize_fp8(const void* x, int64_t ldx, vpa_dtype dtype, int64_t
                             int64_t cols, int32_t block_rows, void* y, int64_t ldy, float* scale,
                             int64_t ld_scale, void* stream);
 
-/* Workspace bytes of vpa_head_linear_fp8 (may be 0; 0 too if the sizes are invalid). */
+/* Workspace bytes of vpa_head_linear_fp8 and of vpa_head_linear_fp8_fast (may be
+ * 0; 0 too if the sizes are invalid). */
 size_t vpa_head_linear_fp8_workspace(int64_t rows, int64_t outer, int64_t inner);
+size_t vpa_head_linear_fp8_fast_workspace(int64_t rows, int64_t outer, int64_t inner);
 
 /* y = residual + act(x W^T + bias) of 8-bit operands: with blocks b of 128 of
  * the inner dimension,
  *   (x W^T)(m, n) = sum_b x_scale(m, b) w_scale(n / 128, b) sum_{k in b} x(m, k) W(n, k),
- * the inner sums exact products added in fp32.  Where y is bf16 and has more
- * than 64 rows they come from the matrix cores' 8-bit instruction, which cuts in
- * every group of 8 products what lies below 2^-13 of the largest: random normal
- * operands end 1.4e-5 (relative) off, a step of bf16 is 2^-8.
+ * the inner sums exact products added in fp32, whatever the sizes and types.
  *  x        e4m3 [rows][ldx], x_scale float [rows][ldxs] (blocks of 1 x 128).
  *  weight   e4m3 [outer][ldw], w_scale float [ceil(outer/128)][ldws] (128 x 128).
  *           Rows of x and weight begin at multiples of 16 bytes (pointer, and
@@ -236,6 +235,21 @@ vpa_status vpa_head_linear_fp8(const void* x, int64_t ldx, const float* x_scale,
                                int64_t rows, int64_t outer, int64_t inner, int32_t act, void* y,
                                int64_t ldy, vpa_dtype out_dtype, void* workspace,
                                size_t workspace_bytes, void* stream);
+
+/* The same with fewer digits in the inner sums, for callers who choose that: where
+ * y is bf16 and has more than 64 rows they come from the matrix cores' 8-bit
+ * instruction, at up to twice the rate of the others.  It cuts in every group of 8
+ * products what lies below 2^-13 of the largest, so an inner sum is off by up to
+ * 7 * 2^-13 of sum |x W|: little beside a result of about that size (random normal
+ * operands end 1.4e-5 off, relatively; a step of bf16 is 2^-8), everything where
+ * large products cancel.  Other results are vpa_head_linear_fp8's.  Workspace:
+ * vpa_head_linear_fp8_fast_workspace() bytes. */
+vpa_status vpa_head_linear_fp8_fast(const void* x, int64_t ldx, const float* x_scale, int64_t ldxs,
+                                    const void* weight, int64_t ldw, const float* w_scale,
+                                    int64_t ldws, const void* bias, const void* residual,
+                                    int64_t ldr, int64_t rows, int64_t outer, int64_t inner,
+                                    int32_t act, void* y, int64_t ldy, vpa_dtype out_dtype,
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -151,6 +151,72 @@ vpa_status rms_forward(const char* call, const void* x, int64_t ldx, int dt, con
     return he == hipSuccess ? ok() : hip_fail(he, call);
 }
 
+// ---- 8-bit products ----
+
+// Both forms of the product.
+vpa_status linear_fp8(const char* call, bool fast, const void* x, int64_t ldx,
+                      const float* x_scale, int64_t ldxs, const void* weight, int64_t ldw,
+                      const float* w_scale, int64_t ldws, const void* bias, const void* residual,
+                      int64_t ldr, int64_t rows, int64_t outer, int64_t inner, int32_t act, void* y,
+                      int64_t ldy, int odt, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream) {
+    vpa_status st;
+    if ((st = check_dtype(odt)) != VPA_OK || (st = check_act(act)) != VPA_OK ||
+        (st = check_sizes(call, rows, outer, inner)) != VPA_OK)
+        return st;
+    if (rows == 0)
+        return ok();
+    const int64_t blocks = (inner + kScaleBlock - 1) / kScaleBlock;
+    if ((st = check_matrix("x", x, 16, ldx, inner)) != VPA_OK ||
+        (st = check_matrix("x_scale", x_scale, 4, ldxs, blocks)) != VPA_OK ||
+        (st = check_matrix("weight", weight, 16, ldw, inner)) != VPA_OK ||
+        (st = check_matrix("w_scale", w_scale, 4, ldws, blocks)) != VPA_OK ||
+        (bias && (st = check_vector("bias", bias, 2)) != VPA_OK) ||
+        (residual && (st = check_matrix("residual", residual, 2, ldr, outer)) != VPA_OK) ||
+        (st = check_matrix("y", y, esize_of(odt), ldy, outer)) != VPA_OK)
+        return st;
+    const int64_t most = (int64_t)1 << 21;
+    if (ldx % 16 || ldw % 16 || ldx > most || ldw > most || ldxs > most || ldws > most)
+        return fail(VPA_ERR_INVALID,
+                    "%s: row strides %lld, %lld (multiples of 16), %lld or %lld (scales) above 2^21",
+                    call, (long long)ldx, (long long)ldw, (long long)ldxs, (long long)ldws);
+    if (y == residual && (ldy != ldr || odt != VPA_BF16))
+        return fail(VPA_ERR_INVALID, "%s: y in the residual's place needs its stride and type",
+                    call);
+    const bool exact = !fast || odt == VPA_F32;
+    if ((st = check_dispatch(fp8_threads(rows, outer, inner, exact), call)) != VPA_OK ||
+        (st = check_workspace(call, workspace, workspace_bytes,
+                              fp8_workspace(rows, outer, inner, exact))) != VPA_OK)
+        return st;
+    Fp8Task t{};
+    t.exact = exact;
+    GemmTask& g = t.g;
+    g.a = x;
+    g.a_m = ldx;
+    g.a_k = 1;
+    g.b = weight;
+    g.b_n = ldw;
+    g.b_k = 1;
+    g.a_k1 = g.b_k1 = true;
+    g.m = g.m_readable = rows;
+    g.n = g.n_readable = outer;
+    g.k = inner;
+    g.bias = bias;
+    g.residual = residual;
+    g.ldr = ldr;
+    g.y = y;
+    g.ldy = ldy;
+    g.out_f32 = odt == VPA_F32;
+    g.act = act;
+    g.ws = workspace;
+    t.a_scale = x_scale;
+    t.lda_scale = ldxs;
+    t.b_scale = w_scale;
+    t.ldb_scale = ldws;
+    const hipError_t e = launch_fp8(t, stream);
+    return e == hipSuccess ? ok() : hip_fail(e, call);
+}
+
 }  // namespace
 
 extern "C" {
@@ -421,6 +487,12 @@ vpa_status vpa_quantize_fp8(const void* x, int64_t ldx, vpa_dtype dtype, int64_t
 size_t vpa_head_linear_fp8_workspace(int64_t rows, int64_t outer, int64_t inner) {
     if (rows < 1 || check_sizes("", rows, outer, inner) != VPA_OK)
         return 0;
+    return fp8_workspace(rows, outer, inner, true);
+}
+
+size_t vpa_head_linear_fp8_fast_workspace(int64_t rows, int64_t outer, int64_t inner) {
+    if (rows < 1 || check_sizes("", rows, outer, inner) != VPA_OK)
+        return 0;
     // for results of either type
     const size_t a = fp8_workspace(rows, outer, inner, false);
     const size_t b = fp8_workspace(rows, outer, inner, true);
@@ -429,68 +501,24 @@ size_t vpa_head_linear_fp8_workspace(int64_t rows, int64_t outer, int64_t inner)
 
 vpa_status vpa_head_linear_fp8(const void* x, int64_t ldx, const float* x_scale, int64_t ldxs,
                                const void* weight, int64_t ldw, const float* w_scale,
-                               int64_t ldws, const void* bias, const void* residual, int64_t ldr,
-                               int64_t rows, int64_t outer, int64_t inner, int32_t act, void* y,
-                               int64_t ldy, vpa_dtype out_dtype, void* workspace,
-                               size_t workspace_bytes, void* stream) {
-    const char* call = "vpa_head_linear_fp8";
-    const int odt = dtype_value(&out_dtype);
-    vpa_status st;
-    if ((st = check_dtype(odt)) != VPA_OK || (st = check_act(act)) != VPA_OK ||
-        (st = check_sizes(call, rows, outer, inner)) != VPA_OK)
-        return st;
-    if (rows == 0)
-        return ok();
-    const int64_t blocks = (inner + kScaleBlock - 1) / kScaleBlock;
-    if ((st = check_matrix("x", x, 16, ldx, inner)) != VPA_OK ||
-        (st = check_matrix("x_scale", x_scale, 4, ldxs, blocks)) != VPA_OK ||
-        (st = check_matrix("weight", weight, 16, ldw, inner)) != VPA_OK ||
-        (st = check_matrix("w_scale", w_scale, 4, ldws, blocks)) != VPA_OK ||
-        (bias && (st = check_vector("bias", bias, 2)) != VPA_OK) ||
-        (residual && (st = check_matrix("residual", residual, 2, ldr, outer)) != VPA_OK) ||
-        (st = check_matrix("y", y, esize_of(odt), ldy, outer)) != VPA_OK)
-        return st;
-    const int64_t most = (int64_t)1 << 21;
-    if (ldx % 16 || ldw % 16 || ldx > most || ldw > most || ldxs > most || ldws > most)
-        return fail(VPA_ERR_INVALID,
-                    "%s: row strides %lld, %lld (multiples of 16), %lld or %lld (scales) above 2^21",
-                    call, (long long)ldx, (long long)ldw, (long long)ldxs, (long long)ldws);
-    if (y == residual && (ldy != ldr || odt != VPA_BF16))
-        return fail(VPA_ERR_INVALID, "%s: y in the residual's place needs its stride and type",
-                    call);
-    // results of more than a step of bf16 take exact products
-    const bool exact = odt == VPA_F32;
-    if ((st = check_dispatch(fp8_threads(rows, outer, inner, exact), call)) != VPA_OK ||
-        (st = check_workspace(call, workspace, workspace_bytes,
-                              fp8_workspace(rows, outer, inner, exact))) != VPA_OK)
-        return st;
-    Fp8Task t{};
-    t.exact = exact;
-    GemmTask& g = t.g;
-    g.a = x;
-    g.a_m = ldx;
-    g.a_k = 1;
-    g.b = weight;
-    g.b_n = ldw;
-    g.b_k = 1;
-    g.a_k1 = g.b_k1 = true;
-    g.m = g.m_readable = rows;
-    g.n = g.n_readable = outer;
-    g.k = inner;
-    g.bias = bias;
-    g.residual = residual;
-    g.ldr = ldr;
-    g.y = y;
-    g.ldy = ldy;
-    g.out_f32 = odt == VPA_F32;
-    g.act = act;
-    g.ws = workspace;
-    t.a_scale = x_scale;
-    t.lda_scale = ldxs;
-    t.b_scale = w_scale;
-    t.ldb_scale = ldws;
-    const hipError_t e = launch_fp8(t, (hipStream_t)stream);
-    return e == hipSuccess ? ok() : hip_fail(e, "vpa_head_linear_fp8 launch");
+                               int64_t ldws, const void* bias, const void* residual,
+                               int64_t ldr, int64_t rows, int64_t outer, int64_t inner,
+                               int32_t act, void* y, int64_t ldy, vpa_dtype out_dtype,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    return linear_fp8("vpa_head_linear_fp8", false, x, ldx, x_scale, ldxs, weight, ldw, w_scale, ldws,
+                      bias, residual, ldr, rows, outer, inner, act, y, ldy, dtype_value(&out_dtype),
+                      workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+vpa_status vpa_head_linear_fp8_fast(const void* x, int64_t ldx, const float* x_scale, int64_t ldxs,
+                                    const void* weight, int64_t ldw, const float* w_scale,
+                                    int64_t ldws, const void* bias, const void* residual,
+                                    int64_t ldr, int64_t rows, int64_t outer, int64_t inner,
+                                    int32_t act, void* y, int64_t ldy, vpa_dtype out_dtype,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+    return linear_fp8("vpa_head_linear_fp8_fast", true, x, ldx, x_scale, ldxs, weight, ldw, w_scale, ldws,
+                      bias, residual, ldr, rows, outer, inner, act, y, ldy, dtype_value(&out_dtype),
+                      workspace, workspace_bytes, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -16,6 +16,8 @@ static __typeof__(&vpa_rms_norm_fp8) p_rms_norm_fp8;
 static __typeof__(&vpa_rms_norm_backward) p_rms_norm_backward;
 static __typeof__(&vpa_quantize_fp8) p_quantize_fp8;
 static __typeof__(&vpa_head_linear_fp8) p_head_linear_fp8;
+static __typeof__(&vpa_head_linear_fp8_fast) p_head_linear_fp8_fast;
+static __typeof__(&vpa_head_linear_fp8_fast_workspace) p_head_linear_fp8_fast_workspace;
 
 static const struct entry k_entries[] = {
     {"vpa_sampled_verify", (void**)&p_sampled_verify},
@@ -27,6 +29,8 @@ static const struct entry k_entries[] = {
     {"vpa_rms_norm_backward", (void**)&p_rms_norm_backward},
     {"vpa_quantize_fp8", (void**)&p_quantize_fp8},
     {"vpa_head_linear_fp8", (void**)&p_head_linear_fp8},
+    {"vpa_head_linear_fp8_fast", (void**)&p_head_linear_fp8_fast},
+    {"vpa_head_linear_fp8_fast_workspace", (void**)&p_head_linear_fp8_fast_workspace},
 };
 #define N_ENTRIES ((int)(sizeof(k_entries) / sizeof(k_entries[0])))
 
@@ -157,20 +161,42 @@ static PyObject* py_quantize_fp8(PyObject* self, PyObject* const* args, Py_ssize
                   stream));
 }
 
-static PyObject* py_head_linear_fp8(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
-    (void)self;
+static PyObject* call_linear_fp8(const char* name, __typeof__(&vpa_head_linear_fp8) fn,
+                                 PyObject* const* args, Py_ssize_t nargs) {
     void *x, *xs, *w, *ws_scale, *bias, *res, *y, *ws, *stream;
     vpa_dtype odtype;
     int64_t ldx, ldxs, ldw, ldws, ldr, rows, outer, inner, ldy;
     int32_t act;
     size_t ws_bytes;
-    if (!bound("vpa_head_linear_fp8", (const void*)p_head_linear_fp8) ||
-        !parse("vpa_head_linear_fp8", args, nargs, "plplplplppllllipldpzp", &x, &ldx, &xs, &ldxs,
-               &w, &ldw, &ws_scale, &ldws, &bias, &res, &ldr, &rows, &outer, &inner, &act, &y, &ldy,
-               &odtype, &ws, &ws_bytes, &stream))
+    if (!bound(name, (const void*)fn) ||
+        !parse(name, args, nargs, "plplplplppllllipldpzp", &x, &ldx, &xs, &ldxs, &w, &ldw,
+               &ws_scale, &ldws, &bias, &res, &ldr, &rows, &outer, &inner, &act, &y, &ldy, &odtype,
+               &ws, &ws_bytes, &stream))
         return NULL;
-    RETURN_STATUS(p_head_linear_fp8(x, ldx, xs, ldxs, w, ldw, ws_scale, ldws, bias, res, ldr,
-                  rows, outer, inner, act, y, ldy, odtype, ws, ws_bytes, stream));
+    RETURN_STATUS(fn(x, ldx, xs, ldxs, w, ldw, ws_scale, ldws, bias, res, ldr, rows, outer, inner,
+                  act, y, ldy, odtype, ws, ws_bytes, stream));
+}
+
+static PyObject* py_head_linear_fp8(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    return call_linear_fp8("vpa_head_linear_fp8", p_head_linear_fp8, args, nargs);
+}
+
+static PyObject* py_head_linear_fp8_fast(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    return call_linear_fp8("vpa_head_linear_fp8_fast", p_head_linear_fp8_fast, args, nargs);
+}
+
+/* Host-only: the bytes of one call's workspace. */
+static PyObject* py_head_linear_fp8_fast_workspace(PyObject* self, PyObject* const* args,
+                                                   Py_ssize_t nargs) {
+    (void)self;
+    int64_t rows, outer, inner;
+    const char* name = "vpa_head_linear_fp8_fast_workspace";
+    if (!bound(name, (const void*)p_head_linear_fp8_fast_workspace) ||
+        !parse(name, args, nargs, "lll", &rows, &outer, &inner))
+        return NULL;
+    return PyLong_FromSize_t(p_head_linear_fp8_fast_workspace(rows, outer, inner));
 }
 
 static PyObject* py_bind(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
@@ -194,6 +220,8 @@ static PyMethodDef k_methods[] = {
     {"vpa_rms_norm_backward", FASTCALL(py_rms_norm_backward), "vpa_rms_norm_backward (include/vpa_draft.h)"},
     {"vpa_quantize_fp8", FASTCALL(py_quantize_fp8), "vpa_quantize_fp8 (include/vpa_draft.h)"},
     {"vpa_head_linear_fp8", FASTCALL(py_head_linear_fp8), "vpa_head_linear_fp8 (include/vpa_draft.h)"},
+    {"vpa_head_linear_fp8_fast", FASTCALL(py_head_linear_fp8_fast), "vpa_head_linear_fp8_fast (include/vpa_draft.h)"},
+    {"vpa_head_linear_fp8_fast_workspace", FASTCALL(py_head_linear_fp8_fast_workspace), "vpa_head_linear_fp8_fast_workspace (include/vpa_draft.h)"},
     {"bind", FASTCALL(py_bind), "bind(name, address): the entry point `name` is at `address`"},
     {"entries", py_entries, METH_NOARGS, "names of the entry points this module calls"},
     {NULL, NULL, 0, NULL},

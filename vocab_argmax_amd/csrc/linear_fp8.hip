@@ -10,8 +10,10 @@
 //
 // The matrix cores' 8-bit instruction cuts, in every group of 8 products, what
 // lies below 2^-13 of the largest (measured; random normal operands end 1.4e-5
-// off in the 2-norm).  Widened to bf16, which holds every e4m3 value, products
-// are summed in full fp32 at half the rate.
+// off in the 2-norm; +-448 * 448 that cancel leave nothing of products of 1 beside
+// them).  Widened to bf16, which holds every e4m3 value, products are summed in full
+// fp32 at half the rate: EXACT, which is what callers get who do not ask for the
+// other.
 #include <type_traits>
 
 #include "gemm_tile.h"
@@ -272,13 +274,15 @@ __device__ __forceinline__ void store_block8(const GemmTask& t, float* part, cha
 // and BUFS of them lie in LDS.  A wavefront holds the stage's fragments of W, and of
 // x a ring of 4 that are read 4 products ahead, so that the accumulators, which
 // the scaling keeps in ordinary registers, leave room.
-// 8192^3 480-490 us, 2240-2290 TFLOP/s, the matrix cores busy half of the clocks: a
-// product's 4 multiply-adds take issue slots beside it (a tenth of the time with
-// everything else left in), and operands come at the rate of LDS and the caches (a
-// fifth).  4096^3 65 us.  The 16-bit product of these sizes takes 790 and 105.
-// The barrier that says that
-// the next stage has landed, and that every wavefront has read this one, stands
-// before the first read from the next.
+// The barrier that says that the next stage has landed, and that every wavefront has
+// read this one, stands before the first read from the next.
+//
+// The fast form: 8192^3 475-490 us, 2240-2310 TFLOP/s, the matrix cores busy half of
+// the clocks: a product's 4 multiply-adds take issue slots beside it (a tenth of the
+// time with everything else left in), and operands come at the rate of LDS and the
+// caches (a fifth).  4096^3 65 us.  EXACT, bound by the matrix cores' bf16 rate, the
+// widening (4 instructions for 16 values) and the traffic of smaller tiles: 937 and
+// 130.  The 16-bit product of these sizes takes 790 and 105.
 template <bool EXACT, int BM, int BN, int WM, int WN, int BUFS>
 __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uint32_t tiles_m,
                                                                uint32_t tiles_n,
@@ -508,7 +512,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
 // which has as many or (see plan_fp8) a few times those, with STAGES - 1 stages on
 // their way (as in the 16-bit products).  Up to 64 rows products are exact: the
 // matrix cores and the widening have time to spare (with the 8-bit instruction 64 x
-// 4096 x 11008 took 24 us for 26).
+// 4096 x 11008 took 24 us for 26), in the fast form too.
 //
 // Workgroups on a CU beside one another hide more than stages on their way: 32 x
 // 2048 x 151936 62 us (5.1 TB/s) with 4 stages, 3 workgroups a CU, and 73 with 6,
@@ -729,8 +733,9 @@ GemmPlan plan_a_round(int tile, int64_t blocks, int64_t k) {
 // 4096 25.6 in the two slices that fit, 28.7 in one, 26.6 in four).  Else the plan of
 // a 16-bit product whose rows have as many bytes, whose stages, tiles and costs are
 // alike.  Exact products have no 256-tiles: widening takes the registers of more.
-// They take up to twice the time from 1024 rows on (4096^3 122 us, by the 8-bit
-// instruction 64), the reason for it where the result is rounded to bf16 anyway.
+// They take up to twice the time from 1024 rows on (4096^3 130 us, by the 8-bit
+// instruction 67; 2048 x 2048 x 50257 417 and 263; 512 x 4096 x 4096 33 and 26), which
+// is what the fast form is for.
 GemmPlan plan_fp8(int64_t m, int64_t n, int64_t k, bool exact) {
     const auto blocks = [&](int64_t tile) {
         return ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
