@@ -64,13 +64,6 @@ __device__ __forceinline__ void each_id(uint64_t lanes, int32_t id, F f) {
     }
 }
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        v += __shfl_xor(v, off, 64);
-    return v;
-}
-
 // What the teacher says of a row, in every lane of a wavefront but p and lp,
 // which are the lane's: the few terms in 64 bits, since what they leave of 1 may
 // be small.

@@ -45,35 +45,6 @@ struct DrawSum {
     double e, w;
 };
 
-// v plus its partner's of a DPP move (vpa_device.h); 0 where a lane has none.
-template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ double add_move_f64(double v) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROW_MASK, 0xF, false);
-    const uint32_t hi =
-        __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROW_MASK, 0xF, false);
-    return v + __builtin_bit_cast(double, lo | (uint64_t)hi << 32);
-}
-// The running sum over the lanes of a wavefront, the lane's own included.
-__device__ __forceinline__ double wave_scan_f64(double v) {
-    constexpr int kRight = 0x110;                  // row_shr:0
-    v = add_move_f64<kRight + 1, 0xF>(v);
-    v = add_move_f64<kRight + 2, 0xF>(v);
-    v = add_move_f64<kRight + 4, 0xF>(v);
-    v = add_move_f64<kRight + 8, 0xF>(v);
-    v = add_move_f64<dpp::kBcast15, 0xA>(v);
-    return add_move_f64<dpp::kBcast31, 0xC>(v);
-}
-__device__ __forceinline__ double lane63_f64(double v) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63);
-    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
-    return __builtin_bit_cast(double, lo | (uint64_t)hi << 32);
-}
-__device__ __forceinline__ double wave_sum_f64(double v) {
-    return lane63_f64(wave_scan_f64(v));
-}
-
 // 2^((x - m) scale) as 2^n (1 + f q(f)): n the nearest whole number, which 1.5 2^52
 // leaves in the last bits of a sum, and q the interpolation of (2^f - 1) / f at the
 // 9 Chebyshev nodes of [-1/2, 1/2], off by 4e-14 at most.  From `least` down (and
