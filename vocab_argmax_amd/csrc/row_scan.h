@@ -9,6 +9,11 @@
 // above it.  A later chunk is one pass: for bf16 an element costs 1.5
 // instructions to unpack it and take the maximum, a multiply-add, 2 slots for
 // 2^z and an add.
+//
+// A vector's terms and a chunk's vectors, 20 at most, are added in fp32, chunks in 64
+// bits: equal terms are rounded in the same direction in every lane, so in fp32
+// alone a row's error would grow with its length (2^21 equal logits in one segment
+// 1e-5 off, 2^24 1e-4).
 #pragma once
 
 #include "vpa_math.h"
@@ -152,10 +157,11 @@ template <int ESIZE, int U>
 __device__ __forceinline__ float chunk_sum(const u32x4_t (&w)[U], const ScaledFrom& base,
                                            float scale) {
     constexpr int VEC = 16 / ESIZE;
-    float s = 0.0f;
+    float sum = 0.0f;
     // (one branch around both loops would have all of the values unpacked before it)
 #pragma unroll
     for (int i = 0; i < U; ++i) {
+        float s = 0.0f;
         if (base.apart) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
@@ -165,9 +171,11 @@ __device__ __forceinline__ float chunk_sum(const u32x4_t (&w)[U], const ScaledFr
             for (int e = 0; e < VEC; ++e)
                 s += exp2_fast(__builtin_fmaf(vec_elem<ESIZE>(w[i], e), scale, -base.b));
         }
+        sum += s;
+        asm volatile("" : "+v"(sum));           // not all vectors' sums first
         __builtin_amdgcn_sched_barrier(0);         // registers for one vector at a time
     }
-    return s * base.fix;
+    return sum * base.fix;
 }
 
 // (m, s) of a set of columns: m near its largest, s = sum 2^((x - m) scale); the
@@ -196,7 +204,7 @@ struct SegmentScan {
     static constexpr int CHUNK = THREADS * U * VEC;
 
     ScaledFrom base = {kMinusInf, 0.0f, 1.0f, false};
-    float s = 0.0f;                                // the lane's
+    double s = 0.0;                                // the lane's
     float best = kMinusInf;                        // the lane's largest value
     int best_at = -1;                              // and its vector's first column
 
@@ -243,19 +251,19 @@ struct SegmentScan {
                 if (m == kMinusInf) {              // nothing but masked columns, or NaN
                     ScaledFrom zero;
                     zero.set(0.0f, scale);
-                    s += chunk_sum<ESIZE, U>(w, zero, scale);
+                    s += (double)chunk_sum<ESIZE, U>(w, zero, scale);
                     continue;
                 }
                 if (base.m != kMinusInf)
-                    s *= exp2_fast((base.m - m) * scale);
+                    s *= (double)exp2_fast((base.m - m) * scale);
                 base.set(m, scale);
             }
-            s += chunk_sum<ESIZE, U>(w, base, scale);
+            s += (double)chunk_sum<ESIZE, U>(w, base, scale);
         }
     }
     // of the wavefront's columns
     __device__ __forceinline__ ExpSum wave() const {
-        return {base.m, wave_sum(s)};
+        return {base.m, (float)wave_sum_f64(s)};
     }
     // The first of the wavefront's columns in the argmax order as one number (0:
     // no columns).  A wavefront with a NaN or +inf goes through its columns again.
