@@ -46,8 +46,8 @@ extern "C" {
  * that one (position K if all are accepted) emits a token drawn from
  *     w = max(p_j - q_j, 0) at a rejected draft, w = p_j otherwise:
  * the least c with  sum of w(0..c) > sample_uniforms[r] * sum of w.
- * Sums and comparisons of that draw are in 64 bits; p_j(d) is within 2^-20 of
- * its value, relatively.
+ * Sums and comparisons of that draw are in 64 bits, and those of an acceptance
+ * where it is near: p_j(d) counts to within 2^-36 of its value, relatively.
  *
  *  - Without draft_probs q_j is 1 at the draft and 0 elsewhere (drafts that no
  *    model drew).

@@ -21,9 +21,6 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMostSegments = 64;
 constexpr float kInf = __builtin_inff();
-// most (of z) that a chunk's maximum may exceed M by: further off, ln s is a
-// large number of which the loss needs the last digits
-constexpr float kLag = 6.0f;
 
 // A row's statistics as the backward pass takes them.  (Of the sums 1 / s: from
 // ln s in fp32 a probability would be off by half a step of ln s, 4e-7 for 2e5
@@ -203,7 +200,7 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillTask t, Cut cu
     const int end = begin + cut.chunks * Scan::CHUNK;
     const int lo = begin < 0 ? 0 : begin, hi = end < t.vocab ? end : t.vocab;
     Scan scan;
-    scan.run(x, begin, lo, hi, scale, kLag, [&](u32x4_t (&w)[kScanVecs], int c0) {
+    scan.run(x, begin, lo, hi, scale, [&](u32x4_t (&w)[kScanVecs], int c0) {
         mask_named<ESIZE, kScanVecs, kThreads>(w, c0, id);
     });
     const ExpSum s = scan.wave();

@@ -5,7 +5,7 @@
 // A workgroup walks its segment in chunks of U 16-byte vectors a thread, held in
 // registers, that begin at aligned columns.  Every lane keeps s = sum 2^z of its
 // own columns, z = (x - M) scale, from an M that its wavefront shares: the first
-// chunk's maximum, moved to a later chunk's where that is more than LAG (of z)
+// chunk's maximum, moved to a later chunk's where that is more than kLag (of z)
 // above it.  A later chunk is one pass: for bf16 an element costs 1.5
 // instructions to unpack it and take the maximum, a multiply-add, 2 slots for
 // 2^z and an add.
@@ -22,6 +22,9 @@ namespace vpa {
 namespace {
 
 constexpr float kMinusInf = -__builtin_inff();
+// most (of z) that a chunk's maximum may exceed M by: an exponent further off is
+// rounded to fewer digits, and ln s is a large number of which a loss needs the last
+constexpr float kLag = 6.0f;
 
 // The largest of three (a NaN among them: any of them or NaN), one instruction.
 __device__ __forceinline__ float largest3(float a, float b, float c) {
@@ -209,10 +212,9 @@ struct SegmentScan {
     int best_at = -1;                              // and its vector's first column
 
     // `masked` is called with a chunk and its first column before it is summed.
-    // LAG in z.
     template <typename Mask>
     __device__ __forceinline__ void run(const T* x, int begin, int lo, int hi, float scale,
-                                        float lag, Mask masked) {
+                                        Mask masked) {
         for (int c0 = begin; c0 < hi; c0 += CHUNK) {
             u32x4_t w[U];
             const int mine = c0 + (int)threadIdx.x * VEC;
@@ -246,7 +248,7 @@ struct SegmentScan {
 #pragma unroll
             for (int i = 0; i < U; ++i)
                 asm volatile("" : "+v"(w[i]));
-            if (base.m == kMinusInf || __ballot((mx - base.m) * scale > lag)) {
+            if (base.m == kMinusInf || __ballot((mx - base.m) * scale > kLag)) {
                 const float m = fmaxf(base.m, wave_max(mx));
                 if (m == kMinusInf) {              // nothing but masked columns, or NaN
                     ScaledFrom zero;

@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleTask t, Sam
     const int end = begin + cut.row_chunks * Scan::CHUNK;
     const int lo = begin < 0 ? 0 : begin, hi = end < t.vocab ? end : t.vocab;
     Scan scan;
-    scan.run(x, begin, lo, hi, scale, 60.0f, [](auto&, int) {});
+    scan.run(x, begin, lo, hi, scale, [](auto&, int) {});
     const ExpSum s = scan.wave();
     const uint64_t best = scan.wave_best(x, begin, lo, hi);
     if ((threadIdx.x & 63) == 0) {
@@ -140,6 +140,51 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleTask t, Sam
     stats[blockIdx.x] = RowStat{all.m, all.s, order};
 }
 
+// Sum over a workgroup of kThreads, of each thread's own, in a fixed order.
+__device__ __forceinline__ double block_sum_f64(double v, double (&lds)[kWaves]) {
+    v = wave_sum_f64(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return ((lds[0] + lds[1]) + lds[2]) + lds[3];
+}
+
+// Sum of a row's exponentials in 64 bits, by a workgroup.
+template <int ESIZE>
+__device__ __forceinline__ double row_sum_f64(const SampleTask& t, int32_t row, const Power& e,
+                                              double (&lds)[kWaves]) {
+    constexpr int VEC = 16 / ESIZE;
+    const auto* x = (const typename elem<ESIZE>::type*)t.logits + (int64_t)row * t.ld;
+    // whole aligned vectors, and what lies before and after them
+    int first = (int)(((16 - ((uintptr_t)x & 15)) & 15) / ESIZE);
+    first = first < t.vocab ? first : t.vocab;
+    const int vecs = (t.vocab - first) / VEC, tail = first + vecs * VEC;
+    double s = 0.0;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < vecs; i += kThreads) {
+        const u32x4_t v = *(const u32x4_t*)(x + first + i * VEC);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            s += e.of(vec_elem<ESIZE>(v, k));
+            asm volatile("" : "+v"(s));            // registers for one at a time
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    const int c = (int)threadIdx.x < first ? (int)threadIdx.x : tail + (int)threadIdx.x - first;
+    if (c < t.vocab && c - tail < VEC)
+        s += e.of(to_f32(x[c]));
+    return block_sum_f64(s, lds);
+}
+
+// How near to its border, relatively, an acceptance is decided again in 64 bits.
+// The rows' fp32 sums are off by less than 2^-17: of the exponents, up to kLag above
+// M and ln V below the maximum on average, a step's half and the rounded scale take
+// 0.5 and 2.2e-6, their joining over wavefronts and segments 2.2e-6 again, the sums
+// themselves 1e-6.  One position in 2^15 or so takes that long: 60 us for 200064
+// columns.
+constexpr double kNear = 0x1p-16;
+
 // The acceptance tests of a request by a workgroup, a wavefront a position, until
 // one is not accepted: the row that the request draws from.  `token` is the argmax
 // where that is what it draws, else -1.
@@ -148,14 +193,17 @@ __device__ __forceinline__ Draw accept_request(const SampleTask& t, const Sample
                                                const RowStat* stats, int32_t req, int32_t& token) {
     using T = typename elem<ESIZE>::type;
     using Q = typename elem<QSIZE>::type;
+    enum { kAccepted, kEnds, kOpen };
     __shared__ Draw ends[kWaves];
-    __shared__ int32_t tokens[kWaves], at_end[kWaves];
+    __shared__ int32_t tokens[kWaves], states[kWaves];
+    __shared__ float logits[kWaves];               // of the open ones: x, and u q
+    __shared__ double borders[kWaves], lds[kWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float temp = temperature_of(t, req);
     const float scale = is_greedy(temp) ? kLog2e : kLog2e / temp;
     for (int first = 0;; first += kWaves) {
         const int pos = first + wave;
-        bool last = true;
+        int32_t state = kEnds;
         if (pos <= t.k) {
             const int32_t row = req * (t.k + 1) + pos;
             RowStat st = {kMinusInf, 0.0f, 0};
@@ -189,7 +237,14 @@ __device__ __forceinline__ Draw accept_request(const SampleTask& t, const Sample
                     p = id == id_of(order) ? 1.0 : 0.0;
                 else
                     p = Power((double)sum.m, d.scale).of(x) / (double)sum.s;
-                last = !((double)u * (double)q < p);
+                const double border = (double)u * (double)q;
+                state = border < p ? kAccepted : kEnds;
+                if (!greedy && fabs(border - p) < kNear * p)
+                    state = kOpen;
+                if (lane == 0) {
+                    logits[wave] = x;
+                    borders[wave] = border;
+                }
                 d.q_row = q_row;
                 d.kind = t.probs ? kMinus : kWithout;
                 d.id = id;
@@ -202,14 +257,18 @@ __device__ __forceinline__ Draw accept_request(const SampleTask& t, const Sample
             }
         }
         if (lane == 0)
-            at_end[wave] = last;
+            states[wave] = state;
         __syncthreads();
-        int found = 0;
-        while (found < kWaves && !at_end[found])
-            ++found;
-        if (found < kWaves) {
-            token = tokens[found];
-            return ends[found];
+        for (int i = 0; i < kWaves; ++i) {         // (the same in all threads)
+            bool end = states[i] == kEnds;
+            if (states[i] == kOpen) {
+                const Power e((double)ends[i].m, ends[i].scale);
+                end = !(borders[i] < e.of(logits[i]) / row_sum_f64<ESIZE>(t, ends[i].row, e, lds));
+            }
+            if (end) {
+                token = tokens[i];
+                return ends[i];
+            }
         }
         __syncthreads();
     }
@@ -304,15 +363,6 @@ __device__ __forceinline__ void with_kind(int32_t kind, F f) {
         f(integral_constant<int, kPlain>{});
 }
 
-// Sum over a workgroup of kThreads, of each thread's own, in a fixed order.
-__device__ __forceinline__ double block_sum_f64(double v, double (&lds)[kWaves]) {
-    v = wave_sum_f64(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return ((lds[0] + lds[1]) + lds[2]) + lds[3];
-}
 __device__ __forceinline__ double sum_of_e(const DrawSum* sums, int blocks, double (&lds)[kWaves]) {
     double v = 0.0;
     for (int i = threadIdx.x; i < blocks; i += kThreads)
@@ -346,10 +396,11 @@ __global__ __launch_bounds__(kThreads) void sample_accept_kernel(SampleTask t, S
 enum SumsStep { kAccept, kFirst, kSecond };
 constexpr int64_t kAcceptInSums = 64;
 
+// (6 wavefronts a SIMD: kAccept's second look at an acceptance would leave 5, and 64 x
+// 4 x 151936 took 37.7 us for 36.8)
 template <int ESIZE, int QSIZE, int STEP>
-__global__ __launch_bounds__(kThreads) void sample_sums_kernel(SampleTask t, SampleCut cut,
-                                                               const RowStat* stats, Draw* draws,
-                                                               DrawSum* sums) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(6))) void
+sample_sums_kernel(SampleTask t, SampleCut cut, const RowStat* stats, Draw* draws, DrawSum* sums) {
     constexpr int VEC = 16 / ESIZE;
     constexpr bool SECOND = STEP == kSecond;
     __shared__ double lds[kWaves];
