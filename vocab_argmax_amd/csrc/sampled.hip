@@ -10,7 +10,9 @@
 // The draw is in 64 bits because a border lies between any two of up to 2^24
 // columns: with sums that are off by 2^-24 one draw in a hundred over a flat
 // row of 2e5 columns would come out a column off.  With e = exp((x - m) / T) and
-// Z its sum, the weights are e - q Z, so nothing is divided.
+// Z its sum, the weights are e - q Z, so nothing is divided.  An acceptance has one
+// border: the row's fp32 sum decides it, and where that is too near to say, a sum in
+// 64 bits.
 #include <type_traits>
 
 #include "row_scan.h"
@@ -544,7 +546,9 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleTask t, Sam
         total = z;
     }
     const bool of_e = kind != d.kind;
-    const double target = (u > 0.0 ? u : 0.0) * total;
+    // (from 1 on nothing passes: the sums' orders differ, and the last columns may be too
+    // small to change one)
+    const double target = u >= 1.0 ? (double)__builtin_inff() : (u > 0.0 ? u : 0.0) * total;
     // the block
     Passing<kWaves> at(found);
     double run = 0.0;
