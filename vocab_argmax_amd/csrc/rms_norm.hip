@@ -3,8 +3,10 @@
 // a scale for each block of 128 columns; its backward pass; and the same 8-bit
 // form of a matrix as it is.
 //
-// The sum of squares is fp32.  The norm is taken of the sum as it is stored
-// (rounded to its type), which is what the backward pass reads.
+// The sum of squares is of 64 bits: squares leave fp32 for values past 1.8e19, or a
+// row's sum of them well before, and for values below 1e-23.  The norm is taken of
+// the sum as it is stored (rounded to its type), which is what the backward pass
+// reads.
 #include "norm_rows.h"
 #include "vpa_draft_internal.h"
 
@@ -53,19 +55,29 @@ __device__ __forceinline__ uint32_t pack_fp8(float a, float b) {
 
 // Sum over a workgroup of WAVES wavefronts through `lds`; every thread holds it.
 // Callers leave a barrier between two uses of an lds.
-template <int WAVES>
-__device__ __forceinline__ float block_sum(float a, float (&lds)[WAVES]) {
-    a = wave_sum(a);
+template <int WAVES, typename S>
+__device__ __forceinline__ S block_sum(S a, S (&lds)[WAVES]) {
+    if constexpr (std::is_same_v<S, double>)
+        a = wave_sum_f64(a);
+    else
+        a = wave_sum(a);
     if constexpr (WAVES > 1) {
         if ((threadIdx.x & 63) == 0)
             lds[threadIdx.x >> 6] = a;
         __syncthreads();
-        a = 0.0f;
+        a = 0;
 #pragma unroll
         for (int i = 0; i < WAVES; ++i)
             a += lds[i];
     }
     return a;
+}
+
+// 1 / sqrt(v), within 2.5 steps of 2^-24: in fp32, of v's part in [1/2, 2).
+__device__ __forceinline__ float inverse_root(double v) {
+    const int half = __builtin_amdgcn_frexp_exp(v) >> 1;            // 0 for 0, infinity and NaN
+    const float part = (float)__builtin_amdgcn_ldexp(v, -2 * half);
+    return __builtin_amdgcn_ldexpf(1.0f / sqrtf(part), -half);
 }
 
 // The largest over aligned groups of LANES (16 or 32) lanes.
@@ -95,8 +107,9 @@ template <typename T, typename W, int WAVES, int NV, bool FP8>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_kernel(RmsTask t) {
     using P = RowPart<T, WAVES, NV>;
     constexpr int VEC = P::VEC, ESIZE = (int)sizeof(T), LANES = kScaleBlock / VEC;
-    __shared__ float lds[2][WAVES];
+    __shared__ double lds[2][WAVES];
     const int cols = (int)t.cols;
+    const double inv_cols = 1.0 / (double)cols;
     const bool res = t.residual != nullptr;
     float w[NV][VEC];
     P::load_weights((const W*)t.weight, cols, 1.0f, w);
@@ -130,16 +143,16 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_kernel(RmsT
         // (outputs may take the inputs' places: the next row is another)
         if (after < t.rows)
             fetch(after);
-        float q = 0.0f;
+        double q = 0.0;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float f = vec_elem<ESIZE>(v[i], e);           // 0 past the row
-                q = __builtin_fmaf(f, f, q);
+                const double f = vec_elem<ESIZE>(v[i], e);          // 0 past the row
+                q = __builtin_fma(f, f, q);
             }
         q = block_sum<WAVES>(q, lds[turn]);
-        const float rstd = 1.0f / sqrtf(q / (float)cols + t.eps);
+        const float rstd = inverse_root(__builtin_fma(q, inv_cols, (double)t.eps));
         if (t.rstd && P::column(0) == 0)
             t.rstd[row] = rstd;
 #pragma unroll
@@ -287,13 +300,13 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_grad_kernel
 // caches hold, an element a lane: 4096 x 12288 bf16 backward 284 us, 1.8 TB/s.
 template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void rms_long_kernel(RmsTask t) {
-    __shared__ float lds[kLongWaves][2];
+    __shared__ double lds[kLongWaves];
     const int64_t row = blockIdx.x;
     const T* x = (const T*)t.x + row * t.ldx;
     const T* r = t.residual ? (const T*)t.residual + row * t.ldr : nullptr;
     T* s = t.residual ? (T*)t.summed + row * t.lds : nullptr;
     const W* w = (const W*)t.weight;
-    float q = 0.0f, none = 0.0f;
+    double q = 0.0;
     for (int64_t c = threadIdx.x; c < t.cols; c += kLongThreads) {
         float v = to_f32(x[c]);
         if (r) {
@@ -302,10 +315,10 @@ __global__ __launch_bounds__(kLongThreads) void rms_long_kernel(RmsTask t) {
             s[c] = sum;
             v = to_f32(sum);
         }
-        q = __builtin_fmaf(v, v, q);
+        q = __builtin_fma((double)v, (double)v, q);
     }
-    block_sum2<kLongWaves>(q, none, lds);
-    const float rstd = 1.0f / sqrtf(q / (float)t.cols + t.eps);
+    q = block_sum<kLongWaves>(q, lds);
+    const float rstd = inverse_root(q / (double)t.cols + (double)t.eps);
     if (t.rstd && threadIdx.x == 0)
         t.rstd[row] = rstd;
     auto value = [&](int64_t c) {
