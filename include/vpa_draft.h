@@ -53,11 +53,13 @@ extern "C" {
  *    model drew).
  *  - A placeholder draft (any id outside [0, V), such as -1) is not accepted,
  *    and its position draws from p_j: a request with fewer drafts ends in
- *    placeholders.  Rows after the first placeholder are not read.
+ *    placeholders.  What rows after the first placeholder hold does not matter.
  *  - A temperature that is not a finite number of at least 2^-100 (0, negative,
  *    NaN) makes p_j 1 at the argmax in vpa.h's order and 0 elsewhere.  So does
  *    a row that has no distribution: all columns -inf, a NaN or +inf among them.
  *  - Where w is 0 everywhere (q_j above p_j at every column), w = p_j.
+ *  - A NaN in draft_probs: a draft with it is not accepted, a column with it has
+ *    w = 0.
  *  - A sample_uniforms value below 0 (or NaN) counts as 0; from 1 on it draws
  *    the last column with w > 0.
  * ------------------------------------------------------------------------ */

@@ -366,9 +366,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uin
             bv[j][h] = LB::fragment(lds + LA::BYTES, p, j, h);
     };
     Wide wide[EXACT ? JN : 1];
-    // A product's scaling, 4 multiply-adds, runs in the shadow of the product after
-    // next: row i's follow row i + 1's products one by one, and the last row's the
-    // next stage's first.
+    // A product's scaling, 4 multiply-adds, runs four products later: row i's follow row
+    // i + 1's products one by one, and the last row's the next stage's first.
     f32x4 p[2][JN] = {};
     float scale[2] = {};
     auto add = [&](int i, int j) {
