@@ -89,8 +89,11 @@ vpa_status vpa_sampled_verify(const void* logits, vpa_dtype dtype, int64_t ld, v
 /* ------------------------------------------------------------------------
  * Distillation from a teacher's top tokens
  *
- * q = softmax(x / t) over a row's V logits, t the temperature.  The teacher
- * names n_top tokens id_j with log probabilities l_j.
+ * q = softmax(x / t) over a row's V logits.  The temperature t is the student's
+ * alone: the teacher names n_top tokens id_j with log probabilities l_j, which are
+ * taken as they are.  A teacher softened by t as well is given by the log
+ * probabilities of its own logits / t (vpa_token_logprobs of those); without a
+ * tail l_j / t says the same, since p is made to sum to 1.
  *  - tail = 0: p_j = exp(l_j) / sum exp(l) over the named tokens, and
  *        loss = sum_j p_j (log p_j - log q(id_j)).
  *  - tail = 1: p_j = exp(l_j), and what they leave, p_0 = max(1 - sum p, 0), is

@@ -248,7 +248,11 @@ def distill_loss(logits, vocab, shard_width, n_shards, teacher_ids, teacher_logp
     row that names nothing has loss 0.  With q = softmax(logits / temperature)
     the loss is sum p (log p - log q), p the teacher's probabilities made to
     sum to 1 over its tokens; with `tail` p is as given and what it leaves of 1
-    is compared with q's sum over all other columns."""
+    is compared with q's sum over all other columns.
+
+    The temperature is the student's alone.  To soften the teacher by it too,
+    give token_logprobs of its logits / temperature (without a tail
+    teacher_logprobs / temperature says the same)."""
     n, _, ld, code = _whole_rows(logits, vocab)
     dev = logits.device
     ids, lp, k = _teacher(teacher_ids, teacher_logprobs, n, dev)
