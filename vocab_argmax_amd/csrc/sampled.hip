@@ -387,19 +387,21 @@ __global__ __launch_bounds__(kThreads) void sample_accept_kernel(SampleTask t, S
 // wavefront a block at a time; of e alone for the requests that subtract a draft
 // distribution, whose weights are summed by a second launch (kSecond).  With
 // kAccept each of a request's workgroups makes its acceptance tests, and the
-// first writes what they say: up to 64 requests that costs less than a launch
-// (1 x 5 x 151936 15.2 us with a launch of its own, 13.2 so; 24 x 4 25.4 and 24.0;
-// 64 x 4 38.9 and 38.6), for more of them more (170 x 6 x 200064 112 and 118).
+// first writes what they say: while the workgroups run at once, 6 a CU, that costs
+// less than a launch (1 x 5 x 151936 14.4 us with a launch of its own, 13.1 so; 24 x 4
+// 23.2 and 21.7; 40 x 4, 1520 workgroups, 28.5 and 27.8; 300 x 3 x 4000 19.4 and 17.5),
+// more of them take as long or longer (48 x 4 x 151936, 1824 of them, 31.8 and 32.0;
+// 64 x 6 x 200064 52.2 and 54.6).
 //
 // Bound by instructions: 18 an element for e, 24 for e - q Z, most of them 64-bit
 // ones, of 5 clocks of a SIMD each: for 170 x 200064 bf16 20 and 27 us of 30 and
 // 32 (the loads alone take 14 and 28).  The next block's loads ahead of a block's
 // sums made it no faster.
 enum SumsStep { kAccept, kFirst, kSecond };
-constexpr int64_t kAcceptInSums = 64;
+constexpr int64_t kAcceptInSums = 6 * 256;         // workgroups
 
-// (6 wavefronts a SIMD: kAccept's second look at an acceptance would leave 5, and 64 x
-// 4 x 151936 took 37.7 us for 36.8)
+// (6 wavefronts a SIMD: kAccept's second look at an acceptance would leave 5, with which
+// 64 x 4 x 151936 took 37.7 us for 36.8)
 template <int ESIZE, int QSIZE, int STEP>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(6))) void
 sample_sums_kernel(SampleTask t, SampleCut cut, const RowStat* stats, Draw* draws, DrawSum* sums) {
@@ -654,7 +656,7 @@ hipError_t launch_typed(const SampleTask& t, void* ws, hipStream_t stream) {
     const dim3 groups((uint32_t)((int64_t)t.n_req * c.draw_groups)), reqs((uint32_t)t.n_req);
     const dim3 block(kThreads);
     hipError_t e = launch(sample_rows_kernel<ESIZE>, rows, block, 0, stream, t, c, stats);
-    if (e == hipSuccess && t.n_req <= kAcceptInSums) {
+    if (e == hipSuccess && groups.x <= kAcceptInSums) {
         e = launch(sample_sums_kernel<ESIZE, QSIZE, kAccept>, groups, block, 0, stream, t, c, stats,
                    draws, sums);
     } else if (e == hipSuccess) {
