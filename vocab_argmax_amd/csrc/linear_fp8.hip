@@ -280,9 +280,10 @@ __device__ __forceinline__ void store_block8(const GemmTask& t, float* part, cha
 // The fast form: 8192^3 475-490 us, 2240-2310 TFLOP/s, the matrix cores busy half of
 // the clocks: a product's 4 multiply-adds take issue slots beside it (a tenth of the
 // time with everything else left in), and operands come at the rate of LDS and the
-// caches (a fifth).  4096^3 65 us.  EXACT, bound by the matrix cores' bf16 rate, the
-// widening (4 instructions for 16 values) and the traffic of smaller tiles: 937 and
-// 130.  The 16-bit product of these sizes takes 790 and 105.
+// caches (a fifth).  4096^3 63-67 us.  EXACT has four bf16 instructions for one of
+// those, the widening (an instruction for 2 values) and smaller tiles, whose operands
+// come twice as often: 916-937 and 120-130.  The 16-bit product of these sizes takes 790
+// and 105.
 template <bool EXACT, int BM, int BN, int WM, int WN, int BUFS>
 __global__ __launch_bounds__(WM* WN * 64, 2) void fp8_tile_kernel(Fp8Task f, uint32_t tiles_m,
                                                                uint32_t tiles_n,
@@ -726,15 +727,16 @@ GemmPlan plan_a_round(int tile, int64_t blocks, int64_t k) {
     return p;
 }
 // More than 64 rows in 64-tiles while a round of workgroups holds them (128 x 4096 x
-// 4096 15.8 us, in 128-tiles 18.5; 100 x 2048 x 8192 11.8 and 16.5; 256 x 4096 x 4096
-// 19.9 and 22.0; 128 x 8192 x 8192 35.7 and 29.9), then in 128-tiles while a round
-// holds those (512 x 8192 x 8192 61 us, in two slices or two rounds 75; 512 x 4096 x
-// 4096 25.6 in the two slices that fit, 28.7 in one, 26.6 in four).  Else the plan of
-// a 16-bit product whose rows have as many bytes, whose stages, tiles and costs are
-// alike.  Exact products have no 256-tiles: widening takes the registers of more.
-// They take up to twice the time from 1024 rows on (4096^3 130 us, by the 8-bit
-// instruction 67; 2048 x 2048 x 50257 417 and 263; 512 x 4096 x 4096 33 and 26), which
-// is what the fast form is for.
+// 4096 18.5 us, in 128-tiles 21.9, fast 15.8 and 18.5; 100 x 2048 x 8192 15.3 and 20.4,
+// fast 11.8 and 16.5; 256 x 4096 x 4096 26.5 and 26.9, fast 19.9 and 22.0; but 128 x
+// 8192 x 8192 48 and 33, fast 35.7 and 29.9), then in 128-tiles while a round holds
+// those (fast, 512 x 8192 x 8192 61 us, in two slices or two rounds 75; 512 x 4096 x 4096
+// 25.6 in the two slices that fit, 28.7 in one, 26.6 in four).  Else the plan of a 16-bit
+// product whose rows have as many bytes, whose stages, tiles and costs are alike.
+// Exact products have no 256-tiles: widening takes the registers of more.
+// They take up to twice the time from 1024 rows on (4096^3 121 us, by the 8-bit
+// instruction 64; 2048 x 2048 x 50257 400 and 257; 512 x 4096 x 4096 30.5 and 25.5),
+// which is what the fast form is for.
 GemmPlan plan_fp8(int64_t m, int64_t n, int64_t k, bool exact) {
     const auto blocks = [&](int64_t tile) {
         return ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
@@ -768,8 +770,10 @@ hipError_t launch_tile(const Fp8Task& f, const GemmPlan& p, hipStream_t stream) 
 
 hipError_t launch_planned(const Fp8Task& f, const GemmPlan& p, hipStream_t stream) {
     hipError_t e;
-    // 128-tiles of which no CU gets a second workgroup have its LDS for 4 stages (512
-    // x 8192 x 8192 61 us, with two 85; 128 x 2048 x 32000 21.8 and 25.8)
+    // The fast form's 128-tiles of which no CU gets a second workgroup have its LDS for
+    // 4 stages (512 x 8192 x 8192 61 us, with two 85; 128 x 2048 x 32000 21.8 and 25.8).
+    // Exact products, which take longer over a stage, have two (512 x 8192 x 8192 72 us,
+    // with four 78; 1024 x 4096 x 4096 40 and 43; 128 x 2048 x 32000 24 and 26).
     const bool deep = ((f.g.m + 127) / 128) * ((f.g.n + 127) / 128) * p.slices <= 256;
     if (p.tile <= 64) {
         const dim3 grid((uint32_t)((f.g.n + kFewRowsCols - 1) / kFewRowsCols), (uint32_t)p.slices,
@@ -782,8 +786,7 @@ hipError_t launch_planned(const Fp8Task& f, const GemmPlan& p, hipStream_t strea
                                                    : fp8_few_rows_kernel<true, 64, 2>;
         e = launch(kernel, grid, dim3(256), 0, stream, f, p.stages_per_slice, part);
     } else if (f.exact) {
-        e = deep ? launch_tile<true, 128, 2, 2, 4>(f, p, stream)
-                 : launch_tile<true, 128, 2, 2, 2>(f, p, stream);
+        e = launch_tile<true, 128, 2, 2, 2>(f, p, stream);
     } else if (p.tile == 256) {
         e = launch_tile<false, 256, 2, 4, 2>(f, p, stream);
     } else {
