@@ -180,7 +180,7 @@ struct Cut {
 };
 
 // A workgroup a segment of a row; with one segment, the whole of it.  Bound by
-// reading: 512 x 50257 fp32 18 us, 1024 x 151936 bf16 54 (5.8-5.9 TB/s).  A chunk is 2
+// reading: 512 x 50257 fp32 18 us, 1024 x 151936 bf16 54-56 (5.7-5.9 TB/s).  A chunk is 2
 // vectors a thread (2048 x 50257 bf16 40.8 us, with 1 40.9, 4 41.5, 8 46.3; 8192 x
 // 16000 57, 61, 58, 77; 64 x 151936 11.2, 11.6, 11.2, 12.1).
 constexpr int kScanVecs = 2;

@@ -102,7 +102,7 @@ struct __attribute__((packed, aligned(1))) LooseBytes {
 // A row in registers: x and the residual of the next one on their way, the weights
 // kept over a workgroup's rows.  With FP8, the 128 columns of a scale lie in 16
 // (bf16) or 32 (fp32) lanes side by side.  Bound by memory: 8192 x 4096 bf16 with
-// a residual 43 us (6.3 TB/s), with y in 8 bits 40 (5.8); 32 rows 4.5, latency.
+// a residual 45 us (6.0 TB/s), with y in 8 bits 40 (5.9); 32 rows 4.4, latency.
 template <typename T, typename W, int WAVES, int NV, bool FP8>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void rms_kernel(RmsTask t) {
     using P = RowPart<T, WAVES, NV>;
@@ -426,7 +426,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void rms_join_kernel(RmsGradTask t
 // A matrix as it is in 8 bits.  LANES lanes side by side hold 128 columns of a row,
 // 16 bytes each; a workgroup takes kThreads / LANES rows of one block of columns at
 // a time, or with SQUARE the 128 rows that share a scale, in registers.  Bound by
-// memory: 151936 x 2048 bf16 192 us (4.9 TB/s), in blocks of 128 x 128 166 (5.6).
+// memory: 151936 x 2048 bf16 179 us (5.3 TB/s), in blocks of 128 x 128 165 (5.7).
 template <typename T, bool SQUARE>
 __global__ __launch_bounds__(kThreads) void quant_kernel(QuantTask t, int64_t blocks_across) {
     constexpr int VEC = 16 / (int)sizeof(T), LANES = kScaleBlock / VEC;

@@ -86,7 +86,7 @@ __device__ __forceinline__ bool is_draft(const SampleTask& t, int32_t id) {
     return id >= 0 && id < t.vocab;
 }
 
-// A workgroup a segment of a row.  Bound by reading: 170 x 6 x 200064 bf16 67 us, 6.0
+// A workgroup a segment of a row.  Bound by reading: 170 x 6 x 200064 bf16 68 us, 6.0
 // TB/s; 1 x 5 x 151936 5.3 us, latency.  A chunk is 2 vectors a thread: 170 x 6 x
 // 200064 bf16 110 us for the whole call, 117 with 8 and 108-117 with 1; 64 x 4 x
 // 151936 37, 39 and 42; 24 x 4 x 32000 14.5, 17.3 and 15.0.
@@ -372,7 +372,7 @@ __device__ __forceinline__ double sum_of_e(const DrawSum* sums, int blocks, doub
     return block_sum_f64(v, lds);
 }
 
-// The acceptance tests alone; a workgroup a request.  5.5 us for 170 of 6 positions,
+// The acceptance tests alone; a workgroup a request.  5.8 us for 170 of 6 positions,
 // latency: the segments' sums, the draft's logit, 64-bit divisions.
 template <int ESIZE, int QSIZE>
 __global__ __launch_bounds__(kThreads) void sample_accept_kernel(SampleTask t, SampleCut cut,
@@ -508,7 +508,7 @@ struct Passing {
 // The column where the running sum passes the random number: its block from the
 // blocks' sums, then its 4 columns a thread.  Where rounding lets none pass, and
 // for random numbers from 1 on, the last one with a weight.  Bound by latency (loads,
-// scans and barriers one after another): 3.4 us for one request, 4.5 for 170.
+// scans and barriers one after another): 3.4 us for one request, 4.3 for 170.
 template <int ESIZE, int QSIZE>
 __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleTask t, SampleCut cut,
                                                                const Draw* draws,
