@@ -18,10 +18,10 @@ constexpr float kFp8Max = 448.0f;
 constexpr uint32_t kAmaxLeast = 0x0D800000u;       // 2^-100
 
 // Quotients by d, those of a division rounded once: a product with a rounded inverse
-// puts one in a thousand ties of e4m3 on the wrong side.  The inverse is in two
-// parts, the second what the first one's rounding left: together they give y / d to
-// 2^-46, so q within its last place, and one step by the remainder, which a
-// multiply-add has exactly, the nearest fp32 value.
+// puts a tie of e4m3 in fourteen on the wrong side.  The inverse is in two parts, the
+// second what the first one's rounding left: together they give y / d to 2^-46, so q
+// within its last place, and one step by the remainder, which a multiply-add has
+// exactly, the nearest fp32 value.
 struct Divisor {
     float d, inverse, rest;
     __device__ __forceinline__ float quotient(float y) const {
