@@ -158,10 +158,11 @@ vpa_status vpa_distill_loss_and_grad(const void* logits, vpa_dtype dtype, int64_
  *
  * s = x + residual, rounded to x's type (s = x without a residual);
  * y = s rstd w, rstd = 1 / sqrt(mean of s^2 over the row + eps).  Squares are
- * summed in 64 bits; rstd is fp32 (+inf for a row of zeros with eps = 0).  The
- * weight is optional.  1 <= cols < 2^31, and fewer than 2^22 rows of those that a
- * workgroup's registers do not hold (past 16384 bf16 or 8192 fp32 columns; in the
- * backward pass 8192 of either).
+ * summed in 64 bits; rstd is fp32 (so +inf where the root is below 2^-128: with
+ * eps = 0, rows of zeros and of the smallest subnormals).  The weight is optional.
+ * 1 <= cols < 2^31, and fewer than 2^22 rows of those that a workgroup's registers
+ * do not hold (past 16384 bf16 or 8192 fp32 columns; in the backward pass 8192 of
+ * either).
  * ------------------------------------------------------------------------ */
 /*  x, residual, y  [rows][cols] of type `dtype`; residual may be NULL.  y may
  *              be x or residual (same pointer and row stride).

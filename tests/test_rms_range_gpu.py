@@ -74,3 +74,17 @@ def test_the_sum_keeps_small_rows_apart_from_eps():
     near(got.rstd, torch.full((1,), 2.0 ** 60, dtype=torch.float64, device=DEV), 4 * U * 2.0 ** 60, "rstd")
     got = vpa.rms_norm(x, eps=0.0, with_rstd=True)
     assert float(got.rstd) == 2.0 ** 80 and bool((got.y == 1).all())
+
+
+@pytest.mark.parametrize("c", [100, 4096, 20000])
+def test_the_ends_of_the_range(c):
+    """Roots below 2^-128 have an infinite rstd; the largest finite rows have their norm."""
+    x = torch.zeros((3, c), device=DEV)
+    x[1] = 2.0 ** -140
+    x[2] = torch.finfo(F32).max
+    got = vpa.rms_norm(x, eps=0.0, with_rstd=True)
+    assert bool(got.rstd[:2].isinf().all()) and bool(got.y[0].isnan().all())
+    assert bool(got.y[1].isinf().all())
+    # (1 / the largest lies below the normal numbers, at a step of 2^-149)
+    near(got.rstd[2:], torch.full((1,), 2.0 ** -128, dtype=torch.float64, device=DEV), 2.0 ** -148, "rstd")
+    near(got.y[2:], torch.ones((1, c), dtype=torch.float64, device=DEV), 2.0 ** -20, "y")
